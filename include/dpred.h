@@ -474,6 +474,114 @@ int dpred_accumulator_save(int32_t world, int64_t n, const float* acc, float* to
 int dpred_accumulator_restore(int32_t world, int64_t n, float* acc, const float* total, void* stream);
 
 /*
+ * Linear-layer products (no counterpart in the pages): what makes the
+ * gradients that the calls above reduce.  Operands are bf16; products are
+ * exact, sums are fp32 in an order fixed by the sizes alone, and every result
+ * is rounded once.  Matrices are row-major with a row stride in elements (at
+ * least the number of columns; ignored where there is one row).  Any size from
+ * 0 (up to 2^30 - 1) and any alignment to the element size is accepted;
+ * operands whose base and row stride are not multiples of 16 bytes are first
+ * copied into `workspace`.
+ *
+ *   dpred_linear:       z = x w^T + bias;  y = act(z) + residual
+ *       x [m, k], w [n, k], y [m, n] of out_dtype; bias [n] of bias_dtype,
+ *       residual [m, n] bf16, preact [m, n] bf16 (receives z) or NULL.
+ *   dpred_linear_dgrad: dx = (dy w + residual) * act'(preact)
+ *       dy [m, n], w [n, k], dx [m, k] of out_dtype; preact [m, k] bf16 is the
+ *       stored pre-activation of the layer before (needed unless act is
+ *       DPRED_ACT_NONE, then ignored), residual [m, k] bf16 or NULL the
+ *       gradient that joins from a residual branch.
+ *   dpred_linear_wgrad: dw = dy^T x, bias_grad = column sums of dy; with
+ *       accumulate != 0 both are added to what the outputs hold.
+ *       dy [m, n], x [m, k], dw [n, k] of out_dtype (bf16: the gradient row a
+ *       flush reads; fp32: the accumulator of the deferred reduction),
+ *       bias_grad [n] fp32 or NULL.
+ *
+ * An empty reduction (k = 0, or n = 0 in dgrad, m = 0 in wgrad) gives the
+ * epilogue of zero.  gelu is the tanh form.  residual may be the output itself
+ * (same type and stride); no output may otherwise overlap an input.
+ * workspace (device, 16-byte aligned): dpred_linear_workspace_bytes() of the
+ * two operands (x and w; dy and w; dy and x), usually 0; it may be reused as
+ * soon as the next call on the same stream.  Asynchronous on `stream`; may be
+ * captured into a CUDA graph.  A bounded device-side wait that gives up
+ * records DPRED_E_TIMEOUT in the device error word.  Errors: DPRED_E_INVAL,
+ * DPRED_E_ALIGN, DPRED_E_SIZE (a row stride less than its columns, a size too
+ * large, workspace too small), DPRED_E_CUDA.
+ */
+#define DPRED_ACT_NONE 0
+#define DPRED_ACT_RELU 1
+#define DPRED_ACT_GELU 2
+#define DPRED_ACT_SILU 3
+size_t dpred_linear_workspace_bytes(const void* a, int64_t a_rows, int64_t a_cols, int64_t lda, const void* b,
+                                    int64_t b_rows, int64_t b_cols, int64_t ldb);
+int dpred_linear(int64_t m, int64_t n, int64_t k, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                 int32_t bias_dtype, const void* bias, int32_t act, const void* residual, int64_t ldr, void* preact,
+                 int64_t ldp, int32_t out_dtype, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                 void* stream);
+int dpred_linear_dgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t lddy, const void* w, int64_t ldw,
+                       int32_t act, const void* preact, int64_t ldp, const void* residual, int64_t ldr,
+                       int32_t out_dtype, void* dx, int64_t lddx, void* workspace, size_t workspace_bytes,
+                       void* stream);
+int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                       int32_t accumulate, int32_t out_dtype, void* dw, int64_t lddw, float* bias_grad,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Orthogonalised updates (no counterpart in the pages): what an owner does
+ * with the whole gradient matrices that reduce-to-owner leaves on it.
+ *
+ *   dpred_newton_schulz: for each of `batch` matrices G (rows x cols):
+ *       X = G / (|G|_F + eps), then `steps` times
+ *       X = a X + (b A + c A^2) X with A = X X^T on the shorter side;
+ *       out = X.  coeffs: host {a, b, c} or NULL for {3.4445, -4.7750, 2.0315}.
+ *   dpred_muon_step: for each matrix, with G = grad, one optimizer step:
+ *       momentum = mu momentum + G          (mu = the argument `momentum`)
+ *       U = nesterov ? G + mu momentum : momentum
+ *       weight = (1 - lr weight_decay) weight - lr scale X(U)
+ *     with X as above.  Weights are bf16 or fp32 (w_dtype), gradients bf16 or
+ *     fp32 (g_dtype), momenta fp32; momentum and weight are updated in place.
+ *
+ * The products run on 16-bit operands (fp16, with the dominant parts kept in
+ * fp32): X is within about 1e-3 (2-norm, relative) of the exact iteration, so
+ * an fp32 out carries that accuracy too.  Norms, sums and accumulators are
+ * fp32: |G|_F must be below about 1e19.  A matrix with a NaN or an infinity
+ * gives an update of NaNs; other matrices of the call are not affected.  A
+ * zero matrix gives zero.  The order of every sum is fixed by the sizes and
+ * the number of matrices of a shape, so a call's results are reproducible.
+ *
+ * Row strides in elements (at least the columns), any size from 0 (long side
+ * up to 2^20, short side up to 65536), any alignment to the element size.
+ * `in` and `out` must not overlap; matrices of one dpred_muon_step call must
+ * not overlap one another.  Matrices of one shape share launches.  mats: host
+ * array, read during the call only.  workspace (device, 256-byte aligned):
+ * dpred_newton_schulz_workspace_bytes() / dpred_muon_workspace_bytes() (only
+ * the shapes matter).  Asynchronous on `stream`; may be captured into a CUDA
+ * graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN, DPRED_E_SIZE, DPRED_E_CUDA; a
+ * bounded device-side wait that gives up records DPRED_E_TIMEOUT in the device
+ * error word.
+ */
+typedef struct {
+    int64_t rows, cols;
+    void* weight;      /* device, [rows, cols] of w_dtype */
+    int64_t ldw;
+    float* momentum;   /* device, [rows, cols] fp32 */
+    int64_t ldm;
+    const void* grad;  /* device, [rows, cols] of g_dtype */
+    int64_t ldg;
+    float scale;       /* factor of the orthogonalised update */
+    int32_t reserved;  /* must be 0 */
+} dpred_muon_matrix;
+size_t dpred_newton_schulz_workspace_bytes(int32_t batch, int64_t rows, int64_t cols);
+int dpred_newton_schulz(int32_t batch, int64_t rows, int64_t cols, int32_t in_dtype, const void* in, int64_t ld,
+                        int64_t batch_stride, int32_t out_dtype, void* out, int64_t ldo, int64_t out_batch_stride,
+                        int32_t steps, const float* coeffs, float eps, void* workspace, size_t workspace_bytes,
+                        void* stream);
+size_t dpred_muon_workspace_bytes(const dpred_muon_matrix* mats, int32_t n);
+int dpred_muon_step(const dpred_muon_matrix* mats, int32_t n, int32_t w_dtype, int32_t g_dtype, float lr,
+                    float momentum, int32_t nesterov, float weight_decay, int32_t steps, const float* coeffs,
+                    float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * ReduceScatter.  [AG] "与 ReduceScatter 的对偶关系" (duality table: M
  * elements in per node, M/N out per node, reduce then shard).
  * in (device) is [n_nodes, m_elems] of in_dtype; out (device) is

@@ -15,6 +15,10 @@ from dataclasses import dataclass
 
 import numpy as np
 
+from . import train
+from .train import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, Muon, linear, linear_dgrad, linear_wgrad,  # noqa: F401
+                    muon_step, newton_schulz, update_scale)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # DPRED_CHECKED=1 in the environment loads the checked build instead (every
 # flush-kernel access bounds-tested on the device; build it with
@@ -110,6 +114,7 @@ def lib() -> ctypes.CDLL:
         L.dpred_selftest_prediv.argtypes = [i32, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint32)]
         L.dpred_host_mapped_pointer.argtypes = [vp, ctypes.POINTER(vp)]
         L.dpred_executor_flush_all_mapped.argtypes = L.dpred_executor_flush_all_from_host.argtypes
+        train.declare(L)
         _lib = L
     return _lib
 

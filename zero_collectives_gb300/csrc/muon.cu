@@ -1,0 +1,569 @@
+// muon.cu -- orthogonalised updates: dpred_newton_schulz and dpred_muon_step.
+//
+// Reduce-to-owner (DeepSpeed issue #8700) leaves every whole reduced gradient
+// matrix on one rank, which is what this update needs: it mixes all rows and
+// columns of a matrix.  For a matrix G with r = min(rows, cols):
+//
+//     X = U / (|U|_F + eps)                     U = G, or the momentum's
+//     repeat:  A = X X^T  (r x r)
+//              X = a X + (b A + c A^2) X
+//
+// (X on its wide side; the polynomial is odd, so the transpose commutes with it.)
+//
+// Precision.  A step's result depends on 1 - sigma^2 style cancellations, so
+// 16-bit roundings of X and of the polynomial are what limits it.  Three
+// choices keep the products at the 16-bit rate with an error of 2e-4 to 1e-3
+// (against 1e-2 to 3e-2 with bf16 everywhere, and 1e-3 to 4e-3 with plain fp16):
+//  - operands are fp16 (11 significant bits, bf16 has 8) scaled by powers of
+//    two so that neither end of the range is reached: X by about sqrt(cols)
+//    (its entries are then near 1, at most the scale), A and the polynomial by 256;
+//  - the diagonals of A and of the polynomial stay in fp32: the polynomial is
+//    near a multiple of the identity, so its diagonal is the only large part;
+//  - X is carried as two fp16 terms (22 bits); only the product with the small
+//    off-diagonal part and the Gram product use the leading term alone.
+// Sums, norms, diagonals and accumulators are fp32.
+//
+// A and the polynomial are symmetric: only tiles that hold an element i <= j
+// are computed, and the epilogue writes each value twice.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "gemm_host.cuh"
+
+namespace dpred {
+namespace gemm {
+namespace {
+
+constexpr int kMaxSteps = 32;
+constexpr int kNormBlocks = 64;   // partial sums of squares per matrix (at most)
+constexpr int kTile = 64;         // the element-wise passes work on 64 x 64 tiles
+constexpr float kOffScale = 256.0f;
+
+// One matrix of a launch as the element-wise passes see it.
+struct MatIn {
+    const void* g;
+    float* mom;        // null: U = G
+    int64_t ldg, ldm;
+};
+
+struct NormArgs {
+    MatIn in[kMaxBatch];
+    int64_t rows, cols;       // as the caller stores them
+    float mu;
+    int nesterov, transposed; // transposed: X is the transpose (rows > cols)
+    int g_vec, m_vec;         // 4-element groups of G / the momentum are aligned
+    float* partial;           // [batch, kNormBlocks]
+    int blocks;               // partials written per matrix
+    float eps, scale;
+    __half* hi;
+    __half* lo;               // [batch, r, ldc]
+    int64_t ldc;
+};
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int valid, bool vec, float (&f)[4]) {
+    if (vec && valid >= 4) {
+        if constexpr (sizeof(T) == 2) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            f[0] = bf16_lo(q.x); f[1] = bf16_hi(q.x); f[2] = bf16_lo(q.y); f[3] = bf16_hi(q.y);
+        } else {
+            const float4 q = *reinterpret_cast<const float4*>(p);
+            f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        f[c] = 0.0f;
+        if (c < valid) {
+            if constexpr (sizeof(T) == 2)
+                f[c] = load_bf16(reinterpret_cast<const __nv_bfloat16*>(p) + c);
+            else
+                f[c] = reinterpret_cast<const float*>(p)[c];
+        }
+    }
+}
+
+__device__ __forceinline__ float block_sum(float v) {
+    __shared__ float warps[8];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int w = 0; w < 8; ++w) v += warps[w];
+    return v;
+}
+
+// m = mu m + g (written back), u = g + mu m or m; the block's share of |U|^2.
+// Bandwidth bound: reads g and m and writes m once.
+template <typename Tg>
+__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormArgs a) {
+    mma::grid_launch_dependents();
+    mma::grid_wait();
+    const MatIn& in = a.in[blockIdx.y];
+    const Tg* g = static_cast<const Tg*>(in.g);
+    const int64_t tr = (a.rows + kTile - 1) / kTile, tc = (a.cols + kTile - 1) / kTile;
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
+    float sum = 0.0f;
+    for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
+        const int64_t i0 = t / tc * kTile, j = t % tc * kTile + c;
+        const int valid = (int)(a.cols - j);
+        if (valid <= 0) continue;
+        float gv[4][4], mv[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + r + 16 * u;
+            if (i < a.rows) {
+                load4(g + i * in.ldg + j, valid, a.g_vec, gv[u]);
+                if (in.mom) load4(in.mom + i * in.ldm + j, valid, a.m_vec, mv[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + r + 16 * u;
+            if (i >= a.rows) continue;
+            if (in.mom) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mv[u][k] = fmaf(a.mu, mv[u][k], gv[u][k]);
+                    gv[u][k] = a.nesterov ? fmaf(a.mu, mv[u][k], gv[u][k]) : mv[u][k];
+                }
+                float* m = in.mom + i * in.ldm + j;
+                if (a.m_vec && valid >= 4) {
+                    *reinterpret_cast<float4*>(m) = make_float4(mv[u][0], mv[u][1], mv[u][2], mv[u][3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < valid) m[k] = mv[u][k];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < valid) sum = fmaf(gv[u][k], gv[u][k], sum);
+        }
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) a.partial[blockIdx.y * kNormBlocks + blockIdx.x] = sum;
+}
+
+// X = scale * U / (|U| + eps) as two fp16 terms, on its wide side.  The
+// partial sums are added in one fixed order by every block.
+template <typename Tg>
+__global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float tile[kTile][kTile + 1];
+    mma::grid_launch_dependents();
+    mma::grid_wait();
+    const MatIn& in = a.in[blockIdx.y];
+    const Tg* g = static_cast<const Tg*>(in.g);
+    float total = 0.0f;
+    for (int k = 0; k < a.blocks; ++k) total += a.partial[blockIdx.y * kNormBlocks + k];
+    const float f = a.scale / (sqrtf(total) + a.eps);
+    const int64_t tr = (a.rows + kTile - 1) / kTile, tc = (a.cols + kTile - 1) / kTile;
+    const int64_t xr = a.transposed ? a.cols : a.rows, xc = a.transposed ? a.rows : a.cols;
+    __half* hi = a.hi + (int64_t)blockIdx.y * xr * a.ldc;
+    __half* lo = a.lo + (int64_t)blockIdx.y * xr * a.ldc;
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
+    for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
+        const int64_t i0 = t / tc * kTile, j0 = t % tc * kTile;
+        float x[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + r + 16 * u;
+            const int valid = (int)(a.cols - j0 - c);
+            if (i < a.rows && valid > 0) {
+                float m[4];
+                load4(g + i * in.ldg + j0 + c, valid, a.g_vec, x[u]);
+                if (in.mom) load4(in.mom + i * in.ldm + j0 + c, valid, a.m_vec, m);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (in.mom) x[u][k] = a.nesterov ? fmaf(a.mu, m[k], x[u][k]) : m[k];
+                    x[u][k] *= f;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[u][k] = 0.0f;
+            }
+        }
+        if (a.transposed) {
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tile[r + 16 * u][c + k] = x[u][k];
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[u][k] = tile[c + k][r + 16 * u];
+        }
+        const int64_t xi0 = a.transposed ? j0 : i0, xj = (a.transposed ? i0 : j0) + c;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = xi0 + r + 16 * u;
+            if (i >= xr || xj >= xc) continue;  // rows are padded to 8 columns, so a group of 4 always fits
+            float h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = __half2float(__float2half_rn(x[u][k]));
+            *reinterpret_cast<uint2*>(hi + i * a.ldc + xj) = make_uint2(pack_half2(h[0], h[1]), pack_half2(h[2], h[3]));
+            *reinterpret_cast<uint2*>(lo + i * a.ldc + xj) =
+                make_uint2(pack_half2(x[u][0] - h[0], x[u][1] - h[1]), pack_half2(x[u][2] - h[2], x[u][3] - h[3]));
+        }
+    }
+}
+
+// -------------------------------------------------------------------- host --
+
+int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// One matrix of a call, in the caller's order and orientation.
+struct Item {
+    MatIn in;
+    void* out;
+    int64_t rows, cols, ldo;
+    float step;  // factor of the orthogonalised value in the output
+};
+
+struct Layout {
+    int64_t r, c, ldr, ldc;
+    int64_t x, gram, diag, per;  // bytes of one X term, of one r x r matrix, of one diagonal, of everything per matrix
+};
+
+Layout layout_of(int64_t rows, int64_t cols) {
+    Layout l;
+    l.r = std::min(rows, cols);
+    l.c = std::max(rows, cols);
+    l.ldr = round8(l.r);
+    l.ldc = round8(l.c);
+    l.x = l.r * l.ldc * 2;
+    l.gram = l.r * l.ldr * 2;
+    l.diag = l.ldr * 4;
+    // X: leading term twice (read and written by the same product), trailing term; A, polynomial; two diagonals; partials
+    l.per = 3 * l.x + 2 * l.gram + 2 * l.diag + kNormBlocks * 4;
+    return l;
+}
+constexpr int kRegions = 8;  // regions of a launch's workspace, each rounded up to 256 bytes
+
+int64_t launch_bytes(const Layout& l, int count) { return l.per * count + 256 * kRegions; }
+
+// Matrices of one shape per launch: all of them up to kMaxBatch.
+int chunk_of(const Layout& l, int count) {
+    (void)l;
+    return std::min(count, kMaxBatch);
+}
+
+struct Params {
+    int g_dtype, out_dtype, nesterov, steps;
+    float mu, keep, eps, a, b, c;
+};
+
+int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cudaStream_t s) {
+    const Item& f = *items[0];
+    const Layout l = layout_of(f.rows, f.cols);
+    const bool transposed = f.rows > f.cols;
+    auto take = [&](int64_t bytes) {
+        char* p = ws;
+        ws += align256(bytes);
+        return p;
+    };
+    __half* hi[2] = {reinterpret_cast<__half*>(take(l.x * count)), reinterpret_cast<__half*>(take(l.x * count))};
+    __half* lo = reinterpret_cast<__half*>(take(l.x * count));
+    __half* gram = reinterpret_cast<__half*>(take(l.gram * count));
+    __half* poly = reinterpret_cast<__half*>(take(l.gram * count));
+    float* diag = reinterpret_cast<float*>(take(l.diag * count));
+    float* coef = reinterpret_cast<float*>(take(l.diag * count));
+    float* partial = reinterpret_cast<float*>(take((int64_t)kNormBlocks * 4 * count));
+
+    // entries of X: near 1 after scaling by about sqrt(c); an orthogonal row of length c has entries near 1/sqrt(c)
+    const float scale = std::exp2(std::round(0.5f * std::log2((float)std::min<int64_t>(l.c, 65536))));
+
+    NormArgs n = {};
+    n.rows = f.rows;
+    n.cols = f.cols;
+    n.mu = q.mu;
+    n.nesterov = q.nesterov;
+    n.transposed = transposed;
+    n.partial = partial;
+    n.eps = q.eps;
+    n.scale = scale;
+    n.hi = hi[0];
+    n.lo = lo;
+    n.ldc = l.ldc;
+    n.g_vec = n.m_vec = 1;
+    const int gs = q.g_dtype == DPRED_F32 ? 4 : 2;
+    for (int k = 0; k < count; ++k) {
+        const MatIn& in = items[k]->in;
+        n.in[k] = in;
+        if (reinterpret_cast<uintptr_t>(in.g) % (4 * gs) || (f.rows > 1 && in.ldg % 4)) n.g_vec = 0;
+        if (in.mom && (reinterpret_cast<uintptr_t>(in.mom) % 16 || (f.rows > 1 && in.ldm % 4))) n.m_vec = 0;
+    }
+    const int64_t tiles = ((f.rows + kTile - 1) / kTile) * ((f.cols + kTile - 1) / kTile);
+    n.blocks = (int)std::min<int64_t>(tiles, kNormBlocks);
+    const dim3 grid1((unsigned)n.blocks, (unsigned)count);
+    const dim3 grid2((unsigned)std::min<int64_t>(tiles, 512), (unsigned)count);
+    if (q.g_dtype == DPRED_F32) {
+        norm_kernel<float><<<grid1, 256, 0, s>>>(n);
+        scale_kernel<float><<<grid2, 256, 0, s>>>(n);
+    } else {
+        norm_kernel<__nv_bfloat16><<<grid1, 256, 0, s>>>(n);
+        scale_kernel<__nv_bfloat16><<<grid2, 256, 0, s>>>(n);
+    }
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return cuda_error(err, "orthogonalised update launch");
+
+    NsEpi e = {};
+    e.gram = gram;
+    e.poly = poly;
+    e.gram_diag = diag;
+    e.coef = coef;
+    e.lo_in = lo;
+    e.lo = lo;
+    e.ldr = l.ldr;
+    e.ldc = l.ldc;
+    e.off_scale = kOffScale;
+    e.off_inv = 1.0f / kOffScale;
+    e.a = q.a;
+    e.b = q.b;
+    e.c = q.c;
+    e.keep = q.keep;
+    e.out_f32 = q.out_dtype == DPRED_F32;
+    const int os = e.out_f32 ? 4 : 2;
+    for (int k = 0; k < count; ++k) {
+        FinalOut& o = e.out[k];
+        o.p = items[k]->out;
+        o.rs = transposed ? 1 : items[k]->ldo;
+        o.cs = transposed ? items[k]->ldo : 1;
+        o.step = items[k]->step / scale;
+        o.vec = !transposed && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (f.rows <= 1 || o.rs * os % 16 == 0);
+    }
+    Plan p = {};
+    p.args.batch = count;
+    p.args.err = device_error_word();
+    for (int step = 0; step < q.steps; ++step) {
+        const Operand x = {hi[step & 1], l.r, l.c, l.ldc, l.r * l.ldc, false};
+        const Operand xt = {hi[step & 1], l.r, l.c, l.ldc, l.r * l.ldc, true};
+        const Operand ga = {gram, l.r, l.r, l.ldr, l.r * l.ldr, false};
+        const Operand pa = {poly, l.r, l.r, l.ldr, l.r * l.ldr, false};
+        const int kc = (int)((l.c + mma::kBlockK - 1) / mma::kBlockK), kr = (int)((l.r + mma::kBlockK - 1) / mma::kBlockK);
+        p.args.m = p.args.n = (int)l.r;
+        p.args.symmetric = 1;
+        p.args.b_mn = 0;
+        p.a = p.b = x;
+        p.args.kblocks = kc;
+        e.alpha = 1.0f / (scale * scale);
+        int rc = run<KIND_GRAM>(p, e, s);
+        if (rc != DPRED_OK) return rc;
+        p.a = p.b = ga;
+        p.args.kblocks = kr;
+        e.alpha = 1.0f / (kOffScale * kOffScale);
+        rc = run<KIND_POLY>(p, e, s);
+        if (rc != DPRED_OK) return rc;
+        p.a = pa;
+        p.b = xt;
+        p.args.b_mn = 1;
+        p.args.n = (int)l.c;
+        p.args.symmetric = 0;
+        e.alpha = 1.0f / kOffScale;
+        e.hi_in = hi[step & 1];
+        e.hi = hi[(step + 1) & 1];
+        rc = step + 1 < q.steps ? run<KIND_APPLY>(p, e, s) : run<KIND_FINAL>(p, e, s);
+        if (rc != DPRED_OK) return rc;
+    }
+    return DPRED_OK;
+}
+
+// Matrices of one shape (up to orientation of the caller's storage) share launches.
+int64_t need_of(std::vector<const Item*>& v) {
+    std::stable_sort(v.begin(), v.end(), [](const Item* x, const Item* y) {
+        return x->rows != y->rows ? x->rows < y->rows : x->cols < y->cols;
+    });
+    int64_t need = 0;
+    for (size_t i = 0; i < v.size();) {
+        size_t j = i;
+        while (j < v.size() && v[j]->rows == v[i]->rows && v[j]->cols == v[i]->cols) ++j;
+        const Layout l = layout_of(v[i]->rows, v[i]->cols);
+        need = std::max(need, launch_bytes(l, chunk_of(l, (int)(j - i))));
+        i = j;
+    }
+    return need;
+}
+
+int run_items(std::vector<Item>& items, const Params& q, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+    std::vector<const Item*> v;
+    for (const Item& it : items)
+        if (it.rows > 0 && it.cols > 0) v.push_back(&it);
+    const int64_t need = need_of(v);
+    if (need == 0) return DPRED_OK;
+    if (!workspace || (int64_t)workspace_bytes < need)
+        return set_error(DPRED_E_SIZE, "workspace of %zu bytes, %lld needed", workspace ? workspace_bytes : (size_t)0, (long long)need);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256) return set_error(DPRED_E_ALIGN, "workspace is not 256-byte aligned");
+    for (size_t i = 0; i < v.size();) {
+        size_t j = i;
+        while (j < v.size() && v[j]->rows == v[i]->rows && v[j]->cols == v[i]->cols) ++j;
+        const int chunk = chunk_of(layout_of(v[i]->rows, v[i]->cols), (int)(j - i));
+        for (; i < j; i += chunk) {
+            const int rc = run_chunk(&v[i], (int)std::min<size_t>(chunk, j - i), q, static_cast<char*>(workspace), s);
+            if (rc != DPRED_OK) return rc;
+        }
+        i = j;
+    }
+    return DPRED_OK;
+}
+
+int check_dtype(int dt, const char* what) {
+    return dt == DPRED_BF16 || dt == DPRED_F32 ? DPRED_OK : set_error(DPRED_E_INVAL, "unknown %s type %d", what, dt);
+}
+
+int check_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return set_error(DPRED_E_INVAL, "a negative size (%lld x %lld)", (long long)rows, (long long)cols);
+    if (rows > (1 << 20) || cols > (1 << 20) || std::min(rows, cols) > 65536)
+        return set_error(DPRED_E_SIZE, "a matrix of %lld x %lld: at most 2^20 on the long and 65536 on the short side",
+                         (long long)rows, (long long)cols);
+    return DPRED_OK;
+}
+
+int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int esize, const char* name) {
+    if (rows == 0 || cols == 0) return DPRED_OK;
+    if (!p) return set_error(DPRED_E_INVAL, "%s is null", name);
+    if (reinterpret_cast<uintptr_t>(p) % esize) return set_error(DPRED_E_ALIGN, "%s is not aligned to its element size", name);
+    if (rows > 1 && ld < cols)
+        return set_error(DPRED_E_SIZE, "%s: row stride %lld is less than its %lld columns", name, (long long)ld, (long long)cols);
+    return DPRED_OK;
+}
+
+int check_params(int steps, const float* coeffs, float eps) {
+    if (steps < 1 || steps > kMaxSteps) return set_error(DPRED_E_INVAL, "steps %d outside 1..%d", steps, kMaxSteps);
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return set_error(DPRED_E_INVAL, "eps must be finite and not negative");
+    if (coeffs)
+        for (int k = 0; k < 3; ++k)
+            if (!std::isfinite(coeffs[k])) return set_error(DPRED_E_INVAL, "a coefficient is not finite");
+    return DPRED_OK;
+}
+
+void set_coeffs(Params& q, const float* coeffs) {
+    // the quintic whose slope at 0 is as steep as keeps [0, 1] within about 0.7 .. 1.2
+    q.a = coeffs ? coeffs[0] : 3.4445f;
+    q.b = coeffs ? coeffs[1] : -4.7750f;
+    q.c = coeffs ? coeffs[2] : 2.0315f;
+}
+
+template <typename F>
+int guarded(F f) {  // no C++ exception leaves a C entry point
+    try {
+        return f();
+    } catch (const std::exception& e) {
+        return set_error(DPRED_E_INVAL, "host failure: %s", e.what());
+    }
+}
+
+}  // namespace
+}  // namespace gemm
+}  // namespace dpred
+
+using namespace dpred;
+using namespace dpred::gemm;
+
+extern "C" size_t dpred_newton_schulz_workspace_bytes(int32_t batch, int64_t rows, int64_t cols) {
+    if (batch <= 0 || rows <= 0 || cols <= 0 || check_shape(rows, cols) != DPRED_OK) return 0;
+    const Layout l = layout_of(rows, cols);
+    return (size_t)launch_bytes(l, chunk_of(l, batch));
+}
+
+extern "C" int dpred_newton_schulz(int32_t batch, int64_t rows, int64_t cols, int32_t in_dtype, const void* in, int64_t ld,
+                                   int64_t batch_stride, int32_t out_dtype, void* out, int64_t ldo,
+                                   int64_t out_batch_stride, int32_t steps, const float* coeffs, float eps,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    return guarded([&]() -> int {
+        int rc;
+        if (batch < 0) return set_error(DPRED_E_INVAL, "batch < 0");
+        if ((rc = check_shape(rows, cols)) != DPRED_OK || (rc = check_params(steps, coeffs, eps)) != DPRED_OK ||
+            (rc = check_dtype(in_dtype, "input")) != DPRED_OK || (rc = check_dtype(out_dtype, "output")) != DPRED_OK)
+            return rc;
+        if (batch == 0 || rows == 0 || cols == 0) return DPRED_OK;
+        const int is = in_dtype == DPRED_F32 ? 4 : 2, os = out_dtype == DPRED_F32 ? 4 : 2;
+        if ((rc = check_matrix(in, rows, cols, ld, is, "in")) != DPRED_OK || (rc = check_matrix(out, rows, cols, ldo, os, "out")) != DPRED_OK)
+            return rc;
+        if (batch > 1 && batch_stride < 0) return set_error(DPRED_E_SIZE, "a negative batch stride");
+        if (batch > 1 && out_batch_stride < (rows - 1) * ldo + cols && out_batch_stride < cols)
+            return set_error(DPRED_E_SIZE, "output matrices overlap (batch stride %lld)", (long long)out_batch_stride);
+        Params q = {};
+        q.g_dtype = in_dtype;
+        q.out_dtype = out_dtype;
+        q.steps = steps;
+        q.eps = eps;
+        set_coeffs(q, coeffs);
+        std::vector<Item> items(batch);
+        for (int k = 0; k < batch; ++k) {
+            Item& it = items[k];
+            it.in = {static_cast<const char*>(in) + (int64_t)k * batch_stride * is, nullptr, ld, 0};
+            it.out = static_cast<char*>(out) + (int64_t)k * out_batch_stride * os;
+            it.rows = rows;
+            it.cols = cols;
+            it.ldo = ldo;
+            it.step = 1.0f;
+        }
+        return run_items(items, q, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    });
+}
+
+extern "C" size_t dpred_muon_workspace_bytes(const dpred_muon_matrix* mats, int32_t n) {
+    if (!mats || n <= 0) return 0;
+    size_t need = 0;
+    guarded([&]() -> int {
+        std::vector<Item> items(n);
+        std::vector<const Item*> v;
+        for (int k = 0; k < n; ++k) {
+            if (check_shape(mats[k].rows, mats[k].cols) != DPRED_OK) return DPRED_E_SIZE;
+            items[k].rows = mats[k].rows;
+            items[k].cols = mats[k].cols;
+            if (mats[k].rows > 0 && mats[k].cols > 0) v.push_back(&items[k]);
+        }
+        need = (size_t)need_of(v);
+        return DPRED_OK;
+    });
+    return need;
+}
+
+extern "C" int dpred_muon_step(const dpred_muon_matrix* mats, int32_t n, int32_t w_dtype, int32_t g_dtype, float lr,
+                               float momentum, int32_t nesterov, float weight_decay, int32_t steps, const float* coeffs,
+                               float eps, void* workspace, size_t workspace_bytes, void* stream) {
+    return guarded([&]() -> int {
+        int rc;
+        if (n < 0 || (n > 0 && !mats)) return set_error(DPRED_E_INVAL, "mats is null or n < 0");
+        if ((rc = check_params(steps, coeffs, eps)) != DPRED_OK || (rc = check_dtype(w_dtype, "weight")) != DPRED_OK ||
+            (rc = check_dtype(g_dtype, "gradient")) != DPRED_OK)
+            return rc;
+        if (!std::isfinite(lr) || !std::isfinite(momentum) || !std::isfinite(weight_decay))
+            return set_error(DPRED_E_INVAL, "lr, momentum and weight_decay must be finite");
+        Params q = {};
+        q.g_dtype = g_dtype;
+        q.out_dtype = w_dtype;
+        q.nesterov = nesterov != 0;
+        q.steps = steps;
+        q.mu = momentum;
+        q.keep = 1.0f - lr * weight_decay;
+        q.eps = eps;
+        set_coeffs(q, coeffs);
+        const int gs = g_dtype == DPRED_F32 ? 4 : 2, wsz = w_dtype == DPRED_F32 ? 4 : 2;
+        std::vector<Item> items(n);
+        for (int k = 0; k < n; ++k) {
+            const dpred_muon_matrix& m = mats[k];
+            if ((rc = check_shape(m.rows, m.cols)) != DPRED_OK ||
+                (rc = check_matrix(m.weight, m.rows, m.cols, m.ldw, wsz, "weight")) != DPRED_OK ||
+                (rc = check_matrix(m.momentum, m.rows, m.cols, m.ldm, 4, "momentum")) != DPRED_OK ||
+                (rc = check_matrix(m.grad, m.rows, m.cols, m.ldg, gs, "grad")) != DPRED_OK)
+                return rc;
+            if (!std::isfinite(m.scale)) return set_error(DPRED_E_INVAL, "a matrix's scale is not finite");
+            Item& it = items[k];
+            it.in = {m.grad, m.momentum, m.ldg, m.ldm};
+            it.out = m.weight;
+            it.rows = m.rows;
+            it.cols = m.cols;
+            it.ldo = m.ldw;
+            it.step = -lr * m.scale;
+        }
+        return run_items(items, q, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    });
+}
