@@ -60,9 +60,48 @@ int64_t tiles_of(const Args& a, int bm, int bn) {
     return n;
 }
 
+int resident_pairs(const void* kernel, int threads, int smem) {
+    static std::mutex mu;
+    static int cached[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(2 * sm_count()));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        cached[dev] = n < sm_count() / 2 ? n : sm_count() / 2;
+    }
+    return cached[dev];
+}
+
 Shape choose_shape(const Args& a) {
     Shape s;
     const int sms = sm_count();
+    s.pairs = false;
+    if (a.kblocks > 0 && a.m > 128) {
+        const int64_t wide = tiles_of(a, 256, 256) * a.batch, narrow = tiles_of(a, 256, 128) * a.batch;
+        if (narrow * 2 >= sms) {
+            s.pairs = true;
+            s.bn = wide * 2 >= sms && a.n > 128 ? 256 : 128;
+            s.tiles = s.bn == 256 ? wide : narrow;
+            s.split = 1;
+            return s;
+        }
+    }
     s.bn = a.n <= 32 && !a.b_mn ? 32 : a.n <= 64 ? 64 : tiles_of(a, 128, 128) * a.batch >= sms ? 128 : 64;
     s.tiles = tiles_of(a, 128, s.bn) * a.batch;
     s.split = 1;

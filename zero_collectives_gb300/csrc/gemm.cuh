@@ -76,6 +76,7 @@ struct Args {
     int symmetric;       // only elements i <= j are needed (the epilogue mirrors them)
     int a_mn, b_mn;      // operand majors
     int split;           // CTAs of a cluster that share the reduction
+    int regions;         // split kernel: accumulators that share a CTA's part of the reduction
     int bf16;
     int* err;
 };
@@ -399,9 +400,10 @@ __device__ __forceinline__ void apply_epilogue(const typename EpiOf<KIND>::T& e,
 // The tile of index t inside one batch entry.  In symmetric mode tile row tm
 // starts at the first tile column that reaches its diagonal.
 __device__ __forceinline__ void tile_at(const Args& g, int t, int bm, int bn, int& tm, int& tn) {
-    if (!g.symmetric) {
-        tm = t % g.tiles_m;
-        tn = t / g.tiles_m;
+    if (!g.symmetric) {  // groups of 16 tile rows, so that tiles in flight share operands in L2
+        const int group = t / (16 * g.tiles_n), rows = min(16, g.tiles_m - group * 16), in = t - group * 16 * g.tiles_n;
+        tm = group * 16 + in % rows;
+        tn = in / rows;
         return;
     }
     tm = 0;
@@ -424,6 +426,10 @@ __device__ __forceinline__ void tile_at(const Args& g, int t, int bm, int bn, in
 // memory in rank order, so a result never depends on timing.  This is the
 // kernel of the calls with few tiles: a short call spreads its weight reads
 // over up to 8 times as many SMs.
+//
+// fp32 results (regions = 256 / BN) give each part of a CTA's reduction its own
+// accumulator in tensor memory, added in fp32 registers at the end: the tensor
+// cores' accumulators truncate, about 1.9e-8 of the sum per 16-element step.
 
 constexpr int kSplitThreads = 192;  // producer warp, issuing warp, four epilogue warps
 
@@ -434,6 +440,20 @@ __host__ __device__ constexpr int split_stages() {
 template <int BN>
 __host__ __device__ constexpr int split_smem() {  // stages + alignment; barriers are static
     return split_stages<BN>() * (128 * 128 + BN * 128) + 1024;
+}
+
+// 32 columns of one row, added over a CTA's accumulators.
+template <int BN>
+__device__ __forceinline__ void read_regions(uint32_t addr, int regions, float (&v)[32]) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+    for (int r = 0; r < regions; ++r) {
+        float w[32];
+        mma::tmem_ld32(addr + r * BN, w);
+        mma::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] += w[c];
+    }
 }
 
 // Adds V columns of one row over the cluster's partial tiles, in rank order.
@@ -458,7 +478,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     using namespace mma;
     constexpr int S = split_stages<BN>();
     constexpr uint32_t kA = 128 * 128, kStage = kA + BN * 128;
-    constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+    constexpr uint32_t kCols = 256;  // two CTAs per SM together allocate all 512
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full[S], empty[S], done;
     __shared__ uint32_t tmem_slot;
@@ -471,6 +491,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     tile_at(g, tile - batch * g.tiles_per_batch, 128, BN, tm, tn);
     const int kb0 = (int)((int64_t)g.kblocks * rank / g.split), kb1 = (int)((int64_t)g.kblocks * (rank + 1) / g.split);
     const int nkb = kb1 - kb0;
+    const int regions = min(g.regions, nkb);
 
     if (threadIdx.x == 0) {
         if (g.kblocks) {
@@ -528,8 +549,14 @@ __global__ void __launch_bounds__(kSplitThreads)
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = instr_desc(128, BN, g.bf16, g.a_mn, g.b_mn);
+            int region = 0;
             for (int it = 0; it < nkb; ++it) {
                 const int s = it % S;
+                bool first = it == 0;
+                if (region + 1 < regions && it >= nkb * (region + 1) / regions) {
+                    ++region;
+                    first = true;
+                }
                 if (!tma::mbar_wait(&full[s], (it / S) & 1)) {
                     record_device_error(g.err, DPRED_E_TIMEOUT);
                     ok = false;
@@ -541,7 +568,7 @@ __global__ void __launch_bounds__(kSplitThreads)
                 for (int k = 0; k < kBlockK / 16; ++k) {
                     const uint64_t da = operand_desc(a + (g.a_mn ? k * 2048 : k * 32), g.a_mn);
                     const uint64_t db = operand_desc(b + (g.b_mn ? k * 2048 : k * 32), g.b_mn);
-                    issue<1>(tmem, da, db, idesc, (it | k) != 0);
+                    issue<1>(tmem + region * BN, da, db, idesc, !first || k != 0);
                 }
                 commit<1>(tma::smem_addr(&empty[s]));
             }
@@ -562,13 +589,7 @@ __global__ void __launch_bounds__(kSplitThreads)
             for (int c0 = 0; c0 < BN; c0 += 32) {
                 float v[32];
                 __syncwarp();
-                if (nkb && ok) {
-                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-                }
+                read_regions<BN>(tmem + ((uint32_t)(q * 32) << 16) + c0, ok ? regions : 0, v);
                 if (i < g.m && ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
@@ -586,13 +607,7 @@ __global__ void __launch_bounds__(kSplitThreads)
             for (int c0 = 0; c0 < BN; c0 += 32) {
                 float v[32];
                 __syncwarp();
-                if (nkb && ok) {
-                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-                }
+                read_regions<BN>(tmem + ((uint32_t)(q * 32) << 16) + c0, ok ? regions : 0, v);
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c0 + c) * 128 + r) * 4), "f"(v[c]) : "memory");
@@ -623,6 +638,232 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
 }
 
+// ------------------------------------------------------------- tile kernel --
+//
+// The kernel of the calls with many tiles: persistent CTA pairs, one
+// 256 x BN tile per pair and step.  The pair's tcgen05.mma (cta_group::2)
+// reads A rows 0..127 and B rows 0..BN/2-1 from the even CTA's shared memory and
+// the other halves from the odd one's, so every operand byte is staged once
+// per pair.  Accumulators are double-buffered in tensor memory: eight epilogue
+// warps drain one while the issuing thread fills the other.
+//
+// PROMOTE (fp32 results): the tensor cores' accumulators truncate, which costs
+// about 1.9e-8 of the sum per 16-element step (measured: 1.9e-5 after 16384
+// elements).  Here an accumulator takes kPromoteBlocks reduction blocks (512
+// elements, 6e-7) and the epilogue threads add it to fp32 registers.
+
+constexpr int kTileThreads = 320;  // producer warp, issuing warp, eight epilogue warps
+constexpr int kPromoteBlocks = 8;
+
+template <int BN>
+__host__ __device__ constexpr int tile_stages() {
+    return BN == 256 ? 6 : 8;
+}
+template <int BN>
+__host__ __device__ constexpr int tile_smem() {
+    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 1024;
+}
+
+template <int KIND, int BN, bool PROMOTE>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::T e) {
+    using namespace mma;
+    constexpr int S = tile_stages<BN>();
+    constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;
+    constexpr uint32_t kCols = 2 * BN;
+    constexpr int kHalf = BN / 2;  // columns per epilogue warp
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int total = g.tiles_per_batch * g.batch;
+    const int chunk = PROMOTE ? kPromoteBlocks : g.kblocks;
+
+    if (threadIdx.x == 0) {
+        prefetch_map(&ma);
+        prefetch_map(&mb);
+        for (int s = 0; s < S; ++s) {
+            tma::mbar_init(&full[s], 1);   // the even CTA's expected bytes (both CTAs' copies)
+            tma::mbar_init(&empty[s], 1);  // the issuing thread's commit
+        }
+        for (int a = 0; a < 2; ++a) {
+            tma::mbar_init(&acc_full[a], 1);
+            tma::mbar_init(&acc_empty[a], 16);  // eight epilogue warps of each CTA
+        }
+        tma::fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc<2>(tma::smem_addr(&tmem_slot), kCols);
+    fence_before();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    grid_launch_dependents();
+    grid_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok; tile += pairs) {
+                const int batch = tile / g.tiles_per_batch;
+                int tm, tn;
+                tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
+                const int i0 = tm * 256 + (int)rank * 128, j0 = tn * BN + (int)rank * (BN / 2);
+                for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
+                    const int s = it % S;
+                    if (it >= S && !tma::mbar_wait(&empty[s], (it / S - 1) & 1)) {
+                        record_device_error(g.err, DPRED_E_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a = base + s * kStage, b = a + kA, bar = tma::smem_addr(&full[s]);
+                    if (rank == 0) tma::mbar_arrive_expect_tx(&full[s], 2 * kStage);
+                    const int k0 = kb * kBlockK;
+                    if (g.a_mn) {
+                        load_box_pair(a, &ma, bar, i0, k0, batch);
+                        load_box_pair(a + 8192, &ma, bar, i0 + 64, k0, batch);
+                    } else {
+                        load_box_pair(a, &ma, bar, k0, i0, batch);
+                    }
+                    if (g.b_mn) {
+#pragma unroll
+                        for (int c = 0; c < BN / 128; ++c) load_box_pair(b + c * 8192, &mb, bar, j0 + c * 64, k0, batch);
+                    } else {
+                        load_box_pair(b, &mb, bar, k0, j0, batch);
+                    }
+                }
+            }
+            if (!ok) {  // copies in flight land within microseconds, or never: leave after a bounded pause
+                const long long t0 = clock64();
+                while (clock64() - t0 < 20000000LL) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = instr_desc(256, BN, g.bf16, g.a_mn, g.b_mn);
+            int it = 0, fill = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok; tile += pairs) {
+                for (int kb = 0; kb < g.kblocks && ok; ++fill) {
+                    const int a = fill & 1;
+                    if (fill >= 2 && !tma::mbar_wait(&acc_empty[a], (fill / 2 - 1) & 1)) {
+                        record_device_error(g.err, DPRED_E_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const int stop = min(kb + chunk, g.kblocks);
+                    for (int first = kb; kb < stop; ++kb, ++it) {
+                        const int s = it % S;
+                        if (!tma::mbar_wait(&full[s], (it / S) & 1)) {
+                            record_device_error(g.err, DPRED_E_TIMEOUT);
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint32_t pa = base + s * kStage, pb = pa + kA;
+#pragma unroll
+                        for (int k = 0; k < kBlockK / 16; ++k) {
+                            const uint64_t da = operand_desc(pa + (g.a_mn ? k * 2048 : k * 32), g.a_mn);
+                            const uint64_t db = operand_desc(pb + (g.b_mn ? k * 2048 : k * 32), g.b_mn);
+                            issue<2>(tmem + a * BN, da, db, idesc, kb != first || k != 0);
+                        }
+                        commit<2>(tma::smem_addr(&empty[s]));
+                    }
+                    if (ok) commit<2>(tma::smem_addr(&acc_full[a]));
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, half = (warp - 2) / 4;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * kHalf;
+        const uint32_t drained0 = map_rank(tma::smem_addr(&acc_empty[0]), 0), drained1 = map_rank(tma::smem_addr(&acc_empty[1]), 0);
+        int fill = 0;
+        bool ok = true;
+        for (int tile = pair; tile < total && ok; tile += pairs) {
+            const int batch = tile / g.tiles_per_batch;
+            int tm, tn;
+            tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
+            const int i = tm * 256 + (int)rank * 128 + q * 32 + lane, j = tn * BN + half * kHalf;
+            if constexpr (PROMOTE) {
+                float sum[kHalf / 32][32];
+#pragma unroll
+                for (int c = 0; c < kHalf / 32; ++c)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) sum[c][x] = 0.0f;
+                for (int kb = 0; kb < g.kblocks && ok; kb += chunk, ++fill) {
+                    const int a = fill & 1;
+                    ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&acc_full[a], (fill / 2) & 1));
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int c = 0; c < kHalf / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(lanes + a * BN + c * 32, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) sum[c][x] += v[x];
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
+                }
+                if (ok && i < g.m) {
+#pragma unroll
+                    for (int c = 0; c < kHalf / 8; ++c) {
+                        float t[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) t[x] = sum[c / 4][(c % 4) * 8 + x];
+                        if (j + c * 8 < g.n) apply_epilogue<KIND, 8>(e, g, batch, i, j + c * 8, t);
+                    }
+                }
+            } else {
+                const int a = fill & 1;
+                ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&acc_full[a], (fill / 2) & 1));
+                if (!ok) break;
+                ++fill;
+                fence_after();
+#pragma unroll 1
+                for (int c = 0; c < kHalf; c += 32) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(lanes + a * BN + c, v);
+                    tmem_wait_ld();
+                    if (c + 32 == kHalf) {  // the accumulator is in registers: the next tile may overwrite it
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
+                    }
+                    if (i < g.m && j + c < g.n) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) {
+                            float t[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) t[y] = v[x + y];
+                            apply_epilogue<KIND, 8>(e, g, batch, i, j + c + x, t);
+                        }
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) record_device_error(g.err, DPRED_E_TIMEOUT);
+        __syncwarp();
+    }
+    fence_before();
+    cluster_sync();  // no CTA leaves while the other may still signal it or read its shared memory
+    if (warp == 1) {
+        fence_after();
+        tmem_free<2>(tmem, kCols);
+    }
+}
+
 // ------------------------------------------------------------ host interface --
 
 // One operand: `rows` rows of `cols` 16-bit elements, `ld` elements apart,
@@ -636,6 +877,7 @@ struct Operand {
 struct Plan {
     Args args;
     Operand a, b;
+    int fp32_result;  // the result is stored in fp32: keep the accumulators' truncation below its precision
 };
 
 }  // namespace gemm

@@ -8,9 +8,13 @@ namespace dpred {
 namespace gemm {
 
 struct Shape {
+    bool pairs;   // tile kernel (CTA pairs, 256 x bn tiles); else split kernel (128 x bn)
     int bn, split;
     int64_t tiles;
 };
+
+// CTA pairs that can be resident at once (all kernels of the family take a whole SM per CTA).
+int resident_pairs(const void* kernel, int threads, int smem);
 
 int make_map(const Operand& o, int batch, int box_rows, bool bf16, CUtensorMap* m);
 bool tma_able(const void* p, int64_t rows, int64_t ld);
@@ -35,6 +39,7 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
     g.tiles_n = (g.n + BN - 1) / BN;
     g.tiles_per_batch = (int)tiles_of(g, 128, BN);
     g.split = sh.split;
+    g.regions = p.fp32_result ? 256 / BN : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sh.tiles * sh.split));
     cfg.blockDim = dim3(kSplitThreads);
@@ -53,10 +58,54 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
     return err == cudaSuccess ? DPRED_OK : cuda_error(err, "matrix product launch");
 }
 
+template <int KIND, int BN, bool PROMOTE>
+int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+    static bool attr[64] = {};
+    auto kernel = tile_kernel<KIND, BN, PROMOTE>;
+    cudaError_t err = ensure_smem_attr(kernel, tile_smem<BN>(), attr);
+    if (err != cudaSuccess) return cuda_error(err, "shared-memory limit of a matrix product");
+    CUtensorMap ma = {}, mb = {};
+    int rc = make_map(p.a, p.args.batch, 128, p.args.bf16, &ma);
+    if (rc != DPRED_OK) return rc;
+    rc = make_map(p.b, p.args.batch, BN / 2, p.args.bf16, &mb);
+    if (rc != DPRED_OK) return rc;
+    Args g = p.args;
+    g.tiles_m = (g.m + 255) / 256;
+    g.tiles_n = (g.n + BN - 1) / BN;
+    g.tiles_per_batch = (int)tiles_of(g, 256, BN);
+    g.split = 1;
+    g.regions = 1;
+    const int pairs = resident_pairs(reinterpret_cast<const void*>(kernel), kTileThreads, tile_smem<BN>());
+    if (pairs < 1) return set_error(DPRED_E_CUDA, "no CTA pair fits on this device");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (sh.tiles < pairs ? sh.tiles : pairs)));
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = tile_smem<BN>();
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, g, e);
+    return err == cudaSuccess ? DPRED_OK : cuda_error(err, "matrix product launch");
+}
+
 template <int KIND>
 int run(const Plan& p, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
     const Shape sh = choose_shape(p.args);
     if (sh.tiles * sh.split > 0x7FFFFFFF) return set_error(DPRED_E_SIZE, "a matrix product of too many tiles");
+    if (sh.pairs) {
+        if constexpr (KIND == KIND_LINEAR) {
+            if (p.fp32_result)
+                return sh.bn == 256 ? launch_tiles<KIND, 256, true>(p, sh, e, s) : launch_tiles<KIND, 128, true>(p, sh, e, s);
+        }
+        return sh.bn == 256 ? launch_tiles<KIND, 256, false>(p, sh, e, s) : launch_tiles<KIND, 128, false>(p, sh, e, s);
+    }
     switch (sh.bn) {
         case 32: return launch_split<KIND, 32>(p, sh, e, s);
         case 64: return launch_split<KIND, 64>(p, sh, e, s);
