@@ -11,6 +11,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "mma.cuh"
 
@@ -26,27 +28,36 @@ enum Kind : int {
     KIND_POLY = 2,    // Newton-Schulz: off-diagonal of b A + c A^2 in fp16, a + its diagonal in fp32
     KIND_APPLY = 3,   // Newton-Schulz: the next X, as two fp16 terms
     KIND_FINAL = 4,   // Newton-Schulz: the last X, stored or applied to a weight
+    // The tile kernel's linear layers, by what their epilogue can contain (its
+    // code then holds nothing else; chosen by linear_kind()):
+    KIND_PLAIN = 5,   // bf16 result, bias and residual at most
+    KIND_ACT = 6,     // bf16 result, forward activation and stored pre-activation
+    KIND_GRAD = 7,    // bf16 result, activation's gradient
+    KIND_F32 = 8,     // fp32 result: everything
 };
+__host__ __device__ constexpr bool is_linear(int kind) { return kind == KIND_LINEAR || kind >= KIND_PLAIN; }
 
 // A linear layer's epilogue.  In order: t += bias; pre_out = t; t = act(t);
-// t += residual; t *= act'(z); t += what the output holds; out = t.
+// t += residual; t *= act'(z); t += what the output holds; out = t.  All
+// matrices are row-major with unit column stride.
 struct LinearEpi {
     void* out;
     const void* bias;
     const __nv_bfloat16* res;
     __nv_bfloat16* pre_out;
     const __nv_bfloat16* z;
-    int64_t o_rs, o_cs, r_rs, r_cs, p_rs, p_cs, z_rs, z_cs;  // element strides along i and j
-    int out_f32, bias_f32, bias_on_row, act, accumulate;
-    int vec;  // every matrix present is contiguous along j with 16-byte aligned rows
+    int64_t o_ld, r_ld, p_ld, z_ld;
+    int out_f32, bias_f32, act, accumulate;
+    int swapped;  // the product computes the output's transpose: its rows (i) are the output's columns
+    int vec;      // every matrix present has 16-byte aligned rows, the bias too
 };
 
 // One matrix of a Newton-Schulz batch as its last product writes it.
 struct FinalOut {
     void* p;
-    int64_t rs, cs;   // element strides along i and j
+    int64_t ld;
     float step;       // multiplies the orthogonalised value (negative: subtracted from the weight)
-    int vec;
+    int vec;          // 16-byte aligned rows
 };
 constexpr int kMaxBatch = 64;  // matrices per Newton-Schulz launch (their output table travels in the launch)
 
@@ -65,6 +76,7 @@ struct NsEpi {
     float a, b, c;     // the polynomial's coefficients
     float keep;        // FINAL: factor of the old weight (0: store)
     int out_f32;       // FINAL
+    int transposed;    // FINAL: the outputs are stored with rows and columns exchanged
     FinalOut out[kMaxBatch];
 };
 
@@ -83,43 +95,64 @@ struct Args {
 
 template <int KIND>
 struct EpiOf {
-    using T = NsEpi;
+    using T = std::conditional_t<is_linear(KIND), LinearEpi, NsEpi>;
 };
-template <>
-struct EpiOf<KIND_LINEAR> {
-    using T = LinearEpi;
-};
+
+// The tile kernel's kind for a linear layer's options.
+inline int linear_kind(const LinearEpi& e) {
+    if (e.out_f32) return KIND_F32;
+    if (e.accumulate || (e.z && e.pre_out)) return KIND_LINEAR;
+    if (e.z) return KIND_GRAD;
+    return e.act || e.pre_out ? KIND_ACT : KIND_PLAIN;
+}
 
 // ------------------------------------------------------------- activations --
 
-// The logistic function; its two approximations (exponential and reciprocal,
-// both within 2 ulp or so in fp32) are far below the bf16 rounding of what is stored.
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// The logistic function of -x / log2(e), 1 / (1 + 2^x), from the hardware's
+// approximate exponential and reciprocal (about 2^-22 relative each, far below
+// the bf16 rounding of what is stored).
+__device__ __forceinline__ float logistic2(float x) {
+    float t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // gelu is the tanh form: 0.5 z (1 + tanh(u)) = z * logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3).
-constexpr float kGeluQ = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGeluQ = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 
-__device__ __forceinline__ float activate(float z, int act) {
-    if (act == ACT_RELU) return z > 0.0f ? z : 0.0f;
-    if (act == ACT_GELU) return z * logistic(kGeluQ * z * fmaf(kGeluC, z * z, 1.0f));
-    if (act == ACT_SILU) return z * logistic(z);
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? z : 0.0f;
+    if constexpr (ACT == ACT_GELU) return z * logistic2(z * fmaf(-kLog2e * kGeluQ * kGeluC, z * z, -kLog2e * kGeluQ));
+    if constexpr (ACT == ACT_SILU) return z * logistic2(-kLog2e * z);
     return z;
 }
 
-__device__ __forceinline__ float activate_grad(float z, int act) {
-    if (act == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == ACT_GELU) {
+template <int ACT>
+__device__ __forceinline__ float activate_grad(float z) {
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == ACT_GELU) {
         // beyond |z| = 1000 the logistic is 0 or 1 exactly; the clamp keeps z^2 finite there
         const float z2 = fminf(z * z, 1e6f);
-        const float p = logistic(kGeluQ * z * fmaf(kGeluC, z2, 1.0f));
-        return fmaf(z * p * (1.0f - p), kGeluQ * fmaf(3.0f * kGeluC, z2, 1.0f), p);
+        const float p = logistic2(z * fmaf(-kLog2e * kGeluQ * kGeluC, z2, -kLog2e * kGeluQ));
+        return fmaf(z * p * (1.0f - p), fmaf(3.0f * kGeluC * kGeluQ, z2, kGeluQ), p);
     }
-    if (act == ACT_SILU) {
-        const float p = logistic(z);
+    if constexpr (ACT == ACT_SILU) {
+        const float p = logistic2(-kLog2e * z);
         return fmaf(z * p, 1.0f - p, p);
     }
     return 1.0f;
+}
+
+__device__ __forceinline__ float activate(float z, int act) {
+    return act == ACT_RELU ? activate<ACT_RELU>(z) : act == ACT_GELU ? activate<ACT_GELU>(z) : act == ACT_SILU ? activate<ACT_SILU>(z) : z;
+}
+
+__device__ __forceinline__ float activate_grad(float z, int act) {
+    return act == ACT_RELU ? activate_grad<ACT_RELU>(z) : act == ACT_GELU ? activate_grad<ACT_GELU>(z) : act == ACT_SILU ? activate_grad<ACT_SILU>(z) : 1.0f;
 }
 
 // ---------------------------------------------------------------- epilogue --
@@ -130,6 +163,22 @@ __device__ __forceinline__ void load8_bf16(const __nv_bfloat16* p, float (&f)[8]
     const uint4 q = *reinterpret_cast<const uint4*>(p);
     f[0] = bf16_lo(q.x); f[1] = bf16_hi(q.x); f[2] = bf16_lo(q.y); f[3] = bf16_hi(q.y);
     f[4] = bf16_lo(q.z); f[5] = bf16_hi(q.z); f[6] = bf16_lo(q.w); f[7] = bf16_hi(q.w);
+}
+
+// Element c of eight packed bf16 values.
+__device__ __forceinline__ float bf16_of(const uint4& q, int c) {
+    const uint32_t w = c < 2 ? q.x : c < 4 ? q.y : c < 6 ? q.z : q.w;
+    return c & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+
+__device__ __forceinline__ void half8(const uint4& q, float (&f)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        f[2 * k] = t.x;
+        f[2 * k + 1] = t.y;
+    }
 }
 
 __device__ __forceinline__ void store8_bf16(__nv_bfloat16* p, const float (&f)[8]) {
@@ -152,249 +201,384 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void load8_half(const __half* p, float (&f)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-        f[2 * k] = t.x;
-        f[2 * k + 1] = t.y;
-    }
-}
-
 __device__ __forceinline__ void store8_half(__half* p, const float (&f)[8]) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
 }
 
-// V consecutive columns of one row (V = 8, or 4 where eight CTAs share 32
-// columns).  i < m is guaranteed by the caller; columns past n are skipped.
-template <int V>
-__device__ __forceinline__ void epilogue(const LinearEpi& e, const Args& g, int batch, int i, int j0, float (&t)[V]) {
-    (void)batch;
-    const bool whole = V == 8 && e.vec && j0 + 8 <= g.n;
-    if (e.bias) {
-        if (e.bias_on_row) {
-            const float b = e.bias_f32 ? static_cast<const float*>(e.bias)[i]
-                                       : load_bf16(static_cast<const __nv_bfloat16*>(e.bias) + i);
+// Eight consecutive columns of one output row of a linear layer, one by one
+// (`cols` columns; those past it are skipped): rows without 16-byte alignment
+// and blocks on the right edge.
+__device__ __forceinline__ void linear_row(const LinearEpi& e, int cols, int64_t row, int j0, float (&t)[8]) {
 #pragma unroll
-            for (int c = 0; c < V; ++c) t[c] += b;
-        } else {
-#pragma unroll
-            for (int c = 0; c < V; ++c)
-                if (j0 + c < g.n)
-                    t[c] += e.bias_f32 ? static_cast<const float*>(e.bias)[j0 + c]
-                                       : load_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j0 + c);
-        }
-    }
-    if constexpr (V == 8) {
-        if (whole) {
-            float f[8];
-            if (e.pre_out) store8_bf16(e.pre_out + (int64_t)i * e.p_rs + j0, t);
-            if (!e.z && e.act) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) t[c] = activate(t[c], e.act);
-            }
-            if (e.res) {
-                load8_bf16(e.res + (int64_t)i * e.r_rs + j0, f);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) t[c] += f[c];
-            }
-            if (e.z) {
-                load8_bf16(e.z + (int64_t)i * e.z_rs + j0, f);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) t[c] *= activate_grad(f[c], e.act);
-            }
-            if (e.out_f32) {
-                float* o = static_cast<float*>(e.out) + (int64_t)i * e.o_rs + j0;
-                if (e.accumulate) {
-                    load8_f32(o, f);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) t[c] += f[c];
-                }
-                store8_f32(o, t);
-            } else {
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + (int64_t)i * e.o_rs + j0;
-                if (e.accumulate) {
-                    load8_bf16(o, f);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) t[c] += f[c];
-                }
-                store8_bf16(o, t);
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
+    for (int c = 0; c < 8; ++c) {
         const int j = j0 + c;
-        if (j >= g.n) break;
+        if (j >= cols) break;
         float x = t[c];
-        if (e.pre_out) e.pre_out[(int64_t)i * e.p_rs + (int64_t)j * e.p_cs] = __float2bfloat16_rn(x);
+        if (e.bias)
+            x += e.bias_f32 ? static_cast<const float*>(e.bias)[j] : load_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j);
+        if (e.pre_out) e.pre_out[row * e.p_ld + j] = __float2bfloat16_rn(x);
         if (!e.z) x = activate(x, e.act);
-        if (e.res) x += load_bf16(e.res + (int64_t)i * e.r_rs + (int64_t)j * e.r_cs);
-        if (e.z) x *= activate_grad(load_bf16(e.z + (int64_t)i * e.z_rs + (int64_t)j * e.z_cs), e.act);
-        const int64_t at = (int64_t)i * e.o_rs + (int64_t)j * e.o_cs;
+        if (e.res) x += load_bf16(e.res + row * e.r_ld + j);
+        if (e.z) x *= activate_grad(load_bf16(e.z + row * e.z_ld + j), e.act);
         if (e.out_f32) {
-            float* o = static_cast<float*>(e.out) + at;
+            float* o = static_cast<float*>(e.out) + row * e.o_ld + j;
             *o = e.accumulate ? *o + x : x;
         } else {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + at;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + row * e.o_ld + j;
             *o = __float2bfloat16_rn(e.accumulate ? load_bf16(o) + x : x);
         }
     }
 }
 
-// Stores V off-diagonal values of row i and their mirror image (a symmetric
-// product computes only i <= j; each pair is written by the one element that
-// holds it).  The diagonal itself goes to fp32 elsewhere and is stored as 0.
-template <int V>
-__device__ __forceinline__ void store_symmetric(__half* d, int64_t ld, const Args& g, int i, int j0,
-                                                const float (&t)[V]) {
-    if (j0 > i && j0 + V <= g.n && V == 8) {
-        float f[8];
+// N rows (row + 8 s) of eight consecutive columns, all inside the matrix's
+// columns and 16-byte aligned; rows past the end are skipped.  One test of each
+// option for the whole block: tested row by row they took four times as long
+// as the arithmetic.
+template <int KIND, int N>
+__device__ __forceinline__ void linear_rows(const LinearEpi& e, int rows, int row, int j0, float (&t)[N][8]) {
+    // what this kind can contain
+    constexpr bool kAll = KIND == KIND_LINEAR || KIND == KIND_F32;
+    const bool pre_out = (kAll || KIND == KIND_ACT) && e.pre_out, grad = (kAll && e.z) || KIND == KIND_GRAD;
+    const bool f32 = KIND == KIND_F32 || (KIND == KIND_LINEAR && e.out_f32), accumulate = kAll && e.accumulate;
+    const bool act = (kAll || KIND == KIND_ACT) && !grad;
+    bool in[N];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = t[c % V];
-        store8_half(d + (int64_t)i * ld + j0, f);
-    } else {
+    for (int s = 0; s < N; ++s) in[s] = row + 8 * s < rows;
+    if (e.bias) {
+        float b[8];
+        if (e.bias_f32)
+            load8_f32(static_cast<const float*>(e.bias) + j0, b);
+        else
+            load8_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j0, b);
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-            if (j0 + c >= i && j0 + c < g.n) d[(int64_t)i * ld + j0 + c] = __float2half_rn(j0 + c == i ? 0.0f : t[c]);
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) t[s][c] += b[c];
     }
+    if (pre_out) {
 #pragma unroll
-    for (int c = 0; c < V; ++c)  // lanes hold consecutive i: one run of the mirrored row
-        if (j0 + c > i && j0 + c < g.n) d[(int64_t)(j0 + c) * ld + i] = __float2half_rn(t[c]);
+        for (int s = 0; s < N; ++s)
+            if (in[s]) store8_bf16(e.pre_out + (int64_t)(row + 8 * s) * e.p_ld + j0, t[s]);
+    }
+#define DPRED_EACH(expr)                                   \
+    _Pragma("unroll") for (int s = 0; s < N; ++s)          \
+        _Pragma("unroll") for (int c = 0; c < 8; ++c) expr
+    uint4 q[N];
+    if (grad) {
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+            q[s] = in[s] ? *reinterpret_cast<const uint4*>(e.z + (int64_t)(row + 8 * s) * e.z_ld + j0) : make_uint4(0, 0, 0, 0);
+    } else if (act && e.act == ACT_GELU) {
+        DPRED_EACH(t[s][c] = activate<ACT_GELU>(t[s][c]);)
+    } else if (act && e.act == ACT_SILU) {
+        DPRED_EACH(t[s][c] = activate<ACT_SILU>(t[s][c]);)
+    } else if (act && e.act == ACT_RELU) {
+        DPRED_EACH(t[s][c] = activate<ACT_RELU>(t[s][c]);)
+    }
+    if (e.res) {
+        uint4 p[N];
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+            p[s] = in[s] ? *reinterpret_cast<const uint4*>(e.res + (int64_t)(row + 8 * s) * e.r_ld + j0) : make_uint4(0, 0, 0, 0);
+        DPRED_EACH(t[s][c] += bf16_of(p[s], c);)
+    }
+    if (grad) {
+        if (e.act == ACT_GELU) {
+            DPRED_EACH(t[s][c] *= activate_grad<ACT_GELU>(bf16_of(q[s], c));)
+        } else if (e.act == ACT_SILU) {
+            DPRED_EACH(t[s][c] *= activate_grad<ACT_SILU>(bf16_of(q[s], c));)
+        } else {
+            DPRED_EACH(t[s][c] *= activate_grad<ACT_RELU>(bf16_of(q[s], c));)
+        }
+    }
+    if (f32) {
+        float* o = static_cast<float*>(e.out) + (int64_t)row * e.o_ld + j0;
+        if (accumulate) {
+            float4 u[N], v[N];
+#pragma unroll
+            for (int s = 0; s < N; ++s)
+                if (in[s]) {
+                    u[s] = *reinterpret_cast<const float4*>(o + 8 * s * e.o_ld);
+                    v[s] = *reinterpret_cast<const float4*>(o + 8 * s * e.o_ld + 4);
+                }
+#pragma unroll
+            for (int s = 0; s < N; ++s) {
+                t[s][0] += u[s].x; t[s][1] += u[s].y; t[s][2] += u[s].z; t[s][3] += u[s].w;
+                t[s][4] += v[s].x; t[s][5] += v[s].y; t[s][6] += v[s].z; t[s][7] += v[s].w;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+            if (in[s]) store8_f32(o + 8 * s * e.o_ld, t[s]);
+    } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.out) + (int64_t)row * e.o_ld + j0;
+        if (accumulate) {
+            uint4 p[N];
+#pragma unroll
+            for (int s = 0; s < N; ++s)
+                p[s] = in[s] ? *reinterpret_cast<const uint4*>(o + 8 * s * e.o_ld) : make_uint4(0, 0, 0, 0);
+            DPRED_EACH(t[s][c] += bf16_of(p[s], c);)
+        }
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+            if (in[s]) store8_bf16(o + 8 * s * e.o_ld, t[s]);
+    }
 }
 
-template <int KIND, int V>
-__device__ __forceinline__ void epilogue_ns(const NsEpi& e, const Args& g, int batch, int i, int j0, float (&t)[V]) {
-    if constexpr (KIND == KIND_GRAM) {
-        if (j0 + V <= i) return;  // below the diagonal
-        __half* d = e.gram + (int64_t)batch * g.m * e.ldr;
+// Eight consecutive columns of one row of a Newton-Schulz result.
+__device__ __forceinline__ void final_row(const NsEpi& e, const FinalOut& f, int cols, int64_t row, int j0,
+                                          const float (&t)[8]) {
+    const int valid = cols - j0;
+    const int64_t o = row * f.ld + j0;
+    float x[8], w[8];
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const float x = t[c] * e.alpha;
-            if (j0 + c == i) e.gram_diag[(int64_t)batch * e.ldr + i] = x;
-            t[c] = x * e.off_scale;
-        }
-        store_symmetric<V>(d, e.ldr, g, i, j0, t);
-    } else if constexpr (KIND == KIND_POLY) {
-        // With A = D + E (D diagonal, E the stored off-diagonal):
-        //   A^2 = D^2 + D E + E D + E^2, so off the diagonal
-        //   (b A + c A^2)_ij = (b + c (d_i + d_j)) E_ij + c (E^2)_ij
-        // and on it b d_i + c d_i^2 + c (E^2)_ii.
-        if (j0 + V <= i) return;
-        const float* diag = e.gram_diag + (int64_t)batch * e.ldr;
-        const __half* a = e.gram + ((int64_t)batch * g.m + i) * e.ldr + j0;
-        const float di = diag[i];
-        float x[8], dj[8];
-        if (V == 8) {  // rows and diagonals are padded to a multiple of 8
-            if (j0 >= g.n) return;
-            load8_half(a, x);
-            load8_f32(diag + j0, dj);
-        } else {
+    for (int c = 0; c < 8; ++c) x[c] = t[c] * f.step;
+    if (f.vec && valid >= 8) {
+        if (e.out_f32) {
+            float* p = static_cast<float*>(f.p) + o;
+            if (e.keep != 0.0f) {
+                load8_f32(p, w);
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                x[c] = j0 + c < g.n ? __half2float(a[c]) : 0.0f;
-                dj[c] = j0 + c < g.n ? diag[j0 + c] : 0.0f;
+                for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, w[c], x[c]);
             }
-        }
+            store8_f32(p, x);
+        } else {
+            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o;
+            if (e.keep != 0.0f) {
+                load8_bf16(p, w);
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const float sq = t[c] * e.alpha;
-            if (j0 + c == i) e.coef[(int64_t)batch * e.ldr + i] = e.a + fmaf(e.c, fmaf(di, di, sq), e.b * di);
-            t[c] = fmaf(fmaf(e.c, di + dj[c], e.b), x[c] * e.off_inv, e.c * sq) * e.off_scale;
+                for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, w[c], x[c]);
+            }
+            store8_bf16(p, x);
         }
-        store_symmetric<V>(e.poly + (int64_t)batch * g.m * e.ldr, e.ldr, g, i, j0, t);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        if (c >= valid) break;
+        if (e.out_f32) {
+            float* p = static_cast<float*>(f.p) + o + c;
+            *p = e.keep != 0.0f ? fmaf(e.keep, *p, x[c]) : x[c];
+        } else {
+            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o + c;
+            *p = __float2bfloat16_rn(e.keep != 0.0f ? fmaf(e.keep, load_bf16(p), x[c]) : x[c]);
+        }
+    }
+}
+
+// ------------------------------------------------------------ staged blocks --
+//
+// The tensor-memory load gives a thread one row; global memory wants a warp to
+// touch few rows at a time (written straight from those registers, a bf16
+// result of 256 columns a row took twice the time of its product).  So a warp
+// passes its accumulators through a 32 x 32 fp32 block of shared memory, 16-byte
+// pieces exchanged within a row by its number so that every access is free of
+// bank conflicts, and reads it back eight columns of a row (or eight rows of a
+// column, for a transposed result) at a time.
+constexpr uint32_t kBlockBytes = 32 * 32 * 4;
+
+__device__ __forceinline__ uint32_t piece(uint32_t block, int r, int c4) { return block + r * 128 + ((c4 ^ (r & 7)) << 4); }
+
+__device__ __forceinline__ void sts4(uint32_t a, float x, float y, float z, float w) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+
+__device__ __forceinline__ void lds4(uint32_t a, float* v) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(a)
+                 : "memory");
+}
+
+__device__ __forceinline__ float lds1(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Row `lane` of the block.
+__device__ __forceinline__ void block_put_row(uint32_t block, int lane, const float (&v)[32]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sts4(piece(block, lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+
+// Columns 8 c8 .. 8 c8 + 7 of row r.
+__device__ __forceinline__ void block_get(uint32_t block, int r, int c8, float (&t)[8]) {
+    lds4(piece(block, r, 2 * c8), t);
+    lds4(piece(block, r, 2 * c8 + 1), t + 4);
+}
+
+__device__ __forceinline__ void block_put(uint32_t block, int r, int c8, const float (&t)[8]) {
+    sts4(piece(block, r, 2 * c8), t[0], t[1], t[2], t[3]);
+    sts4(piece(block, r, 2 * c8 + 1), t[4], t[5], t[6], t[7]);
+}
+
+// Rows 8 r8 .. 8 r8 + 7 of column c.
+__device__ __forceinline__ void block_get_column(uint32_t block, int r8, int c, float (&t)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = lds1(piece(block, 8 * r8 + k, c / 4) + (c % 4) * 4);
+}
+
+// One step (8 rows, or 8 columns of a transposed result) of a linear layer's
+// block, or all four of them.
+template <int KIND, int N>
+__device__ __forceinline__ void linear_steps(const LinearEpi& e, const Args& g, int step, int lane, int i0, int j0,
+                                             float (&t)[N][8]) {
+    const bool swapped = KIND == KIND_LINEAR && e.swapped;  // only the split kernel's calls are
+    const int rows = swapped ? g.n : g.m, cols = swapped ? g.m : g.n;
+    const int row = (swapped ? j0 : i0) + step * 8 + lane / 4, c0 = swapped ? i0 : j0, c = c0 + lane % 4 * 8;
+    if (e.vec && c0 + 32 <= cols) {
+        linear_rows<KIND, N>(e, rows, row, c, t);
     } else {
-        // X' = (a + diagonal) X + E X: the large part of the polynomial is its
-        // diagonal, which multiplies X in full precision (both fp16 terms).
-        const float k = e.coef[(int64_t)batch * e.ldr + i];
-        const int64_t at = ((int64_t)batch * g.m + i) * e.ldc + j0;
-        static_assert(V == 8 || V == 4, "column groups");
-        float hi[8], lo[8];
-        if constexpr (V == 8) {
-            if (j0 >= g.n) return;
-            load8_half(e.hi_in + at, hi);  // rows are padded to a multiple of 8 columns
-            load8_half(e.lo_in + at, lo);
-        } else {
+#pragma unroll 1
+        for (int s = 0; s < N; ++s) {
+            float u[8];
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                const bool in = j0 + c < g.n;
-                hi[c] = in ? __half2float(e.hi_in[at + c]) : 0.0f;
-                lo[c] = in ? __half2float(e.lo_in[at + c]) : 0.0f;
-            }
+            for (int x = 0; x < 8; ++x) u[x] = t[0][x];
+#pragma unroll
+            for (int y = 1; y < N; ++y)
+                if (s == y) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) u[x] = t[y][x];
+                }
+            if (row + 8 * s < rows && c < cols) linear_row(e, cols, row + 8 * s, c, u);
         }
+    }
+}
+
+// The epilogue of a 32 x 32 block at (i0, j0), staged in shared memory by this
+// warp.  mirror: the block lies off the diagonal square of its tile row, so
+// the symmetric counterpart is written as well.
+template <int KIND>
+__device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e, const Args& g, int batch, int i0, int j0,
+                                               uint32_t block, int lane, bool mirror) {
+    const int major = lane / 4, minor = lane % 4;
+    if constexpr (is_linear(KIND)) {
+        // fp32 results: two steps at a time, next to the accumulators in registers
+        constexpr int kSteps = KIND == KIND_F32 ? 2 : 4;
 #pragma unroll
-        for (int c = 0; c < V; ++c) t[c] = fmaf(k, hi[c] + lo[c], t[c] * e.alpha);
-        if constexpr (KIND == KIND_APPLY) {
-            float h[8];
+        for (int s0 = 0; s0 < 4; s0 += kSteps) {
+            float t[kSteps][8];
+            if (KIND == KIND_LINEAR && e.swapped) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) h[c] = c < V ? __half2float(__float2half_rn(t[c % V])) : 0.0f;
-            if constexpr (V == 8) {
-                store8_half(e.hi + at, h);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) h[c] = t[c] - h[c];
-                store8_half(e.lo + at, h);
+                for (int s = 0; s < kSteps; ++s) block_get_column(block, minor, (s0 + s) * 8 + major, t[s]);
             } else {
 #pragma unroll
-                for (int c = 0; c < V; ++c)
-                    if (j0 + c < g.n) {
-                        e.hi[at + c] = __float2half_rn(t[c]);
-                        e.lo[at + c] = __float2half_rn(t[c] - h[c]);
+                for (int s = 0; s < kSteps; ++s) block_get(block, (s0 + s) * 8 + major, minor, t[s]);
+            }
+            linear_steps<KIND, kSteps>(e, g, s0, lane, i0, j0, t);
+        }
+        return;
+    } else {
+        float t[4][8];
+        const int i = i0 + major, j = j0 + minor * 8;  // step s: row i + 8 s
+        bool in[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            in[s] = i + 8 * s < g.m && j < g.n;
+            block_get(block, s * 8 + major, minor, t[s]);
+        }
+        bool again = false;  // a second, transposed pass over the block
+        if constexpr (KIND == KIND_GRAM || KIND == KIND_POLY) again = mirror;
+        if constexpr (KIND == KIND_FINAL) again = e.transposed;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if constexpr (KIND == KIND_GRAM) {
+            __half* d = e.gram + ((int64_t)batch * g.m + i) * e.ldr + j;  // rows are padded to 8 columns
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float x = t[s][c] * e.alpha;
+                    t[s][c] = x * e.off_scale;
+                    if (j + c == i + 8 * s && in[s]) {
+                        e.gram_diag[(int64_t)batch * e.ldr + j + c] = x;
+                        t[s][c] = 0.0f;
                     }
+                }
+                if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
+            }
+        } else if constexpr (KIND == KIND_POLY) {
+            // With A = D + E (D diagonal, E the stored off-diagonal):
+            //   A^2 = D^2 + D E + E D + E^2, so off the diagonal
+            //   (b A + c A^2)_ij = (b + c (d_i + d_j)) E_ij + c (E^2)_ij
+            // and on it b d_i + c d_i^2 + c (E^2)_ii.
+            const float* diag = e.gram_diag + (int64_t)batch * e.ldr;
+            const int64_t at = ((int64_t)batch * g.m + i) * e.ldr + j;
+            uint4 q[4];
+            float di[4], dj[8];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                q[s] = in[s] ? *reinterpret_cast<const uint4*>(e.gram + at + 8 * s * e.ldr) : zero;
+                di[s] = in[s] ? diag[i + 8 * s] : 0.0f;
+            }
+            if (j < g.n) load8_f32(diag + j, dj);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float x[8];
+                half8(q[s], x);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float sq = t[s][c] * e.alpha;
+                    t[s][c] = fmaf(fmaf(e.c, di[s] + dj[c], e.b), x[c] * e.off_inv, e.c * sq) * e.off_scale;
+                    if (j + c == i + 8 * s && in[s]) {
+                        e.coef[(int64_t)batch * e.ldr + j + c] = e.a + fmaf(e.c, fmaf(di[s], di[s], sq), e.b * di[s]);
+                        t[s][c] = 0.0f;
+                    }
+                }
+                if (in[s]) store8_half(e.poly + at + 8 * s * e.ldr, t[s]);
             }
         } else {
-            const FinalOut& f = e.out[batch];
-            if (V == 8 && f.vec && j0 + 8 <= g.n) {
-                const int64_t o = (int64_t)i * f.rs + j0;
-                float w[8], x[8];
+            // X' = (a + diagonal) X + E X: the large part of the polynomial is its
+            // diagonal, which multiplies X in full precision (both fp16 terms).
+            const int64_t at = ((int64_t)batch * g.m + i) * e.ldc + j;
+            uint4 h[4], l[4];
+            float k[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] = t[c % V] * f.step;
-                if (e.out_f32) {
-                    float* p = static_cast<float*>(f.p) + o;
-                    if (e.keep != 0.0f) {
-                        load8_f32(p, w);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, w[c], x[c]);
-                    }
-                    store8_f32(p, x);
-                } else {
-                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o;
-                    if (e.keep != 0.0f) {
-                        load8_bf16(p, w);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, w[c], x[c]);
-                    }
-                    store8_bf16(p, x);
-                }
-                return;
+            for (int s = 0; s < 4; ++s) {
+                h[s] = in[s] ? *reinterpret_cast<const uint4*>(e.hi_in + at + 8 * s * e.ldc) : zero;
+                l[s] = in[s] ? *reinterpret_cast<const uint4*>(e.lo_in + at + 8 * s * e.ldc) : zero;
+                k[s] = in[s] ? e.coef[(int64_t)batch * e.ldr + i + 8 * s] : 0.0f;
             }
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                if (j0 + c >= g.n) break;
-                const int64_t o = (int64_t)i * f.rs + (int64_t)(j0 + c) * f.cs;
-                float x = t[c] * f.step;
-                if (e.out_f32) {
-                    float* p = static_cast<float*>(f.p) + o;
-                    *p = e.keep != 0.0f ? fmaf(e.keep, *p, x) : x;
-                } else {
-                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o;
-                    *p = __float2bfloat16_rn(e.keep != 0.0f ? fmaf(e.keep, load_bf16(p), x) : x);
+            for (int s = 0; s < 4; ++s) {
+                float hi[8], lo[8];
+                half8(h[s], hi);
+                half8(l[s], lo);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(k[s], hi[c] + lo[c], t[s][c] * e.alpha);
+                if constexpr (KIND == KIND_APPLY) {
+                    if (in[s]) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) hi[c] = __half2float(__float2half_rn(t[s][c]));
+                        store8_half(e.hi + at + 8 * s * e.ldc, hi);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) lo[c] = t[s][c] - hi[c];
+                        store8_half(e.lo + at + 8 * s * e.ldc, lo);
+                    }
+                } else if (!again) {
+                    if (in[s]) final_row(e, e.out[batch], g.n, i + 8 * s, j, t[s]);
                 }
             }
         }
+        if (again) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) block_put(block, s * 8 + major, minor, t[s]);
+            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int col = j0 + s * 8 + major, row = i0 + minor * 8;
+                block_get_column(block, minor, s * 8 + major, t[s]);
+                if (col >= g.n || row >= g.m) continue;
+                if constexpr (KIND == KIND_GRAM)
+                    store8_half(e.gram + ((int64_t)batch * g.m + col) * e.ldr + row, t[s]);
+                else if constexpr (KIND == KIND_POLY)
+                    store8_half(e.poly + ((int64_t)batch * g.m + col) * e.ldr + row, t[s]);
+                else if constexpr (KIND == KIND_FINAL)
+                    final_row(e, e.out[batch], g.m, col, row, t[s]);
+            }
+        }
     }
-}
-
-template <int KIND, int V>
-__device__ __forceinline__ void apply_epilogue(const typename EpiOf<KIND>::T& e, const Args& g, int batch, int i, int j0,
-                                               float (&t)[V]) {
-    if constexpr (KIND == KIND_LINEAR)
-        epilogue<V>(e, g, batch, i, j0, t);
-    else
-        epilogue_ns<KIND, V>(e, g, batch, i, j0, t);
 }
 
 // The tile of index t inside one batch entry.  In symmetric mode tile row tm
@@ -456,19 +640,15 @@ __device__ __forceinline__ void read_regions(uint32_t addr, int regions, float (
     }
 }
 
-// Adds V columns of one row over the cluster's partial tiles, in rank order.
-template <int KIND, int V>
-__device__ __forceinline__ void reduce_columns(const typename EpiOf<KIND>::T& e, const Args& g, int batch, int i, int j0,
-                                               uint32_t at) {
-    float t[V];
+// Element pieces of a block added over the cluster's partial tiles, in rank order.
+__device__ __forceinline__ void cluster_get(uint32_t at, int split, float* t) {
+    t[0] = t[1] = t[2] = t[3] = 0.0f;
+    for (int p = 0; p < split; ++p) {
+        float v[4];
+        mma::ld_cluster4(mma::map_rank(at, p), v);
 #pragma unroll
-    for (int x = 0; x < V; ++x) t[x] = 0.0f;
-    for (int p = 0; p < g.split; ++p) {
-        const uint32_t from = mma::map_rank(at, p);
-#pragma unroll
-        for (int x = 0; x < V; ++x) t[x] += mma::ld_cluster(from + x * 512);
+        for (int x = 0; x < 4; ++x) t[x] += v[x];
     }
-    apply_epilogue<KIND, V>(e, g, batch, i, j0, t);
 }
 
 template <int KIND, int BN>
@@ -492,6 +672,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     const int kb0 = (int)((int64_t)g.kblocks * rank / g.split), kb1 = (int)((int64_t)g.kblocks * (rank + 1) / g.split);
     const int nkb = kb1 - kb0;
     const int regions = min(g.regions, nkb);
+    const bool mirror = g.symmetric && tn * BN >= (tm + 1) * 128;
 
     if (threadIdx.x == 0) {
         if (g.kblocks) {
@@ -583,34 +764,18 @@ __global__ void __launch_bounds__(kSplitThreads)
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         fence_after();
-        const int r = q * 32 + lane, i = tm * 128 + r;
-        if (g.split == 1) {
+        // accumulators to the blocks of this warp's rows, 32 columns each (the
+        // pipeline's stages are free: every load was consumed)
 #pragma unroll
-            for (int c0 = 0; c0 < BN; c0 += 32) {
-                float v[32];
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+            float v[32];
+            __syncwarp();
+            read_regions<BN>(tmem + ((uint32_t)(q * 32) << 16) + c0, ok ? regions : 0, v);
+            const uint32_t block = base + (c0 / 32 * 4 + q) * kBlockBytes;
+            block_put_row(block, lane, v);
+            if (g.split == 1) {
                 __syncwarp();
-                read_regions<BN>(tmem + ((uint32_t)(q * 32) << 16) + c0, ok ? regions : 0, v);
-                if (i < g.m && ok) {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        float t[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) t[x] = v[c + x];
-                        apply_epilogue<KIND, 8>(e, g, batch, i, tn * BN + c0 + c, t);
-                    }
-                }
-            }
-        } else {
-            // partial tile to this CTA's shared memory, column by column (the
-            // pipeline's stages are free: every load was consumed)
-#pragma unroll
-            for (int c0 = 0; c0 < BN; c0 += 32) {
-                float v[32];
-                __syncwarp();
-                read_regions<BN>(tmem + ((uint32_t)(q * 32) << 16) + c0, ok ? regions : 0, v);
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c0 + c) * 128 + r) * 4), "f"(v[c]) : "memory");
+                if (ok) block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, block, lane, mirror);
             }
         }
         fence_before();
@@ -618,13 +783,44 @@ __global__ void __launch_bounds__(kSplitThreads)
     if (g.split > 1) {
         cluster_sync();
         if (warp >= 2) {
-            const int r = (warp & 3) * 32 + lane, i = tm * 128 + r;
-            const int per = BN / g.split, c_lo = rank * per;
-            if (i < g.m && ok) {
-                if (per % 8 == 0) {
-                    for (int c = 0; c < per; c += 8) reduce_columns<KIND, 8>(e, g, batch, i, tn * BN + c_lo + c, base + ((c_lo + c) * 128 + r) * 4);
+            // the tile's blocks (their steps, for a linear layer) spread over the cluster's epilogue warps
+            constexpr int kSteps = KIND == KIND_LINEAR ? 4 : 1;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            const int major = lane / 4, minor = lane % 4;
+            for (int u = rank * 4 + (warp & 3); u < BN / 8 * kSteps && ok; u += 4 * g.split) {
+                const int id = u / kSteps, q = id & 3, c0 = id / 4 * 32;
+                const uint32_t block = base + id * kBlockBytes;
+                const int i0 = tm * 128 + q * 32, j0 = tn * BN + c0;
+                float t[1][8];
+                if constexpr (KIND == KIND_LINEAR) {
+                    const int step = u % 4;
+                    if (e.swapped) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) t[0][k] = 0.0f;
+                        for (int p = 0; p < g.split; ++p) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                t[0][k] += ld_cluster(map_rank(piece(block, 8 * minor + k, (step * 8 + major) / 4) + major % 4 * 4, p));
+                        }
+                    } else {
+                        const int r = step * 8 + major;
+                        cluster_get(piece(block, r, 2 * minor), g.split, t[0]);
+                        cluster_get(piece(block, r, 2 * minor + 1), g.split, t[0] + 4);
+                    }
+                    linear_steps<KIND, 1>(e, g, step, lane, i0, j0, t);
                 } else {
-                    for (int c = 0; c < per; c += 4) reduce_columns<KIND, 4>(e, g, batch, i, tn * BN + c_lo + c, base + ((c_lo + c) * 128 + r) * 4);
+                    // into a block of this CTA's own, past the partial tile
+                    const uint32_t mine = base + (BN / 8 + (warp & 3)) * kBlockBytes;
+                    __syncwarp();
+#pragma unroll
+                    for (int step = 0; step < 4; ++step) {
+                        const int r = step * 8 + major;
+                        cluster_get(piece(block, r, 2 * minor), g.split, t[0]);
+                        cluster_get(piece(block, r, 2 * minor + 1), g.split, t[0] + 4);
+                        block_put(mine, r, minor, t[0]);
+                    }
+                    __syncwarp();
+                    block_epilogue<KIND>(e, g, batch, i0, j0, mine, lane, mirror);
                 }
             }
         }
@@ -652,16 +848,20 @@ __global__ void __launch_bounds__(kSplitThreads)
 // elements).  Here an accumulator takes kPromoteBlocks reduction blocks (512
 // elements, 6e-7) and the epilogue threads add it to fp32 registers.
 
-constexpr int kTileThreads = 320;  // producer warp, issuing warp, eight epilogue warps
+// Twelve warps: producer, issuer (two more idle), eight of the epilogue.  The
+// epilogue holds up to 128 accumulators a thread: the control warps hand their
+// registers over (168 each at launch: 128 * 56 + 256 * 224 = 384 * 168).
+constexpr int kTileThreads = 384;
+constexpr int kEpilogueWarp0 = 4;
 constexpr int kPromoteBlocks = 8;
 
 template <int BN>
 __host__ __device__ constexpr int tile_stages() {
-    return BN == 256 ? 6 : 8;
+    return BN == 256 ? 6 : 7;
 }
 template <int BN>
 __host__ __device__ constexpr int tile_smem() {
-    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 1024;
+    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 8 * (int)kBlockBytes + 1024;
 }
 
 template <int KIND, int BN, bool PROMOTE>
@@ -781,9 +981,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
         __syncwarp();
-    } else {
-        const int q = warp & 3, half = (warp - 2) / 4;
+    } else if (warp >= kEpilogueWarp0) {
+        const int q = warp & 3, half = (warp - kEpilogueWarp0) / 4;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * kHalf;
+        const uint32_t block = base + S * kStage + (warp - kEpilogueWarp0) * kBlockBytes;
         const uint32_t drained0 = map_rank(tma::smem_addr(&acc_empty[0]), 0), drained1 = map_rank(tma::smem_addr(&acc_empty[1]), 0);
         int fill = 0;
         bool ok = true;
@@ -791,7 +992,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int batch = tile / g.tiles_per_batch;
             int tm, tn;
             tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
-            const int i = tm * 256 + (int)rank * 128 + q * 32 + lane, j = tn * BN + half * kHalf;
+            const int i = tm * 256 + (int)rank * 128 + q * 32, j = tn * BN + half * kHalf;
+            const bool mirror = g.symmetric && tn * BN >= (tm + 1) * 256;
             if constexpr (PROMOTE) {
                 float sum[kHalf / 32][32];
 #pragma unroll
@@ -817,11 +1019,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 if (ok && i < g.m) {
 #pragma unroll
-                    for (int c = 0; c < kHalf / 8; ++c) {
-                        float t[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) t[x] = sum[c / 4][(c % 4) * 8 + x];
-                        if (j + c * 8 < g.n) apply_epilogue<KIND, 8>(e, g, batch, i, j + c * 8, t);
+                    for (int c = 0; c < kHalf / 32; ++c) {
+                        if (j + c * 32 >= g.n) break;
+                        __syncwarp();
+                        block_put_row(block, lane, sum[c]);
+                        __syncwarp();
+                        block_epilogue<KIND>(e, g, batch, i, j + c * 32, block, lane, mirror);
                     }
                 }
             } else {
@@ -842,13 +1045,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
                     }
                     if (i < g.m && j + c < g.n) {
-#pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            float t[8];
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) t[y] = v[x + y];
-                            apply_epilogue<KIND, 8>(e, g, batch, i, j + c + x, t);
-                        }
+                        block_put_row(block, lane, v);
+                        __syncwarp();
+                        block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, mirror);
                     }
                 }
             }

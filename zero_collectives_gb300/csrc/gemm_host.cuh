@@ -96,16 +96,38 @@ int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
 }
 
 template <int KIND>
+int tiles_of_kind(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+    constexpr bool kPromote = KIND == KIND_F32;
+    return sh.bn == 256 ? launch_tiles<KIND, 256, kPromote>(p, sh, e, s) : launch_tiles<KIND, 128, kPromote>(p, sh, e, s);
+}
+
+// The tile kernels of the linear layers, one translation unit per kind.
+int linear_tiles_any(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s);
+int linear_tiles_plain(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s);
+int linear_tiles_act(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s);
+int linear_tiles_grad(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s);
+int linear_tiles_f32(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s);
+
+template <int KIND>
+int run_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+    if constexpr (KIND == KIND_LINEAR) {
+        switch (linear_kind(e)) {
+            case KIND_PLAIN: return linear_tiles_plain(p, sh, e, s);
+            case KIND_ACT: return linear_tiles_act(p, sh, e, s);
+            case KIND_GRAD: return linear_tiles_grad(p, sh, e, s);
+            case KIND_F32: return linear_tiles_f32(p, sh, e, s);
+            default: return linear_tiles_any(p, sh, e, s);
+        }
+    } else {
+        return tiles_of_kind<KIND>(p, sh, e, s);
+    }
+}
+
+template <int KIND>
 int run(const Plan& p, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
     const Shape sh = choose_shape(p.args);
     if (sh.tiles * sh.split > 0x7FFFFFFF) return set_error(DPRED_E_SIZE, "a matrix product of too many tiles");
-    if (sh.pairs) {
-        if constexpr (KIND == KIND_LINEAR) {
-            if (p.fp32_result)
-                return sh.bn == 256 ? launch_tiles<KIND, 256, true>(p, sh, e, s) : launch_tiles<KIND, 128, true>(p, sh, e, s);
-        }
-        return sh.bn == 256 ? launch_tiles<KIND, 256, false>(p, sh, e, s) : launch_tiles<KIND, 128, false>(p, sh, e, s);
-    }
+    if (sh.pairs) return run_tiles<KIND>(p, sh, e, s);
     switch (sh.bn) {
         case 32: return launch_split<KIND, 32>(p, sh, e, s);
         case 64: return launch_split<KIND, 64>(p, sh, e, s);

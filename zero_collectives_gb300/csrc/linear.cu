@@ -228,16 +228,13 @@ extern "C" int dpred_linear(int64_t m, int64_t n, int64_t k, const void* x, int6
     e.pre_out = static_cast<__nv_bfloat16*>(preact);
     e.out_f32 = out_dtype == DPRED_F32;
     e.bias_f32 = bias_dtype == DPRED_F32;
-    e.bias_on_row = few;
     e.act = act;
-    (few ? e.o_cs : e.o_rs) = ldy;
-    (few ? e.o_rs : e.o_cs) = 1;
-    (few ? e.r_cs : e.r_rs) = ldr;
-    (few ? e.r_rs : e.r_cs) = 1;
-    (few ? e.p_cs : e.p_rs) = ldp;
-    (few ? e.p_rs : e.p_cs) = 1;
-    e.vec = !few && aligned_rows(y, m, ldy, osize) && (!residual || aligned_rows(residual, m, ldr, 2)) &&
-            (!preact || aligned_rows(preact, m, ldp, 2));
+    e.swapped = few;
+    e.o_ld = ldy;
+    e.r_ld = ldr;
+    e.p_ld = ldp;
+    e.vec = aligned_rows(y, m, ldy, osize) && (!residual || aligned_rows(residual, m, ldr, 2)) &&
+            (!preact || aligned_rows(preact, m, ldp, 2)) && reinterpret_cast<uintptr_t>(bias) % 16 == 0;
     const Operand tokens = {x, m, k, ldx, 0, false}, weight = {w, n, k, ldw, 0, false};
     const size_t need = k > 0 ? dpred_linear_workspace_bytes(x, m, k, ldx, w, n, k, ldw) : 0;
     return launch(few ? weight : tokens, few ? tokens : weight, k, e, workspace, workspace_bytes, need,
@@ -267,13 +264,11 @@ extern "C" int dpred_linear_dgrad(int64_t m, int64_t n, int64_t k, const void* d
     e.z = act != ACT_NONE ? static_cast<const __nv_bfloat16*>(preact) : nullptr;
     e.out_f32 = out_dtype == DPRED_F32;
     e.act = act;
-    (few ? e.o_cs : e.o_rs) = lddx;
-    (few ? e.o_rs : e.o_cs) = 1;
-    (few ? e.r_cs : e.r_rs) = ldr;
-    (few ? e.r_rs : e.r_cs) = 1;
-    (few ? e.z_cs : e.z_rs) = ldp;
-    (few ? e.z_rs : e.z_cs) = 1;
-    e.vec = !few && aligned_rows(dx, m, lddx, osize) && (!residual || aligned_rows(residual, m, ldr, 2)) &&
+    e.swapped = few;
+    e.o_ld = lddx;
+    e.r_ld = ldr;
+    e.z_ld = ldp;
+    e.vec = aligned_rows(dx, m, lddx, osize) && (!residual || aligned_rows(residual, m, ldr, 2)) &&
             (!e.z || aligned_rows(preact, m, ldp, 2));
     const Operand tokens = {dy, m, n, lddy, 0, false}, weight = {w, n, k, ldw, 0, true};
     const size_t need = n > 0 ? dpred_linear_workspace_bytes(dy, m, n, lddy, w, n, k, ldw) : 0;
@@ -299,8 +294,7 @@ extern "C" int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* d
         e.out = dw;
         e.out_f32 = out_dtype == DPRED_F32;
         e.accumulate = accumulate != 0;
-        e.o_rs = lddw;
-        e.o_cs = 1;
+        e.o_ld = lddw;
         e.vec = aligned_rows(dw, n, lddw, osize);
         const size_t need = m > 0 ? dpred_linear_workspace_bytes(dy, m, n, lddy, x, m, k, ldx) : 0;
         if ((rc = launch(a, b, m, e, workspace, workspace_bytes, need, s)) != DPRED_OK) return rc;

@@ -1,0 +1,12 @@
+// linear_act.cu -- the tile kernel of the linear layers of KIND_ACT.
+#include "gemm_host.cuh"
+
+namespace dpred {
+namespace gemm {
+
+int linear_tiles_act(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s) {
+    return tiles_of_kind<KIND_ACT>(p, sh, e, s);
+}
+
+}  // namespace gemm
+}  // namespace dpred

@@ -1,0 +1,12 @@
+// linear_plain.cu -- the tile kernel of the linear layers of KIND_PLAIN.
+#include "gemm_host.cuh"
+
+namespace dpred {
+namespace gemm {
+
+int linear_tiles_plain(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s) {
+    return tiles_of_kind<KIND_PLAIN>(p, sh, e, s);
+}
+
+}  // namespace gemm
+}  // namespace dpred

@@ -50,8 +50,18 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void ld_cluster4(uint32_t addr, float (&v)[4]) {
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Arrival that publishes no memory: it says that tensor memory was read.  A
+// releasing arrival would first wait for this thread's global stores to
+// reach L2 (1400 cycles in the epilogue of a 256 x 256 tile).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // ------------------------------------------- programmatic dependent launch --
@@ -61,6 +71,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 // touched before it.  A no-op in a launch without the attribute.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Registers per thread of this warpgroup from here on: up from, or down to
+// less than, the launch's share.  Executed by all of its warps.
+template <int N, bool UP>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (UP)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // ------------------------------------------------------------- tensor maps --
 

@@ -329,14 +329,14 @@ int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cu
     e.c = q.c;
     e.keep = q.keep;
     e.out_f32 = q.out_dtype == DPRED_F32;
+    e.transposed = transposed;
     const int os = e.out_f32 ? 4 : 2;
     for (int k = 0; k < count; ++k) {
         FinalOut& o = e.out[k];
         o.p = items[k]->out;
-        o.rs = transposed ? 1 : items[k]->ldo;
-        o.cs = transposed ? items[k]->ldo : 1;
+        o.ld = items[k]->ldo;
         o.step = items[k]->step / scale;
-        o.vec = !transposed && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (f.rows <= 1 || o.rs * os % 16 == 0);
+        o.vec = reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (f.rows <= 1 || o.ld * os % 16 == 0);
     }
     Plan p = {};
     p.args.batch = count;
