@@ -58,6 +58,7 @@ struct FinalOut {
     int64_t ld;
     float step;       // multiplies the orthogonalised value (negative: subtracted from the weight)
     int vec;          // 16-byte aligned rows
+    int transposed;   // stored with rows and columns exchanged
 };
 constexpr int kMaxBatch = 64;  // matrices per Newton-Schulz launch (their output table travels in the launch)
 
@@ -72,11 +73,10 @@ struct NsEpi {
     __half* lo;
     int64_t ldr, ldc;
     float alpha;       // multiplies the accumulator
-    float off_scale, off_inv;  // GRAM, POLY: scale of the stored off-diagonals (a power of two), its reciprocal
+    float off_scale;   // GRAM, POLY: scale of the stored off-diagonals (a power of two)
     float a, b, c;     // the polynomial's coefficients
     float keep;        // FINAL: factor of the old weight (0: store)
     int out_f32;       // FINAL
-    int transposed;    // FINAL: the outputs are stored with rows and columns exchanged
     FinalOut out[kMaxBatch];
 };
 
@@ -326,43 +326,57 @@ __device__ __forceinline__ void linear_rows(const LinearEpi& e, int rows, int ro
     }
 }
 
-// Eight consecutive columns of one row of a Newton-Schulz result.
-__device__ __forceinline__ void final_row(const NsEpi& e, const FinalOut& f, int cols, int64_t row, int j0,
-                                          const float (&t)[8]) {
-    const int valid = cols - j0;
-    const int64_t o = row * f.ld + j0;
-    float x[8], w[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = t[c] * f.step;
-    if (f.vec && valid >= 8) {
+// A Newton-Schulz result: N rows (row + 8 s) of eight consecutive columns.
+template <int N>
+__device__ __forceinline__ void final_rows(const NsEpi& e, const FinalOut& f, int rows, int cols, int row, int j0,
+                                           const float (&t)[N][8]) {
+    if (f.vec && j0 + 8 <= cols) {
         if (e.out_f32) {
-            float* p = static_cast<float*>(f.p) + o;
-            if (e.keep != 0.0f) {
-                load8_f32(p, w);
+            float* p = static_cast<float*>(f.p) + (int64_t)row * f.ld + j0;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, w[c], x[c]);
+            for (int s0 = 0; s0 < N; s0 += 2) {
+                float w[2][8] = {};
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (e.keep != 0.0f && row + 8 * (s0 + s) < rows) load8_f32(p + 8 * (s0 + s) * f.ld, w[s]);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) w[s][c] = fmaf(e.keep, w[s][c], t[s0 + s][c] * f.step);
+                    if (row + 8 * (s0 + s) < rows) store8_f32(p + 8 * (s0 + s) * f.ld, w[s]);
+                }
             }
-            store8_f32(p, x);
         } else {
-            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o;
-            if (e.keep != 0.0f) {
-                load8_bf16(p, w);
+            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + (int64_t)row * f.ld + j0;
+            uint4 q[N];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, w[c], x[c]);
+            for (int s = 0; s < N; ++s)
+                q[s] = e.keep != 0.0f && row + 8 * s < rows ? *reinterpret_cast<const uint4*>(p + 8 * s * f.ld)
+                                                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int s = 0; s < N; ++s) {
+                float x[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[c] = fmaf(e.keep, bf16_of(q[s], c), t[s][c] * f.step);
+                if (row + 8 * s < rows) store8_bf16(p + 8 * s * f.ld, x);
             }
-            store8_bf16(p, x);
         }
         return;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        if (c >= valid) break;
-        if (e.out_f32) {
-            float* p = static_cast<float*>(f.p) + o + c;
-            *p = e.keep != 0.0f ? fmaf(e.keep, *p, x[c]) : x[c];
-        } else {
-            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o + c;
-            *p = __float2bfloat16_rn(e.keep != 0.0f ? fmaf(e.keep, load_bf16(p), x[c]) : x[c]);
+    for (int s = 0; s < N; ++s) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (row + 8 * s >= rows || j0 + c >= cols) continue;
+            const int64_t o = (int64_t)(row + 8 * s) * f.ld + j0 + c;
+            const float x = t[s][c] * f.step;
+            if (e.out_f32) {
+                float* p = static_cast<float*>(f.p) + o;
+                *p = e.keep != 0.0f ? fmaf(e.keep, *p, x) : x;
+            } else {
+                __nv_bfloat16* p = static_cast<__nv_bfloat16*>(f.p) + o;
+                *p = __float2bfloat16_rn(e.keep != 0.0f ? fmaf(e.keep, load_bf16(p), x) : x);
+            }
         }
     }
 }
@@ -447,12 +461,57 @@ __device__ __forceinline__ void linear_steps(const LinearEpi& e, const Args& g, 
     }
 }
 
+// What a Newton-Schulz block's epilogue reads from global memory, loaded ahead
+// of the block's accumulators (their latency, about 1000 cycles, would otherwise
+// come on top of every block).
+template <int KIND>
+struct Ahead {};
+template <>
+struct Ahead<KIND_POLY> {
+    uint4 q[4];
+    float di[4], dj[8];
+};
+template <>
+struct Ahead<KIND_APPLY> {
+    uint4 h[4], l[4];
+    float k[4];
+};
+template <>
+struct Ahead<KIND_FINAL> : Ahead<KIND_APPLY> {};
+
+template <int KIND>
+__device__ __forceinline__ void load_ahead(const typename EpiOf<KIND>::T& e, const Args& g, int batch, int i0, int j0,
+                                           int lane, Ahead<KIND>& a) {
+    const int i = i0 + lane / 4, j = j0 + lane % 4 * 8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if constexpr (KIND == KIND_POLY) {
+        const float* diag = e.gram_diag + (int64_t)batch * e.ldr;
+        const __half* p = e.gram + ((int64_t)batch * g.m + i) * e.ldr + j;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bool in = i + 8 * s < g.m && j < g.n;
+            a.q[s] = in ? *reinterpret_cast<const uint4*>(p + 8 * s * e.ldr) : zero;
+            a.di[s] = in ? diag[i + 8 * s] : 0.0f;
+        }
+        if (j < g.n) load8_f32(diag + j, a.dj);  // rows and diagonals are padded to 8 elements
+    } else if constexpr (KIND == KIND_APPLY || KIND == KIND_FINAL) {
+        const int64_t at = ((int64_t)batch * g.m + i) * e.ldc + j;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bool in = i + 8 * s < g.m && j < g.n;
+            a.h[s] = in ? *reinterpret_cast<const uint4*>(e.hi_in + at + 8 * s * e.ldc) : zero;
+            a.l[s] = in ? *reinterpret_cast<const uint4*>(e.lo_in + at + 8 * s * e.ldc) : zero;
+            a.k[s] = in ? e.coef[(int64_t)batch * e.ldr + i + 8 * s] : 0.0f;
+        }
+    }
+}
+
 // The epilogue of a 32 x 32 block at (i0, j0), staged in shared memory by this
 // warp.  mirror: the block lies off the diagonal square of its tile row, so
 // the symmetric counterpart is written as well.
 template <int KIND>
 __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e, const Args& g, int batch, int i0, int j0,
-                                               uint32_t block, int lane, bool mirror) {
+                                               uint32_t block, int lane, bool mirror, const Ahead<KIND>& a) {
     const int major = lane / 4, minor = lane % 4;
     if constexpr (is_linear(KIND)) {
         // fp32 results: two steps at a time, next to the accumulators in registers
@@ -481,21 +540,25 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
         }
         bool again = false;  // a second, transposed pass over the block
         if constexpr (KIND == KIND_GRAM || KIND == KIND_POLY) again = mirror;
-        if constexpr (KIND == KIND_FINAL) again = e.transposed;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if constexpr (KIND == KIND_FINAL) again = e.out[batch].transposed;
+        const bool diagonal = i0 < j0 + 32 && j0 < i0 + 32;
         if constexpr (KIND == KIND_GRAM) {
             __half* d = e.gram + ((int64_t)batch * g.m + i) * e.ldr + j;  // rows are padded to 8 columns
+            if (diagonal) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (j + c == i + 8 * s && in[s]) {
+                            e.gram_diag[(int64_t)batch * e.ldr + j + c] = t[s][c] * e.alpha;
+                            t[s][c] = 0.0f;
+                        }
+            }
+            const float f = e.alpha * e.off_scale;  // powers of two
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float x = t[s][c] * e.alpha;
-                    t[s][c] = x * e.off_scale;
-                    if (j + c == i + 8 * s && in[s]) {
-                        e.gram_diag[(int64_t)batch * e.ldr + j + c] = x;
-                        t[s][c] = 0.0f;
-                    }
-                }
+                for (int c = 0; c < 8; ++c) t[s][c] *= f;
                 if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
             }
         } else if constexpr (KIND == KIND_POLY) {
@@ -503,50 +566,37 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
             //   A^2 = D^2 + D E + E D + E^2, so off the diagonal
             //   (b A + c A^2)_ij = (b + c (d_i + d_j)) E_ij + c (E^2)_ij
             // and on it b d_i + c d_i^2 + c (E^2)_ii.
-            const float* diag = e.gram_diag + (int64_t)batch * e.ldr;
-            const int64_t at = ((int64_t)batch * g.m + i) * e.ldr + j;
-            uint4 q[4];
-            float di[4], dj[8];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                q[s] = in[s] ? *reinterpret_cast<const uint4*>(e.gram + at + 8 * s * e.ldr) : zero;
-                di[s] = in[s] ? diag[i + 8 * s] : 0.0f;
-            }
-            if (j < g.n) load8_f32(diag + j, dj);
+            __half* d = e.poly + ((int64_t)batch * g.m + i) * e.ldr + j;
+            const float f = e.c * e.alpha * e.off_scale;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 float x[8];
-                half8(q[s], x);
+                half8(a.q[s], x);
+                const float base = fmaf(e.c, a.di[s], e.b);
+                if (diagonal) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float sq = t[s][c] * e.alpha;
-                    t[s][c] = fmaf(fmaf(e.c, di[s] + dj[c], e.b), x[c] * e.off_inv, e.c * sq) * e.off_scale;
-                    if (j + c == i + 8 * s && in[s]) {
-                        e.coef[(int64_t)batch * e.ldr + j + c] = e.a + fmaf(e.c, fmaf(di[s], di[s], sq), e.b * di[s]);
-                        t[s][c] = 0.0f;
-                    }
+                    for (int c = 0; c < 8; ++c)
+                        if (j + c == i + 8 * s && in[s]) {
+                            e.coef[(int64_t)batch * e.ldr + j + c] =
+                                e.a + fmaf(e.c, fmaf(a.di[s], a.di[s], t[s][c] * e.alpha), e.b * a.di[s]);
+                            t[s][c] = 0.0f;  // and the stored diagonal of E is 0
+                        }
                 }
-                if (in[s]) store8_half(e.poly + at + 8 * s * e.ldr, t[s]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(fmaf(e.c, a.dj[c], base), x[c], f * t[s][c]);
+                if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
             }
         } else {
             // X' = (a + diagonal) X + E X: the large part of the polynomial is its
             // diagonal, which multiplies X in full precision (both fp16 terms).
             const int64_t at = ((int64_t)batch * g.m + i) * e.ldc + j;
-            uint4 h[4], l[4];
-            float k[4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                h[s] = in[s] ? *reinterpret_cast<const uint4*>(e.hi_in + at + 8 * s * e.ldc) : zero;
-                l[s] = in[s] ? *reinterpret_cast<const uint4*>(e.lo_in + at + 8 * s * e.ldc) : zero;
-                k[s] = in[s] ? e.coef[(int64_t)batch * e.ldr + i + 8 * s] : 0.0f;
-            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 float hi[8], lo[8];
-                half8(h[s], hi);
-                half8(l[s], lo);
+                half8(a.h[s], hi);
+                half8(a.l[s], lo);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(k[s], hi[c] + lo[c], t[s][c] * e.alpha);
+                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(a.k[s], hi[c] + lo[c], t[s][c] * e.alpha);
                 if constexpr (KIND == KIND_APPLY) {
                     if (in[s]) {
 #pragma unroll
@@ -556,26 +606,26 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
                         for (int c = 0; c < 8; ++c) lo[c] = t[s][c] - hi[c];
                         store8_half(e.lo + at + 8 * s * e.ldc, lo);
                     }
-                } else if (!again) {
-                    if (in[s]) final_row(e, e.out[batch], g.n, i + 8 * s, j, t[s]);
                 }
+            }
+            if constexpr (KIND == KIND_FINAL) {
+                if (!again && j < g.n) final_rows<4>(e, e.out[batch], g.m, g.n, i, j, t);
             }
         }
         if (again) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) block_put(block, s * 8 + major, minor, t[s]);
             __syncwarp();
+            const int col = j0 + major, row = i0 + minor * 8;  // step s: column col + 8 s, rows row .. row + 7
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int col = j0 + s * 8 + major, row = i0 + minor * 8;
-                block_get_column(block, minor, s * 8 + major, t[s]);
-                if (col >= g.n || row >= g.m) continue;
-                if constexpr (KIND == KIND_GRAM)
-                    store8_half(e.gram + ((int64_t)batch * g.m + col) * e.ldr + row, t[s]);
-                else if constexpr (KIND == KIND_POLY)
-                    store8_half(e.poly + ((int64_t)batch * g.m + col) * e.ldr + row, t[s]);
-                else if constexpr (KIND == KIND_FINAL)
-                    final_row(e, e.out[batch], g.m, col, row, t[s]);
+            for (int s = 0; s < 4; ++s) block_get_column(block, minor, s * 8 + major, t[s]);
+            if constexpr (KIND == KIND_FINAL) {
+                if (row < g.m) final_rows<4>(e, e.out[batch], g.n, g.m, col, row, t);
+            } else if constexpr (KIND == KIND_GRAM || KIND == KIND_POLY) {
+                __half* d = (KIND == KIND_GRAM ? e.gram : e.poly) + ((int64_t)batch * g.m + col) * e.ldr + row;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (col + 8 * s < g.n && row < g.m) store8_half(d + 8 * s * e.ldr, t[s]);
             }
         }
     }
@@ -775,7 +825,9 @@ __global__ void __launch_bounds__(kSplitThreads)
             block_put_row(block, lane, v);
             if (g.split == 1) {
                 __syncwarp();
-                if (ok) block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, block, lane, mirror);
+                Ahead<KIND> ahead;
+                load_ahead<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, lane, ahead);
+                if (ok) block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, block, lane, mirror, ahead);
             }
         }
         fence_before();
@@ -811,6 +863,8 @@ __global__ void __launch_bounds__(kSplitThreads)
                 } else {
                     // into a block of this CTA's own, past the partial tile
                     const uint32_t mine = base + (BN / 8 + (warp & 3)) * kBlockBytes;
+                    Ahead<KIND> ahead;
+                    load_ahead<KIND>(e, g, batch, i0, j0, lane, ahead);
                     __syncwarp();
 #pragma unroll
                     for (int step = 0; step < 4; ++step) {
@@ -820,7 +874,7 @@ __global__ void __launch_bounds__(kSplitThreads)
                         block_put(mine, r, minor, t[0]);
                     }
                     __syncwarp();
-                    block_epilogue<KIND>(e, g, batch, i0, j0, mine, lane, mirror);
+                    block_epilogue<KIND>(e, g, batch, i0, j0, mine, lane, mirror, ahead);
                 }
             }
         }
@@ -1024,11 +1078,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         __syncwarp();
                         block_put_row(block, lane, sum[c]);
                         __syncwarp();
-                        block_epilogue<KIND>(e, g, batch, i, j + c * 32, block, lane, mirror);
+                        block_epilogue<KIND>(e, g, batch, i, j + c * 32, block, lane, mirror, Ahead<KIND>());
                     }
                 }
             } else {
                 const int a = fill & 1;
+                Ahead<KIND> ahead;
+                load_ahead<KIND>(e, g, batch, i, j, lane, ahead);
                 ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&acc_full[a], (fill / 2) & 1));
                 if (!ok) break;
                 ++fill;
@@ -1046,8 +1102,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     if (i < g.m && j + c < g.n) {
                         block_put_row(block, lane, v);
+                        const Ahead<KIND> now = ahead;
+                        if (c + 32 < kHalf) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
                         __syncwarp();
-                        block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, mirror);
+                        block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, mirror, now);
                     }
                 }
             }

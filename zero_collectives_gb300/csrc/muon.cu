@@ -36,7 +36,7 @@ namespace gemm {
 namespace {
 
 constexpr int kMaxSteps = 32;
-constexpr int kNormBlocks = 64;   // partial sums of squares per matrix (at most)
+constexpr int kNormBlocks = 256;  // partial sums of squares per matrix (at most)
 constexpr int kTile = 64;         // the element-wise passes work on 64 x 64 tiles
 constexpr float kOffScale = 256.0f;
 
@@ -45,14 +45,15 @@ struct MatIn {
     const void* g;
     float* mom;        // null: U = G
     int64_t ldg, ldm;
+    int transposed;    // X is the transpose (more rows than columns)
+    int g_vec, m_vec;  // 4-element groups of G / the momentum are aligned
 };
 
 struct NormArgs {
     MatIn in[kMaxBatch];
-    int64_t rows, cols;       // as the caller stores them
+    int64_t r, c;             // X is r x c, r <= c; the caller's matrix is that or its transpose
     float mu;
-    int nesterov, transposed; // transposed: X is the transpose (rows > cols)
-    int g_vec, m_vec;         // 4-element groups of G / the momentum are aligned
+    int nesterov;
     float* partial;           // [batch, kNormBlocks]
     int blocks;               // partials written per matrix
     float eps, scale;
@@ -104,26 +105,27 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
     mma::grid_wait();
     const MatIn& in = a.in[blockIdx.y];
     const Tg* g = static_cast<const Tg*>(in.g);
-    const int64_t tr = (a.rows + kTile - 1) / kTile, tc = (a.cols + kTile - 1) / kTile;
+    const int64_t rows = in.transposed ? a.c : a.r, cols = in.transposed ? a.r : a.c;
+    const int64_t tr = (rows + kTile - 1) / kTile, tc = (cols + kTile - 1) / kTile;
     const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
     float sum = 0.0f;
     for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
         const int64_t i0 = t / tc * kTile, j = t % tc * kTile + c;
-        const int valid = (int)(a.cols - j);
+        const int valid = (int)(cols - j);
         if (valid <= 0) continue;
         float gv[4][4], mv[4][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t i = i0 + r + 16 * u;
-            if (i < a.rows) {
-                load4(g + i * in.ldg + j, valid, a.g_vec, gv[u]);
-                if (in.mom) load4(in.mom + i * in.ldm + j, valid, a.m_vec, mv[u]);
+            if (i < rows) {
+                load4(g + i * in.ldg + j, valid, in.g_vec, gv[u]);
+                if (in.mom) load4(in.mom + i * in.ldm + j, valid, in.m_vec, mv[u]);
             }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t i = i0 + r + 16 * u;
-            if (i >= a.rows) continue;
+            if (i >= rows) continue;
             if (in.mom) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
                     gv[u][k] = a.nesterov ? fmaf(a.mu, mv[u][k], gv[u][k]) : mv[u][k];
                 }
                 float* m = in.mom + i * in.ldm + j;
-                if (a.m_vec && valid >= 4) {
+                if (in.m_vec && valid >= 4) {
                     *reinterpret_cast<float4*>(m) = make_float4(mv[u][0], mv[u][1], mv[u][2], mv[u][3]);
                 } else {
 #pragma unroll
@@ -157,11 +159,11 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
     mma::grid_wait();
     const MatIn& in = a.in[blockIdx.y];
     const Tg* g = static_cast<const Tg*>(in.g);
-    float total = 0.0f;
-    for (int k = 0; k < a.blocks; ++k) total += a.partial[blockIdx.y * kNormBlocks + k];
+    const float total = block_sum(threadIdx.x < a.blocks ? a.partial[blockIdx.y * kNormBlocks + threadIdx.x] : 0.0f);
     const float f = a.scale / (sqrtf(total) + a.eps);
-    const int64_t tr = (a.rows + kTile - 1) / kTile, tc = (a.cols + kTile - 1) / kTile;
-    const int64_t xr = a.transposed ? a.cols : a.rows, xc = a.transposed ? a.rows : a.cols;
+    const int64_t rows = in.transposed ? a.c : a.r, cols = in.transposed ? a.r : a.c;
+    const int64_t tr = (rows + kTile - 1) / kTile, tc = (cols + kTile - 1) / kTile;
+    const int64_t xr = a.r, xc = a.c;
     __half* hi = a.hi + (int64_t)blockIdx.y * xr * a.ldc;
     __half* lo = a.lo + (int64_t)blockIdx.y * xr * a.ldc;
     const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
@@ -171,11 +173,11 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t i = i0 + r + 16 * u;
-            const int valid = (int)(a.cols - j0 - c);
-            if (i < a.rows && valid > 0) {
+            const int valid = (int)(cols - j0 - c);
+            if (i < rows && valid > 0) {
                 float m[4];
-                load4(g + i * in.ldg + j0 + c, valid, a.g_vec, x[u]);
-                if (in.mom) load4(in.mom + i * in.ldm + j0 + c, valid, a.m_vec, m);
+                load4(g + i * in.ldg + j0 + c, valid, in.g_vec, x[u]);
+                if (in.mom) load4(in.mom + i * in.ldm + j0 + c, valid, in.m_vec, m);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (in.mom) x[u][k] = a.nesterov ? fmaf(a.mu, m[k], x[u][k]) : m[k];
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
                 for (int k = 0; k < 4; ++k) x[u][k] = 0.0f;
             }
         }
-        if (a.transposed) {
+        if (in.transposed) {
             __syncthreads();
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x[u][k] = tile[c + k][r + 16 * u];
         }
-        const int64_t xi0 = a.transposed ? j0 : i0, xj = (a.transposed ? i0 : j0) + c;
+        const int64_t xi0 = in.transposed ? j0 : i0, xj = (in.transposed ? i0 : j0) + c;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t i = xi0 + r + 16 * u;
@@ -260,9 +262,7 @@ struct Params {
 };
 
 int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cudaStream_t s) {
-    const Item& f = *items[0];
-    const Layout l = layout_of(f.rows, f.cols);
-    const bool transposed = f.rows > f.cols;
+    const Layout l = layout_of(items[0]->rows, items[0]->cols);
     auto take = [&](int64_t bytes) {
         char* p = ws;
         ws += align256(bytes);
@@ -280,26 +280,25 @@ int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cu
     const float scale = std::exp2(std::round(0.5f * std::log2((float)std::min<int64_t>(l.c, 65536))));
 
     NormArgs n = {};
-    n.rows = f.rows;
-    n.cols = f.cols;
+    n.r = l.r;
+    n.c = l.c;
     n.mu = q.mu;
     n.nesterov = q.nesterov;
-    n.transposed = transposed;
     n.partial = partial;
     n.eps = q.eps;
     n.scale = scale;
     n.hi = hi[0];
     n.lo = lo;
     n.ldc = l.ldc;
-    n.g_vec = n.m_vec = 1;
     const int gs = q.g_dtype == DPRED_F32 ? 4 : 2;
     for (int k = 0; k < count; ++k) {
-        const MatIn& in = items[k]->in;
-        n.in[k] = in;
-        if (reinterpret_cast<uintptr_t>(in.g) % (4 * gs) || (f.rows > 1 && in.ldg % 4)) n.g_vec = 0;
-        if (in.mom && (reinterpret_cast<uintptr_t>(in.mom) % 16 || (f.rows > 1 && in.ldm % 4))) n.m_vec = 0;
+        MatIn& in = n.in[k];
+        in = items[k]->in;
+        in.transposed = items[k]->rows > items[k]->cols;
+        in.g_vec = reinterpret_cast<uintptr_t>(in.g) % (4 * gs) == 0 && (items[k]->rows <= 1 || in.ldg % 4 == 0);
+        in.m_vec = reinterpret_cast<uintptr_t>(in.mom) % 16 == 0 && (items[k]->rows <= 1 || in.ldm % 4 == 0);
     }
-    const int64_t tiles = ((f.rows + kTile - 1) / kTile) * ((f.cols + kTile - 1) / kTile);
+    const int64_t tiles = ((l.r + kTile - 1) / kTile) * ((l.c + kTile - 1) / kTile);
     n.blocks = (int)std::min<int64_t>(tiles, kNormBlocks);
     const dim3 grid1((unsigned)n.blocks, (unsigned)count);
     const dim3 grid2((unsigned)std::min<int64_t>(tiles, 512), (unsigned)count);
@@ -323,20 +322,19 @@ int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cu
     e.ldr = l.ldr;
     e.ldc = l.ldc;
     e.off_scale = kOffScale;
-    e.off_inv = 1.0f / kOffScale;
     e.a = q.a;
     e.b = q.b;
     e.c = q.c;
     e.keep = q.keep;
     e.out_f32 = q.out_dtype == DPRED_F32;
-    e.transposed = transposed;
     const int os = e.out_f32 ? 4 : 2;
     for (int k = 0; k < count; ++k) {
         FinalOut& o = e.out[k];
         o.p = items[k]->out;
         o.ld = items[k]->ldo;
         o.step = items[k]->step / scale;
-        o.vec = reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (f.rows <= 1 || o.ld * os % 16 == 0);
+        o.vec = reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (items[k]->rows <= 1 || o.ld * os % 16 == 0);
+        o.transposed = items[k]->rows > items[k]->cols;
     }
     Plan p = {};
     p.args.batch = count;
@@ -374,15 +372,21 @@ int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cu
     return DPRED_OK;
 }
 
-// Matrices of one shape (up to orientation of the caller's storage) share launches.
-int64_t need_of(std::vector<const Item*>& v) {
+// Matrices of one shape, or of its transpose, share launches.
+bool same_shape(const Item* x, const Item* y) {
+    return std::min(x->rows, x->cols) == std::min(y->rows, y->cols) && std::max(x->rows, x->cols) == std::max(y->rows, y->cols);
+}
+
+// Sorts the matrices so that those of one shape are neighbours; the workspace of the largest launch.
+int64_t group(std::vector<const Item*>& v) {
     std::stable_sort(v.begin(), v.end(), [](const Item* x, const Item* y) {
-        return x->rows != y->rows ? x->rows < y->rows : x->cols < y->cols;
+        const int64_t a = std::min(x->rows, x->cols), b = std::min(y->rows, y->cols);
+        return a != b ? a < b : std::max(x->rows, x->cols) < std::max(y->rows, y->cols);
     });
     int64_t need = 0;
     for (size_t i = 0; i < v.size();) {
         size_t j = i;
-        while (j < v.size() && v[j]->rows == v[i]->rows && v[j]->cols == v[i]->cols) ++j;
+        while (j < v.size() && same_shape(v[i], v[j])) ++j;
         const Layout l = layout_of(v[i]->rows, v[i]->cols);
         need = std::max(need, launch_bytes(l, chunk_of(l, (int)(j - i))));
         i = j;
@@ -394,14 +398,14 @@ int run_items(std::vector<Item>& items, const Params& q, void* workspace, size_t
     std::vector<const Item*> v;
     for (const Item& it : items)
         if (it.rows > 0 && it.cols > 0) v.push_back(&it);
-    const int64_t need = need_of(v);
+    const int64_t need = group(v);
     if (need == 0) return DPRED_OK;
     if (!workspace || (int64_t)workspace_bytes < need)
         return set_error(DPRED_E_SIZE, "workspace of %zu bytes, %lld needed", workspace ? workspace_bytes : (size_t)0, (long long)need);
     if (reinterpret_cast<uintptr_t>(workspace) % 256) return set_error(DPRED_E_ALIGN, "workspace is not 256-byte aligned");
     for (size_t i = 0; i < v.size();) {
         size_t j = i;
-        while (j < v.size() && v[j]->rows == v[i]->rows && v[j]->cols == v[i]->cols) ++j;
+        while (j < v.size() && same_shape(v[i], v[j])) ++j;
         const int chunk = chunk_of(layout_of(v[i]->rows, v[i]->cols), (int)(j - i));
         for (; i < j; i += chunk) {
             const int rc = run_chunk(&v[i], (int)std::min<size_t>(chunk, j - i), q, static_cast<char*>(workspace), s);
@@ -497,7 +501,7 @@ extern "C" int dpred_newton_schulz(int32_t batch, int64_t rows, int64_t cols, in
         std::vector<Item> items(batch);
         for (int k = 0; k < batch; ++k) {
             Item& it = items[k];
-            it.in = {static_cast<const char*>(in) + (int64_t)k * batch_stride * is, nullptr, ld, 0};
+            it.in = {static_cast<const char*>(in) + (int64_t)k * batch_stride * is, nullptr, ld, 0, 0, 0, 0};
             it.out = static_cast<char*>(out) + (int64_t)k * out_batch_stride * os;
             it.rows = rows;
             it.cols = cols;
@@ -520,7 +524,7 @@ extern "C" size_t dpred_muon_workspace_bytes(const dpred_muon_matrix* mats, int3
             items[k].cols = mats[k].cols;
             if (mats[k].rows > 0 && mats[k].cols > 0) v.push_back(&items[k]);
         }
-        need = (size_t)need_of(v);
+        need = (size_t)group(v);
         return DPRED_OK;
     });
     return need;
@@ -557,7 +561,7 @@ extern "C" int dpred_muon_step(const dpred_muon_matrix* mats, int32_t n, int32_t
                 return rc;
             if (!std::isfinite(m.scale)) return set_error(DPRED_E_INVAL, "a matrix's scale is not finite");
             Item& it = items[k];
-            it.in = {m.grad, m.momentum, m.ldg, m.ldm};
+            it.in = {m.grad, m.momentum, m.ldg, m.ldm, 0, 0, 0};
             it.out = m.weight;
             it.rows = m.rows;
             it.cols = m.cols;
