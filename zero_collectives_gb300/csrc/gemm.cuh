@@ -88,6 +88,7 @@ struct Args {
     int symmetric;       // only elements i <= j are needed (the epilogue mirrors them)
     int a_mn, b_mn;      // operand majors
     int split;           // CTAs of a cluster that share the reduction
+    int stages;          // split kernel: pipeline stages
     int regions;         // split kernel: accumulators that share a CTA's part of the reduction
     int bf16;
     int* err;
@@ -665,15 +666,26 @@ __device__ __forceinline__ void tile_at(const Args& g, int t, int bm, int bn, in
 // accumulator in tensor memory, added in fp32 registers at the end: the tensor
 // cores' accumulators truncate, about 1.9e-8 of the sum per 16-element step.
 
+//
+// Stages: a copy takes about 1500 cycles from its issue until its stage is free
+// again, so a CTA that has an SM to itself takes all the shared memory (`deep`:
+// a reduction of 640 elements at BN = 32 is in flight at once); launches of
+// more CTAs than SMs use half of it and run two CTAs per SM.
+
 constexpr int kSplitThreads = 192;  // producer warp, issuing warp, four epilogue warps
+constexpr int kMaxStages = 10;
 
 template <int BN>
-__host__ __device__ constexpr int split_stages() {
-    return BN == 32 ? 5 : BN == 64 ? 4 : 3;
+__host__ __device__ constexpr int split_stage_bytes() {
+    return 128 * 128 + BN * 128;
 }
 template <int BN>
-__host__ __device__ constexpr int split_smem() {  // stages + alignment; barriers are static
-    return split_stages<BN>() * (128 * 128 + BN * 128) + 1024;
+__host__ __device__ constexpr int split_stages(bool deep) {
+    return (BN == 32 ? 5 : BN == 64 ? 4 : 3) * (deep ? 2 : 1);
+}
+template <int BN>
+__host__ __device__ constexpr int split_smem(bool deep) {  // stages + alignment; barriers are static
+    return split_stages<BN>(deep) * split_stage_bytes<BN>() + 1024;
 }
 
 // 32 columns of one row, added over a CTA's accumulators.
@@ -706,11 +718,11 @@ __global__ void __launch_bounds__(kSplitThreads)
     split_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::T e) {
     using namespace mma;
-    constexpr int S = split_stages<BN>();
+    const int S = g.stages;
     constexpr uint32_t kA = 128 * 128, kStage = kA + BN * 128;
     constexpr uint32_t kCols = 256;  // two CTAs per SM together allocate all 512
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], done;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -746,11 +758,10 @@ __global__ void __launch_bounds__(kSplitThreads)
 
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {
-            int issued = 0;
+        if (elect_one()) {
+            int issued = 0, s = 0, round = 0;
             for (int it = 0; it < nkb; ++it) {
-                const int s = it % S;
-                if (it >= S && !tma::mbar_wait(&empty[s], (it / S - 1) & 1)) {
+                if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
                     record_device_error(g.err, DPRED_E_TIMEOUT);
                     ok = false;
                     break;
@@ -772,36 +783,42 @@ __global__ void __launch_bounds__(kSplitThreads)
                     load_box(b, &mb, bar, k0, tn * BN, batch);
                 }
                 ++issued;
+                if (++s == S) {
+                    s = 0;
+                    ++round;
+                }
             }
             if (!ok)  // let the copies in flight land before the CTA can leave
                 for (int it = issued > S ? issued - S : 0; it < issued; ++it) tma::mbar_wait(&full[it % S], (it / S) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
+            const uint64_t da0 = operand_desc(base, g.a_mn), db0 = operand_desc(base + kA, g.b_mn);
+            const uint32_t sa = g.a_mn ? 128 : 2, sb = g.b_mn ? 128 : 2;  // 16 reduction elements, in 16-byte units
             const uint32_t idesc = instr_desc(128, BN, g.bf16, g.a_mn, g.b_mn);
-            int region = 0;
+            int region = 0, s = 0, round = 0;
             for (int it = 0; it < nkb; ++it) {
-                const int s = it % S;
                 bool first = it == 0;
                 if (region + 1 < regions && it >= nkb * (region + 1) / regions) {
                     ++region;
                     first = true;
                 }
-                if (!tma::mbar_wait(&full[s], (it / S) & 1)) {
+                if (!tma::mbar_wait(&full[s], round & 1)) {
                     record_device_error(g.err, DPRED_E_TIMEOUT);
                     ok = false;
                     break;
                 }
                 fence_after();
-                const uint32_t a = base + s * kStage, b = a + kA;
+                const uint64_t da = da0 + s * (kStage >> 4), db = db0 + s * (kStage >> 4);
 #pragma unroll
-                for (int k = 0; k < kBlockK / 16; ++k) {
-                    const uint64_t da = operand_desc(a + (g.a_mn ? k * 2048 : k * 32), g.a_mn);
-                    const uint64_t db = operand_desc(b + (g.b_mn ? k * 2048 : k * 32), g.b_mn);
-                    issue<1>(tmem + region * BN, da, db, idesc, !first || k != 0);
-                }
+                for (int k = 0; k < kBlockK / 16; ++k)
+                    issue<1>(tmem + region * BN, da + k * sa, db + k * sb, idesc, !first || k != 0);
                 commit<1>(tma::smem_addr(&empty[s]));
+                if (++s == S) {
+                    s = 0;
+                    ++round;
+                }
             }
             if (ok && nkb) commit<1>(tma::smem_addr(&done));
         }
@@ -959,17 +976,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
+        if (elect_one()) {
+            int s = 0, round = 0;
             bool ok = true;
             for (int tile = pair; tile < total && ok; tile += pairs) {
                 const int batch = tile / g.tiles_per_batch;
                 int tm, tn;
                 tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
                 const int i0 = tm * 256 + (int)rank * 128, j0 = tn * BN + (int)rank * (BN / 2);
-                for (int kb = 0; kb < g.kblocks; ++kb, ++it) {
-                    const int s = it % S;
-                    if (it >= S && !tma::mbar_wait(&empty[s], (it / S - 1) & 1)) {
+                for (int kb = 0; kb < g.kblocks; ++kb) {
+                    if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
                         record_device_error(g.err, DPRED_E_TIMEOUT);
                         ok = false;
                         break;
@@ -989,6 +1005,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     } else {
                         load_box_pair(b, &mb, bar, k0, j0, batch);
                     }
+                    if (++s == S) {
+                        s = 0;
+                        ++round;
+                    }
                 }
             }
             if (!ok) {  // copies in flight land within microseconds, or never: leave after a bounded pause
@@ -999,9 +1019,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
+            const uint64_t da0 = operand_desc(base, g.a_mn), db0 = operand_desc(base + kA, g.b_mn);
+            const uint32_t sa = g.a_mn ? 128 : 2, sb = g.b_mn ? 128 : 2;  // 16 reduction elements, in 16-byte units
             const uint32_t idesc = instr_desc(256, BN, g.bf16, g.a_mn, g.b_mn);
-            int it = 0, fill = 0;
+            int s = 0, round = 0, fill = 0;
             bool ok = true;
             for (int tile = pair; tile < total && ok; tile += pairs) {
                 for (int kb = 0; kb < g.kblocks && ok; ++fill) {
@@ -1013,22 +1035,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     fence_after();
                     const int stop = min(kb + chunk, g.kblocks);
-                    for (int first = kb; kb < stop; ++kb, ++it) {
-                        const int s = it % S;
-                        if (!tma::mbar_wait(&full[s], (it / S) & 1)) {
+                    for (int first = kb; kb < stop; ++kb) {
+                        if (!tma::mbar_wait(&full[s], round & 1)) {
                             record_device_error(g.err, DPRED_E_TIMEOUT);
                             ok = false;
                             break;
                         }
                         fence_after();
-                        const uint32_t pa = base + s * kStage, pb = pa + kA;
+                        const uint64_t da = da0 + s * (kStage >> 4), db = db0 + s * (kStage >> 4);
 #pragma unroll
-                        for (int k = 0; k < kBlockK / 16; ++k) {
-                            const uint64_t da = operand_desc(pa + (g.a_mn ? k * 2048 : k * 32), g.a_mn);
-                            const uint64_t db = operand_desc(pb + (g.b_mn ? k * 2048 : k * 32), g.b_mn);
-                            issue<2>(tmem + a * BN, da, db, idesc, kb != first || k != 0);
-                        }
+                        for (int k = 0; k < kBlockK / 16; ++k)
+                            issue<2>(tmem + a * BN, da + k * sa, db + k * sb, idesc, kb != first || k != 0);
                         commit<2>(tma::smem_addr(&empty[s]));
+                        if (++s == S) {
+                            s = 0;
+                            ++round;
+                        }
                     }
                     if (ok) commit<2>(tma::smem_addr(&acc_full[a]));
                 }

@@ -25,7 +25,7 @@ template <int KIND, int BN>
 int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
     static bool attr[64] = {};
     auto kernel = split_kernel<KIND, BN>;
-    cudaError_t err = ensure_smem_attr(kernel, split_smem<BN>(), attr);
+    cudaError_t err = ensure_smem_attr(kernel, split_smem<BN>(true), attr);
     if (err != cudaSuccess) return cuda_error(err, "shared-memory limit of a matrix product");
     CUtensorMap ma = {}, mb = {};
     if (p.args.kblocks) {  // an empty reduction loads nothing
@@ -39,11 +39,13 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
     g.tiles_n = (g.n + BN - 1) / BN;
     g.tiles_per_batch = (int)tiles_of(g, 128, BN);
     g.split = sh.split;
+    const bool deep = sh.tiles * sh.split <= sm_count();
+    g.stages = split_stages<BN>(deep);
     g.regions = p.fp32_result ? 256 / BN : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sh.tiles * sh.split));
     cfg.blockDim = dim3(kSplitThreads);
-    cfg.dynamicSmemBytes = split_smem<BN>();
+    cfg.dynamicSmemBytes = split_smem<BN>(deep);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -22,6 +22,16 @@ namespace mma {
 
 constexpr int kBlockK = 64;  // reduction elements per pipeline stage (one 128-byte swizzle row of 16-bit values)
 
+// True in one thread of the (converged) warp.  The compiler knows that what
+// follows runs in a single thread, so the operands of the copy and matrix
+// instructions go to uniform registers without a per-lane loop.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- clusters --
 
 __device__ __forceinline__ uint32_t cluster_rank() {
