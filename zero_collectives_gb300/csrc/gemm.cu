@@ -1,6 +1,7 @@
 // gemm.cu -- host side of the matrix products: tensor maps, launch shapes.
 #include "gemm_host.cuh"
 
+#include <cmath>
 #include <mutex>
 
 namespace dpred {
@@ -88,26 +89,56 @@ int resident_pairs(const void* kernel, int threads, int smem) {
     return cached[dev];
 }
 
-Shape choose_shape(const Args& a) {
-    Shape s;
+// The estimated time (us) of a product on one kernel.  The form is that of the
+// kernels: a start, then waves of tiles, each reduction block costing what its
+// copies and matrix instructions take and each tile its epilogue (which the
+// tile kernel hides behind the next tile's reduction).  The constants were
+// fitted to 1000 timings of every kernel on 95 shapes from 1 to 16384 rows and
+// 256 to 8192 columns (forward, dgrad, wgrad; bf16 and fp32 results); the
+// choice by these estimates is 4% slower on average than the best kernel of each.
+static double split_time(const Args& a, int bn, int split, int sms) {
+    const double start = bn == 32 ? 0.6 : bn == 64 ? 2.0 : 1.2;
+    const double block = bn == 32 ? 0.23 : bn == 64 ? 0.25 : 0.335, epilogue = bn == 32 ? 2.3 : bn == 64 ? 2.6 : 5.1;
+    const double ctas = (double)tiles_of(a, 128, bn) * a.batch * split;
+    const double per_wave = split_alone(ctas, split, sms) ? sms : 2 * sms;
+    double load = (ctas < 2 * sms ? ctas : 2 * sms) / sms;  // CTAs per SM, sharing its bandwidth and issue slots
+    if (load < 1) load = 1;
+    const double join = split == 1 ? 0.0 : split < 8 ? 1.75 : 2.9;
+    return 0.6 + start + std::ceil(ctas / per_wave) * (a.kblocks / (double)split * block * std::pow(load, 0.23) + epilogue * load) + join;
+}
+
+static double tile_time(const Args& a, int bn, bool fp32, int pairs) {
+    const double start = bn == 128 ? 3.3 : 2.9, block = bn == 128 ? 0.262 : 0.313;
+    const double epilogue = (bn == 128 ? 1.1 : 3.3) * (fp32 ? 2.5 : 1.0), reduction = a.kblocks * block;
+    const double waves = std::ceil((double)tiles_of(a, 256, bn) * a.batch / pairs);
+    return start + (waves - 1) * (reduction > epilogue ? reduction : epilogue) + reduction + epilogue;
+}
+
+bool split_alone(double ctas, int split, int sms) { return ctas <= (split < 8 ? sms : sms * 5 / 8); }
+
+Shape choose_shape(const Args& a, bool fp32) {
     const int sms = sm_count();
-    s.pairs = false;
-    if (a.kblocks > 0 && a.m > 128) {
-        const int64_t wide = tiles_of(a, 256, 256) * a.batch, narrow = tiles_of(a, 256, 128) * a.batch;
-        if (narrow * 2 >= sms) {
-            s.pairs = true;
-            s.bn = wide * 2 >= sms && a.n > 128 ? 256 : 128;
-            s.tiles = s.bn == 256 ? wide : narrow;
-            s.split = 1;
-            return s;
+    Shape best = {};
+    double t = 1e30;
+    for (int bn = 32; bn <= 128; bn *= 2) {
+        if (bn == 32 && a.b_mn) continue;  // MN-major copies are 64 columns wide
+        for (int split = 1; split <= 8 && (split == 1 || split <= a.kblocks); split *= 2) {
+            const double u = split_time(a, bn, split, sms);
+            if (u < t) {
+                t = u;
+                best = {false, bn, split, tiles_of(a, 128, bn) * a.batch};
+            }
         }
     }
-    s.bn = a.n <= 32 && !a.b_mn ? 32 : a.n <= 64 ? 64 : tiles_of(a, 128, 128) * a.batch >= sms ? 128 : 64;
-    s.tiles = tiles_of(a, 128, s.bn) * a.batch;
-    s.split = 1;
-    // twice as many CTAs while the SMs are not filled once and every CTA keeps two reduction blocks
-    while (s.split < 8 && s.tiles * s.split * 2 <= 2 * sms && a.kblocks >= s.split * 4) s.split *= 2;
-    return s;
+    if (a.kblocks > 0 && !a.columns_only)
+        for (int bn = 128; bn <= 256; bn *= 2) {
+            const double u = tile_time(a, bn, fp32, sms / 2);
+            if (u < t) {
+                t = u;
+                best = {true, bn, 1, tiles_of(a, 256, bn) * a.batch};
+            }
+        }
+    return best;
 }
 
 }  // namespace gemm

@@ -87,6 +87,7 @@ struct Args {
     int tiles_m, tiles_n, tiles_per_batch;
     int symmetric;       // only elements i <= j are needed (the epilogue mirrors them)
     int a_mn, b_mn;      // operand majors
+    int columns_only;    // a swapped epilogue: split kernel only
     int split;           // CTAs of a cluster that share the reduction
     int stages;          // split kernel: pipeline stages
     int regions;         // split kernel: accumulators that share a CTA's part of the reduction
@@ -1082,12 +1083,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!ok) break;
                     fence_after();
 #pragma unroll
-                    for (int c = 0; c < kHalf / 32; ++c) {
-                        float v[32];
-                        tmem_ld32(lanes + a * BN + c * 32, v);
+                    for (int c = 0; c < kHalf / 16; ++c) {  // 16 columns: the sums take most of the registers
+                        float v[16];
+                        tmem_ld16(lanes + a * BN + c * 16, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) sum[c][x] += v[x];
+                        for (int x = 0; x < 16; ++x) sum[c / 2][c % 2 * 16 + x] += v[x];
                     }
                     fence_before();
                     __syncwarp();

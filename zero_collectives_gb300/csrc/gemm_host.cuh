@@ -19,7 +19,9 @@ int resident_pairs(const void* kernel, int threads, int smem);
 int make_map(const Operand& o, int batch, int box_rows, bool bf16, CUtensorMap* m);
 bool tma_able(const void* p, int64_t rows, int64_t ld);
 int64_t tiles_of(const Args& a, int bm, int bn);
-Shape choose_shape(const Args& a);
+Shape choose_shape(const Args& a, bool fp32);
+// Whether a split launch gives every CTA an SM of its own (eight-CTA clusters do not fit every SM of a GPC).
+bool split_alone(double ctas, int split, int sms);
 
 template <int KIND, int BN>
 int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
@@ -39,7 +41,7 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
     g.tiles_n = (g.n + BN - 1) / BN;
     g.tiles_per_batch = (int)tiles_of(g, 128, BN);
     g.split = sh.split;
-    const bool deep = sh.tiles * sh.split <= sm_count();
+    const bool deep = split_alone((double)sh.tiles * sh.split, sh.split, sm_count());
     g.stages = split_stages<BN>(deep);
     g.regions = p.fp32_result ? 256 / BN : 1;
     cudaLaunchConfig_t cfg = {};
@@ -127,7 +129,7 @@ int run_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, 
 
 template <int KIND>
 int run(const Plan& p, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
-    const Shape sh = choose_shape(p.args);
+    const Shape sh = choose_shape(p.args, p.fp32_result);
     if (sh.tiles * sh.split > 0x7FFFFFFF) return set_error(DPRED_E_SIZE, "a matrix product of too many tiles");
     if (sh.pairs) return run_tiles<KIND>(p, sh, e, s);
     switch (sh.bn) {
