@@ -7,7 +7,8 @@
  * 1.3 us); here they are converted once, by prepare(), into a C struct kept in
  * a capsule, and flush() passes them on together with the per-call stream and
  * probe.  call() makes one unprepared call from plain integers, for the
- * binding's flush_bucket.  The function called is the library's own dpred_flush_bucket, whose
+ * binding's flush_bucket; linear(), linear_dgrad() and linear_wgrad() do the
+ * same for the linear-layer products.  The function called is the library's own dpred_flush_bucket, whose
  * address the Python binding hands over (the library is loaded once, by the
  * binding, so the plan cache and the error state are the ones every other
  * call uses).  This module adds no arithmetic: argument marshalling only.
@@ -203,7 +204,75 @@ static PyObject* call_once(PyObject* self, PyObject* const* args, Py_ssize_t nar
     return probe_tuple(rc, &probe, p.world);
 }
 
+/* linear(fn, ...), linear_dgrad(fn, ...), linear_wgrad(fn, ...): one call of the
+ * entry point at address fn with its arguments as integers (addresses too; 0 =
+ * NULL), returning its status code. */
+#define DPRED_MAX_INTS 20
+static int integers(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want, long long* v) {
+    if (nargs != want) {
+        PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", want, nargs);
+        return -1;
+    }
+    for (Py_ssize_t i = 0; i < want; ++i) {
+        v[i] = PyLong_AsLongLong(args[i]);
+        if (v[i] == -1 && PyErr_Occurred()) return -1;
+    }
+    if (!v[0]) {
+        PyErr_SetString(PyExc_ValueError, "null function address");
+        return -1;
+    }
+    return 0;
+}
+#define DPRED_I32(i) ((int32_t)v[i])
+#define DPRED_PTR(i) ((void*)(uintptr_t)v[i])
+
+static PyObject* linear(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_INTS + 1];
+    if (integers(args, nargs, 21, v)) return NULL;
+    int (*fn)(int64_t, int64_t, int64_t, const void*, int64_t, const void*, int64_t, int32_t, const void*, int32_t,
+              const void*, int64_t, void*, int64_t, int32_t, void*, int64_t, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], v[3], DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_I32(8), DPRED_PTR(9), DPRED_I32(10),
+            DPRED_PTR(11), v[12], DPRED_PTR(13), v[14], DPRED_I32(15), DPRED_PTR(16), v[17], DPRED_PTR(18),
+            (size_t)v[19], DPRED_PTR(20));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* linear_dgrad(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_INTS + 1];
+    if (integers(args, nargs, 19, v)) return NULL;
+    int (*fn)(int64_t, int64_t, int64_t, const void*, int64_t, const void*, int64_t, int32_t, const void*, int64_t,
+              const void*, int64_t, int32_t, void*, int64_t, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], v[3], DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_I32(8), DPRED_PTR(9), v[10], DPRED_PTR(11),
+            v[12], DPRED_I32(13), DPRED_PTR(14), v[15], DPRED_PTR(16), (size_t)v[17], DPRED_PTR(18));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* linear_wgrad(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_INTS + 1];
+    if (integers(args, nargs, 16, v)) return NULL;
+    int (*fn)(int64_t, int64_t, int64_t, const void*, int64_t, const void*, int64_t, int32_t, int32_t, void*, int64_t,
+              float*, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], v[3], DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_I32(8), DPRED_I32(9), DPRED_PTR(10), v[11],
+            DPRED_PTR(12), DPRED_PTR(13), (size_t)v[14], DPRED_PTR(15));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 static PyMethodDef kMethods[] = {
+    {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, "One dpred_linear call from integers."},
+    {"linear_dgrad", (PyCFunction)(void (*)(void))linear_dgrad, METH_FASTCALL, "One dpred_linear_dgrad call from integers."},
+    {"linear_wgrad", (PyCFunction)(void (*)(void))linear_wgrad, METH_FASTCALL, "One dpred_linear_wgrad call from integers."},
     {"prepare", prepare, METH_VARARGS, "Convert one dpred_flush_bucket call's arguments once."},
     {"flush", (PyCFunction)(void (*)(void))flush, METH_FASTCALL, "Make a prepared dpred_flush_bucket call."},
     {"flush_probed", (PyCFunction)(void (*)(void))flush_probed, METH_FASTCALL,

@@ -39,29 +39,56 @@ def declare(L) -> None:
     L.dpred_muon_step.argtypes = [vp, i32, i32, i32, f32, f32, i32, f32, i32, vp, f32, vp, sz, vp]
 
 
-def _zc():
+torch = _zc = _BF = _OK = None  # bound by the first call (the package imports without torch)
+
+
+def _bind() -> None:
+    global torch, _zc, _BF, _OK
+    import torch as t
+
     import zero_collectives_gb300 as zc
-    return zc
+    torch, _zc = t, zc
+    _BF, _OK = (t.bfloat16,), (t.bfloat16, t.float32)
 
 
-def _matrix(t, name: str, dtypes, shape=None):
-    """(data pointer, row stride) of a 2-D CUDA tensor with unit column stride."""
-    import torch
+def _device() -> int:
+    if torch is None:
+        _bind()
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _matrix(t, name: str, dtypes, device: int, rows=None, cols=None):
+    """(data pointer, row stride, rows, columns) of a 2-D tensor on the current
+    device with unit column stride."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != 2 or not t.is_cuda or t.device.index != torch.cuda.current_device():
+    shape = t.shape
+    if len(shape) != 2 or t.get_device() != device:
         raise ValueError(f"{name} must be a 2-D tensor on the current CUDA device")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    r, c = shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must have shape ({'*' if rows is None else rows}, {'*' if cols is None else cols}), "
+                         f"got {tuple(shape)}")
     rs, cs = t.stride()
-    if cs != 1 and t.shape[1] > 1:
+    if cs != 1 and c > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), (rs if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), (rs if r > 1 else c), r, c
+
+
+def _vector(t, name: str, dtypes, device: int, n: int) -> int:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous tensor of {n} elements on the current CUDA device")
+    return t.data_ptr()
+
+
+def _code(t) -> int:
+    return 0 if t.dtype is _BF[0] else 1
 
 
 def _empty(shape, dtype, stream):
     """Device memory that belongs to the stream of the call."""
-    import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device="cuda")
     if not hasattr(stream, "cuda_stream"):
@@ -71,23 +98,45 @@ def _empty(shape, dtype, stream):
 
 
 def _workspace(need: int, given, stream):
-    import torch
     if given is not None:
         return given, given.data_ptr(), given.numel() * given.element_size()
     if not need:
-        return None, None, 0
+        return None, 0, 0
     ws = _empty(need, torch.uint8, stream)
     return ws, ws.data_ptr(), need
+
+
+def _pack_space(L, a, ar, ac, lda, b, br, bc, ldb, given, stream):
+    """Workspace of a product: only operands without 16-byte aligned rows need one."""
+    if given is None and not (a % 16 or b % 16 or (ar > 1 and lda % 8) or (br > 1 and ldb % 8)):
+        return None, 0, 0
+    return _workspace(L.dpred_linear_workspace_bytes(a, ar, ac, lda, b, br, bc, ldb) if given is None else 0, given,
+                      stream)
+
+
+_fn: dict = {}
+
+
+def _call(name: str, *args) -> None:
+    """One entry point with integer arguments (0 = NULL): through the CPython
+    module where it was built, else through ctypes."""
+    fc = _zc._FC if _zc._FC is not None else _zc._fast_call_module()
+    L = _zc.lib()
+    if fc is not None:
+        fn = _fn.get(name)
+        if fn is None:
+            fn = _fn[name] = (getattr(fc, name), ctypes.cast(getattr(L, "dpred_" + name), ctypes.c_void_p).value)
+        rc = fn[0](fn[1], *args)
+    else:
+        rc = getattr(L, "dpred_" + name)(*args)
+    if rc:
+        _zc._check(rc)
 
 
 def _act(act) -> int:
     if act not in _ACTS:
         raise ValueError(f"unknown activation {act!r}: none, relu, gelu or silu")
     return _ACTS[act]
-
-
-def _unaligned(*mats) -> bool:
-    return any(p % 16 or (r > 1 and ld % 8) for p, r, ld in mats)
 
 
 def linear(x, w, bias=None, act="none", residual=None, preact=None, out=None, out_dtype=None, workspace=None,
@@ -97,29 +146,23 @@ def linear(x, w, bias=None, act="none", residual=None, preact=None, out=None, ou
     x w^T + bias (what linear_dgrad of the next layer down needs).  out: bf16
     or fp32 [m, n] (allocated on the call's stream when None).  Rows may be
     strided; m may be 1 (a single token)."""
-    import torch
-    zc = _zc()
-    bf, ok = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    xp, ldx = _matrix(x, "x", bf)
-    m, k = x.shape
-    wp, ldw = _matrix(w, "w", bf, (w.shape[0], k))
-    n = w.shape[0]
+    dev = _device()
+    xp, ldx, m, k = _matrix(x, "x", _BF, dev)
+    wp, ldw, n, _ = _matrix(w, "w", _BF, dev, None, k)
+    a = _act(act)
     if out is None:
-        out = _empty((m, n), out_dtype or torch.bfloat16, stream)
-    yp, ldy = _matrix(out, "out", ok, (m, n))
-    rp, ldr = (None, 0) if residual is None else _matrix(residual, "residual", bf, (m, n))
-    pp, ldp = (None, 0) if preact is None else _matrix(preact, "preact", bf, (m, n))
-    bp, bdt = None, 0
+        out = _empty((m, n), out_dtype or _BF[0], stream)
+    yp, ldy, _, _ = _matrix(out, "out", _OK, dev, m, n)
+    rp = ldr = pp = ldp = bp = bdt = 0
+    if residual is not None:
+        rp, ldr, _, _ = _matrix(residual, "residual", _BF, dev, m, n)
+    if preact is not None:
+        pp, ldp, _, _ = _matrix(preact, "preact", _BF, dev, m, n)
     if bias is not None:
-        if tuple(bias.shape) != (n,) or bias.dtype not in ok or not bias.is_cuda or (n > 1 and bias.stride(0) != 1):
-            raise ValueError("bias must be a contiguous bf16 or fp32 CUDA tensor of n elements")
-        bp, bdt = bias.data_ptr(), zc._dtype_code(bias)
-    L = zc.lib()
-    need = L.dpred_linear_workspace_bytes(xp, m, k, ldx, wp, n, k, ldw) \
-        if workspace is None and _unaligned((xp, m, ldx), (wp, n, ldw)) else 0
-    ws, wsp, wsb = _workspace(need, workspace, stream)
-    zc._check(L.dpred_linear(m, n, k, xp, ldx, wp, ldw, bdt, bp, _act(act), rp, ldr, pp, ldp, zc._dtype_code(out), yp,
-                             ldy, wsp, wsb, zc._stream(stream)))
+        bp, bdt = _vector(bias, "bias", _OK, dev, n), _code(bias)
+    ws, wsp, wsb = _pack_space(_zc.lib(), xp, m, k, ldx, wp, n, k, ldw, workspace, stream)
+    _call("linear", m, n, k, xp, ldx, wp, ldw, bdt, bp, a, rp, ldr, pp, ldp, _code(out), yp, ldy, wsp, wsb,
+          _zc._stream(stream))
     return out
 
 
@@ -129,27 +172,23 @@ def linear_dgrad(dy, w, preact=None, act="none", residual=None, out=None, out_dt
     preact: the stored pre-activation of the layer below, bf16 [m, k] (needed
     unless act is "none"); residual: bf16 [m, k], the gradient that joins from
     a residual branch.  out: bf16 or fp32 [m, k]."""
-    import torch
-    zc = _zc()
-    bf, ok = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    dp, ldd = _matrix(dy, "dy", bf)
-    m, n = dy.shape
-    wp, ldw = _matrix(w, "w", bf, (n, w.shape[1]))
-    k = w.shape[1]
-    if out is None:
-        out = _empty((m, k), out_dtype or torch.bfloat16, stream)
-    op, ldo = _matrix(out, "out", ok, (m, k))
+    dev = _device()
+    dp, ldd, m, n = _matrix(dy, "dy", _BF, dev)
+    wp, ldw, _, k = _matrix(w, "w", _BF, dev, n, None)
     a = _act(act)
     if a != ACT_NONE and preact is None:
         raise ValueError("an activation's gradient needs preact")
-    zp, ldz = (None, 0) if preact is None or a == ACT_NONE else _matrix(preact, "preact", bf, (m, k))
-    rp, ldr = (None, 0) if residual is None else _matrix(residual, "residual", bf, (m, k))
-    L = zc.lib()
-    need = L.dpred_linear_workspace_bytes(dp, m, n, ldd, wp, n, k, ldw) \
-        if workspace is None and _unaligned((dp, m, ldd), (wp, n, ldw)) else 0
-    ws, wsp, wsb = _workspace(need, workspace, stream)
-    zc._check(L.dpred_linear_dgrad(m, n, k, dp, ldd, wp, ldw, a, zp, ldz, rp, ldr, zc._dtype_code(out), op, ldo, wsp,
-                                   wsb, zc._stream(stream)))
+    if out is None:
+        out = _empty((m, k), out_dtype or _BF[0], stream)
+    op, ldo, _, _ = _matrix(out, "out", _OK, dev, m, k)
+    zp = ldz = rp = ldr = 0
+    if a != ACT_NONE:
+        zp, ldz, _, _ = _matrix(preact, "preact", _BF, dev, m, k)
+    if residual is not None:
+        rp, ldr, _, _ = _matrix(residual, "residual", _BF, dev, m, k)
+    ws, wsp, wsb = _pack_space(_zc.lib(), dp, m, n, ldd, wp, n, k, ldw, workspace, stream)
+    _call("linear_dgrad", m, n, k, dp, ldd, wp, ldw, a, zp, ldz, rp, ldr, _code(out), op, ldo, wsp, wsb,
+          _zc._stream(stream))
     return out
 
 
@@ -158,26 +197,14 @@ def linear_wgrad(dy, x, out, bias_grad=None, accumulate: bool = False, workspace
     the outputs hold (accumulate=True).  dy: bf16 [m, n]; x: bf16 [m, k]; out:
     [n, k] bf16 (a view of the gradient row that a flush reads) or fp32 (a view
     of the accumulator of accumulate_microbatch); bias_grad: fp32 [n]."""
-    import torch
-    zc = _zc()
-    bf, ok = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    dp, ldd = _matrix(dy, "dy", bf)
-    m, n = dy.shape
-    xp, ldx = _matrix(x, "x", bf, (m, x.shape[1]))
-    k = x.shape[1]
-    op, ldo = _matrix(out, "out", ok, (n, k))
-    bp = None
-    if bias_grad is not None:
-        if tuple(bias_grad.shape) != (n,) or bias_grad.dtype != torch.float32 or not bias_grad.is_cuda \
-                or (n > 1 and bias_grad.stride(0) != 1):
-            raise ValueError("bias_grad must be a contiguous fp32 CUDA tensor of n elements")
-        bp = bias_grad.data_ptr()
-    L = zc.lib()
-    need = L.dpred_linear_workspace_bytes(dp, m, n, ldd, xp, m, k, ldx) \
-        if workspace is None and _unaligned((dp, m, ldd), (xp, m, ldx)) else 0
-    ws, wsp, wsb = _workspace(need, workspace, stream)
-    zc._check(L.dpred_linear_wgrad(m, n, k, dp, ldd, xp, ldx, int(accumulate), zc._dtype_code(out), op, ldo, bp, wsp,
-                                   wsb, zc._stream(stream)))
+    dev = _device()
+    dp, ldd, m, n = _matrix(dy, "dy", _BF, dev)
+    xp, ldx, _, k = _matrix(x, "x", _BF, dev, m, None)
+    op, ldo, _, _ = _matrix(out, "out", _OK, dev, n, k)
+    bp = 0 if bias_grad is None else _vector(bias_grad, "bias_grad", _OK[1:], dev, n)
+    ws, wsp, wsb = _pack_space(_zc.lib(), dp, m, n, ldd, xp, m, k, ldx, workspace, stream)
+    _call("linear_wgrad", m, n, k, dp, ldd, xp, ldx, 1 if accumulate else 0, _code(out), op, ldo, bp, wsp, wsb,
+          _zc._stream(stream))
     return out
 
 
@@ -190,27 +217,25 @@ def newton_schulz(g, out=None, steps: int = 5, eps: float = 1e-7, coeffs=None, w
     bf16 or fp32): `steps` steps of X = a X + (b A + c A^2) X, A = X X^T, from
     g / (|g|_F + eps).  out: bf16 (the default) or fp32, same shape; it carries
     16-bit accuracy either way (see dpred_newton_schulz)."""
-    import torch
-    zc = _zc()
-    ok = (torch.bfloat16, torch.float32)
+    dev = _device()
+    zc = _zc
     if g.dim() not in (2, 3):
         raise ValueError("g must be [m, n] or [batch, m, n]")
     if out is None:
-        out = _empty(tuple(g.shape), torch.bfloat16, stream)
+        out = _empty(tuple(g.shape), _BF[0], stream)
     if tuple(out.shape) != tuple(g.shape):
         raise ValueError("out must have the shape of g")
     batch = g.shape[0] if g.dim() == 3 else 1
     if batch == 0:
         return out
-    gp, ldg = _matrix(g[0] if g.dim() == 3 else g, "g", ok)
-    op, ldo = _matrix(out[0] if g.dim() == 3 else out, "out", ok)
+    gp, ldg, m, n = _matrix(g[0] if g.dim() == 3 else g, "g", _OK, dev)
+    op, ldo, _, _ = _matrix(out[0] if g.dim() == 3 else out, "out", _OK, dev)
     gb, ob = (g.stride(0), out.stride(0)) if g.dim() == 3 else (0, 0)
-    m, n = g.shape[-2:]
     L = zc.lib()
     need = L.dpred_newton_schulz_workspace_bytes(batch, m, n) if workspace is None else 0
     ws, wsp, wsb = _workspace(need, workspace, stream)
-    zc._check(L.dpred_newton_schulz(batch, m, n, zc._dtype_code(g), gp, ldg, gb, zc._dtype_code(out), op, ldo, ob,
-                                    int(steps), _coeffs(coeffs), float(eps), wsp, wsb, zc._stream(stream)))
+    zc._check(L.dpred_newton_schulz(batch, m, n, _code(g), gp, ldg, gb, _code(out), op, ldo, ob, int(steps),
+                                    _coeffs(coeffs), float(eps), wsp or None, wsb, zc._stream(stream)))
     return out
 
 
@@ -226,21 +251,18 @@ def update_scale(rows: int, cols: int, rule) -> float:
 
 
 def _muon_table(weights, momenta, grads, scale):
-    import torch
+    dev = _device()
     if not (len(weights) == len(momenta) == len(grads)):
         raise ValueError("weights, momenta and grads must have one entry per matrix")
-    ok = (torch.bfloat16, torch.float32)
     table = (_MuonMatrix * max(len(weights), 1))()
     for i, (w, m, g) in enumerate(zip(weights, momenta, grads)):
         if w.dtype != weights[0].dtype or g.dtype != grads[0].dtype:
             raise TypeError("all weights must have one dtype, and all grads one")
-        shape = tuple(w.shape)
         t = table[i]
-        t.weight, t.ldw = _matrix(w, "weight", ok)
-        t.momentum, t.ldm = _matrix(m, "momentum", (torch.float32,), shape)
-        t.grad, t.ldg = _matrix(g, "grad", ok, shape)
-        t.rows, t.cols = shape
-        t.scale = update_scale(*shape, scale)
+        t.weight, t.ldw, r, c = _matrix(w, "weight", _OK, dev)
+        t.momentum, t.ldm, _, _ = _matrix(m, "momentum", _OK[1:], dev, r, c)
+        t.grad, t.ldg, _, _ = _matrix(g, "grad", _OK, dev, r, c)
+        t.rows, t.cols, t.scale = r, c, update_scale(r, c, scale)
     return table
 
 
@@ -252,17 +274,16 @@ def muon_step(weights, momenta, grads, lr: float, momentum: float = 0.95, nester
     lr scale X with X the orthogonalised grad + mu momentum (or momentum when
     nesterov is False).  weights: bf16 or fp32; momenta: fp32; grads: bf16 or
     fp32, e.g. an owner's views in GradBuffers.  scale: see update_scale."""
-    zc = _zc()
     n = len(weights)
     table = _muon_table(weights, momenta, grads, scale)
     if n == 0:
         return
-    L = zc.lib()
+    zc, L = _zc, _zc.lib()
     need = L.dpred_muon_workspace_bytes(table, n) if workspace is None else 0
     ws, wsp, wsb = _workspace(need, workspace, stream)
-    zc._check(L.dpred_muon_step(table, n, zc._dtype_code(weights[0]), zc._dtype_code(grads[0]), float(lr),
+    zc._check(L.dpred_muon_step(table, n, _code(weights[0]), _code(grads[0]), float(lr),
                                 float(momentum), int(nesterov), float(weight_decay), int(steps), _coeffs(coeffs),
-                                float(eps), wsp, wsb, zc._stream(stream)))
+                                float(eps), wsp or None, wsb, zc._stream(stream)))
 
 
 class Muon:
@@ -272,13 +293,13 @@ class Muon:
 
     def __init__(self, weights, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
                  scale="spectral", steps: int = 5, eps: float = 1e-7, coeffs=None):
-        import torch
+        _device()
         self.weights = list(weights)
         self.momenta = [torch.zeros(tuple(w.shape), dtype=torch.float32, device=w.device) for w in self.weights]
         self.momentum, self.nesterov, self.weight_decay = momentum, nesterov, weight_decay
         self.scale, self.steps, self.eps, self.coeffs = scale, steps, eps, coeffs
         table = _muon_table(self.weights, self.momenta, self.momenta, scale)
-        need = _zc().lib().dpred_muon_workspace_bytes(table, len(self.weights))
+        need = _zc.lib().dpred_muon_workspace_bytes(table, len(self.weights))
         self.workspace = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
 
     def step(self, grads, lr: float, stream=None) -> None:
