@@ -44,7 +44,8 @@ def rel(got, want):
 
 
 SHAPES = [(1, 1), (1, 77), (50, 1), (2, 3), (8, 8), (63, 65), (64, 64), (127, 129), (128, 333), (333, 128), (256, 256),
-          (300, 1000), (1000, 300), (512, 512), (1024, 256), (777, 1535), (2048, 130)]
+          (300, 1000), (1000, 300), (512, 512), (1024, 256), (777, 1535), (2048, 130), (100, 2048), (2048, 128),
+          (5, 1999), (128, 2049), (129, 140), (90, 513)]
 
 
 @pytest.mark.parametrize("m,n", SHAPES)

@@ -67,6 +67,18 @@ __device__ __forceinline__ void ld_cluster4(uint32_t addr, float (&v)[4]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster2(uint32_t addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
+// Order this thread's writes of any shared memory of the cluster before later
+// reads of them by copies or matrix instructions (the async proxy).
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 // Arrival that publishes no memory: it says that tensor memory was read.  A
 // releasing arrival would first wait for this thread's global stores to
 // reach L2 (1400 cycles in the epilogue of a 256 x 256 tile).
@@ -189,8 +201,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
 // K-major: the stride field holds the 8-row group stride, the leading field is
 // unused.  MN-major: the leading field holds the stride between 64-wide chunks,
 // the stride field the stride between groups of 8 reduction rows.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major) {
-    const uint32_t lead = mn_major ? kBlockK * 128u : 16u, stride = 1024u;
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major, uint32_t chunk_bytes = kBlockK * 128u) {
+    const uint32_t lead = mn_major ? chunk_bytes : 16u, stride = 1024u;
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }

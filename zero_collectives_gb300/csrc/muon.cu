@@ -30,6 +30,7 @@
 #include <vector>
 
 #include "gemm_host.cuh"
+#include "muon_small.cuh"
 
 namespace dpred {
 namespace gemm {
@@ -377,6 +378,42 @@ bool same_shape(const Item* x, const Item* y) {
     return std::min(x->rows, x->cols) == std::min(y->rows, y->cols) && std::max(x->rows, x->cols) == std::max(y->rows, y->cols);
 }
 
+// Takes out the matrices that fit the single-launch kernel (muon_small.cu).
+std::vector<const Item*> take_small(std::vector<const Item*>& v) {
+    std::vector<const Item*> small;
+    size_t kept = 0;
+    for (const Item* it : v) (small_split(it->rows, it->cols) ? small.push_back(it) : void(v[kept++] = it));
+    v.resize(kept);
+    return small;
+}
+
+int run_small_items(std::vector<const Item*>& v, const Params& q, cudaStream_t s) {
+    std::stable_sort(v.begin(), v.end(),
+                     [](const Item* x, const Item* y) { return small_split(x->rows, x->cols) < small_split(y->rows, y->cols); });
+    SmallArgs a = {};
+    a.steps = q.steps;
+    a.nesterov = q.nesterov;
+    a.g_f32 = q.g_dtype == DPRED_F32;
+    a.out_f32 = q.out_dtype == DPRED_F32;
+    a.mu = q.mu;
+    a.eps = q.eps;
+    a.a = q.a;
+    a.b = q.b;
+    a.c = q.c;
+    a.keep = q.keep;
+    a.err = device_error_word();
+    for (size_t i = 0; i < v.size();) {
+        a.split = small_split(v[i]->rows, v[i]->cols);
+        for (a.count = 0; i < v.size() && a.count < kSmallBatch && small_split(v[i]->rows, v[i]->cols) == a.split; ++i) {
+            const Item& it = *v[i];
+            a.m[a.count++] = {it.in.g, it.in.mom, it.out, it.in.ldg, it.in.ldm, it.ldo, (int)it.rows, (int)it.cols, it.step};
+        }
+        const int rc = run_small(a, s);
+        if (rc != DPRED_OK) return rc;
+    }
+    return DPRED_OK;
+}
+
 // Sorts the matrices so that those of one shape are neighbours; the workspace of the largest launch.
 int64_t group(std::vector<const Item*>& v) {
     std::stable_sort(v.begin(), v.end(), [](const Item* x, const Item* y) {
@@ -398,11 +435,14 @@ int run_items(std::vector<Item>& items, const Params& q, void* workspace, size_t
     std::vector<const Item*> v;
     for (const Item& it : items)
         if (it.rows > 0 && it.cols > 0) v.push_back(&it);
+    std::vector<const Item*> small = take_small(v);
     const int64_t need = group(v);
-    if (need == 0) return DPRED_OK;
-    if (!workspace || (int64_t)workspace_bytes < need)
+    if (need && (!workspace || (int64_t)workspace_bytes < need))
         return set_error(DPRED_E_SIZE, "workspace of %zu bytes, %lld needed", workspace ? workspace_bytes : (size_t)0, (long long)need);
-    if (reinterpret_cast<uintptr_t>(workspace) % 256) return set_error(DPRED_E_ALIGN, "workspace is not 256-byte aligned");
+    if (need && reinterpret_cast<uintptr_t>(workspace) % 256)
+        return set_error(DPRED_E_ALIGN, "workspace is not 256-byte aligned");
+    const int rc = run_small_items(small, q, s);
+    if (rc != DPRED_OK) return rc;
     for (size_t i = 0; i < v.size();) {
         size_t j = i;
         while (j < v.size() && same_shape(v[i], v[j])) ++j;
@@ -471,6 +511,7 @@ using namespace dpred::gemm;
 
 extern "C" size_t dpred_newton_schulz_workspace_bytes(int32_t batch, int64_t rows, int64_t cols) {
     if (batch <= 0 || rows <= 0 || cols <= 0 || check_shape(rows, cols) != DPRED_OK) return 0;
+    if (small_split(rows, cols)) return 0;
     const Layout l = layout_of(rows, cols);
     return (size_t)launch_bytes(l, chunk_of(l, batch));
 }
@@ -524,6 +565,7 @@ extern "C" size_t dpred_muon_workspace_bytes(const dpred_muon_matrix* mats, int3
             items[k].cols = mats[k].cols;
             if (mats[k].rows > 0 && mats[k].cols > 0) v.push_back(&items[k]);
         }
+        take_small(v);
         need = (size_t)group(v);
         return DPRED_OK;
     });
