@@ -508,6 +508,17 @@ __device__ __forceinline__ void load_ahead(const typename EpiOf<KIND>::T& e, con
     }
 }
 
+// Takes t[k] out of t (0 stays in its place; 0 where k is not 0..7), without a branch per element.
+__device__ __forceinline__ float take(float (&t)[8], int k) {
+    float d = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        d = c == k ? t[c] : d;
+        t[c] = c == k ? 0.0f : t[c];
+    }
+    return d;
+}
+
 // The epilogue of a 32 x 32 block at (i0, j0), staged in shared memory by this
 // warp.  mirror: the block lies off the diagonal square of its tile row, so
 // the symmetric counterpart is written as well.
@@ -548,13 +559,10 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
             __half* d = e.gram + ((int64_t)batch * g.m + i) * e.ldr + j;  // rows are padded to 8 columns
             if (diagonal) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (j + c == i + 8 * s && in[s]) {
-                            e.gram_diag[(int64_t)batch * e.ldr + j + c] = t[s][c] * e.alpha;
-                            t[s][c] = 0.0f;
-                        }
+                for (int s = 0; s < 4; ++s) {
+                    const float x = take(t[s], i + 8 * s - j);
+                    if (in[s] && (unsigned)(i + 8 * s - j) < 8u) e.gram_diag[(int64_t)batch * e.ldr + i + 8 * s] = x * e.alpha;
+                }
             }
             const float f = e.alpha * e.off_scale;  // powers of two
 #pragma unroll
@@ -575,14 +583,10 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
                 float x[8];
                 half8(a.q[s], x);
                 const float base = fmaf(e.c, a.di[s], e.b);
-                if (diagonal) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (j + c == i + 8 * s && in[s]) {
-                            e.coef[(int64_t)batch * e.ldr + j + c] =
-                                e.a + fmaf(e.c, fmaf(a.di[s], a.di[s], t[s][c] * e.alpha), e.b * a.di[s]);
-                            t[s][c] = 0.0f;  // and the stored diagonal of E is 0
-                        }
+                if (diagonal) {  // the stored diagonal of E is 0, so the result's is too
+                    const float sq = take(t[s], i + 8 * s - j) * e.alpha;
+                    if (in[s] && (unsigned)(i + 8 * s - j) < 8u)
+                        e.coef[(int64_t)batch * e.ldr + i + 8 * s] = e.a + fmaf(e.c, fmaf(a.di[s], a.di[s], sq), e.b * a.di[s]);
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) t[s][c] = fmaf(fmaf(e.c, a.dj[c], base), x[c], f * t[s][c]);

@@ -2,18 +2,20 @@
 // up to 128 x 2048.
 //
 // The general path takes 17 launches, each a few microseconds whatever the
-// size.  Here a cluster keeps a matrix in shared memory for the whole update:
-// each of its 1 to 8 CTAs holds up to 256 columns of X (both fp16 terms), and
-// a step is
+// size.  Here a cluster keeps a matrix on chip for the whole update: each of
+// its 1 to 8 CTAs holds up to 256 columns of X, and a step is
 //   Gram    every CTA multiplies its own columns, 128 x 128 partial sums; they
 //           are added through distributed shared memory, each CTA summing a
 //           band of rows in rank order and sending the result to all;
 //   poly    every CTA computes the whole 128 x 128 polynomial;
 //   apply   every CTA updates its own columns in place.
-// The arithmetic and its precision are those of the general path (muon.cu).
-// Tiles lie in the 128-byte swizzle, 64 columns wide: the same bytes serve the
-// Gram product as K-major rows and the apply product as an MN-major operand.
-// What bounds it is latency: 2 cluster barriers and 3 dependent products a step.
+// The arithmetic is that of the general path (muon.cu), except that X is kept
+// in fp32: a thread owns the same row and columns in every step, so X stays in
+// its registers and only the fp16 operand goes through shared memory.
+// Operand tiles lie in the 128-byte swizzle, 64 columns wide: the same bytes
+// serve the Gram product as K-major rows and the apply product as an MN-major
+// operand.  What bounds it is latency: three dependent products a step, with
+// two cluster barriers (about 1100 cycles each) where there is a cluster.
 #include "muon_small.cuh"
 
 #include <algorithm>
@@ -25,21 +27,19 @@ namespace {
 constexpr int kThreads = 512;
 constexpr uint32_t kChunk = 128 * 128;           // 128 rows x 64 columns of fp16
 constexpr float kOffScale = 256.0f;
-// shared memory: X leading terms, X trailing terms (4 chunks each), E (2), partial sums (128 x 128 fp32; P lies over them)
-constexpr uint32_t kHi = 0, kLo = 4 * kChunk, kE = 8 * kChunk, kPart = 10 * kChunk, kP = kPart;
-constexpr uint32_t kSmem = 14 * kChunk + 1024;
+// shared memory: X operand (4 chunks), E (2), partial sums (128 x 128 fp32; P
+// lies over them).  X passes through as fp32 once, over X and the partial sums.
+constexpr uint32_t kX = 0, kPart = 4 * kChunk, kP = kPart, kE = 8 * kChunk;
+constexpr uint32_t kSmem = 10 * kChunk + 1024;
 
 // Byte of element (row, col) of a matrix stored in 64-column chunks.
 __device__ __forceinline__ uint32_t at(int row, int col) {
     return (col >> 6) * kChunk + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
 }
-// 16-byte piece c4 of a row of the fp32 partial sums.
-__device__ __forceinline__ uint32_t part_at(int row, int c4) { return row * 512 + ((c4 ^ (row & 7)) << 4); }
+// 16-byte piece c4 of a row of `pieces` pieces of fp32.
+template <int PIECES>
+__device__ __forceinline__ uint32_t f32_at(int row, int c4) { return row * (PIECES * 16) + ((c4 ^ (row & 7)) << 4); }
 
-__device__ __forceinline__ void sts2(uint32_t a, float x) {
-    const __half h = __float2half_rn(x);
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(*reinterpret_cast<const uint16_t*>(&h)) : "memory");
-}
 __device__ __forceinline__ uint4 ldsq(uint32_t a) {
     uint4 q;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(a) : "memory");
@@ -48,8 +48,8 @@ __device__ __forceinline__ uint4 ldsq(uint32_t a) {
 __device__ __forceinline__ void stsq(uint32_t a, uint4 q) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+__device__ __forceinline__ void sts1(uint32_t a, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
 
 template <typename T>
@@ -60,112 +60,203 @@ __device__ __forceinline__ float load1(const T* p) {
         return *p;
 }
 
+// Takes v[lane] out of v (0 stays in its place), without a branch per element.
+__device__ __forceinline__ float take_lane(float (&v)[32], int lane) {
+    float d = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+        d = q == lane ? v[q] : d;
+        v[q] = q == lane ? 0.0f : v[q];
+    }
+    return d;
+}
+
+// 32 values of U (the gradient, or the updated momentum's): 8 stored rows
+// (major0 + 16 k) by 4 columns (lane + 32 q) of the CTA's part of the matrix.
+// Loads are clamped to valid elements rather than branched around, so that all
+// of them are in flight together.
 template <typename Tg>
+__device__ __forceinline__ void load_update(const SmallArgs& a, const SmallMat& m, int64_t row0, int64_t col0, int rows,
+                                            int cols, int major0, int minor0, float (&u)[8][4]) {
+    const Tg* g = static_cast<const Tg*>(m.g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int64_t i = row0 + min(major0 + 16 * k, rows - 1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[k][q] = load1(g + i * m.ldg + col0 + min(minor0 + 32 * q, cols - 1));
+    }
+    if (m.mom) {
+        float v[8][4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t i = row0 + min(major0 + 16 * k, rows - 1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[k][q] = m.mom[i * m.ldm + col0 + min(minor0 + 32 * q, cols - 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[k][q] = fmaf(a.mu, v[k][q], u[k][q]);
+                if (major0 + 16 * k < rows && minor0 + 32 * q < cols)
+                    m.mom[(row0 + major0 + 16 * k) * m.ldm + col0 + minor0 + 32 * q] = v[k][q];
+                u[k][q] = a.nesterov ? fmaf(a.mu, v[k][q], u[k][q]) : v[k][q];
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (!(major0 + 16 * k < rows && minor0 + 32 * q < cols)) u[k][q] = 0.0f;
+}
+
+// 32 values of the result, from the fp32 stage to the output (or the weight), in load_update's layout.
+template <typename To>
+__device__ __forceinline__ void store_update(const SmallArgs& a, const SmallMat& m, uint32_t stage, bool transposed, int j0,
+                                             int rows, int cols, int major0, int minor0) {
+    To* out = static_cast<To*>(m.out) + (transposed ? (int64_t)j0 * m.ldo : j0);
+    float y[8][4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int major = min(major0 + 16 * k, rows - 1), minor = min(minor0 + 32 * q, cols - 1);
+            const int i = transposed ? minor : major, j = transposed ? major : minor;
+            y[k][q] = lds1(stage + f32_at<64>(i, j >> 2) + (j & 3) * 4);
+        }
+    if (a.keep != 0.0f) {
+        float v[8][4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[k][q] = load1(out + (int64_t)min(major0 + 16 * k, rows - 1) * m.ldo + min(minor0 + 32 * q, cols - 1));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[k][q] = fmaf(a.keep, v[k][q], y[k][q]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (major0 + 16 * k < rows && minor0 + 32 * q < cols) {
+                To* p = out + (int64_t)(major0 + 16 * k) * m.ldo + minor0 + 32 * q;
+                if constexpr (sizeof(To) == 2)
+                    *p = __float2bfloat16_rn(y[k][q]);
+                else
+                    *p = y[k][q];
+            }
+}
+
+// S: CTAs of the cluster.
+template <typename Tg, int S>
 __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constant__ SmallArgs a) {
     using namespace mma;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t done;
     __shared__ uint32_t tmem_slot;
-    __shared__ float diag[kSmallRows], coef[kSmallRows], warp_sum[16], rank_sum[8];
+    __shared__ __align__(16) float diag[kSmallRows];
+    __shared__ float coef[kSmallRows], warp_sum[16], rank_sum[8];
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = (int)cluster_rank(), S = a.split;
+    const int rank = S > 1 ? (int)cluster_rank() : 0;
     const SmallMat& m = a.m[blockIdx.x / S];
     const bool transposed = m.rows > m.cols;
     const int r = transposed ? m.cols : m.rows, c = transposed ? m.rows : m.cols;
     const int chunks = (c + 63) / 64, ch0 = chunks * rank / S, nch = chunks * (rank + 1) / S - ch0;
-    const int j0 = ch0 * 64, w = min(nch * 64, c - j0);  // this CTA's columns (none where w <= 0)
+    const int j0 = ch0 * 64, w = min(nch * 64, c - j0);  // this CTA's columns (none where nch = 0)
+    auto barrier = [&]() {
+        fence_before();
+        if constexpr (S > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        fence_after();
+    };
 
     if (threadIdx.x == 0) {
         tma::mbar_init(&done, 1);
         tma::fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<1>(tma::smem_addr(&tmem_slot), 512);
-    for (uint32_t b = threadIdx.x * 16; b < (uint32_t)nch * kChunk; b += kThreads * 16) {
-        stsq(base + kHi + b, make_uint4(0, 0, 0, 0));
-        stsq(base + kLo + b, make_uint4(0, 0, 0, 0));
-    }
     grid_launch_dependents();
     grid_wait();
 
-    // U in registers, 64 values a thread: along the stored rows (rows warp + 16 k,
-    // columns lane + 32 q of X; or of its transpose, columns warp + 16 k, rows lane + 32 q)
-    const Tg* g = static_cast<const Tg*>(m.g);
-    float u[64], sum = 0.0f;
-    const int n_major = transposed ? 16 : 8, n_minor = transposed ? 4 : 8;
+    // U to shared memory as fp32 (rows and columns past the matrix as zeros), and its sum of squares
+    float sum = 0.0f;
+    if (nch) {
+        const int rows = transposed ? w : r, cols = transposed ? r : w;  // of this CTA's part, as stored
+        const int rows_all = transposed ? nch * 64 : 128, cols_all = transposed ? 128 : nch * 64;
+        for (int i0 = 0; i0 < rows_all; i0 += 128)
+            for (int c0 = 0; c0 < cols_all; c0 += 128) {
+                float u[8][4];
+                load_update<Tg>(a, m, transposed ? j0 : 0, transposed ? 0 : j0, rows, cols, i0 + warp, c0 + lane, u);
 #pragma unroll
-    for (int x = 0; x < 64; ++x) {
-        const int major = warp + 16 * (transposed ? x >> 2 : x >> 3), minor = lane + 32 * (transposed ? x & 3 : x & 7);
-        const int i = transposed ? minor : major, j = transposed ? major : minor;
-        u[x] = 0.0f;
-        if (i < r && j < w) u[x] = load1(g + (transposed ? (int64_t)(j0 + j) * m.ldg + i : (int64_t)i * m.ldg + j0 + j));
-    }
-    (void)n_major;
-    (void)n_minor;
-    if (m.mom) {
+                for (int k = 0; k < 8; ++k)
 #pragma unroll
-        for (int h = 0; h < 64; h += 32) {
-            float v[32];
-#pragma unroll
-            for (int y = 0; y < 32; ++y) {
-                const int x = h + y;
-                const int major = warp + 16 * (transposed ? x >> 2 : x >> 3), minor = lane + 32 * (transposed ? x & 3 : x & 7);
-                const int i = transposed ? minor : major, j = transposed ? major : minor;
-                v[y] = 0.0f;
-                if (i < r && j < w) v[y] = m.mom[transposed ? (int64_t)(j0 + j) * m.ldm + i : (int64_t)i * m.ldm + j0 + j];
+                    for (int q = 0; q < 4; ++q) {
+                        const int major = i0 + warp + 16 * k, minor = c0 + lane + 32 * q;
+                        const int i = transposed ? minor : major, j = transposed ? major : minor;
+                        sum = fmaf(u[k][q], u[k][q], sum);
+                        sts1(base + f32_at<64>(i, j >> 2) + (j & 3) * 4, u[k][q]);  // inside the 128 x 256 of the stage
+                    }
             }
-#pragma unroll
-            for (int y = 0; y < 32; ++y) {
-                const int x = h + y;
-                const int major = warp + 16 * (transposed ? x >> 2 : x >> 3), minor = lane + 32 * (transposed ? x & 3 : x & 7);
-                const int i = transposed ? minor : major, j = transposed ? major : minor;
-                if (i < r && j < w) {
-                    v[y] = fmaf(a.mu, v[y], u[x]);
-                    m.mom[transposed ? (int64_t)(j0 + j) * m.ldm + i : (int64_t)i * m.ldm + j0 + j] = v[y];
-                    u[x] = a.nesterov ? fmaf(a.mu, v[y], u[x]) : v[y];
-                }
-            }
-        }
     }
-#pragma unroll
-    for (int x = 0; x < 64; ++x) sum = fmaf(u[x], u[x], sum);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) warp_sum[warp] = sum;
-    fence_before();
-    cluster_sync();  // the other CTAs have started: their shared memory may be written
-    fence_after();
+    barrier();  // with a cluster: the other CTAs have started, so their shared memory may be written
     const uint32_t tmem = tmem_slot;
-    if (threadIdx.x < S) {
-        float t = 0.0f;
-        for (int k = 0; k < 16; ++k) t += warp_sum[k];
-        st_cluster(map_rank(tma::smem_addr(&rank_sum[rank]), threadIdx.x), t);
-    }
-    cluster_sync();
     float norm = 0.0f;
-    for (int p = 0; p < S; ++p) norm += rank_sum[p];
+    for (int k = 0; k < 16; ++k) norm += warp_sum[k];
+    if constexpr (S > 1) {
+        if (threadIdx.x < S) st_cluster(map_rank(tma::smem_addr(&rank_sum[rank]), threadIdx.x), norm);
+        cluster_sync();
+        norm = 0.0f;
+#pragma unroll
+        for (int p = 0; p < S; ++p) norm += rank_sum[p];
+    }
     // entries of X near 1 (see muon.cu); a power of two
     const float scale = exp2f(rintf(0.5f * log2f((float)c)));
     const float f = scale / (sqrtf(norm) + a.eps);
+
+    // Every thread owns a row (its tensor-memory lane) and columns quarter * 32 + 128 h + 0..31, h = 0, 1.
+    const int row = (warp & 3) * 32 + lane, quarter = warp >> 2;
+    float x[2][32];
 #pragma unroll
-    for (int x = 0; x < 64; ++x) {
-        const int major = warp + 16 * (transposed ? x >> 2 : x >> 3), minor = lane + 32 * (transposed ? x & 3 : x & 7);
-        const int i = transposed ? minor : major, j = transposed ? major : minor;
-        if (i < r && j < w) {
-            const float v = u[x] * f, h = __half2float(__float2half_rn(v));
-            sts2(base + kHi + at(i, j), h);
-            sts2(base + kLo + at(i, j), v - h);
+    for (int h = 0; h < 2; ++h) {
+        const int j = quarter * 32 + 128 * h;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float v[4] = {};
+            if (j < nch * 64) lds4(base + f32_at<64>(row, j / 4 + q), v);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) x[h][4 * q + y] = v[y] * f;
         }
     }
+    __syncthreads();
+    auto store_operand = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = quarter * 32 + 128 * h;
+            if (j < nch * 64) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    stsq(base + kX + at(row, j + 8 * q),
+                         make_uint4(pack_half2(x[h][8 * q], x[h][8 * q + 1]), pack_half2(x[h][8 * q + 2], x[h][8 * q + 3]),
+                                    pack_half2(x[h][8 * q + 4], x[h][8 * q + 5]), pack_half2(x[h][8 * q + 6], x[h][8 * q + 7])));
+            }
+        }
+    };
+    store_operand();
 
-    // Every thread owns a tensor-memory row and a quarter of its columns.
-    const int row = (warp & 3) * 32 + lane, quarter = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), acc = lanes + 256;
     const uint32_t idesc = instr_desc(128, 128, false, false, false);
+    const bool diagonal = quarter == (warp & 3);  // this thread's 32 columns of a 128 x 128 matrix hold its diagonal element
     uint32_t phase = 0;
     bool ok = true;
-    // one product: issued by one thread, waited for by all; the operands were
-    // written by this CTA (or its peers, before a cluster barrier)
+    // Every product is issued by one thread and waited for by all.
     auto wait_product = [&]() {
         if (ok && !tma::mbar_wait(&done, phase)) {
             record_device_error(a.err, DPRED_E_TIMEOUT);
@@ -184,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         if (warp == 0) {
             if (elect_one()) {
                 fence_after();
-                const uint64_t d = operand_desc(base + kHi, false);
+                const uint64_t d = operand_desc(base + kX, false);
                 for (int k = 0; k < nch * 4; ++k) {
                     const uint64_t dk = d + (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
                     issue<1>(tmem + 256, dk, dk, idesc, k != 0);
@@ -194,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
             __syncwarp();
         }
         wait_product();
+        const float alpha = 1.0f / (scale * scale);
         {
             float v[32];
             if (nch) {
@@ -201,36 +293,61 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                 tmem_wait_ld();
             } else {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = 0.0f;
+                for (int q = 0; q < 32; ++q) v[q] = 0.0f;
             }
+            if constexpr (S == 1) {  // straight to the operand: off-diagonal in fp16, diagonal in fp32
+                if (diagonal) diag[row] = take_lane(v, lane) * alpha;
+                const float to = alpha * kOffScale;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) sts4(base + kPart + part_at(row, quarter * 8 + x), v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-        }
-        cluster_sync();
-        const float alpha = 1.0f / (scale * scale);
-        for (int t = threadIdx.x; t < 128 / S * 32; t += kThreads) {
-            const int i = 128 / S * rank + t / 32, c4 = t % 32;
-            float v[4];
-            cluster_get(base + kPart + part_at(i, c4), S, v);
+                for (int q = 0; q < 4; ++q)
+                    stsq(base + kE + at(row, quarter * 32 + 8 * q),
+                         make_uint4(pack_half2(v[8 * q] * to, v[8 * q + 1] * to), pack_half2(v[8 * q + 2] * to, v[8 * q + 3] * to),
+                                    pack_half2(v[8 * q + 4] * to, v[8 * q + 5] * to), pack_half2(v[8 * q + 6] * to, v[8 * q + 7] * to)));
+                tma::fence_proxy_async_shared();
+                barrier();
+            } else {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                v[x] *= alpha;
-                if (c4 * 4 + x == i) {
-                    for (int p = 0; p < S; ++p) st_cluster(map_rank(tma::smem_addr(&diag[i]), p), v[x]);
-                    v[x] = 0.0f;
+                for (int q = 0; q < 8; ++q)
+                    sts4(base + kPart + f32_at<32>(row, quarter * 8 + q), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                cluster_sync();
+                // 128 / S rows of 32 pieces; every load of this thread in flight at once
+                constexpr int kEach = 8 / S;
+                float t[kEach][S][4];
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int i = 128 / S * rank + warp + 16 * k;
+#pragma unroll
+                    for (int p = 0; p < S; ++p) ld_cluster4(map_rank(base + kPart + f32_at<32>(i, lane), p), t[k][p]);
                 }
-                v[x] *= kOffScale;
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int i = 128 / S * rank + warp + 16 * k;
+                    float z[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        z[y] = t[k][0][y];
+#pragma unroll
+                        for (int p = 1; p < S; ++p) z[y] += t[k][p][y];
+                        z[y] *= alpha;
+                    }
+                    if (lane == i / 4) {
+                        const float d = i % 4 == 0 ? z[0] : i % 4 == 1 ? z[1] : i % 4 == 2 ? z[2] : z[3];
+#pragma unroll
+                        for (int p = 0; p < S; ++p) st_cluster(map_rank(tma::smem_addr(&diag[i]), p), d);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) z[y] = lane * 4 + y == i ? 0.0f : z[y] * kOffScale;
+                    const uint32_t lo = pack_half2(z[0], z[1]), hi = pack_half2(z[2], z[3]), to = base + kE + at(i, lane * 4);
+#pragma unroll
+                    for (int p = 0; p < S; ++p) st_cluster2(map_rank(to, p), lo, hi);
+                }
+                fence_proxy_async();
+                barrier();
             }
-            const uint32_t lo = pack_half2(v[0], v[1]), hi = pack_half2(v[2], v[3]), to = base + kE + at(i, c4 * 4);
-            for (int p = 0; p < S; ++p) st_cluster2(map_rank(to, p), lo, hi);
         }
-        fence_proxy_async();
-        fence_before();
-        cluster_sync();
         // ------------------------------------------------------------- polynomial
         if (warp == 0) {
             if (elect_one()) {
-                fence_after();
                 fence_proxy_async();
                 const uint64_t d = operand_desc(base + kE, false);
                 for (int k = 0; k < 8; ++k) {
@@ -241,26 +358,28 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
             }
             __syncwarp();
         }
+        // while it runs: this thread's factors of E
+        const float di = diag[row], lin = fmaf(a.c, di, a.b), sq = a.c / kOffScale;  // E^2 is scaled by 256^2, the result by 256
+        uint4 e8[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e8[q] = ldsq(base + kE + at(row, quarter * 32 + 8 * q));
         wait_product();
         {
             float v[32];
             tmem_ld32(acc + quarter * 32, v);
             tmem_wait_ld();
-            const float di = diag[row], lin = fmaf(a.c, di, a.b), sq = a.c / kOffScale;  // E^2 is scaled by 256^2, the result by 256
+            if (diagonal)  // E's stored diagonal is 0, so P's becomes 0 too
+                coef[row] = a.a + fmaf(a.c, fmaf(di, di, take_lane(v, lane) * (1.0f / (kOffScale * kOffScale))), a.b * di);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int j = quarter * 32 + x * 8;
-                float e8[8], t[8];
-                half8(ldsq(base + kE + at(row, j)), e8);
+            for (int q = 0; q < 4; ++q) {
+                float e[8], dj[8], t[8];
+                half8(e8[q], e);
+                lds4(tma::smem_addr(&diag[quarter * 32 + 8 * q]), dj);
+                lds4(tma::smem_addr(&diag[quarter * 32 + 8 * q + 4]), dj + 4);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    t[y] = fmaf(fmaf(a.c, diag[j + y], lin), e8[y], sq * v[8 * x + y]);
-                    if (j + y == row) {
-                        coef[row] = a.a + fmaf(a.c, fmaf(di, di, v[8 * x + y] / (kOffScale * kOffScale)), a.b * di);
-                        t[y] = 0.0f;
-                    }
-                }
-                stsq(base + kP + at(row, j), pack8(t));
+                for (int y = 0; y < 8; ++y) t[y] = fmaf(fmaf(a.c, dj[y], lin), e[y], sq * v[8 * q + y]);
+                stsq(base + kP + at(row, quarter * 32 + 8 * q),
+                     make_uint4(pack_half2(t[0], t[1]), pack_half2(t[2], t[3]), pack_half2(t[4], t[5]), pack_half2(t[6], t[7])));
             }
         }
         // ------------------------------------------------------------- apply
@@ -274,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                     const uint32_t id = instr_desc(128, nch * 64, false, false, true);
                     const uint64_t da = operand_desc(base + kP, false);
                     // MN-major: 64-column chunks kChunk apart, 8 reduction rows 1024 bytes apart
-                    const uint64_t db = operand_desc(base + kHi, true, kChunk);
+                    const uint64_t db = operand_desc(base + kX, true, kChunk);
                     for (int k = 0; k < 8; ++k)
                         issue<1>(tmem, da + (k >> 2) * (kChunk >> 4) + (k & 3) * 2, db + k * 128, id, k != 0);
                 }
@@ -283,61 +402,52 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
             __syncwarp();
         }
         wait_product();
-        const bool last = step + 1 == a.steps;
         const float k1 = coef[row], inv = 1.0f / kOffScale;
-        for (int j = quarter * 32; j < nch * 64; j += 128) {
-            float v[32];
-            tmem_ld32(lanes + j, v);
-            tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint32_t p = at(row, j + 8 * x);
-                float h[8], l[8];
-                half8(ldsq(base + kHi + p), h);
-                half8(ldsq(base + kLo + p), l);
+        for (int h = 0; h < 2; ++h) {
+            const int j = quarter * 32 + 128 * h;
+            if (j < nch * 64) {  // the same in the whole warp
+                float v[32];
+                tmem_ld32(lanes + j, v);
+                tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 8; ++y) v[8 * x + y] = fmaf(k1, h[y] + l[y], v[8 * x + y] * inv);
-                if (!last) {
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        h[y] = __half2float(__float2half_rn(v[8 * x + y]));
-                        l[y] = v[8 * x + y] - h[y];
-                    }
-                    stsq(base + kHi + p, pack8(h));
-                    stsq(base + kLo + p, pack8(l));
-                }
+                for (int q = 0; q < 32; ++q) x[h][q] = fmaf(k1, x[h][q], v[q] * inv);
             }
-            if (last && ok && row < r) {
-                const float scl = m.step / scale;
+        }
+        if (step + 1 < a.steps) store_operand();
+    }
+
+    // the result, through shared memory so that global rows are written by whole warps
+    __syncthreads();
+    const float scl = m.step / scale;
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    if (j + x >= w) break;
-                    const int64_t o = transposed ? (int64_t)(j0 + j + x) * m.ldo + row : (int64_t)row * m.ldo + j0 + j + x;
-                    const float y = v[x] * scl;
-                    if (a.out_f32) {
-                        float* q = static_cast<float*>(m.out) + o;
-                        *q = a.keep != 0.0f ? fmaf(a.keep, *q, y) : y;
-                    } else {
-                        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(m.out) + o;
-                        *q = __float2bfloat16_rn(a.keep != 0.0f ? fmaf(a.keep, load_bf16(q), y) : y);
-                    }
-                }
-            }
-            __syncwarp();
+    for (int h = 0; h < 2; ++h) {
+        const int j = quarter * 32 + 128 * h;
+        if (j < nch * 64) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                sts4(base + f32_at<64>(row, j / 4 + q), x[h][4 * q] * scl, x[h][4 * q + 1] * scl, x[h][4 * q + 2] * scl,
+                     x[h][4 * q + 3] * scl);
         }
     }
-    fence_before();
-    cluster_sync();  // no CTA leaves while another may still read its shared memory
-    if (warp == 1) {
-        fence_after();
-        tmem_free<1>(tmem, 512);
+    __syncthreads();
+    if (nch && ok) {
+        const int rows = transposed ? w : r, cols = transposed ? r : w;
+        for (int i0 = 0; i0 < rows; i0 += 128)
+            for (int c0 = 0; c0 < cols; c0 += 128)
+                if (a.out_f32)
+                    store_update<float>(a, m, base, transposed, j0, rows, cols, i0 + warp, c0 + lane);
+                else
+                    store_update<__nv_bfloat16>(a, m, base, transposed, j0, rows, cols, i0 + warp, c0 + lane);
     }
+    barrier();  // no CTA leaves while another may still read its shared memory
+    if (warp == 1) tmem_free<1>(tmem, 512);
 }
 
-template <typename Tg>
+template <typename Tg, int S>
 int launch(const SmallArgs& a, cudaStream_t s) {
     static bool attr[64] = {};
-    auto kernel = small_kernel<Tg>;
+    auto kernel = small_kernel<Tg, S>;
     cudaError_t e = ensure_smem_attr(kernel, (int)kSmem, attr);
     if (e != cudaSuccess) return cuda_error(e, "shared-memory limit of a small orthogonalised update");
     cudaLaunchConfig_t cfg = {};
@@ -358,6 +468,16 @@ int launch(const SmallArgs& a, cudaStream_t s) {
     return e == cudaSuccess ? DPRED_OK : cuda_error(e, "small orthogonalised update launch");
 }
 
+template <typename Tg>
+int launch_split(const SmallArgs& a, cudaStream_t s) {
+    switch (a.split) {
+        case 1: return launch<Tg, 1>(a, s);
+        case 2: return launch<Tg, 2>(a, s);
+        case 4: return launch<Tg, 4>(a, s);
+        default: return launch<Tg, 8>(a, s);
+    }
+}
+
 }  // namespace
 
 int small_split(int64_t rows, int64_t cols) {
@@ -368,7 +488,7 @@ int small_split(int64_t rows, int64_t cols) {
     return s;
 }
 
-int run_small(const SmallArgs& a, cudaStream_t s) { return a.g_f32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s); }
+int run_small(const SmallArgs& a, cudaStream_t s) { return a.g_f32 ? launch_split<float>(a, s) : launch_split<__nv_bfloat16>(a, s); }
 
 }  // namespace gemm
 }  // namespace dpred
