@@ -71,82 +71,93 @@ __device__ __forceinline__ float take_lane(float (&v)[32], int lane) {
     return d;
 }
 
-// 32 values of U (the gradient, or the updated momentum's): 8 stored rows
-// (major0 + 16 k) by 4 columns (lane + 32 q) of the CTA's part of the matrix.
-// Loads are clamped to valid elements rather than branched around, so that all
-// of them are in flight together.
-template <typename Tg>
-__device__ __forceinline__ void load_update(const SmallArgs& a, const SmallMat& m, int64_t row0, int64_t col0, int rows,
-                                            int cols, int major0, int minor0, float (&u)[8][4]) {
-    const Tg* g = static_cast<const Tg*>(m.g);
+// The passes between global memory and the fp32 stage work on 32 values a
+// thread: 8 stored rows (major0 + 16 k) by 4 columns (minor0 + 32 q) of the
+// CTA's part of the matrix (rows x cols as stored; T: X is its transpose).
+// Addresses are clamped to valid elements rather than branched around, so that
+// all loads are in flight together.
+template <bool T>
+__device__ __forceinline__ uint32_t stage_at(int major, int minor) {
+    const int i = T ? minor : major, j = T ? major : minor;
+    return f32_at<64>(i, j >> 2) + (j & 3) * 4;
+}
+
+// U (the gradient, or the updated momentum's) to the stage, zeros past the
+// matrix; returns the sum of its squares.
+template <typename Tg, bool T>
+__device__ __forceinline__ float load_update(const SmallArgs& a, const SmallMat& m, uint32_t stage, int j0, int rows, int cols,
+                                             int major0, int minor0) {
+    const Tg* g = static_cast<const Tg*>(m.g) + (T ? (int64_t)j0 * m.ldg : j0);
+    float* mom = m.mom ? m.mom + (T ? (int64_t)j0 * m.ldm : j0) : nullptr;
+    int col[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) col[q] = min(minor0 + 32 * q, cols - 1);
+    float u[8][4], sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const int64_t i = row0 + min(major0 + 16 * k, rows - 1);
+        const Tg* p = g + (int64_t)min(major0 + 16 * k, rows - 1) * m.ldg;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) u[k][q] = load1(g + i * m.ldg + col0 + min(minor0 + 32 * q, cols - 1));
+        for (int q = 0; q < 4; ++q) u[k][q] = load1(p + col[q]);
     }
-    if (m.mom) {
+    if (mom) {
         float v[8][4];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int64_t i = row0 + min(major0 + 16 * k, rows - 1);
+            const float* p = mom + (int64_t)min(major0 + 16 * k, rows - 1) * m.ldm;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[k][q] = m.mom[i * m.ldm + col0 + min(minor0 + 32 * q, cols - 1)];
+            for (int q = 0; q < 4; ++q) v[k][q] = p[col[q]];
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 8; ++k) {
+            float* p = mom + (int64_t)(major0 + 16 * k) * m.ldm;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 v[k][q] = fmaf(a.mu, v[k][q], u[k][q]);
-                if (major0 + 16 * k < rows && minor0 + 32 * q < cols)
-                    m.mom[(row0 + major0 + 16 * k) * m.ldm + col0 + minor0 + 32 * q] = v[k][q];
+                if (major0 + 16 * k < rows && minor0 + 32 * q < cols) p[minor0 + 32 * q] = v[k][q];
                 u[k][q] = a.nesterov ? fmaf(a.mu, v[k][q], u[k][q]) : v[k][q];
             }
+        }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (!(major0 + 16 * k < rows && minor0 + 32 * q < cols)) u[k][q] = 0.0f;
-}
-
-// 32 values of the result, from the fp32 stage to the output (or the weight), in load_update's layout.
-template <typename To>
-__device__ __forceinline__ void store_update(const SmallArgs& a, const SmallMat& m, uint32_t stage, bool transposed, int j0,
-                                             int rows, int cols, int major0, int minor0) {
-    To* out = static_cast<To*>(m.out) + (transposed ? (int64_t)j0 * m.ldo : j0);
-    float y[8][4];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int major = min(major0 + 16 * k, rows - 1), minor = min(minor0 + 32 * q, cols - 1);
-            const int i = transposed ? minor : major, j = transposed ? major : minor;
-            y[k][q] = lds1(stage + f32_at<64>(i, j >> 2) + (j & 3) * 4);
+            if (!(major0 + 16 * k < rows && minor0 + 32 * q < cols)) u[k][q] = 0.0f;
+            sum = fmaf(u[k][q], u[k][q], sum);
+            sts1(stage + stage_at<T>(major0 + 16 * k, minor0 + 32 * q), u[k][q]);  // inside the 128 x 256 of the stage
         }
-    if (a.keep != 0.0f) {
-        float v[8][4];
+    return sum;
+}
+
+// The result, from the stage to the output (or the weight).
+template <typename To, bool T>
+__device__ __forceinline__ void store_update(const SmallArgs& a, const SmallMat& m, uint32_t stage, int j0, int rows, int cols,
+                                             int major0, int minor0) {
+    To* out = static_cast<To*>(m.out) + (T ? (int64_t)j0 * m.ldo : j0);
+    int col[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+    for (int q = 0; q < 4; ++q) col[q] = min(minor0 + 32 * q, cols - 1);
+    float v[8][4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                v[k][q] = load1(out + (int64_t)min(major0 + 16 * k, rows - 1) * m.ldo + min(minor0 + 32 * q, cols - 1));
+    for (int k = 0; k < 8; ++k) {
+        const To* p = out + (int64_t)min(major0 + 16 * k, rows - 1) * m.ldo;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) y[k][q] = fmaf(a.keep, v[k][q], y[k][q]);
+        for (int q = 0; q < 4; ++q) v[k][q] = a.keep != 0.0f ? load1(p + col[q]) : 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 8; ++k) {
+        To* p = out + (int64_t)(major0 + 16 * k) * m.ldo + minor0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
+            const float y = fmaf(a.keep, v[k][q], lds1(stage + stage_at<T>(major0 + 16 * k, minor0 + 32 * q)));
             if (major0 + 16 * k < rows && minor0 + 32 * q < cols) {
-                To* p = out + (int64_t)(major0 + 16 * k) * m.ldo + minor0 + 32 * q;
                 if constexpr (sizeof(To) == 2)
-                    *p = __float2bfloat16_rn(y[k][q]);
+                    p[32 * q] = __float2bfloat16_rn(y);
                 else
-                    *p = y[k][q];
+                    p[32 * q] = y;
             }
+        }
+    }
 }
 
 // S: CTAs of the cluster.
@@ -185,23 +196,13 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
 
     // U to shared memory as fp32 (rows and columns past the matrix as zeros), and its sum of squares
     float sum = 0.0f;
+    const int rows = transposed ? w : r, cols = transposed ? r : w;  // of this CTA's part, as stored
     if (nch) {
-        const int rows = transposed ? w : r, cols = transposed ? r : w;  // of this CTA's part, as stored
         const int rows_all = transposed ? nch * 64 : 128, cols_all = transposed ? 128 : nch * 64;
         for (int i0 = 0; i0 < rows_all; i0 += 128)
-            for (int c0 = 0; c0 < cols_all; c0 += 128) {
-                float u[8][4];
-                load_update<Tg>(a, m, transposed ? j0 : 0, transposed ? 0 : j0, rows, cols, i0 + warp, c0 + lane, u);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int major = i0 + warp + 16 * k, minor = c0 + lane + 32 * q;
-                        const int i = transposed ? minor : major, j = transposed ? major : minor;
-                        sum = fmaf(u[k][q], u[k][q], sum);
-                        sts1(base + f32_at<64>(i, j >> 2) + (j & 3) * 4, u[k][q]);  // inside the 128 x 256 of the stage
-                    }
-            }
+            for (int c0 = 0; c0 < cols_all; c0 += 128)
+                sum += transposed ? load_update<Tg, true>(a, m, base, j0, rows, cols, i0 + warp, c0 + lane)
+                                  : load_update<Tg, false>(a, m, base, j0, rows, cols, i0 + warp, c0 + lane);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -432,13 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     }
     __syncthreads();
     if (nch && ok) {
-        const int rows = transposed ? w : r, cols = transposed ? r : w;
         for (int i0 = 0; i0 < rows; i0 += 128)
-            for (int c0 = 0; c0 < cols; c0 += 128)
+            for (int c0 = 0; c0 < cols; c0 += 128) {
                 if (a.out_f32)
-                    store_update<float>(a, m, base, transposed, j0, rows, cols, i0 + warp, c0 + lane);
+                    transposed ? store_update<float, true>(a, m, base, j0, rows, cols, i0 + warp, c0 + lane)
+                               : store_update<float, false>(a, m, base, j0, rows, cols, i0 + warp, c0 + lane);
                 else
-                    store_update<__nv_bfloat16>(a, m, base, transposed, j0, rows, cols, i0 + warp, c0 + lane);
+                    transposed ? store_update<__nv_bfloat16, true>(a, m, base, j0, rows, cols, i0 + warp, c0 + lane)
+                               : store_update<__nv_bfloat16, false>(a, m, base, j0, rows, cols, i0 + warp, c0 + lane);
+            }
     }
     barrier();  // no CTA leaves while another may still read its shared memory
     if (warp == 1) tmem_free<1>(tmem, 512);
