@@ -190,3 +190,22 @@ def test_muon_object_streams_and_graph():
     torch.cuda.synchronize()
     for x, y, z in zip(a.weights + a.momenta, b.weights + b.momenta, c.weights + c.momenta):
         assert torch.equal(x, y) and torch.equal(x, z)
+
+
+@pytest.mark.parametrize("shapes", [[(1024, 1024)] * 8, [(700, 1300), (1300, 700), (700, 1300), (900, 900)] * 6,
+                                    [(300, 4000)] * 3 + [(257, 2500)] * 5 + [(1030, 520)] * 4 + [(64, 96)] * 2,
+                                    [(512 + 8 * i, 777) for i in range(11)], [(260, 1000)] * 70])
+def test_many_large_matrices(shapes):
+    """Batches whose products run chained in one launch: several shapes, ragged tiles, more shapes or matrices than a launch takes."""
+    ws = [gradient(*s, seed=i, scale=0.02, rank=1) for i, s in enumerate(shapes)]
+    gs = [gradient(*s, seed=100 + i).bfloat16() for i, s in enumerate(shapes)]
+    ms = [torch.zeros(s, device="cuda") for s in shapes]
+    w0 = [w.clone() for w in ws]
+    zc.muon_step(ws, ms, gs, lr=0.1, scale=1.0)
+    for w, w1, g, s in zip(w0, ws, gs, shapes):
+        want = muon64(w, torch.zeros(s, device="cuda"), g, 0.1, 0.95, True, 0.0, 1.0)[0]
+        assert float((w1.double() - want).norm()) <= 2.0 ** -22 * float(want.norm()) + TOL * 0.1 * math.sqrt(min(s)) * 1.3
+    again = [w.clone() for w in w0]
+    zc.muon_step(again, [torch.zeros(s, device="cuda") for s in shapes], gs, lr=0.1, scale=1.0)
+    assert all(torch.equal(x, y) for x, y in zip(again, ws)), "two runs differ"
+    assert zc.device_status() == 0

@@ -25,7 +25,8 @@ FLUSH_UNITS = [f"flush_w{w}.cu" for w in (*(str(w) for w in range(2, 17)), "gen"
 LINEAR_UNITS = [f"linear_{k}.cu" for k in ("any", "plain", "act", "grad", "f32")]
 SOURCES = ["abi.cu", "flush_dispatch.cu", *FLUSH_UNITS, "accumulate.cu", "allgather.cu", "noalloc.cu", "selftest.cu",
            "relayout.cu", "schedule.cu", "owner_map.cu", "executor.cu", "ceiling.cu", "gemm.cu", "linear.cu",
-           *LINEAR_UNITS, "muon.cu", "muon_small.cu"]
+           *LINEAR_UNITS, "muon.cu", "muon_small.cu",
+           "muon_chain.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", *ARCH, "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-I", CSRC]

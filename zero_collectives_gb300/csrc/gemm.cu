@@ -116,10 +116,10 @@ static double tile_time(const Args& a, int bn, bool fp32, int pairs) {
 
 bool split_alone(double ctas, int split, int sms) { return ctas <= (split < 8 ? sms : sms * 5 / 8); }
 
-Shape choose_shape(const Args& a, bool fp32) {
+static Shape choose(const Args& a, bool fp32, double& t) {
     const int sms = sm_count();
     Shape best = {};
-    double t = 1e30;
+    t = 1e30;
     for (int bn = 32; bn <= 128; bn *= 2) {
         if (bn == 32 && a.b_mn) continue;  // MN-major copies are 64 columns wide
         for (int split = 1; split <= 8 && (split == 1 || split <= a.kblocks); split *= 2) {
@@ -130,7 +130,7 @@ Shape choose_shape(const Args& a, bool fp32) {
             }
         }
     }
-    if (a.kblocks > 0 && !a.columns_only)
+    if (a.kblocks > 0 && !a.split_only)
         for (int bn = 128; bn <= 256; bn *= 2) {
             const double u = tile_time(a, bn, fp32, sms / 2);
             if (u < t) {
@@ -139,6 +139,17 @@ Shape choose_shape(const Args& a, bool fp32) {
             }
         }
     return best;
+}
+
+Shape choose_shape(const Args& a, bool fp32) {
+    double t;
+    return choose(a, fp32, t);
+}
+
+double estimate(const Args& a, bool fp32) {
+    double t;
+    choose(a, fp32, t);
+    return t;
 }
 
 }  // namespace gemm

@@ -77,8 +77,20 @@ struct NsEpi {
     float a, b, c;     // the polynomial's coefficients
     float keep;        // FINAL: factor of the old weight (0: store)
     int out_f32;       // FINAL
-    FinalOut out[kMaxBatch];
+    const FinalOut* out;  // FINAL: one entry per matrix of the batch
 };
+
+// The same as it travels in a launch, with its table.
+struct NsParams {
+    NsEpi e;
+    FinalOut table[kMaxBatch];
+};
+__device__ __forceinline__ NsEpi epilogue_of(const NsParams& p) {
+    NsEpi e = p.e;
+    e.out = p.table;
+    return e;
+}
+__device__ __forceinline__ const LinearEpi& epilogue_of(const LinearEpi& e) { return e; }
 
 struct Args {
     int m, n;            // rows of A, rows of B
@@ -87,7 +99,7 @@ struct Args {
     int tiles_m, tiles_n, tiles_per_batch;
     int symmetric;       // only elements i <= j are needed (the epilogue mirrors them)
     int a_mn, b_mn;      // operand majors
-    int columns_only;    // a swapped epilogue: split kernel only
+    int split_only;    // split kernel only (a swapped epilogue, a Newton-Schulz product)
     int split;           // CTAs of a cluster that share the reduction
     int stages;          // split kernel: pipeline stages
     int regions;         // split kernel: accumulators that share a CTA's part of the reduction
@@ -97,7 +109,8 @@ struct Args {
 
 template <int KIND>
 struct EpiOf {
-    using T = std::conditional_t<is_linear(KIND), LinearEpi, NsEpi>;
+    using T = std::conditional_t<is_linear(KIND), LinearEpi, NsEpi>;      // as the epilogue sees it
+    using Param = std::conditional_t<is_linear(KIND), LinearEpi, NsParams>;  // as the launch carries it
 };
 
 // The tile kernel's kind for a linear layer's options.
@@ -465,7 +478,8 @@ __device__ __forceinline__ void linear_steps(const LinearEpi& e, const Args& g, 
 
 // What a Newton-Schulz block's epilogue reads from global memory, loaded ahead
 // of the block's accumulators (their latency, about 1000 cycles, would otherwise
-// come on top of every block).
+// come on top of every block), and past the first-level cache: in the chained
+// kernel other SMs wrote it earlier in the same launch.
 template <int KIND>
 struct Ahead {};
 template <>
@@ -492,18 +506,21 @@ __device__ __forceinline__ void load_ahead(const typename EpiOf<KIND>::T& e, con
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const bool in = i + 8 * s < g.m && j < g.n;
-            a.q[s] = in ? *reinterpret_cast<const uint4*>(p + 8 * s * e.ldr) : zero;
-            a.di[s] = in ? diag[i + 8 * s] : 0.0f;
+            a.q[s] = in ? __ldcg(reinterpret_cast<const uint4*>(p + 8 * s * e.ldr)) : zero;
+            a.di[s] = in ? __ldcg(diag + i + 8 * s) : 0.0f;
         }
-        if (j < g.n) load8_f32(diag + j, a.dj);  // rows and diagonals are padded to 8 elements
+        if (j < g.n) {  // rows and diagonals are padded to 8 elements
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(diag + j)), y = __ldcg(reinterpret_cast<const float4*>(diag + j + 4));
+            a.dj[0] = x.x; a.dj[1] = x.y; a.dj[2] = x.z; a.dj[3] = x.w; a.dj[4] = y.x; a.dj[5] = y.y; a.dj[6] = y.z; a.dj[7] = y.w;
+        }
     } else if constexpr (KIND == KIND_APPLY || KIND == KIND_FINAL) {
         const int64_t at = ((int64_t)batch * g.m + i) * e.ldc + j;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const bool in = i + 8 * s < g.m && j < g.n;
-            a.h[s] = in ? *reinterpret_cast<const uint4*>(e.hi_in + at + 8 * s * e.ldc) : zero;
-            a.l[s] = in ? *reinterpret_cast<const uint4*>(e.lo_in + at + 8 * s * e.ldc) : zero;
-            a.k[s] = in ? e.coef[(int64_t)batch * e.ldr + i + 8 * s] : 0.0f;
+            a.h[s] = in ? __ldcg(reinterpret_cast<const uint4*>(e.hi_in + at + 8 * s * e.ldc)) : zero;
+            a.l[s] = in ? __ldcg(reinterpret_cast<const uint4*>(e.lo_in + at + 8 * s * e.ldc)) : zero;
+            a.k[s] = in ? __ldcg(e.coef + (int64_t)batch * e.ldr + i + 8 * s) : 0.0f;
         }
     }
 }
@@ -721,8 +738,9 @@ __device__ __forceinline__ void cluster_get(uint32_t at, int split, float* t) {
 template <int KIND, int BN>
 __global__ void __launch_bounds__(kSplitThreads)
     split_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                 const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::T e) {
+                 const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::Param ep) {
     using namespace mma;
+    const auto& e = epilogue_of(ep);
     const int S = g.stages;
     constexpr uint32_t kA = 128 * 128, kStage = kA + BN * 128;
     constexpr uint32_t kCols = 256;  // two CTAs per SM together allocate all 512
@@ -943,8 +961,9 @@ __host__ __device__ constexpr int tile_smem() {
 template <int KIND, int BN, bool PROMOTE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::T e) {
+                const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::Param ep) {
     using namespace mma;
+    const auto& e = epilogue_of(ep);
     constexpr int S = tile_stages<BN>();
     constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;
     constexpr uint32_t kCols = 2 * BN;

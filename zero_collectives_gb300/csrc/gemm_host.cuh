@@ -20,11 +20,12 @@ int make_map(const Operand& o, int batch, int box_rows, bool bf16, CUtensorMap* 
 bool tma_able(const void* p, int64_t rows, int64_t ld);
 int64_t tiles_of(const Args& a, int bm, int bn);
 Shape choose_shape(const Args& a, bool fp32);
+double estimate(const Args& a, bool fp32);  // time of the chosen shape, us
 // Whether a split launch gives every CTA an SM of its own (eight-CTA clusters do not fit every SM of a GPC).
 bool split_alone(double ctas, int split, int sms);
 
 template <int KIND, int BN>
-int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
     static bool attr[64] = {};
     auto kernel = split_kernel<KIND, BN>;
     cudaError_t err = ensure_smem_attr(kernel, split_smem<BN>(true), attr);
@@ -63,7 +64,7 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
 }
 
 template <int KIND, int BN, bool PROMOTE>
-int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
     static bool attr[64] = {};
     auto kernel = tile_kernel<KIND, BN, PROMOTE>;
     cudaError_t err = ensure_smem_attr(kernel, tile_smem<BN>(), attr);
@@ -100,7 +101,7 @@ int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& 
 }
 
 template <int KIND>
-int tiles_of_kind(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+int tiles_of_kind(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
     constexpr bool kPromote = KIND == KIND_F32;
     return sh.bn == 256 ? launch_tiles<KIND, 256, kPromote>(p, sh, e, s) : launch_tiles<KIND, 128, kPromote>(p, sh, e, s);
 }
@@ -113,25 +114,23 @@ int linear_tiles_grad(const Plan& p, const Shape& sh, const LinearEpi& e, cudaSt
 int linear_tiles_f32(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s);
 
 template <int KIND>
-int run_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
-    if constexpr (KIND == KIND_LINEAR) {
-        switch (linear_kind(e)) {
-            case KIND_PLAIN: return linear_tiles_plain(p, sh, e, s);
-            case KIND_ACT: return linear_tiles_act(p, sh, e, s);
-            case KIND_GRAD: return linear_tiles_grad(p, sh, e, s);
-            case KIND_F32: return linear_tiles_f32(p, sh, e, s);
-            default: return linear_tiles_any(p, sh, e, s);
-        }
-    } else {
-        return tiles_of_kind<KIND>(p, sh, e, s);
+int run_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
+    switch (linear_kind(e)) {
+        case KIND_PLAIN: return linear_tiles_plain(p, sh, e, s);
+        case KIND_ACT: return linear_tiles_act(p, sh, e, s);
+        case KIND_GRAD: return linear_tiles_grad(p, sh, e, s);
+        case KIND_F32: return linear_tiles_f32(p, sh, e, s);
+        default: return linear_tiles_any(p, sh, e, s);
     }
 }
 
 template <int KIND>
-int run(const Plan& p, const typename EpiOf<KIND>::T& e, cudaStream_t s) {
+int run(const Plan& p, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
     const Shape sh = choose_shape(p.args, p.fp32_result);
     if (sh.tiles * sh.split > 0x7FFFFFFF) return set_error(DPRED_E_SIZE, "a matrix product of too many tiles");
-    if (sh.pairs) return run_tiles<KIND>(p, sh, e, s);
+    if constexpr (is_linear(KIND)) {
+        if (sh.pairs) return run_tiles<KIND>(p, sh, e, s);
+    }
     switch (sh.bn) {
         case 32: return launch_split<KIND, 32>(p, sh, e, s);
         case 64: return launch_split<KIND, 64>(p, sh, e, s);

@@ -186,7 +186,7 @@ int launch(Operand a, Operand b, int64_t red, const LinearEpi& e, void* workspac
     p.args.a_mn = a.reduce_rows;
     p.args.b_mn = b.reduce_rows;
     p.args.bf16 = 1;
-    p.args.columns_only = e.swapped;
+    p.args.split_only = e.swapped;
     p.fp32_result = e.out_f32;
     return run<KIND_LINEAR>(p, e, s);
 }

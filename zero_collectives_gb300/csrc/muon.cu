@@ -30,6 +30,7 @@
 #include <vector>
 
 #include "gemm_host.cuh"
+#include "muon_chain.cuh"
 #include "muon_small.cuh"
 
 namespace dpred {
@@ -56,6 +57,7 @@ struct NormArgs {
     float mu;
     int nesterov;
     float* partial;           // [batch, kNormBlocks]
+    unsigned* counter;        // [batch] finished tiles of the chained products, cleared here
     int blocks;               // partials written per matrix
     float eps, scale;
     __half* hi;
@@ -148,7 +150,10 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
         }
     }
     sum = block_sum(sum);
-    if (threadIdx.x == 0) a.partial[blockIdx.y * kNormBlocks + blockIdx.x] = sum;
+    if (threadIdx.x == 0) {
+        a.partial[blockIdx.y * kNormBlocks + blockIdx.x] = sum;
+        if (blockIdx.x == 0) a.counter[blockIdx.y] = 0;
+    }
 }
 
 // X = scale * U / (|U| + eps) as two fp16 terms, on its wide side.  The
@@ -243,66 +248,78 @@ Layout layout_of(int64_t rows, int64_t cols) {
     l.x = l.r * l.ldc * 2;
     l.gram = l.r * l.ldr * 2;
     l.diag = l.ldr * 4;
-    // X: leading term twice (read and written by the same product), trailing term; A, polynomial; two diagonals; partials
-    l.per = 3 * l.x + 2 * l.gram + 2 * l.diag + kNormBlocks * 4;
+    // X: leading term twice (read and written by the same product), trailing term; A, polynomial; two diagonals;
+    // partial sums; counter
+    l.per = 3 * l.x + 2 * l.gram + 2 * l.diag + kNormBlocks * 4 + 4;
     return l;
 }
-constexpr int kRegions = 8;  // regions of a launch's workspace, each rounded up to 256 bytes
+constexpr int kRegions = 9;  // regions of a group's workspace, each rounded up to 256 bytes
 
-int64_t launch_bytes(const Layout& l, int count) { return l.per * count + 256 * kRegions; }
-
-// Matrices of one shape per launch: all of them up to kMaxBatch.
-int chunk_of(const Layout& l, int count) {
-    (void)l;
-    return std::min(count, kMaxBatch);
-}
+int64_t group_bytes(const Layout& l, int count) { return l.per * count + 256 * kRegions; }
 
 struct Params {
     int g_dtype, out_dtype, nesterov, steps;
     float mu, keep, eps, a, b, c;
 };
 
-int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cudaStream_t s) {
-    const Layout l = layout_of(items[0]->rows, items[0]->cols);
+// The matrices of one shape (or of its transpose) in one launch.
+struct Group {
+    const Item* const* items;
+    int count;
+    Layout l;
+    // workspace
+    __half *hi[2], *lo, *gram, *poly;
+    float *diag, *coef, *partial;
+    unsigned* counter;
+    float scale;
+};
+
+void place(Group& g, char*& ws) {
     auto take = [&](int64_t bytes) {
         char* p = ws;
         ws += align256(bytes);
         return p;
     };
-    __half* hi[2] = {reinterpret_cast<__half*>(take(l.x * count)), reinterpret_cast<__half*>(take(l.x * count))};
-    __half* lo = reinterpret_cast<__half*>(take(l.x * count));
-    __half* gram = reinterpret_cast<__half*>(take(l.gram * count));
-    __half* poly = reinterpret_cast<__half*>(take(l.gram * count));
-    float* diag = reinterpret_cast<float*>(take(l.diag * count));
-    float* coef = reinterpret_cast<float*>(take(l.diag * count));
-    float* partial = reinterpret_cast<float*>(take((int64_t)kNormBlocks * 4 * count));
-
+    const Layout& l = g.l;
+    g.hi[0] = reinterpret_cast<__half*>(take(l.x * g.count));
+    g.hi[1] = reinterpret_cast<__half*>(take(l.x * g.count));
+    g.lo = reinterpret_cast<__half*>(take(l.x * g.count));
+    g.gram = reinterpret_cast<__half*>(take(l.gram * g.count));
+    g.poly = reinterpret_cast<__half*>(take(l.gram * g.count));
+    g.diag = reinterpret_cast<float*>(take(l.diag * g.count));
+    g.coef = reinterpret_cast<float*>(take(l.diag * g.count));
+    g.partial = reinterpret_cast<float*>(take((int64_t)kNormBlocks * 4 * g.count));
     // entries of X: near 1 after scaling by about sqrt(c); an orthogonal row of length c has entries near 1/sqrt(c)
-    const float scale = std::exp2(std::round(0.5f * std::log2((float)std::min<int64_t>(l.c, 65536))));
+    g.scale = std::exp2(std::round(0.5f * std::log2((float)std::min<int64_t>(l.c, 65536))));
+}
 
+// The element-wise passes: momentum, norm, X as two fp16 terms.
+int start_group(const Group& g, const Params& q, cudaStream_t s) {
+    const Layout& l = g.l;
     NormArgs n = {};
     n.r = l.r;
     n.c = l.c;
     n.mu = q.mu;
     n.nesterov = q.nesterov;
-    n.partial = partial;
+    n.partial = g.partial;
+    n.counter = g.counter;
     n.eps = q.eps;
-    n.scale = scale;
-    n.hi = hi[0];
-    n.lo = lo;
+    n.scale = g.scale;
+    n.hi = g.hi[0];
+    n.lo = g.lo;
     n.ldc = l.ldc;
     const int gs = q.g_dtype == DPRED_F32 ? 4 : 2;
-    for (int k = 0; k < count; ++k) {
+    for (int k = 0; k < g.count; ++k) {
         MatIn& in = n.in[k];
-        in = items[k]->in;
-        in.transposed = items[k]->rows > items[k]->cols;
-        in.g_vec = reinterpret_cast<uintptr_t>(in.g) % (4 * gs) == 0 && (items[k]->rows <= 1 || in.ldg % 4 == 0);
-        in.m_vec = reinterpret_cast<uintptr_t>(in.mom) % 16 == 0 && (items[k]->rows <= 1 || in.ldm % 4 == 0);
+        in = g.items[k]->in;
+        in.transposed = g.items[k]->rows > g.items[k]->cols;
+        in.g_vec = reinterpret_cast<uintptr_t>(in.g) % (4 * gs) == 0 && (g.items[k]->rows <= 1 || in.ldg % 4 == 0);
+        in.m_vec = reinterpret_cast<uintptr_t>(in.mom) % 16 == 0 && (g.items[k]->rows <= 1 || in.ldm % 4 == 0);
     }
     const int64_t tiles = ((l.r + kTile - 1) / kTile) * ((l.c + kTile - 1) / kTile);
     n.blocks = (int)std::min<int64_t>(tiles, kNormBlocks);
-    const dim3 grid1((unsigned)n.blocks, (unsigned)count);
-    const dim3 grid2((unsigned)std::min<int64_t>(tiles, 512), (unsigned)count);
+    const dim3 grid1((unsigned)n.blocks, (unsigned)g.count);
+    const dim3 grid2((unsigned)std::min<int64_t>(tiles, 512), (unsigned)g.count);
     if (q.g_dtype == DPRED_F32) {
         norm_kernel<float><<<grid1, 256, 0, s>>>(n);
         scale_kernel<float><<<grid2, 256, 0, s>>>(n);
@@ -311,66 +328,145 @@ int run_chunk(const Item* const* items, int count, const Params& q, char* ws, cu
         scale_kernel<__nv_bfloat16><<<grid2, 256, 0, s>>>(n);
     }
     const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return cuda_error(err, "orthogonalised update launch");
+    return err == cudaSuccess ? DPRED_OK : cuda_error(err, "orthogonalised update launch");
+}
 
+NsEpi epilogue_of_group(const Group& g, const Params& q) {
     NsEpi e = {};
-    e.gram = gram;
-    e.poly = poly;
-    e.gram_diag = diag;
-    e.coef = coef;
-    e.lo_in = lo;
-    e.lo = lo;
-    e.ldr = l.ldr;
-    e.ldc = l.ldc;
+    e.gram = g.gram;
+    e.poly = g.poly;
+    e.gram_diag = g.diag;
+    e.coef = g.coef;
+    e.hi_in = g.hi[0];
+    e.hi = g.hi[1];
+    e.lo_in = g.lo;
+    e.lo = g.lo;
+    e.ldr = g.l.ldr;
+    e.ldc = g.l.ldc;
     e.off_scale = kOffScale;
     e.a = q.a;
     e.b = q.b;
     e.c = q.c;
     e.keep = q.keep;
     e.out_f32 = q.out_dtype == DPRED_F32;
-    const int os = e.out_f32 ? 4 : 2;
-    for (int k = 0; k < count; ++k) {
-        FinalOut& o = e.out[k];
-        o.p = items[k]->out;
-        o.ld = items[k]->ldo;
-        o.step = items[k]->step / scale;
-        o.vec = reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (items[k]->rows <= 1 || o.ld * os % 16 == 0);
-        o.transposed = items[k]->rows > items[k]->cols;
-    }
+    return e;
+}
+
+FinalOut output_of(const Group& g, int k, const Params& q) {
+    const Item& it = *g.items[k];
+    FinalOut o;
+    o.p = it.out;
+    o.ld = it.ldo;
+    o.step = it.step / g.scale;
+    o.vec = reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (it.rows <= 1 || o.ld * (q.out_dtype == DPRED_F32 ? 4 : 2) % 16 == 0);
+    o.transposed = it.rows > it.cols;
+    return o;
+}
+
+int blocks_of(int64_t n) { return (int)((n + mma::kBlockK - 1) / mma::kBlockK); }
+
+// A group's products of one step: 0 Gram, 1 polynomial, 2 apply.
+Plan product_plan(const Group& g, int product, int buffer) {
+    const Layout& l = g.l;
     Plan p = {};
-    p.args.batch = count;
+    p.args.batch = g.count;
     p.args.err = device_error_word();
+    p.args.m = (int)l.r;
+    p.args.n = (int)(product == 2 ? l.c : l.r);
+    p.args.symmetric = product < 2;
+    p.args.b_mn = product == 2;
+    p.args.kblocks = blocks_of(product == 0 ? l.c : l.r);
+    p.args.split_only = 1;
+    const Operand x = {g.hi[buffer], l.r, l.c, l.ldc, l.r * l.ldc, product == 2};
+    const Operand a = {product == 1 ? g.gram : g.poly, l.r, l.r, l.ldr, l.r * l.ldr, false};
+    p.a = product == 0 ? x : a;
+    p.b = product == 1 ? a : x;
+    return p;
+}
+
+// One launch per product: the matrices of a group that are too small, or too few, for the chained kernel.
+int run_products(const Group& g, const Params& q, cudaStream_t s) {
+    NsParams n = {};
+    NsEpi& e = n.e;
+    e = epilogue_of_group(g, q);
+    for (int k = 0; k < g.count; ++k) n.table[k] = output_of(g, k, q);
     for (int step = 0; step < q.steps; ++step) {
-        const Operand x = {hi[step & 1], l.r, l.c, l.ldc, l.r * l.ldc, false};
-        const Operand xt = {hi[step & 1], l.r, l.c, l.ldc, l.r * l.ldc, true};
-        const Operand ga = {gram, l.r, l.r, l.ldr, l.r * l.ldr, false};
-        const Operand pa = {poly, l.r, l.r, l.ldr, l.r * l.ldr, false};
-        const int kc = (int)((l.c + mma::kBlockK - 1) / mma::kBlockK), kr = (int)((l.r + mma::kBlockK - 1) / mma::kBlockK);
-        p.args.m = p.args.n = (int)l.r;
-        p.args.symmetric = 1;
-        p.args.b_mn = 0;
-        p.a = p.b = x;
-        p.args.kblocks = kc;
-        e.alpha = 1.0f / (scale * scale);
-        int rc = run<KIND_GRAM>(p, e, s);
+        e.alpha = 1.0f / (g.scale * g.scale);
+        int rc = run<KIND_GRAM>(product_plan(g, 0, step & 1), n, s);
         if (rc != DPRED_OK) return rc;
-        p.a = p.b = ga;
-        p.args.kblocks = kr;
         e.alpha = 1.0f / (kOffScale * kOffScale);
-        rc = run<KIND_POLY>(p, e, s);
+        rc = run<KIND_POLY>(product_plan(g, 1, step & 1), n, s);
         if (rc != DPRED_OK) return rc;
-        p.a = pa;
-        p.b = xt;
-        p.args.b_mn = 1;
-        p.args.n = (int)l.c;
-        p.args.symmetric = 0;
         e.alpha = 1.0f / kOffScale;
-        e.hi_in = hi[step & 1];
-        e.hi = hi[(step + 1) & 1];
-        rc = step + 1 < q.steps ? run<KIND_APPLY>(p, e, s) : run<KIND_FINAL>(p, e, s);
+        e.hi_in = g.hi[step & 1];
+        e.hi = g.hi[(step + 1) & 1];
+        const Plan p = product_plan(g, 2, step & 1);
+        rc = step + 1 < q.steps ? run<KIND_APPLY>(p, n, s) : run<KIND_FINAL>(p, n, s);
         if (rc != DPRED_OK) return rc;
     }
     return DPRED_OK;
+}
+
+int run_chained(const std::vector<Group>& groups, const Params& q, cudaStream_t s) {
+    ChainArgs a = {};
+    a.groups = (int)groups.size();
+    a.steps = q.steps;
+    a.counter = groups[0].counter;  // the groups' counters are neighbours
+    a.err = device_error_word();
+    int first = 0;
+    for (size_t i = 0; i < groups.size(); ++i) {
+        const Group& g = groups[i];
+        ChainGroup& d = a.g[i];
+        const Operand x0 = {g.hi[0], g.l.r, g.l.c, g.l.ldc, g.l.r * g.l.ldc, false};
+        const Operand ga = {g.gram, g.l.r, g.l.r, g.l.ldr, g.l.r * g.l.ldr, false};
+        Operand x1 = x0, t0 = x0, t1 = x0, pa = ga;
+        x1.p = g.hi[1];
+        t0.reduce_rows = t1.reduce_rows = true;
+        t1.p = g.hi[1];
+        pa.p = g.poly;
+        const struct {
+            const Operand& o;
+            CUtensorMap* m;
+        } maps[] = {{x0, &d.x[0]}, {x1, &d.x[1]}, {t0, &d.xt[0]}, {t1, &d.xt[1]}, {ga, &d.gram}, {pa, &d.poly}};
+        for (const auto& m : maps) {
+            const int rc = make_map(m.o, g.count, 128, false, m.m);
+            if (rc != DPRED_OK) return rc;
+        }
+        d.e = epilogue_of_group(g, q);
+        d.r = (int)g.l.r;
+        d.c = (int)g.l.c;
+        d.count = g.count;
+        d.first = first;
+        d.tiles_r = (d.r + 255) / 256;
+        d.tiles_c = (d.c + 255) / 256;
+        d.gram_tiles = d.tiles_r * (d.tiles_r + 1) / 2;
+        d.gram_alpha = 1.0f / (g.scale * g.scale);
+        a.gram_total += d.gram_tiles * d.count;
+        a.apply_total += d.tiles_r * d.tiles_c * d.count;
+        for (int k = 0; k < g.count; ++k) a.out[first + k] = output_of(g, k, q);
+        first += g.count;
+    }
+    return run_chain(a, s);
+}
+
+// Estimated times (us) of the two ways.  The chained kernel is bound by its
+// tiles' total over the CTA pairs, or by one matrix's chain of products; a tile
+// costs about 0.3 us a reduction block, 5 for its epilogue, 2 to start.
+double chained_time(const std::vector<Group>& groups, int steps) {
+    double work = 0, chain = 0;
+    for (const Group& g : groups) {
+        const double tr = (double)((g.l.r + 255) / 256), tc = (double)((g.l.c + 255) / 256), sym = tr * (tr + 1) / 2;
+        const double kc = 0.3 * blocks_of(g.l.c), kr = 0.3 * blocks_of(g.l.r);
+        work += g.count * (sym * std::max(kc, 5.0) + (sym + tr * tc) * std::max(kr, 5.0));
+        chain = std::max(chain, kc + 2 * kr + 3 * 7.0);
+    }
+    return 12 + steps * std::max(chain, work / (sm_count() / 2));
+}
+
+double products_time(const Group& g, int steps) {
+    double t = 0;
+    for (int p = 0; p < 3; ++p) t += estimate(product_plan(g, p, 0).args, false);
+    return steps * t;
 }
 
 // Matrices of one shape, or of its transpose, share launches.
@@ -414,19 +510,41 @@ int run_small_items(std::vector<const Item*>& v, const Params& q, cudaStream_t s
     return DPRED_OK;
 }
 
-// Sorts the matrices so that those of one shape are neighbours; the workspace of the largest launch.
-int64_t group(std::vector<const Item*>& v) {
+// The launches of a call: matrices of one shape are neighbours, and a launch
+// takes up to kMaxBatch matrices of up to kChainGroups shapes.
+std::vector<std::vector<Group>> launches_of(std::vector<const Item*>& v) {
     std::stable_sort(v.begin(), v.end(), [](const Item* x, const Item* y) {
         const int64_t a = std::min(x->rows, x->cols), b = std::min(y->rows, y->cols);
         return a != b ? a < b : std::max(x->rows, x->cols) < std::max(y->rows, y->cols);
     });
-    int64_t need = 0;
+    std::vector<std::vector<Group>> launches;
+    int room = 0;
     for (size_t i = 0; i < v.size();) {
         size_t j = i;
         while (j < v.size() && same_shape(v[i], v[j])) ++j;
-        const Layout l = layout_of(v[i]->rows, v[i]->cols);
-        need = std::max(need, launch_bytes(l, chunk_of(l, (int)(j - i))));
-        i = j;
+        while (i < j) {
+            if (room == 0 || launches.back().size() == (size_t)kChainGroups) {
+                launches.emplace_back();
+                room = kMaxBatch;
+            }
+            Group g = {};
+            g.items = &v[i];
+            g.count = (int)std::min<size_t>(j - i, room);
+            g.l = layout_of(v[i]->rows, v[i]->cols);
+            launches.back().push_back(g);
+            room -= g.count;
+            i += g.count;
+        }
+    }
+    return launches;
+}
+
+int64_t workspace_of(const std::vector<std::vector<Group>>& launches) {
+    int64_t need = 0;
+    for (const auto& groups : launches) {
+        int64_t bytes = 0;
+        for (const Group& g : groups) bytes += group_bytes(g.l, g.count);
+        need = std::max(need, bytes);
     }
     return need;
 }
@@ -436,24 +554,33 @@ int run_items(std::vector<Item>& items, const Params& q, void* workspace, size_t
     for (const Item& it : items)
         if (it.rows > 0 && it.cols > 0) v.push_back(&it);
     std::vector<const Item*> small = take_small(v);
-    const int64_t need = group(v);
+    std::vector<std::vector<Group>> launches = launches_of(v);
+    const int64_t need = workspace_of(launches);
     if (need && (!workspace || (int64_t)workspace_bytes < need))
         return set_error(DPRED_E_SIZE, "workspace of %zu bytes, %lld needed", workspace ? workspace_bytes : (size_t)0, (long long)need);
     if (need && reinterpret_cast<uintptr_t>(workspace) % 256)
         return set_error(DPRED_E_ALIGN, "workspace is not 256-byte aligned");
-    const int rc = run_small_items(small, q, s);
-    if (rc != DPRED_OK) return rc;
-    for (size_t i = 0; i < v.size();) {
-        size_t j = i;
-        while (j < v.size() && same_shape(v[i], v[j])) ++j;
-        const int chunk = chunk_of(layout_of(v[i]->rows, v[i]->cols), (int)(j - i));
-        for (; i < j; i += chunk) {
-            const int rc = run_chunk(&v[i], (int)std::min<size_t>(chunk, j - i), q, static_cast<char*>(workspace), s);
-            if (rc != DPRED_OK) return rc;
+    int rc = run_small_items(small, q, s);
+    for (size_t i = 0; i < launches.size() && rc == DPRED_OK; ++i) {
+        std::vector<Group>& groups = launches[i];
+        char* ws = static_cast<char*>(workspace);
+        unsigned* counter = reinterpret_cast<unsigned*>(ws);
+        ws += 256;  // counters of up to kMaxBatch matrices
+        double separate = 0;
+        for (Group& g : groups) {
+            place(g, ws);
+            g.counter = counter;
+            counter += g.count;
+            separate += products_time(g, q.steps);
+            if ((rc = start_group(g, q, s)) != DPRED_OK) return rc;
         }
-        i = j;
+        if (chained_time(groups, q.steps) < separate) {
+            rc = run_chained(groups, q, s);
+        } else {
+            for (size_t k = 0; k < groups.size() && rc == DPRED_OK; ++k) rc = run_products(groups[k], q, s);
+        }
     }
-    return DPRED_OK;
+    return rc;
 }
 
 int check_dtype(int dt, const char* what) {
@@ -512,8 +639,7 @@ using namespace dpred::gemm;
 extern "C" size_t dpred_newton_schulz_workspace_bytes(int32_t batch, int64_t rows, int64_t cols) {
     if (batch <= 0 || rows <= 0 || cols <= 0 || check_shape(rows, cols) != DPRED_OK) return 0;
     if (small_split(rows, cols)) return 0;
-    const Layout l = layout_of(rows, cols);
-    return (size_t)launch_bytes(l, chunk_of(l, batch));
+    return (size_t)group_bytes(layout_of(rows, cols), std::min(batch, kMaxBatch));
 }
 
 extern "C" int dpred_newton_schulz(int32_t batch, int64_t rows, int64_t cols, int32_t in_dtype, const void* in, int64_t ld,
@@ -566,7 +692,7 @@ extern "C" size_t dpred_muon_workspace_bytes(const dpred_muon_matrix* mats, int3
             if (mats[k].rows > 0 && mats[k].cols > 0) v.push_back(&items[k]);
         }
         take_small(v);
-        need = (size_t)group(v);
+        need = (size_t)workspace_of(launches_of(v));
         return DPRED_OK;
     });
     return need;

@@ -1,0 +1,308 @@
+// muon_chain.cu -- every product of the orthogonalised updates of a batch, as
+// one launch of the tile kernel's pipeline.
+//
+// Launched one by one, the three products of a step leave most SMs idle at
+// every boundary: 8 matrices of 1024 x 1024 are 80 symmetric tiles for 76 CTA
+// pairs, twice as long as 76.  Here the pairs walk one list of tiles in the order
+// (step, product, matrix): the first matrices' next product starts while the
+// last ones' current product is still running.  What a tile needs is its own
+// matrix's previous product, complete: a counter per matrix says so (every
+// epilogue warp adds one when its part of a tile is in memory), and since the
+// list is in dependency order and all pairs are resident (a cooperative
+// launch), every wait ends.  Waits are bounded all the same.
+#include "muon_chain.cuh"
+
+namespace dpred {
+namespace gemm {
+namespace {
+
+constexpr int kBN = 256;
+constexpr int kStages = 6;
+constexpr uint32_t kStageBytes = 2 * 128 * 128;
+constexpr int kSmem = kStages * (int)kStageBytes + 8 * (int)kBlockBytes + 1024;
+
+// A pair's position in the list of tiles.
+struct Cursor {
+    int step = 0, product = 0, offset;  // product: 0 Gram, 1 polynomial, 2 apply
+    // of the tile at this position
+    int group, batch, tm, tn;
+
+    __device__ __forceinline__ Cursor(int first) : offset(first) {}
+
+    __device__ __forceinline__ bool settle(const ChainArgs& a) {
+        for (;;) {
+            const int total = product < 2 ? a.gram_total : a.apply_total;
+            if (offset < total) break;
+            offset -= total;
+            if (++product == 3) {
+                product = 0;
+                if (++step == a.steps) return false;
+            }
+        }
+        int t = offset;
+        for (group = 0;; ++group) {
+            const ChainGroup& g = a.g[group];
+            const int per = product < 2 ? g.gram_tiles : g.tiles_r * g.tiles_c, n = per * g.count;
+            if (t < n) {
+                batch = t / per;
+                t -= batch * per;
+                if (product < 2) {  // row tm starts at the diagonal
+                    for (tm = 0; t >= g.tiles_r - tm; ++tm) t -= g.tiles_r - tm;
+                    tn = tm + t;
+                } else {
+                    tm = t % g.tiles_r;
+                    tn = t / g.tiles_r;
+                }
+                return true;
+            }
+            t -= n;
+        }
+    }
+
+    // What the matrix's counter must have reached before this product may start.
+    __device__ __forceinline__ unsigned needed(const ChainGroup& g) const {
+        const int apply = g.tiles_r * g.tiles_c;
+        return 16u * (unsigned)(step * (2 * g.gram_tiles + apply) + product * g.gram_tiles);
+    }
+};
+
+__device__ __forceinline__ bool wait_counter(const unsigned* p, unsigned need) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    if (v >= need) return true;
+    const long long t0 = clock64();
+    do {
+        __nanosleep(64);
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        if (v >= need) return true;
+    } while (clock64() - t0 <= tma::kWaitBudgetCycles);
+    return false;
+}
+
+// One tile's epilogue by one warp: 32 rows of 128 columns.
+template <int KIND>
+__device__ __forceinline__ bool tile_epilogue(const NsEpi& e, const Args& g, int batch, int i, int j, uint32_t acc,
+                                              uint32_t block, int lane, bool mirror, uint64_t* full, uint32_t parity,
+                                              uint32_t drained) {
+    Ahead<KIND> ahead;
+    load_ahead<KIND>(e, g, batch, i, j, lane, ahead);
+    if (!__all_sync(0xFFFFFFFFu, tma::mbar_wait(full, parity))) return false;
+    mma::fence_after();
+#pragma unroll 1
+    for (int c = 0; c < kBN / 2; c += 32) {
+        float v[32];
+        __syncwarp();
+        mma::tmem_ld32(acc + c, v);
+        mma::tmem_wait_ld();
+        if (c + 32 == kBN / 2) {  // the accumulator is in registers: the next tile may overwrite it
+            mma::fence_before();
+            __syncwarp();
+            if (lane == 0) mma::mbar_arrive_cluster(drained);
+        }
+        if (i < g.m && j + c < g.n) {
+            block_put_row(block, lane, v);
+            const Ahead<KIND> now = ahead;
+            if (c + 32 < kBN / 2) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
+            __syncwarp();
+            block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, mirror, now);
+        }
+    }
+    return true;
+}
+
+__global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_constant__ ChainArgs a) {
+    using namespace mma;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tma::mbar_init(&full[s], 1);
+            tma::mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tma::mbar_init(&acc_full[i], 1);
+            tma::mbar_init(&acc_empty[i], 16);
+        }
+        tma::fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc<2>(tma::smem_addr(&tmem_slot), 512);
+    fence_before();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            int s = 0, round = 0;
+            bool ok = true;
+            for (Cursor at(pair); ok && at.settle(a); at.offset += pairs) {
+                const ChainGroup& g = a.g[at.group];
+                if (!wait_counter(a.counter + g.first + at.batch, at.needed(g))) {
+                    record_device_error(a.err, DPRED_E_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                fence_proxy_async();  // what other SMs stored is about to be read by copies
+                const int x = at.step & 1, n = at.product == 0 ? g.c : g.r;
+                const CUtensorMap* ma = at.product == 0 ? &g.x[x] : at.product == 1 ? &g.gram : &g.poly;
+                const CUtensorMap* mb = at.product == 2 ? &g.xt[x] : ma;
+                const int i0 = at.tm * 256 + (int)rank * 128, j0 = at.tn * 256 + (int)rank * 128;
+                for (int k0 = 0; k0 < n; k0 += kBlockK) {
+                    if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
+                        record_device_error(a.err, DPRED_E_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t pa = base + s * kStageBytes, pb = pa + 128 * 128, bar = tma::smem_addr(&full[s]);
+                    if (rank == 0) tma::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    load_box_pair(pa, ma, bar, k0, i0, at.batch);
+                    if (at.product == 2) {
+                        load_box_pair(pb, mb, bar, j0, k0, at.batch);
+                        load_box_pair(pb + 8192, mb, bar, j0 + 64, k0, at.batch);
+                    } else {
+                        load_box_pair(pb, mb, bar, k0, j0, at.batch);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            if (!ok) {  // copies in flight land within microseconds, or never: leave after a bounded pause
+                const long long t0 = clock64();
+                while (clock64() - t0 < 20000000LL) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {
+            const uint64_t da0 = operand_desc(base, false), dbk = operand_desc(base + 128 * 128, false),
+                           dbm = operand_desc(base + 128 * 128, true);
+            int s = 0, round = 0, fill = 0;
+            bool ok = true;
+            for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
+                const ChainGroup& g = a.g[at.group];
+                const int n = at.product == 0 ? g.c : g.r, acc = fill & 1;
+                const bool mn = at.product == 2;
+                const uint32_t idesc = instr_desc(256, kBN, false, false, mn), sb = mn ? 128 : 2;
+                const uint64_t db0 = mn ? dbm : dbk;
+                if (fill >= 2 && !tma::mbar_wait(&acc_empty[acc], (fill / 2 - 1) & 1)) {
+                    record_device_error(a.err, DPRED_E_TIMEOUT);
+                    break;
+                }
+                fence_after();
+                for (int k0 = 0; k0 < n; k0 += kBlockK) {
+                    // the copies may wait for other SMs' tiles first, hence twice the budget
+                    if (!tma::mbar_wait(&full[s], round & 1, 2 * tma::kWaitBudgetCycles)) {
+                        record_device_error(a.err, DPRED_E_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 16; ++k)
+                        issue<2>(tmem + acc * kBN, da + k * 2, db + k * sb, idesc, k0 != 0 || k != 0);
+                    commit<2>(tma::smem_addr(&empty[s]));
+                    if (++s == kStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+                if (ok) commit<2>(tma::smem_addr(&acc_full[acc]));
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kEpilogueWarp0) {
+        const int q = warp & 3, half = (warp - kEpilogueWarp0) / 4;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * (kBN / 2);
+        const uint32_t block = base + kStages * kStageBytes + (warp - kEpilogueWarp0) * kBlockBytes;
+        const uint32_t drained0 = map_rank(tma::smem_addr(&acc_empty[0]), 0), drained1 = map_rank(tma::smem_addr(&acc_empty[1]), 0);
+        int fill = 0;
+        bool ok = true;
+        for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
+            const ChainGroup& g = a.g[at.group];
+            unsigned* counter = a.counter + g.first + at.batch;
+            const int acc = fill & 1;
+            if (at.product) {  // the epilogue reads what earlier products stored
+                if (lane == 0) ok = wait_counter(counter, at.needed(g));
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+            }
+            NsEpi e = g.e;
+            e.out = a.out + g.first;
+            Args d;
+            d.m = g.r;
+            d.n = at.product == 2 ? g.c : g.r;
+            const int i = at.tm * 256 + (int)rank * 128 + q * 32, j = at.tn * 256 + half * (kBN / 2);
+            const uint32_t from = lanes + acc * kBN, parity = (fill / 2) & 1, drained = acc ? drained1 : drained0;
+            const bool mirror = at.tn > at.tm;
+            if (at.product == 0) {
+                e.alpha = g.gram_alpha;
+                ok = tile_epilogue<KIND_GRAM>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
+            } else if (at.product == 1) {
+                e.alpha = 1.0f / (e.off_scale * e.off_scale);
+                ok = tile_epilogue<KIND_POLY>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
+            } else {
+                e.alpha = 1.0f / e.off_scale;
+                if (at.step & 1) {
+                    const __half* other = e.hi;
+                    e.hi = const_cast<__half*>(e.hi_in);
+                    e.hi_in = other;
+                }
+                if (at.step + 1 < a.steps)
+                    ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
+                else
+                    ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
+            }
+            fence_proxy_async();  // these stores will be read by other SMs' copies
+            __syncwarp();
+            if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(counter), "r"(1u) : "memory");
+        }
+        if (!ok && lane == 0) record_device_error(a.err, DPRED_E_TIMEOUT);
+        __syncwarp();
+    }
+    fence_before();
+    cluster_sync();  // no CTA leaves while the other may still signal it or read its shared memory
+    if (warp == 1) {
+        fence_after();
+        tmem_free<2>(tmem, 512);
+    }
+}
+
+}  // namespace
+
+int run_chain(const ChainArgs& a, cudaStream_t s) {
+    static bool attr[64] = {};
+    cudaError_t err = ensure_smem_attr(chain_kernel, kSmem, attr);
+    if (err != cudaSuccess) return cuda_error(err, "shared-memory limit of the chained products");
+    const int pairs = resident_pairs(reinterpret_cast<const void*>(chain_kernel), kTileThreads, kSmem);
+    if (pairs < 1) return set_error(DPRED_E_CUDA, "no CTA pair fits on this device");
+    const int most = a.gram_total > a.apply_total ? a.gram_total : a.apply_total;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, chain_kernel, a);
+    return err == cudaSuccess ? DPRED_OK : cuda_error(err, "chained products launch");
+}
+
+}  // namespace gemm
+}  // namespace dpred
