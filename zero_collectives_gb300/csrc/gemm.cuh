@@ -10,6 +10,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include <type_traits>
 
@@ -26,7 +27,7 @@ enum Kind : int {
     KIND_LINEAR = 0,  // linear layers: bias, activation or its gradient, residual, accumulation
     KIND_GRAM = 1,    // Newton-Schulz: off-diagonal of X X^T in fp16, its diagonal in fp32
     KIND_POLY = 2,    // Newton-Schulz: off-diagonal of b A + c A^2 in fp16, a + its diagonal in fp32
-    KIND_APPLY = 3,   // Newton-Schulz: the next X, as two fp16 terms
+    KIND_APPLY = 3,   // Newton-Schulz: the next X, as two terms
     KIND_FINAL = 4,   // Newton-Schulz: the last X, stored or applied to a weight
     // The tile kernel's linear layers, by what their epilogue can contain (its
     // code then holds nothing else; chosen by linear_kind()):
@@ -63,17 +64,15 @@ struct FinalOut {
 constexpr int kMaxBatch = 64;  // matrices per Newton-Schulz launch (their output table travels in the launch)
 
 struct NsEpi {
-    __half* gram;      // [batch, r, ldr] off-diagonal of X X^T, scaled (in for POLY, out for GRAM)
-    __half* poly;      // [batch, r, ldr] off-diagonal of the polynomial, scaled
+    __half* gram;      // [batch, r, ldr] off-diagonal of X X^T (in for POLY, out for GRAM)
+    __half* poly;      // [batch, r, ldr] off-diagonal of the polynomial
     float* gram_diag;  // [batch, ldr]
     float* coef;       // [batch, ldr] a + diagonal of the polynomial
-    const __half* hi_in;  // [batch, r, ldc]
-    const __half* lo_in;
-    __half* hi;
-    __half* lo;
+    const __half* hi_in;  // [batch, r, ldc] X's leading term, the products' operand
+    __half* hi;           // the next X's
+    uint8_t* lo;          // [batch, r, ldc] X's trailing term, updated in place (every element by the thread that reads it)
     int64_t ldr, ldc;
-    float alpha;       // multiplies the accumulator
-    float off_scale;   // GRAM, POLY: scale of the stored off-diagonals (a power of two)
+    float alpha;       // GRAM: multiplies the accumulator
     float a, b, c;     // the polynomial's coefficients
     float keep;        // FINAL: factor of the old weight (0: store)
     int out_f32;       // FINAL
@@ -214,6 +213,37 @@ __device__ __forceinline__ void store8_f32(float* p, const float (&f)[8]) {
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// X as two terms: the leading one in fp16 (what the matrix instructions read),
+// the rest, times 2^12, in fp8 (e4m3).  Together about 15 significant bits in 3
+// bytes: the products round X to 11 anyway, and the passes over X are bound by
+// its bytes (6 matrices of 1024 x 4096 take 511 us; with the rest in fp32, 661).
+constexpr float kLoScale = 4096.0f;
+
+__device__ __forceinline__ void split8(const float (&t)[8], uint4& hi, uint2& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2 p = __floats2half2_rn(t[2 * k], t[2 * k + 1]);
+        const float2 f = __half22float2(p);
+        h[k] = *reinterpret_cast<const uint32_t*>(&p);
+        l[k] = __nv_cvt_float2_to_fp8x2(make_float2((t[2 * k] - f.x) * kLoScale, (t[2 * k + 1] - f.y) * kLoScale), __NV_SATFINITE,
+                                        __NV_E4M3);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+}
+
+__device__ __forceinline__ void join8(const uint4& hi, const uint2& lo, float (&x)[8]) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x & 0xFFFF, lo.x >> 16, lo.y & 0xFFFF, lo.y >> 16};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)l[k], __NV_E4M3);
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[k])), q = __half22float2(__half2(r));
+        x[2 * k] = fmaf(q.x, 1.0f / kLoScale, p.x);
+        x[2 * k + 1] = fmaf(q.y, 1.0f / kLoScale, p.y);
+    }
 }
 
 __device__ __forceinline__ void store8_half(__half* p, const float (&f)[8]) {
@@ -489,7 +519,8 @@ struct Ahead<KIND_POLY> {
 };
 template <>
 struct Ahead<KIND_APPLY> {
-    uint4 h[4], l[4];
+    uint4 h[4];
+    uint2 l[4];
     float k[4];
 };
 template <>
@@ -519,7 +550,7 @@ __device__ __forceinline__ void load_ahead(const typename EpiOf<KIND>::T& e, con
         for (int s = 0; s < 4; ++s) {
             const bool in = i + 8 * s < g.m && j < g.n;
             a.h[s] = in ? __ldcg(reinterpret_cast<const uint4*>(e.hi_in + at + 8 * s * e.ldc)) : zero;
-            a.l[s] = in ? __ldcg(reinterpret_cast<const uint4*>(e.lo_in + at + 8 * s * e.ldc)) : zero;
+            a.l[s] = in ? __ldcg(reinterpret_cast<const uint2*>(e.lo + at + 8 * s * e.ldc)) : make_uint2(0, 0);
             a.k[s] = in ? __ldcg(e.coef + (int64_t)batch * e.ldr + i + 8 * s) : 0.0f;
         }
     }
@@ -581,11 +612,10 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
                     if (in[s] && (unsigned)(i + 8 * s - j) < 8u) e.gram_diag[(int64_t)batch * e.ldr + i + 8 * s] = x * e.alpha;
                 }
             }
-            const float f = e.alpha * e.off_scale;  // powers of two
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) t[s][c] *= f;
+                for (int c = 0; c < 8; ++c) t[s][c] *= e.alpha;
                 if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
             }
         } else if constexpr (KIND == KIND_POLY) {
@@ -594,40 +624,37 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
             //   (b A + c A^2)_ij = (b + c (d_i + d_j)) E_ij + c (E^2)_ij
             // and on it b d_i + c d_i^2 + c (E^2)_ii.
             __half* d = e.poly + ((int64_t)batch * g.m + i) * e.ldr + j;
-            const float f = e.c * e.alpha * e.off_scale;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 float x[8];
                 half8(a.q[s], x);
                 const float base = fmaf(e.c, a.di[s], e.b);
                 if (diagonal) {  // the stored diagonal of E is 0, so the result's is too
-                    const float sq = take(t[s], i + 8 * s - j) * e.alpha;
+                    const float sq = take(t[s], i + 8 * s - j);
                     if (in[s] && (unsigned)(i + 8 * s - j) < 8u)
                         e.coef[(int64_t)batch * e.ldr + i + 8 * s] = e.a + fmaf(e.c, fmaf(a.di[s], a.di[s], sq), e.b * a.di[s]);
                 }
 #pragma unroll
-                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(fmaf(e.c, a.dj[c], base), x[c], f * t[s][c]);
+                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(fmaf(e.c, a.dj[c], base), x[c], e.c * t[s][c]);
                 if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
             }
         } else {
             // X' = (a + diagonal) X + E X: the large part of the polynomial is its
-            // diagonal, which multiplies X in full precision (both fp16 terms).
+            // diagonal, which multiplies both terms of X.
             const int64_t at = ((int64_t)batch * g.m + i) * e.ldc + j;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                float hi[8], lo[8];
-                half8(a.h[s], hi);
-                half8(a.l[s], lo);
+                float x[8];
+                join8(a.h[s], a.l[s], x);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(a.k[s], hi[c] + lo[c], t[s][c] * e.alpha);
+                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(a.k[s], x[c], t[s][c]);
                 if constexpr (KIND == KIND_APPLY) {
+                    uint4 h;
+                    uint2 l;
+                    split8(t[s], h, l);
                     if (in[s]) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) hi[c] = __half2float(__float2half_rn(t[s][c]));
-                        store8_half(e.hi + at + 8 * s * e.ldc, hi);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) lo[c] = t[s][c] - hi[c];
-                        store8_half(e.lo + at + 8 * s * e.ldc, lo);
+                        *reinterpret_cast<uint4*>(e.hi + at + 8 * s * e.ldc) = h;
+                        *reinterpret_cast<uint2*>(e.lo + at + 8 * s * e.ldc) = l;
                     }
                 }
             }

@@ -10,17 +10,17 @@
 //
 // (X on its wide side; the polynomial is odd, so the transpose commutes with it.)
 //
-// Precision.  A step's result depends on 1 - sigma^2 style cancellations, so
-// 16-bit roundings of X and of the polynomial are what limits it.  Three
-// choices keep the products at the 16-bit rate with an error of 2e-4 to 1e-3
-// (against 1e-2 to 3e-2 with bf16 everywhere, and 1e-3 to 4e-3 with plain fp16):
-//  - operands are fp16 (11 significant bits, bf16 has 8) scaled by powers of
-//    two so that neither end of the range is reached: X by about sqrt(cols)
-//    (its entries are then near 1, at most the scale), A and the polynomial by 256;
+// Precision.  What limits a step's result is the rounding of X and of the
+// polynomial to the 16 bits that the matrix instructions take.  Three choices
+// keep the products at the 16-bit rate with an error of 2e-4 to 1e-3 of the
+// result (against 1e-2 to 3e-2 with bf16 everywhere, 1e-3 to 4e-3 with plain fp16):
+//  - operands are fp16 (11 significant bits, bf16 has 8); X is scaled by a
+//    power of two near sqrt(cols), which brings its entries near 1;
 //  - the diagonals of A and of the polynomial stay in fp32: the polynomial is
 //    near a multiple of the identity, so its diagonal is the only large part;
-//  - X is carried as two fp16 terms (22 bits); only the product with the small
-//    off-diagonal part and the Gram product use the leading term alone.
+//  - X carries a second, 8-bit term (about 15 bits together), and that diagonal
+//    multiplies both: only the products with the small off-diagonal part and the
+//    Gram product see the leading term alone.
 // Sums, norms, diagonals and accumulators are fp32.
 //
 // A and the polynomial are symmetric: only tiles that hold an element i <= j
@@ -40,7 +40,6 @@ namespace {
 constexpr int kMaxSteps = 32;
 constexpr int kNormBlocks = 256;  // partial sums of squares per matrix (at most)
 constexpr int kTile = 64;         // the element-wise passes work on 64 x 64 tiles
-constexpr float kOffScale = 256.0f;
 
 // One matrix of a launch as the element-wise passes see it.
 struct MatIn {
@@ -60,8 +59,8 @@ struct NormArgs {
     unsigned* counter;        // [batch] finished tiles of the chained products, cleared here
     int blocks;               // partials written per matrix
     float eps, scale;
-    __half* hi;
-    __half* lo;               // [batch, r, ldc]
+    __half* hi;               // [batch, r, ldc]
+    uint8_t* lo;
     int64_t ldc;
 };
 
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
     }
 }
 
-// X = scale * U / (|U| + eps) as two fp16 terms, on its wide side.  The
+// X = scale * U / (|U| + eps) on its wide side, as two terms (see split8).  The
 // partial sums are added in one fixed order by every block.
 template <typename Tg>
 __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ NormArgs a) {
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
     const int64_t tr = (rows + kTile - 1) / kTile, tc = (cols + kTile - 1) / kTile;
     const int64_t xr = a.r, xc = a.c;
     __half* hi = a.hi + (int64_t)blockIdx.y * xr * a.ldc;
-    __half* lo = a.lo + (int64_t)blockIdx.y * xr * a.ldc;
+    uint8_t* lo = a.lo + (int64_t)blockIdx.y * xr * a.ldc;
     const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
     for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
         const int64_t i0 = t / tc * kTile, j0 = t % tc * kTile;
@@ -211,12 +210,12 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
         for (int u = 0; u < 4; ++u) {
             const int64_t i = xi0 + r + 16 * u;
             if (i >= xr || xj >= xc) continue;  // rows are padded to 8 columns, so a group of 4 always fits
-            float h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = __half2float(__float2half_rn(x[u][k]));
-            *reinterpret_cast<uint2*>(hi + i * a.ldc + xj) = make_uint2(pack_half2(h[0], h[1]), pack_half2(h[2], h[3]));
-            *reinterpret_cast<uint2*>(lo + i * a.ldc + xj) =
-                make_uint2(pack_half2(x[u][0] - h[0], x[u][1] - h[1]), pack_half2(x[u][2] - h[2], x[u][3] - h[3]));
+            const float t[8] = {x[u][0], x[u][1], x[u][2], x[u][3]};
+            uint4 h;
+            uint2 l;
+            split8(t, h, l);
+            *reinterpret_cast<uint2*>(hi + i * a.ldc + xj) = make_uint2(h.x, h.y);
+            *reinterpret_cast<uint32_t*>(lo + i * a.ldc + xj) = l.x;
         }
     }
 }
@@ -236,7 +235,7 @@ struct Item {
 
 struct Layout {
     int64_t r, c, ldr, ldc;
-    int64_t x, gram, diag, per;  // bytes of one X term, of one r x r matrix, of one diagonal, of everything per matrix
+    int64_t x, gram, diag, per;  // bytes of one leading term of X, of one r x r matrix, of one diagonal, of everything per matrix
 };
 
 Layout layout_of(int64_t rows, int64_t cols) {
@@ -250,7 +249,7 @@ Layout layout_of(int64_t rows, int64_t cols) {
     l.diag = l.ldr * 4;
     // X: leading term twice (read and written by the same product), trailing term; A, polynomial; two diagonals;
     // partial sums; counter
-    l.per = 3 * l.x + 2 * l.gram + 2 * l.diag + kNormBlocks * 4 + 4;
+    l.per = 2 * l.x + l.x / 2 + 2 * l.gram + 2 * l.diag + kNormBlocks * 4 + 4;
     return l;
 }
 constexpr int kRegions = 9;  // regions of a group's workspace, each rounded up to 256 bytes
@@ -268,7 +267,8 @@ struct Group {
     int count;
     Layout l;
     // workspace
-    __half *hi[2], *lo, *gram, *poly;
+    __half *hi[2], *gram, *poly;
+    uint8_t* lo;
     float *diag, *coef, *partial;
     unsigned* counter;
     float scale;
@@ -283,7 +283,7 @@ void place(Group& g, char*& ws) {
     const Layout& l = g.l;
     g.hi[0] = reinterpret_cast<__half*>(take(l.x * g.count));
     g.hi[1] = reinterpret_cast<__half*>(take(l.x * g.count));
-    g.lo = reinterpret_cast<__half*>(take(l.x * g.count));
+    g.lo = reinterpret_cast<uint8_t*>(take(l.x / 2 * g.count));
     g.gram = reinterpret_cast<__half*>(take(l.gram * g.count));
     g.poly = reinterpret_cast<__half*>(take(l.gram * g.count));
     g.diag = reinterpret_cast<float*>(take(l.diag * g.count));
@@ -337,13 +337,9 @@ NsEpi epilogue_of_group(const Group& g, const Params& q) {
     e.poly = g.poly;
     e.gram_diag = g.diag;
     e.coef = g.coef;
-    e.hi_in = g.hi[0];
-    e.hi = g.hi[1];
-    e.lo_in = g.lo;
     e.lo = g.lo;
     e.ldr = g.l.ldr;
     e.ldc = g.l.ldc;
-    e.off_scale = kOffScale;
     e.a = q.a;
     e.b = q.b;
     e.c = q.c;
@@ -394,10 +390,8 @@ int run_products(const Group& g, const Params& q, cudaStream_t s) {
         e.alpha = 1.0f / (g.scale * g.scale);
         int rc = run<KIND_GRAM>(product_plan(g, 0, step & 1), n, s);
         if (rc != DPRED_OK) return rc;
-        e.alpha = 1.0f / (kOffScale * kOffScale);
         rc = run<KIND_POLY>(product_plan(g, 1, step & 1), n, s);
         if (rc != DPRED_OK) return rc;
-        e.alpha = 1.0f / kOffScale;
         e.hi_in = g.hi[step & 1];
         e.hi = g.hi[(step + 1) & 1];
         const Plan p = product_plan(g, 2, step & 1);
@@ -419,20 +413,24 @@ int run_chained(const std::vector<Group>& groups, const Params& q, cudaStream_t 
         ChainGroup& d = a.g[i];
         const Operand x0 = {g.hi[0], g.l.r, g.l.c, g.l.ldc, g.l.r * g.l.ldc, false};
         const Operand ga = {g.gram, g.l.r, g.l.r, g.l.ldr, g.l.r * g.l.ldr, false};
-        Operand x1 = x0, t0 = x0, t1 = x0, pa = ga;
+        Operand x1 = x0, t0 = x0, t1 = x0, pa = ga, gt = ga, pt = ga;
         x1.p = g.hi[1];
         t0.reduce_rows = t1.reduce_rows = true;
         t1.p = g.hi[1];
-        pa.p = g.poly;
+        pa.p = pt.p = g.poly;
+        gt.reduce_rows = pt.reduce_rows = true;
         const struct {
             const Operand& o;
             CUtensorMap* m;
-        } maps[] = {{x0, &d.x[0]}, {x1, &d.x[1]}, {t0, &d.xt[0]}, {t1, &d.xt[1]}, {ga, &d.gram}, {pa, &d.poly}};
+        } maps[] = {{x0, &d.x[0]}, {x1, &d.x[1]}, {t0, &d.xt[0]}, {t1, &d.xt[1]}, {ga, &d.gram[0]}, {gt, &d.gram[1]},
+                     {pa, &d.poly[0]}, {pt, &d.poly[1]}};
         for (const auto& m : maps) {
             const int rc = make_map(m.o, g.count, 128, false, m.m);
             if (rc != DPRED_OK) return rc;
         }
         d.e = epilogue_of_group(g, q);
+        d.hi[0] = g.hi[0];
+        d.hi[1] = g.hi[1];
         d.r = (int)g.l.r;
         d.c = (int)g.l.c;
         d.count = g.count;
@@ -449,18 +447,19 @@ int run_chained(const std::vector<Group>& groups, const Params& q, cudaStream_t 
     return run_chain(a, s);
 }
 
-// Estimated times (us) of the two ways.  The chained kernel is bound by its
-// tiles' total over the CTA pairs, or by one matrix's chain of products; a tile
-// costs about 0.3 us a reduction block, 5 for its epilogue, 2 to start.
+// Estimated times (us) of the two ways, fitted to batches of 1 to 16 matrices
+// from 256 x 256 to 2048 x 4096.  The chained kernel is bound by one matrix's
+// chain of products (a tile costs 0.3 a reduction block and 7 to start, drain
+// and hand over) and by its tiles' total over the CTA pairs.
 double chained_time(const std::vector<Group>& groups, int steps) {
     double work = 0, chain = 0;
     for (const Group& g : groups) {
         const double tr = (double)((g.l.r + 255) / 256), tc = (double)((g.l.c + 255) / 256), sym = tr * (tr + 1) / 2;
         const double kc = 0.3 * blocks_of(g.l.c), kr = 0.3 * blocks_of(g.l.r);
-        work += g.count * (sym * std::max(kc, 5.0) + (sym + tr * tc) * std::max(kr, 5.0));
+        work += g.count * (sym * std::max(kc, 6.5) + (sym + tr * tc) * std::max(kr, 6.5));
         chain = std::max(chain, kc + 2 * kr + 3 * 7.0);
     }
-    return 12 + steps * std::max(chain, work / (sm_count() / 2));
+    return 12 + steps * (0.88 * chain + 0.8 * work / (sm_count() / 2));
 }
 
 double products_time(const Group& g, int steps) {

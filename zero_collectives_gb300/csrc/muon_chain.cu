@@ -10,6 +10,12 @@
 // epilogue warp adds one when its part of a tile is in memory), and since the
 // list is in dependency order and all pairs are resident (a cooperative
 // launch), every wait ends.  Waits are bounded all the same.
+//
+// The symmetric products store only their tiles on and above the diagonal.
+// Where a later product needs the part below, it loads the mirror image as an
+// operand of the other major (rows and columns exchanged), which the matrix
+// instruction takes as it is: writing the mirror image cost the epilogue a
+// transposition through shared memory and the same stores again.
 #include "muon_chain.cuh"
 
 namespace dpred {
@@ -82,8 +88,7 @@ __device__ __forceinline__ bool wait_counter(const unsigned* p, unsigned need) {
 // One tile's epilogue by one warp: 32 rows of 128 columns.
 template <int KIND>
 __device__ __forceinline__ bool tile_epilogue(const NsEpi& e, const Args& g, int batch, int i, int j, uint32_t acc,
-                                              uint32_t block, int lane, bool mirror, uint64_t* full, uint32_t parity,
-                                              uint32_t drained) {
+                                              uint32_t block, int lane, uint64_t* full, uint32_t parity, uint32_t drained) {
     Ahead<KIND> ahead;
     load_ahead<KIND>(e, g, batch, i, j, lane, ahead);
     if (!__all_sync(0xFFFFFFFFu, tma::mbar_wait(full, parity))) return false;
@@ -104,7 +109,7 @@ __device__ __forceinline__ bool tile_epilogue(const NsEpi& e, const Args& g, int
             const Ahead<KIND> now = ahead;
             if (c + 32 < kBN / 2) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
             __syncwarp();
-            block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, mirror, now);
+            block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, false, now);
         }
     }
     return true;
@@ -150,9 +155,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                 }
                 fence_proxy_async();  // what other SMs stored is about to be read by copies
                 const int x = at.step & 1, n = at.product == 0 ? g.c : g.r;
-                const CUtensorMap* ma = at.product == 0 ? &g.x[x] : at.product == 1 ? &g.gram : &g.poly;
+                // product 0: X by X; 1: E by E; 2: P by X (MN-major).  A row block of E or P is stored from its
+                // diagonal tile on; before that its mirror image is loaded.
+                const CUtensorMap* ma = at.product == 0 ? &g.x[x] : at.product == 1 ? g.gram : g.poly;
                 const CUtensorMap* mb = at.product == 2 ? &g.xt[x] : ma;
                 const int i0 = at.tm * 256 + (int)rank * 128, j0 = at.tn * 256 + (int)rank * 128;
+                const int a_from = at.product == 0 ? 0 : at.tm * 256, b_from = at.product == 1 ? at.tn * 256 : at.product == 2 ? n + kBlockK : 0;
                 for (int k0 = 0; k0 < n; k0 += kBlockK) {
                     if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
                         record_device_error(a.err, DPRED_E_TIMEOUT);
@@ -161,10 +169,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                     }
                     const uint32_t pa = base + s * kStageBytes, pb = pa + 128 * 128, bar = tma::smem_addr(&full[s]);
                     if (rank == 0) tma::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                    load_box_pair(pa, ma, bar, k0, i0, at.batch);
-                    if (at.product == 2) {
-                        load_box_pair(pb, mb, bar, j0, k0, at.batch);
-                        load_box_pair(pb + 8192, mb, bar, j0 + 64, k0, at.batch);
+                    if (k0 < a_from) {
+                        load_box_pair(pa, ma + 1, bar, i0, k0, at.batch);
+                        load_box_pair(pa + 8192, ma + 1, bar, i0 + 64, k0, at.batch);
+                    } else {
+                        load_box_pair(pa, ma, bar, k0, i0, at.batch);
+                    }
+                    if (k0 < b_from) {
+                        const CUtensorMap* mt = at.product == 2 ? mb : mb + 1;
+                        load_box_pair(pb, mt, bar, j0, k0, at.batch);
+                        load_box_pair(pb + 8192, mt, bar, j0 + 64, k0, at.batch);
                     } else {
                         load_box_pair(pb, mb, bar, k0, j0, at.batch);
                     }
@@ -183,16 +197,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            const uint64_t da0 = operand_desc(base, false), dbk = operand_desc(base + 128 * 128, false),
-                           dbm = operand_desc(base + 128 * 128, true);
+            const uint64_t dk = operand_desc(base, false), dm = operand_desc(base, true);
             int s = 0, round = 0, fill = 0;
             bool ok = true;
             for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
                 const ChainGroup& g = a.g[at.group];
                 const int n = at.product == 0 ? g.c : g.r, acc = fill & 1;
-                const bool mn = at.product == 2;
-                const uint32_t idesc = instr_desc(256, kBN, false, false, mn), sb = mn ? 128 : 2;
-                const uint64_t db0 = mn ? dbm : dbk;
+                const int a_from = at.product == 0 ? 0 : at.tm * 256, b_from = at.product == 1 ? at.tn * 256 : at.product == 2 ? n + kBlockK : 0;
                 if (fill >= 2 && !tma::mbar_wait(&acc_empty[acc], (fill / 2 - 1) & 1)) {
                     record_device_error(a.err, DPRED_E_TIMEOUT);
                     break;
@@ -206,10 +217,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                         break;
                     }
                     fence_after();
-                    const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+                    const bool am = k0 < a_from, bm = k0 < b_from;
+                    const uint64_t da = (am ? dm : dk) + s * (kStageBytes >> 4), db = (bm ? dm : dk) + s * (kStageBytes >> 4) + (128 * 128 >> 4);
+                    const uint32_t idesc = instr_desc(256, kBN, false, am, bm), sa = am ? 128 : 2, sb = bm ? 128 : 2;
 #pragma unroll
                     for (int k = 0; k < kBlockK / 16; ++k)
-                        issue<2>(tmem + acc * kBN, da + k * 2, db + k * sb, idesc, k0 != 0 || k != 0);
+                        issue<2>(tmem + acc * kBN, da + k * sa, db + k * sb, idesc, k0 != 0 || k != 0);
                     commit<2>(tma::smem_addr(&empty[s]));
                     if (++s == kStages) {
                         s = 0;
@@ -243,25 +256,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
             d.n = at.product == 2 ? g.c : g.r;
             const int i = at.tm * 256 + (int)rank * 128 + q * 32, j = at.tn * 256 + half * (kBN / 2);
             const uint32_t from = lanes + acc * kBN, parity = (fill / 2) & 1, drained = acc ? drained1 : drained0;
-            const bool mirror = at.tn > at.tm;
-            if (at.product == 0) {
-                e.alpha = g.gram_alpha;
-                ok = tile_epilogue<KIND_GRAM>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
-            } else if (at.product == 1) {
-                e.alpha = 1.0f / (e.off_scale * e.off_scale);
-                ok = tile_epilogue<KIND_POLY>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
-            } else {
-                e.alpha = 1.0f / e.off_scale;
-                if (at.step & 1) {
-                    const __half* other = e.hi;
-                    e.hi = const_cast<__half*>(e.hi_in);
-                    e.hi_in = other;
-                }
-                if (at.step + 1 < a.steps)
-                    ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
-                else
-                    ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, mirror, &acc_full[acc], parity, drained);
-            }
+            e.alpha = g.gram_alpha;
+            e.hi_in = g.hi[at.step & 1];
+            e.hi = g.hi[(at.step + 1) & 1];
+            if (at.product == 0)
+                ok = tile_epilogue<KIND_GRAM>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
+            else if (at.product == 1)
+                ok = tile_epilogue<KIND_POLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
+            else if (at.step + 1 < a.steps)
+                ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
+            else
+                ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
             fence_proxy_async();  // these stores will be read by other SMs' copies
             __syncwarp();
             if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(counter), "r"(1u) : "memory");

@@ -10,10 +10,12 @@ constexpr int kChainGroups = 8;  // shapes per launch
 
 // The matrices of one shape: X is r x c (r <= c), `count` of them.
 struct ChainGroup {
-    CUtensorMap x[2];       // leading terms of X, K-major (boxes of 128 rows), two buffers
-    CUtensorMap xt[2];      // the same as an MN-major operand
-    CUtensorMap gram, poly; // K-major
-    NsEpi e;                // both X buffers: hi_in = buffer 0, hi = buffer 1
+    CUtensorMap x[2];     // X's leading term, K-major (boxes of 128 rows), two buffers
+    CUtensorMap xt[2];    // the same as an MN-major operand
+    CUtensorMap gram[2];  // K-major, MN-major
+    CUtensorMap poly[2];
+    NsEpi e;
+    __half* hi[2];
     int r, c, count, first; // first: index of the group's first matrix (counter, output entry)
     int tiles_r, tiles_c;   // 256 x 256 tiles of the r x r products' rows, of X's columns
     int gram_tiles;         // tiles of a symmetric product
