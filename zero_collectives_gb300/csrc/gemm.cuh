@@ -35,8 +35,9 @@ enum Kind : int {
     KIND_ACT = 6,     // bf16 result, forward activation and stored pre-activation
     KIND_GRAD = 7,    // bf16 result, activation's gradient
     KIND_F32 = 8,     // fp32 result: everything
+    KIND_MUL = 9,     // Newton-Schulz: product of two polynomials of one A, split as A is
 };
-__host__ __device__ constexpr bool is_linear(int kind) { return kind == KIND_LINEAR || kind >= KIND_PLAIN; }
+__host__ __device__ constexpr bool is_linear(int kind) { return kind == KIND_LINEAR || (kind >= KIND_PLAIN && kind <= KIND_F32); }
 
 // A linear layer's epilogue.  In order: t += bias; pre_out = t; t = act(t);
 // t += residual; t *= act'(z); t += what the output holds; out = t.  All
@@ -64,10 +65,12 @@ struct FinalOut {
 constexpr int kMaxBatch = 64;  // matrices per Newton-Schulz launch (their output table travels in the launch)
 
 struct NsEpi {
-    __half* gram;      // [batch, r, ldr] off-diagonal of X X^T (in for POLY, out for GRAM)
-    __half* poly;      // [batch, r, ldr] off-diagonal of the polynomial
+    __half* gram;      // [batch, r, ldr] off-diagonal of A (in for POLY, out for GRAM) or of a product (MUL, out)
+    __half* poly;      // [batch, r, ldr] off-diagonal of the polynomial (out for POLY)
     float* gram_diag;  // [batch, ldr]
-    float* coef;       // [batch, ldr] a + diagonal of the polynomial
+    float* coef;       // [batch, ldr] diagonal of a + b A + c A^2 (out for POLY, in for APPLY, FINAL)
+    const __half *m1, *m2;  // MUL: the factors' off-diagonals
+    const float *d1, *d2;   // and their diagonals
     const __half* hi_in;  // [batch, r, ldc] X's leading term, the products' operand
     __half* hi;           // the next X's
     uint8_t* lo;          // [batch, r, ldc] X's trailing term, updated in place (every element by the thread that reads it)
@@ -518,6 +521,11 @@ struct Ahead<KIND_POLY> {
     float di[4], dj[8];
 };
 template <>
+struct Ahead<KIND_MUL> {
+    uint4 p[4], q[4];
+    float di[4], dj[8];
+};
+template <>
 struct Ahead<KIND_APPLY> {
     uint4 h[4];
     uint2 l[4];
@@ -542,6 +550,21 @@ __device__ __forceinline__ void load_ahead(const typename EpiOf<KIND>::T& e, con
         }
         if (j < g.n) {  // rows and diagonals are padded to 8 elements
             const float4 x = __ldcg(reinterpret_cast<const float4*>(diag + j)), y = __ldcg(reinterpret_cast<const float4*>(diag + j + 4));
+            a.dj[0] = x.x; a.dj[1] = x.y; a.dj[2] = x.z; a.dj[3] = x.w; a.dj[4] = y.x; a.dj[5] = y.y; a.dj[6] = y.z; a.dj[7] = y.w;
+        }
+    } else if constexpr (KIND == KIND_MUL) {
+        const int64_t at = ((int64_t)batch * g.m + i) * e.ldr + j;
+        const float* d1 = e.d1 + (int64_t)batch * e.ldr;
+        const float* d2 = e.d2 + (int64_t)batch * e.ldr;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bool in = i + 8 * s < g.m && j < g.n;
+            a.p[s] = in ? __ldcg(reinterpret_cast<const uint4*>(e.m1 + at + 8 * s * e.ldr)) : zero;
+            a.q[s] = in ? __ldcg(reinterpret_cast<const uint4*>(e.m2 + at + 8 * s * e.ldr)) : zero;
+            a.di[s] = in ? __ldcg(d1 + i + 8 * s) : 0.0f;
+        }
+        if (j < g.n) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(d2 + j)), y = __ldcg(reinterpret_cast<const float4*>(d2 + j + 4));
             a.dj[0] = x.x; a.dj[1] = x.y; a.dj[2] = x.z; a.dj[3] = x.w; a.dj[4] = y.x; a.dj[5] = y.y; a.dj[6] = y.z; a.dj[7] = y.w;
         }
     } else if constexpr (KIND == KIND_APPLY || KIND == KIND_FINAL) {
@@ -636,6 +659,26 @@ __device__ __forceinline__ void block_epilogue(const typename EpiOf<KIND>::T& e,
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) t[s][c] = fmaf(fmaf(e.c, a.dj[c], base), x[c], e.c * t[s][c]);
+                if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
+            }
+        } else if constexpr (KIND == KIND_MUL) {
+            // (D1 + E1)(D2 + E2) = D1 D2 + D1 E2 + E1 D2 + E1 E2; symmetric, since the factors commute.
+            __half* d = e.gram + ((int64_t)batch * g.m + i) * e.ldr + j;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float x[8], y[8];
+                half8(a.p[s], x);
+                half8(a.q[s], y);
+                if (diagonal) {  // both factors' stored diagonals are 0, so the result's is too
+                    const int k = i + 8 * s - j;
+                    const float sq = take(t[s], k);
+                    float dk = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) dk = c == k ? a.dj[c] : dk;
+                    if (in[s] && (unsigned)k < 8u) e.gram_diag[(int64_t)batch * e.ldr + i + 8 * s] = fmaf(a.di[s], dk, sq);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) t[s][c] = fmaf(a.di[s], y[c], fmaf(x[c], a.dj[c], t[s][c]));
                 if (in[s]) store8_half(d + 8 * s * e.ldr, t[s]);
             }
         } else {

@@ -247,12 +247,12 @@ Layout layout_of(int64_t rows, int64_t cols) {
     l.x = l.r * l.ldc * 2;
     l.gram = l.r * l.ldr * 2;
     l.diag = l.ldr * 4;
-    // X: leading term twice (read and written by the same product), trailing term; A, polynomial; two diagonals;
-    // partial sums; counter
-    l.per = 2 * l.x + l.x / 2 + 2 * l.gram + 2 * l.diag + kNormBlocks * 4 + 4;
+    // X: leading term twice (read and written by the same product), trailing term; four r x r matrices and their
+    // diagonals; partial sums; counter
+    l.per = 2 * l.x + l.x / 2 + kSquares * (l.gram + l.diag) + kNormBlocks * 4 + 4;
     return l;
 }
-constexpr int kRegions = 9;  // regions of a group's workspace, each rounded up to 256 bytes
+constexpr int kRegions = 5 + 2 * kSquares;  // regions of a group's workspace, each rounded up to 256 bytes
 
 int64_t group_bytes(const Layout& l, int count) { return l.per * count + 256 * kRegions; }
 
@@ -267,9 +267,9 @@ struct Group {
     int count;
     Layout l;
     // workspace
-    __half *hi[2], *gram, *poly;
+    __half *hi[2], *square[kSquares];
     uint8_t* lo;
-    float *diag, *coef, *partial;
+    float *diag[kSquares], *partial;
     unsigned* counter;
     float scale;
 };
@@ -284,10 +284,10 @@ void place(Group& g, char*& ws) {
     g.hi[0] = reinterpret_cast<__half*>(take(l.x * g.count));
     g.hi[1] = reinterpret_cast<__half*>(take(l.x * g.count));
     g.lo = reinterpret_cast<uint8_t*>(take(l.x / 2 * g.count));
-    g.gram = reinterpret_cast<__half*>(take(l.gram * g.count));
-    g.poly = reinterpret_cast<__half*>(take(l.gram * g.count));
-    g.diag = reinterpret_cast<float*>(take(l.diag * g.count));
-    g.coef = reinterpret_cast<float*>(take(l.diag * g.count));
+    for (int k = 0; k < kSquares; ++k) {
+        g.square[k] = reinterpret_cast<__half*>(take(l.gram * g.count));
+        g.diag[k] = reinterpret_cast<float*>(take(l.diag * g.count));
+    }
     g.partial = reinterpret_cast<float*>(take((int64_t)kNormBlocks * 4 * g.count));
     // entries of X: near 1 after scaling by about sqrt(c); an orthogonal row of length c has entries near 1/sqrt(c)
     g.scale = std::exp2(std::round(0.5f * std::log2((float)std::min<int64_t>(l.c, 65536))));
@@ -333,10 +333,10 @@ int start_group(const Group& g, const Params& q, cudaStream_t s) {
 
 NsEpi epilogue_of_group(const Group& g, const Params& q) {
     NsEpi e = {};
-    e.gram = g.gram;
-    e.poly = g.poly;
-    e.gram_diag = g.diag;
-    e.coef = g.coef;
+    e.gram = g.square[0];
+    e.poly = g.square[1];
+    e.gram_diag = g.diag[0];
+    e.coef = g.diag[1];
     e.lo = g.lo;
     e.ldr = g.l.ldr;
     e.ldc = g.l.ldc;
@@ -345,6 +345,7 @@ NsEpi epilogue_of_group(const Group& g, const Params& q) {
     e.c = q.c;
     e.keep = q.keep;
     e.out_f32 = q.out_dtype == DPRED_F32;
+    e.alpha = 1.0f / (g.scale * g.scale);
     return e;
 }
 
@@ -374,7 +375,7 @@ Plan product_plan(const Group& g, int product, int buffer) {
     p.args.kblocks = blocks_of(product == 0 ? l.c : l.r);
     p.args.split_only = 1;
     const Operand x = {g.hi[buffer], l.r, l.c, l.ldc, l.r * l.ldc, product == 2};
-    const Operand a = {product == 1 ? g.gram : g.poly, l.r, l.r, l.ldr, l.r * l.ldr, false};
+    const Operand a = {g.square[product == 1 ? 0 : 1], l.r, l.r, l.ldr, l.r * l.ldr, false};
     p.a = product == 0 ? x : a;
     p.b = product == 1 ? a : x;
     return p;
@@ -387,7 +388,6 @@ int run_products(const Group& g, const Params& q, cudaStream_t s) {
     e = epilogue_of_group(g, q);
     for (int k = 0; k < g.count; ++k) n.table[k] = output_of(g, k, q);
     for (int step = 0; step < q.steps; ++step) {
-        e.alpha = 1.0f / (g.scale * g.scale);
         int rc = run<KIND_GRAM>(product_plan(g, 0, step & 1), n, s);
         if (rc != DPRED_OK) return rc;
         rc = run<KIND_POLY>(product_plan(g, 1, step & 1), n, s);
@@ -401,65 +401,108 @@ int run_products(const Group& g, const Params& q, cudaStream_t s) {
     return DPRED_OK;
 }
 
+// A matrix's products.  A plain step is Gram, polynomial, apply.  A double
+// step works out two steps from one Gram product: with P = p(A), the next Gram
+// matrix is A' = P A P (everything is a polynomial of A and commutes), so
+//     A, P = p(A), T = P A, A' = P T, P' = p(A'), Q = P' P, X = Q X
+// reads and writes X once and trades a Gram and an apply product (3 r^2 c flops,
+// the symmetric halves counted) for three r x r ones (3 r^3).  A' inherits A's
+// rounding, amplified for the small singular values as one more plain step
+// would amplify X's; three steps in a row measured 1.2e-3 to 1.9e-3, two 2e-4 to 1e-3.
+// Matrices: 0 = A, A'; 1 = P; 2 = T, Q; 3 = P'.
+int chain_program(ChainOp* op, int steps, bool pairs) {
+    int n = 0;
+    uint8_t x = 0, squares = 0, applies = 0;
+    auto add = [&](uint8_t kind, uint8_t a, uint8_t b, uint8_t out) {
+        op[n++] = {kind, a, b, out, x, squares, applies, 0};
+        if (kind < CHAIN_APPLY)
+            ++squares;
+        else
+            ++applies;
+    };
+    while (steps > 0) {
+        const bool two = pairs && steps >= 2;
+        steps -= two ? 2 : 1;
+        add(CHAIN_GRAM, 0, 0, 0);
+        add(CHAIN_POLY, 0, 0, 1);
+        if (two) {
+            add(CHAIN_MUL, 1, 0, 2);
+            add(CHAIN_MUL, 1, 2, 0);
+            add(CHAIN_POLY, 0, 0, 3);
+            add(CHAIN_MUL, 3, 1, 2);
+        }
+        add(steps ? CHAIN_APPLY : CHAIN_FINAL, two ? 2 : 1, 0, 0);
+        x ^= 1;
+    }
+    return n;
+}
+
+// Double steps pay where the products with X are much the longer ones (plain
+// -> double): 6 of 1024 x 4096 513 -> 454 us, 24 of 512 x 2048 440 -> 399; 6 of
+// 1024 x 2048 305 -> 322, 8 of 1024 x 1024 241 -> 275.
+bool double_steps(const Layout& l) { return l.c >= 3 * l.r; }
+
 int run_chained(const std::vector<Group>& groups, const Params& q, cudaStream_t s) {
     ChainArgs a = {};
     a.groups = (int)groups.size();
-    a.steps = q.steps;
     a.counter = groups[0].counter;  // the groups' counters are neighbours
     a.err = device_error_word();
-    int first = 0;
+    const int ops[2] = {chain_program(a.program[0], q.steps, false), chain_program(a.program[1], q.steps, true)};
+    int first = 0, squares = 0, applies = 0;
     for (size_t i = 0; i < groups.size(); ++i) {
         const Group& g = groups[i];
         ChainGroup& d = a.g[i];
-        const Operand x0 = {g.hi[0], g.l.r, g.l.c, g.l.ldc, g.l.r * g.l.ldc, false};
-        const Operand ga = {g.gram, g.l.r, g.l.r, g.l.ldr, g.l.r * g.l.ldr, false};
-        Operand x1 = x0, t0 = x0, t1 = x0, pa = ga, gt = ga, pt = ga;
-        x1.p = g.hi[1];
-        t0.reduce_rows = t1.reduce_rows = true;
-        t1.p = g.hi[1];
-        pa.p = pt.p = g.poly;
-        gt.reduce_rows = pt.reduce_rows = true;
-        const struct {
-            const Operand& o;
-            CUtensorMap* m;
-        } maps[] = {{x0, &d.x[0]}, {x1, &d.x[1]}, {t0, &d.xt[0]}, {t1, &d.xt[1]}, {ga, &d.gram[0]}, {gt, &d.gram[1]},
-                     {pa, &d.poly[0]}, {pt, &d.poly[1]}};
-        for (const auto& m : maps) {
-            const int rc = make_map(m.o, g.count, 128, false, m.m);
+        for (int k = 0; k < 2; ++k) {
+            Operand x = {g.hi[k], g.l.r, g.l.c, g.l.ldc, g.l.r * g.l.ldc, false};
+            int rc = make_map(x, g.count, 128, false, &d.x[k]);
             if (rc != DPRED_OK) return rc;
+            x.reduce_rows = true;
+            if ((rc = make_map(x, g.count, 128, false, &d.xt[k])) != DPRED_OK) return rc;
+            d.hi[k] = g.hi[k];
+        }
+        for (int k = 0; k < kSquares; ++k) {
+            for (int t = 0; t < 2; ++t) {
+                const Operand m = {g.square[k], g.l.r, g.l.r, g.l.ldr, g.l.r * g.l.ldr, t == 1};
+                const int rc = make_map(m, g.count, 128, false, &d.square[k][t]);
+                if (rc != DPRED_OK) return rc;
+            }
+            d.sq[k] = g.square[k];
+            d.diag[k] = g.diag[k];
         }
         d.e = epilogue_of_group(g, q);
-        d.hi[0] = g.hi[0];
-        d.hi[1] = g.hi[1];
         d.r = (int)g.l.r;
         d.c = (int)g.l.c;
         d.count = g.count;
         d.first = first;
         d.tiles_r = (d.r + 255) / 256;
         d.tiles_c = (d.c + 255) / 256;
-        d.gram_tiles = d.tiles_r * (d.tiles_r + 1) / 2;
-        d.gram_alpha = 1.0f / (g.scale * g.scale);
-        a.gram_total += d.gram_tiles * d.count;
-        a.apply_total += d.tiles_r * d.tiles_c * d.count;
+        d.square_tiles = d.tiles_r * (d.tiles_r + 1) / 2;
+        d.program = double_steps(g.l);
+        d.ops = ops[d.program];
+        a.ops = std::max(a.ops, d.ops);
+        squares += d.square_tiles * d.count;
+        applies += d.tiles_r * d.tiles_c * d.count;
         for (int k = 0; k < g.count; ++k) a.out[first + k] = output_of(g, k, q);
         first += g.count;
     }
+    a.most = std::max(squares, applies);
     return run_chain(a, s);
 }
 
 // Estimated times (us) of the two ways, fitted to batches of 1 to 16 matrices
-// from 256 x 256 to 2048 x 4096.  The chained kernel is bound by one matrix's
-// chain of products (a tile costs 0.3 a reduction block and 7 to start, drain
-// and hand over) and by its tiles' total over the CTA pairs.
+// from 256 x 256 to 2048 x 4096 (within 12%).  The chained kernel is bound by
+// one matrix's chain of products (a tile costs 0.3 a reduction block and 7 to
+// start, drain and hand over) and by its tiles' total over the CTA pairs.
 double chained_time(const std::vector<Group>& groups, int steps) {
     double work = 0, chain = 0;
     for (const Group& g : groups) {
         const double tr = (double)((g.l.r + 255) / 256), tc = (double)((g.l.c + 255) / 256), sym = tr * (tr + 1) / 2;
         const double kc = 0.3 * blocks_of(g.l.c), kr = 0.3 * blocks_of(g.l.r);
-        work += g.count * (sym * std::max(kc, 6.5) + (sym + tr * tc) * std::max(kr, 6.5));
-        chain = std::max(chain, kc + 2 * kr + 3 * 7.0);
+        const int twos = double_steps(g.l) ? steps / 2 : 0, passes = steps - twos, squares = steps + 3 * twos;
+        work += g.count * (passes * (sym * std::max(kc, 6.5) + tr * tc * std::max(kr, 6.5)) + squares * sym * std::max(kr, 6.5));
+        chain = std::max(chain, passes * (kc + kr + 2 * 7.0) + squares * (kr + 7.0));
     }
-    return 12 + steps * (0.88 * chain + 0.8 * work / (sm_count() / 2));
+    return 12 + std::hypot(0.93 * chain, 1.45 * work / (sm_count() / 2));
 }
 
 double products_time(const Group& g, int steps) {

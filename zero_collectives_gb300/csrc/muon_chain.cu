@@ -4,7 +4,7 @@
 // Launched one by one, the three products of a step leave most SMs idle at
 // every boundary: 8 matrices of 1024 x 1024 are 80 symmetric tiles for 76 CTA
 // pairs, twice as long as 76.  Here the pairs walk one list of tiles in the order
-// (step, product, matrix): the first matrices' next product starts while the
+// (product, matrix): the first matrices' next product starts while the
 // last ones' current product is still running.  What a tile needs is its own
 // matrix's previous product, complete: a counter per matrix says so (every
 // epilogue warp adds one when its part of a tile is in memory), and since the
@@ -29,47 +29,51 @@ constexpr int kSmem = kStages * (int)kStageBytes + 8 * (int)kBlockBytes + 1024;
 
 // A pair's position in the list of tiles.
 struct Cursor {
-    int step = 0, product = 0, offset;  // product: 0 Gram, 1 polynomial, 2 apply
+    int at = 0, offset;  // product (of every matrix's program), tile within it
     // of the tile at this position
     int group, batch, tm, tn;
+    ChainOp op;
 
     __device__ __forceinline__ Cursor(int first) : offset(first) {}
 
     __device__ __forceinline__ bool settle(const ChainArgs& a) {
-        for (;;) {
-            const int total = product < 2 ? a.gram_total : a.apply_total;
-            if (offset < total) break;
-            offset -= total;
-            if (++product == 3) {
-                product = 0;
-                if (++step == a.steps) return false;
-            }
-        }
-        int t = offset;
-        for (group = 0;; ++group) {
-            const ChainGroup& g = a.g[group];
-            const int per = product < 2 ? g.gram_tiles : g.tiles_r * g.tiles_c, n = per * g.count;
-            if (t < n) {
-                batch = t / per;
-                t -= batch * per;
-                if (product < 2) {  // row tm starts at the diagonal
-                    for (tm = 0; t >= g.tiles_r - tm; ++tm) t -= g.tiles_r - tm;
-                    tn = tm + t;
-                } else {
-                    tm = t % g.tiles_r;
-                    tn = t / g.tiles_r;
+        for (; at < a.ops; ++at) {
+            int t = offset;
+            for (group = 0; group < a.groups; ++group) {
+                const ChainGroup& g = a.g[group];
+                if (at >= g.ops) continue;
+                op = a.program[g.program][at];
+                const bool square = op.kind < CHAIN_APPLY;
+                const int per = square ? g.square_tiles : g.tiles_r * g.tiles_c, n = per * g.count;
+                if (t < n) {
+                    batch = t / per;
+                    t -= batch * per;
+                    if (square) {  // row tm starts at the diagonal
+                        for (tm = 0; t >= g.tiles_r - tm; ++tm) t -= g.tiles_r - tm;
+                        tn = tm + t;
+                    } else {
+                        tm = t % g.tiles_r;
+                        tn = t / g.tiles_r;
+                    }
+                    return true;
                 }
-                return true;
+                t -= n;
             }
-            t -= n;
+            offset = t;
         }
+        return false;
     }
 
     // What the matrix's counter must have reached before this product may start.
     __device__ __forceinline__ unsigned needed(const ChainGroup& g) const {
-        const int apply = g.tiles_r * g.tiles_c;
-        return 16u * (unsigned)(step * (2 * g.gram_tiles + apply) + product * g.gram_tiles);
+        return 16u * (unsigned)(op.squares * g.square_tiles + op.applies * g.tiles_r * g.tiles_c);
     }
+    __device__ __forceinline__ int reduction(const ChainGroup& g) const { return op.kind == CHAIN_GRAM ? g.c : g.r; }
+    // A row block of a stored r x r matrix exists from its diagonal tile on:
+    // reduction indexes below these are loaded from the mirror image.  X as the
+    // second factor is MN-major throughout.
+    __device__ __forceinline__ int a_from() const { return op.kind == CHAIN_GRAM ? 0 : tm * 256; }
+    __device__ __forceinline__ int b_from() const { return op.kind == CHAIN_GRAM ? 0 : op.kind >= CHAIN_APPLY ? 0x7FFFFFFF : tn * 256; }
 };
 
 __device__ __forceinline__ bool wait_counter(const unsigned* p, unsigned need) {
@@ -89,6 +93,9 @@ __device__ __forceinline__ bool wait_counter(const unsigned* p, unsigned need) {
 template <int KIND>
 __device__ __forceinline__ bool tile_epilogue(const NsEpi& e, const Args& g, int batch, int i, int j, uint32_t acc,
                                               uint32_t block, int lane, uint64_t* full, uint32_t parity, uint32_t drained) {
+    // the next block's operands are loaded while this one is worked on; two factors (MUL) would not fit the
+    // registers twice, and theirs are loaded at the block
+    constexpr bool kNext = KIND != KIND_MUL;
     Ahead<KIND> ahead;
     load_ahead<KIND>(e, g, batch, i, j, lane, ahead);
     if (!__all_sync(0xFFFFFFFFu, tma::mbar_wait(full, parity))) return false;
@@ -106,10 +113,16 @@ __device__ __forceinline__ bool tile_epilogue(const NsEpi& e, const Args& g, int
         }
         if (i < g.m && j + c < g.n) {
             block_put_row(block, lane, v);
-            const Ahead<KIND> now = ahead;
-            if (c + 32 < kBN / 2) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
-            __syncwarp();
-            block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, false, now);
+            if constexpr (kNext) {
+                const Ahead<KIND> now = ahead;
+                if (c + 32 < kBN / 2) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
+                __syncwarp();
+                block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, false, now);
+            } else {
+                __syncwarp();
+                block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, false, ahead);
+                if (c + 32 < kBN / 2) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
+            }
         }
     }
     return true;
@@ -154,13 +167,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                     break;
                 }
                 fence_proxy_async();  // what other SMs stored is about to be read by copies
-                const int x = at.step & 1, n = at.product == 0 ? g.c : g.r;
-                // product 0: X by X; 1: E by E; 2: P by X (MN-major).  A row block of E or P is stored from its
-                // diagonal tile on; before that its mirror image is loaded.
-                const CUtensorMap* ma = at.product == 0 ? &g.x[x] : at.product == 1 ? g.gram : g.poly;
-                const CUtensorMap* mb = at.product == 2 ? &g.xt[x] : ma;
+                const ChainOp op = at.op;
+                const CUtensorMap* ma = op.kind == CHAIN_GRAM ? &g.x[op.x] : g.square[op.a];
+                const CUtensorMap* mb = op.kind >= CHAIN_APPLY ? &g.xt[op.x] : op.kind == CHAIN_GRAM ? ma : g.square[op.b];
+                const int n = at.reduction(g), a_from = at.a_from(), b_from = at.b_from();
                 const int i0 = at.tm * 256 + (int)rank * 128, j0 = at.tn * 256 + (int)rank * 128;
-                const int a_from = at.product == 0 ? 0 : at.tm * 256, b_from = at.product == 1 ? at.tn * 256 : at.product == 2 ? n + kBlockK : 0;
                 for (int k0 = 0; k0 < n; k0 += kBlockK) {
                     if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
                         record_device_error(a.err, DPRED_E_TIMEOUT);
@@ -176,7 +187,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                         load_box_pair(pa, ma, bar, k0, i0, at.batch);
                     }
                     if (k0 < b_from) {
-                        const CUtensorMap* mt = at.product == 2 ? mb : mb + 1;
+                        const CUtensorMap* mt = op.kind >= CHAIN_APPLY ? mb : mb + 1;
                         load_box_pair(pb, mt, bar, j0, k0, at.batch);
                         load_box_pair(pb + 8192, mt, bar, j0 + 64, k0, at.batch);
                     } else {
@@ -202,8 +213,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
             bool ok = true;
             for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
                 const ChainGroup& g = a.g[at.group];
-                const int n = at.product == 0 ? g.c : g.r, acc = fill & 1;
-                const int a_from = at.product == 0 ? 0 : at.tm * 256, b_from = at.product == 1 ? at.tn * 256 : at.product == 2 ? n + kBlockK : 0;
+                const int n = at.reduction(g), acc = fill & 1, a_from = at.a_from(), b_from = at.b_from();
                 if (fill >= 2 && !tma::mbar_wait(&acc_empty[acc], (fill / 2 - 1) & 1)) {
                     record_device_error(a.err, DPRED_E_TIMEOUT);
                     break;
@@ -244,7 +254,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
             const ChainGroup& g = a.g[at.group];
             unsigned* counter = a.counter + g.first + at.batch;
             const int acc = fill & 1;
-            if (at.product) {  // the epilogue reads what earlier products stored
+            const ChainOp op = at.op;
+            if (op.kind != CHAIN_GRAM) {  // the epilogue reads what earlier products stored
                 if (lane == 0) ok = wait_counter(counter, at.needed(g));
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -253,20 +264,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
             e.out = a.out + g.first;
             Args d;
             d.m = g.r;
-            d.n = at.product == 2 ? g.c : g.r;
+            d.n = op.kind >= CHAIN_APPLY ? g.c : g.r;
             const int i = at.tm * 256 + (int)rank * 128 + q * 32, j = at.tn * 256 + half * (kBN / 2);
             const uint32_t from = lanes + acc * kBN, parity = (fill / 2) & 1, drained = acc ? drained1 : drained0;
-            e.alpha = g.gram_alpha;
-            e.hi_in = g.hi[at.step & 1];
-            e.hi = g.hi[(at.step + 1) & 1];
-            if (at.product == 0)
-                ok = tile_epilogue<KIND_GRAM>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
-            else if (at.product == 1)
-                ok = tile_epilogue<KIND_POLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
-            else if (at.step + 1 < a.steps)
-                ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
-            else
-                ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained);
+            e.gram = g.sq[op.kind == CHAIN_POLY ? op.a : op.out];
+            e.gram_diag = g.diag[op.kind == CHAIN_POLY ? op.a : op.out];
+            e.poly = g.sq[op.out];
+            e.coef = g.diag[op.kind == CHAIN_POLY ? op.out : op.a];
+            e.m1 = g.sq[op.a];
+            e.d1 = g.diag[op.a];
+            e.m2 = g.sq[op.b];
+            e.d2 = g.diag[op.b];
+            e.hi_in = g.hi[op.x];
+            e.hi = g.hi[op.x ^ 1];
+            switch (op.kind) {
+                case CHAIN_GRAM: ok = tile_epilogue<KIND_GRAM>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
+                case CHAIN_POLY: ok = tile_epilogue<KIND_POLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
+                case CHAIN_MUL: ok = tile_epilogue<KIND_MUL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
+                case CHAIN_APPLY: ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
+                default: ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
+            }
             fence_proxy_async();  // these stores will be read by other SMs' copies
             __syncwarp();
             if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(counter), "r"(1u) : "memory");
@@ -290,9 +307,8 @@ int run_chain(const ChainArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return cuda_error(err, "shared-memory limit of the chained products");
     const int pairs = resident_pairs(reinterpret_cast<const void*>(chain_kernel), kTileThreads, kSmem);
     if (pairs < 1) return set_error(DPRED_E_CUDA, "no CTA pair fits on this device");
-    const int most = a.gram_total > a.apply_total ? a.gram_total : a.apply_total;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
+    cfg.gridDim = dim3((unsigned)(2 * (a.most < pairs ? a.most : pairs)));
     cfg.blockDim = dim3(kTileThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
