@@ -241,6 +241,35 @@ def test_output_offsets_beyond_32_bits():
         close(y[rows], x[rows].double() @ w.double().T, x[rows].double().abs() @ w.double().abs().T, k)
 
 
+@pytest.mark.parametrize("m,n,k", [(4096, 8192, 64), (2100, 16000, 64), (5000, 3900, 128), (16000, 2056, 192)])
+@pytest.mark.parametrize("form", ["plain", "act", "pre", "residual", "all", "grad", "f32", "f32 add"])
+def test_many_short_tiles(m, n, k, form):
+    """Reductions so short that every tile's epilogue overtakes the copies of the one before."""
+    x, w, b = randn(m, k, seed=1), randn(n, k, seed=2, scale=1 / math.sqrt(k)), randn(1, n, seed=3)[0]
+    z64 = x.double() @ w.double().T
+    mags = x.double().abs() @ w.double().abs().T
+    if form in ("plain", "f32", "f32 add"):
+        if form == "f32 add":  # the same product as a weight gradient added to an accumulator
+            out = randn(m, n, seed=4, dtype=torch.float32)
+            want = out.double() + z64
+            zc.linear_wgrad(x.T.contiguous(), w.T.contiguous(), out, accumulate=True)
+            return close(out, want, mags + want.abs(), k)
+        return close(zc.linear(x, w, out_dtype=torch.float32 if form == "f32" else None), z64, mags, k)
+    if form == "grad":
+        z = randn(m, n, seed=5)
+        dx = zc.linear_dgrad(x, w.T.contiguous(), preact=z, act="gelu")
+        return close(dx, z64 * act_grad64(z.double(), "gelu"), mags, k, 2.0 ** -18 * mags * (z.double().abs() + 1))
+    z64, mags = z64 + b.double(), mags + b.double().abs()
+    r = randn(m, n, seed=4) if form in ("residual", "all") else None
+    z = torch.empty(m, n, dtype=torch.bfloat16, device="cuda") if form in ("pre", "all") else None
+    act = "none" if form == "residual" else "silu"
+    y = zc.linear(x, w, bias=b, act=act, residual=r, preact=z)
+    r64 = r.double() if r is not None else torch.zeros_like(z64)
+    close(y, act64(z64, act) + r64, mags + r64.abs(), k, 2.0 ** -18 * (z64.abs() + 1))
+    if z is not None:
+        close(z, z64, mags, k)
+
+
 def test_residual_in_place():
     m, n, k = 200, 264, 128
     x, w, r = randn(m, k, seed=1), randn(n, k, seed=2), randn(m, n, seed=3)

@@ -48,6 +48,24 @@ int make_map(const Operand& o, int batch, int box_rows, bool bf16, CUtensorMap* 
     return DPRED_OK;
 }
 
+int make_box_map(const void* p, int64_t rows, int64_t cols, int64_t ld, bool fp32, CUtensorMap* m) {
+    EncodeFn f = encoder();
+    if (!f) return set_error(DPRED_E_CUDA, "the driver has no tensor-map encoder");
+    const int esize = fp32 ? 4 : 2;
+    const cuuint64_t row = rows > 1 ? (cuuint64_t)ld * esize : (cuuint64_t)((cols * esize + 15) / 16 * 16);
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+    cuuint64_t strides[2] = {row, row * (cuuint64_t)rows};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / esize), 32, 1};
+    cuuint32_t one[3] = {1, 1, 1};
+    const CUresult r = f(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p),
+                         dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(DPRED_E_CUDA, "tensor map of a %lld x %lld matrix (stride %lld): driver error %d", (long long)rows,
+                         (long long)cols, (long long)ld, (int)r);
+    return DPRED_OK;
+}
+
 bool tma_able(const void* p, int64_t rows, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % 8 == 0);
 }

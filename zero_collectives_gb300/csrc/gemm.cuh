@@ -54,6 +54,15 @@ struct LinearEpi {
     int vec;      // every matrix present has 16-byte aligned rows, the bias too
 };
 
+// The same for the tile kernel, with the maps of the matrices that its
+// streaming epilogue moves (boxes of 32 rows x 128 bytes): the output, the
+// stored pre-activation, and the residual or the pre-activation that is read.
+struct TileParams {
+    LinearEpi e;
+    int stream;
+    CUtensorMap out, pre, in;
+};
+
 // One matrix of a Newton-Schulz batch as its last product writes it.
 struct FinalOut {
     void* p;
@@ -1019,27 +1028,121 @@ constexpr int kTileThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 constexpr int kPromoteBlocks = 8;
 
+//
+// Streaming epilogue (16-byte aligned matrices).  A warp owns 32 rows; a thread
+// computes one row, 32 columns at a time, straight from the tensor-memory load,
+// and packs it into a 32-row x 128-byte box of shared memory (128-byte swizzle:
+// no bank conflicts), which one bulk tensor copy writes; the copies' bounds
+// checks take care of ragged edges.  What is read per element (residual, stored
+// pre-activation) comes in as a box the same way, requested before the
+// accumulator is waited for.  fp32 accumulation is a bulk copy that adds.
+// Against writing global memory from the registers by way of an fp32 block
+// (block_epilogue, which remains for unaligned matrices), a tile of 256 x 256
+// with bias, gelu and stored pre-activation went from 15,000 cycles to less
+// than its reduction of 1024 takes (9,000).
+
 template <int BN>
 __host__ __device__ constexpr int tile_stages() {
-    return BN == 256 ? 6 : 7;
+    return BN == 256 ? 5 : 6;
 }
+constexpr uint32_t kBoxBytes = 32 * 128;         // one box
+constexpr uint32_t kWarpBytes = 2 * kBoxBytes;   // two per epilogue warp
 template <int BN>
 __host__ __device__ constexpr int tile_smem() {
-    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 8 * (int)kBlockBytes + 1024;
+    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 8 * (int)kWarpBytes + 1024;
+}
+
+// Adds the bias of 32 columns from j on (`cols` in all); every lane the same ones.
+__device__ __forceinline__ void add_bias(const LinearEpi& e, int cols, int j, float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 32; q += 8) {
+        float b[8];
+        if (j + q + 8 <= cols) {
+            if (e.bias_f32)
+                load8_f32(static_cast<const float*>(e.bias) + j + q, b);
+            else
+                load8_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j + q, b);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                b[c] = 0.0f;
+                if (j + q + c < cols)
+                    b[c] = e.bias_f32 ? static_cast<const float*>(e.bias)[j + q + c]
+                                      : load_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j + q + c);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[q + c] += b[c];
+    }
+}
+
+// 32 bf16 columns (half h of the 64 in a box) of row `lane`.
+__device__ __forceinline__ void box_put(uint32_t box, int lane, int h, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t w0 = pack_bf16x2(v[8 * q], v[8 * q + 1]), w1 = pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                       w2 = pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), w3 = pack_bf16x2(v[8 * q + 6], v[8 * q + 7]);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(box, lane, 4 * h + q)), "r"(w0), "r"(w1), "r"(w2),
+                     "r"(w3)
+                     : "memory");
+    }
+}
+
+__device__ __forceinline__ uint4 box_get(uint32_t box, int lane, int c) {
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                 : "r"(piece(box, lane, c))
+                 : "memory");
+    return q;
+}
+
+#define DPRED_EACH32(expr) _Pragma("unroll") for (int x = 0; x < 32; ++x) expr
+
+template <int KIND>
+__device__ __forceinline__ void box_activate(const LinearEpi& e, float (&v)[32]) {
+    if constexpr (KIND == KIND_ACT) {
+        if (e.act == ACT_GELU) {
+            DPRED_EACH32(v[x] = activate<ACT_GELU>(v[x]);)
+        } else if (e.act == ACT_SILU) {
+            DPRED_EACH32(v[x] = activate<ACT_SILU>(v[x]);)
+        } else if (e.act == ACT_RELU) {
+            DPRED_EACH32(v[x] = activate<ACT_RELU>(v[x]);)
+        }
+    }
+}
+
+// Residual (added) or stored pre-activation (its gradient multiplies).
+template <int KIND>
+__device__ __forceinline__ void box_combine(const LinearEpi& e, uint32_t box, int lane, int h, float (&v)[32]) {
+    uint4 q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = box_get(box, lane, 4 * h + k);
+    if constexpr (KIND == KIND_GRAD) {
+        if (e.act == ACT_GELU) {
+            DPRED_EACH32(v[x] *= activate_grad<ACT_GELU>(bf16_of(q[x / 8], x % 8));)
+        } else if (e.act == ACT_SILU) {
+            DPRED_EACH32(v[x] *= activate_grad<ACT_SILU>(bf16_of(q[x / 8], x % 8));)
+        } else {
+            DPRED_EACH32(v[x] *= activate_grad<ACT_RELU>(bf16_of(q[x / 8], x % 8));)
+        }
+    } else {
+        DPRED_EACH32(v[x] += bf16_of(q[x / 8], x % 8);)
+    }
 }
 
 template <int KIND, int BN, bool PROMOTE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::Param ep) {
+                const __grid_constant__ Args g, const __grid_constant__ TileParams tp) {
     using namespace mma;
-    const auto& e = epilogue_of(ep);
+    const LinearEpi& e = tp.e;
     constexpr int S = tile_stages<BN>();
     constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128, kStage = kA + kB;
     constexpr uint32_t kCols = 2 * BN;
     constexpr int kHalf = BN / 2;  // columns per epilogue warp
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], in_full[8][2];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1058,6 +1161,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int a = 0; a < 2; ++a) {
             tma::mbar_init(&acc_full[a], 1);
             tma::mbar_init(&acc_empty[a], 16);  // eight epilogue warps of each CTA
+            for (int w = 0; w < 8; ++w) tma::mbar_init(&in_full[w][a], 1);
         }
         tma::fence_barrier_init();
     }
@@ -1154,7 +1258,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp >= kEpilogueWarp0) {
         const int q = warp & 3, half = (warp - kEpilogueWarp0) / 4;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * kHalf;
-        const uint32_t block = base + S * kStage + (warp - kEpilogueWarp0) * kBlockBytes;
+        const uint32_t block = base + S * kStage + (warp - kEpilogueWarp0) * kWarpBytes;  // two boxes, or one block
+        uint64_t* in_bar = in_full[warp - kEpilogueWarp0];
+        uint32_t in_parity = 0;  // one bit per box
+        int used = 0;            // boxes written so far: they alternate, and at most the latest copy is still reading
         const uint32_t drained0 = map_rank(tma::smem_addr(&acc_empty[0]), 0), drained1 = map_rank(tma::smem_addr(&acc_empty[1]), 0);
         int fill = 0;
         bool ok = true;
@@ -1163,7 +1270,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int tm, tn;
             tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
             const int i = tm * 256 + (int)rank * 128 + q * 32, j = tn * BN + half * kHalf;
-            const bool mirror = g.symmetric && tn * BN >= (tm + 1) * 256;
             if constexpr (PROMOTE) {
                 float sum[kHalf / 32][32];
 #pragma unroll
@@ -1191,16 +1297,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kHalf / 32; ++c) {
                         if (j + c * 32 >= g.n) break;
-                        __syncwarp();
-                        block_put_row(block, lane, sum[c]);
-                        __syncwarp();
-                        block_epilogue<KIND>(e, g, batch, i, j + c * 32, block, lane, mirror, Ahead<KIND>());
+                        if (tp.stream) {
+                            const uint32_t box = block + (used++ & 1) * kBoxBytes;
+                            if (lane == 0) tma::bulk_wait_read<1>();  // the copy that last used this box
+                            __syncwarp();
+                            if (e.bias) add_bias(e, g.n, j + c * 32, sum[c]);
+                            block_put_row(box, lane, sum[c]);
+                            tma::fence_proxy_async_shared();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (e.accumulate)
+                                    add_box(&tp.out, box, j + c * 32, i, 0);
+                                else
+                                    store_box(&tp.out, box, j + c * 32, i, 0);
+                                tma::bulk_commit();
+                            }
+                        } else {
+                            __syncwarp();
+                            block_put_row(block, lane, sum[c]);
+                            __syncwarp();
+                            block_epilogue<KIND>(e, g, batch, i, j + c * 32, block, lane, false, Ahead<KIND>());
+                        }
                     }
                 }
             } else {
                 const int a = fill & 1;
-                Ahead<KIND> ahead;
-                load_ahead<KIND>(e, g, batch, i, j, lane, ahead);
+                const bool pre = KIND == KIND_ACT && e.pre_out;                   // box 0 holds z, box 1 y
+                const bool in = KIND == KIND_GRAD || (KIND != KIND_LINEAR && e.res);
+                auto request = [&](int c, int b) {  // lane 0: what the epilogue of columns j + 64 c reads, into its box
+                    tma::mbar_arrive_expect_tx(&in_bar[b], kBoxBytes);
+                    load_box(block + b * kBoxBytes, &tp.in, tma::smem_addr(&in_bar[b]), j + 64 * c, i, 0);
+                };
+                if (KIND != KIND_LINEAR && tp.stream && in && lane == 0 && i < g.m) {
+                    tma::bulk_wait_read<0>();
+                    for (int c = 0; c < (pre ? 1 : kHalf / 64); ++c)
+                        if (j + 64 * c < g.n) request(c, pre ? 1 : (used + c) & 1);
+                }
                 ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&acc_full[a], (fill / 2) & 1));
                 if (!ok) break;
                 ++fill;
@@ -1216,16 +1348,49 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
                     }
-                    if (i < g.m && j + c < g.n) {
+                    if (KIND != KIND_LINEAR && tp.stream) {
+                        const int c64 = c / 64, h = c / 32 % 2, b = pre ? 1 : used & 1;
+                        const uint32_t box = block + b * kBoxBytes;
+                        if (i >= g.m || j + 64 * c64 >= g.n) continue;
+                        if (h == 0) {
+                            if (lane == 0) {
+                                // the boxes' earlier copies have read them (a requested box was checked before)
+                                if (pre)
+                                    tma::bulk_wait_read<0>();
+                                else if (!in)
+                                    tma::bulk_wait_read<1>();
+                                if (in && pre && c64) request(c64, 1);
+                            }
+                            __syncwarp();
+                            if (in) {
+                                ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&in_bar[b], (in_parity >> b) & 1)) && ok;
+                                in_parity ^= 1u << b;
+                            }
+                        }
+                        if (e.bias) add_bias(e, g.n, j + c, v);
+                        if (pre) box_put(block, lane, h, v);
+                        box_activate<KIND>(e, v);
+                        if (in) box_combine<KIND>(e, box, lane, h, v);
+                        box_put(box, lane, h, v);
+                        if (h == 1) {
+                            ++used;
+                            tma::fence_proxy_async_shared();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (pre) store_box(&tp.pre, block, j + 64 * c64, i, 0);
+                                store_box(&tp.out, box, j + 64 * c64, i, 0);
+                                tma::bulk_commit();
+                            }
+                        }
+                    } else if (i < g.m && j + c < g.n) {
                         block_put_row(block, lane, v);
-                        const Ahead<KIND> now = ahead;
-                        if (c + 32 < kHalf) load_ahead<KIND>(e, g, batch, i, j + c + 32, lane, ahead);
                         __syncwarp();
-                        block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, mirror, now);
+                        block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, false, Ahead<KIND>());
                     }
                 }
             }
         }
+        if (lane == 0) tma::bulk_wait<0>();  // shared memory stays valid until its last copy is done
         if (!ok && lane == 0) record_device_error(g.err, DPRED_E_TIMEOUT);
         __syncwarp();
     }

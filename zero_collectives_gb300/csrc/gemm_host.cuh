@@ -17,6 +17,8 @@ struct Shape {
 int resident_pairs(const void* kernel, int threads, int smem);
 
 int make_map(const Operand& o, int batch, int box_rows, bool bf16, CUtensorMap* m);
+// A row-major matrix as the streaming epilogue moves it: boxes of 32 rows x 128 bytes.
+int make_box_map(const void* p, int64_t rows, int64_t cols, int64_t ld, bool fp32, CUtensorMap* m);
 bool tma_able(const void* p, int64_t rows, int64_t ld);
 int64_t tiles_of(const Args& a, int bm, int bn);
 Shape choose_shape(const Args& a, bool fp32);
@@ -64,7 +66,7 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Par
 }
 
 template <int KIND, int BN, bool PROMOTE>
-int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
+int launch_tiles(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s) {
     static bool attr[64] = {};
     auto kernel = tile_kernel<KIND, BN, PROMOTE>;
     cudaError_t err = ensure_smem_attr(kernel, tile_smem<BN>(), attr);
@@ -74,6 +76,18 @@ int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Par
     if (rc != DPRED_OK) return rc;
     rc = make_map(p.b, p.args.batch, BN / 2, p.args.bf16, &mb);
     if (rc != DPRED_OK) return rc;
+    TileParams t = {};
+    t.e = e;
+    // what the streaming epilogue covers; block_epilogue does the rest
+    t.stream = e.vec && (KIND == KIND_F32 ? !e.z && !e.res && !e.pre_out && !e.act : KIND != KIND_LINEAR && !(e.res && e.z));
+    if (t.stream) {
+        rc = make_box_map(e.out, p.args.m, p.args.n, e.o_ld, e.out_f32, &t.out);
+        if (rc == DPRED_OK && e.pre_out) rc = make_box_map(e.pre_out, p.args.m, p.args.n, e.p_ld, false, &t.pre);
+        if (rc == DPRED_OK && (e.res || e.z))
+            rc = e.z ? make_box_map(e.z, p.args.m, p.args.n, e.z_ld, false, &t.in)
+                     : make_box_map(e.res, p.args.m, p.args.n, e.r_ld, false, &t.in);
+        if (rc != DPRED_OK) return rc;
+    }
     Args g = p.args;
     g.tiles_m = (g.m + 255) / 256;
     g.tiles_n = (g.n + BN - 1) / BN;
@@ -96,7 +110,7 @@ int launch_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Par
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, g, e);
+    err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, g, t);
     return err == cudaSuccess ? DPRED_OK : cuda_error(err, "matrix product launch");
 }
 

@@ -131,6 +131,25 @@ __device__ __forceinline__ void load_box_pair(uint32_t dst, const CUtensorMap* m
         : "memory");
 }
 
+// A box from shared memory to a 3-d tensor (elements outside it are not
+// written), or added to it: part of this thread's bulk group.  Coordinates are
+// never negative and the innermost one is a multiple of 128 bytes.
+__device__ __forceinline__ void store_box(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(m)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void add_box(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(m)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 // ------------------------------------------------------------ tensor memory --
 
 // Allocates columns (a power of two, at least 32) and gives up the right to
