@@ -1052,27 +1052,28 @@ __host__ __device__ constexpr int tile_smem() {
     return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 8 * (int)kWarpBytes + 1024;
 }
 
-// Adds the bias of 32 columns from j on (`cols` in all); every lane the same ones.
-__device__ __forceinline__ void add_bias(const LinearEpi& e, int cols, int j, float (&v)[32]) {
+#define DPRED_EACH32(expr) _Pragma("unroll") for (int x = 0; x < 32; ++x) expr
+
+// The bias of 32 columns from j on (`cols` in all), every lane the same ones.
+// Loaded before the accumulators are waited for, without a test per column: read
+// where it is added, it cost as much as the gelu.
+__device__ __forceinline__ void load_bias(const LinearEpi& e, int cols, int j, float (&b)[32]) {
+    if (!e.bias) {
+        DPRED_EACH32(b[x] = 0.0f;)
+    } else if (j + 32 <= cols && !e.bias_f32) {
+        uint4 q[4];
 #pragma unroll
-    for (int q = 0; q < 32; q += 8) {
-        float b[8];
-        if (j + q + 8 <= cols) {
-            if (e.bias_f32)
-                load8_f32(static_cast<const float*>(e.bias) + j + q, b);
-            else
-                load8_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j + q, b);
-        } else {
+        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.bias) + j + 8 * k);
+        DPRED_EACH32(b[x] = bf16_of(q[x / 8], x % 8);)
+    } else if (j + 32 <= cols) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                b[c] = 0.0f;
-                if (j + q + c < cols)
-                    b[c] = e.bias_f32 ? static_cast<const float*>(e.bias)[j + q + c]
-                                      : load_bf16(static_cast<const __nv_bfloat16*>(e.bias) + j + q + c);
-            }
+        for (int k = 0; k < 8; ++k) {
+            const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + j + 4 * k);
+            b[4 * k] = q.x; b[4 * k + 1] = q.y; b[4 * k + 2] = q.z; b[4 * k + 3] = q.w;
         }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[q + c] += b[c];
+    } else {  // clamped to the last column: what lies past it is never stored
+        DPRED_EACH32(b[x] = e.bias_f32 ? static_cast<const float*>(e.bias)[min(j + x, cols - 1)]
+                                       : load_bf16(static_cast<const __nv_bfloat16*>(e.bias) + min(j + x, cols - 1));)
     }
 }
 
@@ -1096,8 +1097,6 @@ __device__ __forceinline__ uint4 box_get(uint32_t box, int lane, int c) {
                  : "memory");
     return q;
 }
-
-#define DPRED_EACH32(expr) _Pragma("unroll") for (int x = 0; x < 32; ++x) expr
 
 template <int KIND>
 __device__ __forceinline__ void box_activate(const LinearEpi& e, float (&v)[32]) {
@@ -1301,7 +1300,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             const uint32_t box = block + (used++ & 1) * kBoxBytes;
                             if (lane == 0) tma::bulk_wait_read<1>();  // the copy that last used this box
                             __syncwarp();
-                            if (e.bias) add_bias(e, g.n, j + c * 32, sum[c]);
+                            if (e.bias) {
+                                float bias[32];
+                                load_bias(e, g.n, j + c * 32, bias);
+                                DPRED_EACH32(sum[c][x] += bias[x];)
+                            }
                             block_put_row(box, lane, sum[c]);
                             tma::fence_proxy_async_shared();
                             __syncwarp();
@@ -1339,8 +1342,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 fence_after();
 #pragma unroll 1
                 for (int c = 0; c < kHalf; c += 32) {
-                    float v[32];
+                    float v[32], bias[32];
                     __syncwarp();
+                    if (KIND != KIND_LINEAR && tp.stream) load_bias(e, g.n, min(j + c, g.n - 1), bias);
                     tmem_ld32(lanes + a * BN + c, v);
                     tmem_wait_ld();
                     if (c + 32 == kHalf) {  // the accumulator is in registers: the next tile may overwrite it
@@ -1367,7 +1371,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 in_parity ^= 1u << b;
                             }
                         }
-                        if (e.bias) add_bias(e, g.n, j + c, v);
+                        DPRED_EACH32(v[x] += bias[x];)
                         if (pre) box_put(block, lane, h, v);
                         box_activate<KIND>(e, v);
                         if (in) box_combine<KIND>(e, box, lane, h, v);
