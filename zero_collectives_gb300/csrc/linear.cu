@@ -17,21 +17,31 @@ namespace {
 // copied once into the workspace with its rows padded to 8 elements: 2 bytes
 // read and 2 written per element, against 2 * (the other side) flops per
 // element of the product.
-__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows,
-                                                   int64_t cols, uint16_t* __restrict__ dst, int64_t ldd) {
+struct PackJob {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t ld, rows, cols, ldd;
+};
+
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackJob first, const __grid_constant__ PackJob second,
+                                                   int first_blocks) {
+    const bool one = (int)blockIdx.x < first_blocks;
+    const PackJob& j = one ? first : second;
+    const int64_t block = one ? blockIdx.x : blockIdx.x - first_blocks;
+    const int64_t blocks = one ? first_blocks : (int64_t)gridDim.x - first_blocks;
+    const int64_t per = j.ldd / 8, total = j.rows * per, step = blocks * 256;
     mma::grid_launch_dependents();
     mma::grid_wait();
-    const int64_t per = ldd / 8, total = rows * per, step = (int64_t)gridDim.x * 256;
-    for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < total; v += step) {
+    for (int64_t v = block * 256 + threadIdx.x; v < total; v += step) {
         const int64_t r = v / per, c = (v - r * per) * 8;
-        const uint16_t* p = src + r * ld + c;
+        const uint16_t* p = j.src + r * j.ld + c;
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = c + 2 * k < cols ? p[2 * k] : 0, hi = c + 2 * k + 1 < cols ? p[2 * k + 1] : 0;
+            const uint32_t lo = c + 2 * k < j.cols ? p[2 * k] : 0, hi = c + 2 * k + 1 < j.cols ? p[2 * k + 1] : 0;
             w[k] = lo | (hi << 16);
         }
-        *reinterpret_cast<uint4*>(dst + r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(j.dst + r * j.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -43,20 +53,34 @@ size_t pack_need(const void* p, int64_t rows, int64_t cols, int64_t ld) {
     return tma_able(p, rows, ld) ? 0 : packed_bytes(rows, cols);
 }
 
-int pack(Operand& o, char*& ws, cudaStream_t s) {
-    if (tma_able(o.p, o.rows, o.ld)) return DPRED_OK;
-    const int64_t ldd = round8(o.cols), items = o.rows * (ldd / 8);
-    int64_t grid = (items + 255) / 256;
+// Packs the operands that need it, in one launch.
+int pack(Operand* const (&ops)[2], char* ws, cudaStream_t s) {
+    PackJob jobs[2] = {};
+    int64_t blocks[2] = {0, 0};
     const int64_t most = (int64_t)sm_count() * 16;
-    if (grid > most) grid = most;
-    pack_kernel<<<(unsigned)grid, 256, 0, s>>>(static_cast<const uint16_t*>(o.p), o.ld, o.rows, o.cols,
-                                               reinterpret_cast<uint16_t*>(ws), ldd);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_error(e, "operand packing launch");
-    o.p = ws;
-    o.ld = ldd;
-    ws += packed_bytes(o.rows, o.cols);
-    return DPRED_OK;
+    for (int k = 0; k < 2; ++k) {
+        Operand& o = *ops[k];
+        if (tma_able(o.p, o.rows, o.ld)) continue;
+        const int64_t ldd = round8(o.cols);
+        jobs[k] = {static_cast<const uint16_t*>(o.p), reinterpret_cast<uint16_t*>(ws), o.ld, o.rows, o.cols, ldd};
+        blocks[k] = (o.rows * (ldd / 8) + 255) / 256;
+        if (blocks[k] > most) blocks[k] = most;
+        o.p = ws;
+        o.ld = ldd;
+        ws += packed_bytes(o.rows, o.cols);
+    }
+    if (blocks[0] + blocks[1] == 0) return DPRED_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks[0] + blocks[1]));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, pack_kernel, jobs[0], jobs[1], (int)blocks[0]);
+    return e == cudaSuccess ? DPRED_OK : cuda_error(e, "operand packing launch");
 }
 
 // ------------------------------------------------------------- bias gradient --
@@ -170,11 +194,9 @@ int launch(Operand a, Operand b, int64_t red, const LinearEpi& e, void* workspac
         return set_error(DPRED_E_ALIGN, "workspace is not 16-byte aligned");
     Plan p = {};
     p.args.err = device_error_word();
-    char* ws = static_cast<char*>(workspace);
     if (red > 0) {
-        int rc = pack(a, ws, s);
-        if (rc != DPRED_OK) return rc;
-        rc = pack(b, ws, s);
+        Operand* const both[2] = {&a, &b};
+        const int rc = pack(both, static_cast<char*>(workspace), s);
         if (rc != DPRED_OK) return rc;
     }
     p.a = a;

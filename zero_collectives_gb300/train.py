@@ -106,12 +106,17 @@ def _workspace(need: int, given, stream):
     return ws, ws.data_ptr(), need
 
 
-def _pack_space(L, a, ar, ac, lda, b, br, bc, ldb, given, stream):
-    """Workspace of a product: only operands without 16-byte aligned rows need one."""
-    if given is None and not (a % 16 or b % 16 or (ar > 1 and lda % 8) or (br > 1 and ldb % 8)):
-        return None, 0, 0
-    return _workspace(L.dpred_linear_workspace_bytes(a, ar, ac, lda, b, br, bc, ldb) if given is None else 0, given,
-                      stream)
+def _pack_space(a, ar, ac, lda, b, br, bc, ldb, given, stream):
+    """Workspace of a product: only operands without 16-byte aligned rows need
+    one (the sizes of dpred_linear_workspace_bytes)."""
+    if given is not None:
+        return _workspace(0, given, stream)
+    need = 0
+    if a % 16 or (ar > 1 and lda % 8):
+        need = (ar * (ac + 7 & -8) * 2 + 255) & -256
+    if b % 16 or (br > 1 and ldb % 8):
+        need += (br * (bc + 7 & -8) * 2 + 255) & -256
+    return _workspace(need, None, stream) if need else (None, 0, 0)
 
 
 _fn: dict = {}
@@ -160,7 +165,7 @@ def linear(x, w, bias=None, act="none", residual=None, preact=None, out=None, ou
         pp, ldp, _, _ = _matrix(preact, "preact", _BF, dev, m, n)
     if bias is not None:
         bp, bdt = _vector(bias, "bias", _OK, dev, n), _code(bias)
-    ws, wsp, wsb = _pack_space(_zc.lib(), xp, m, k, ldx, wp, n, k, ldw, workspace, stream)
+    ws, wsp, wsb = _pack_space(xp, m, k, ldx, wp, n, k, ldw, workspace, stream)
     _call("linear", m, n, k, xp, ldx, wp, ldw, bdt, bp, a, rp, ldr, pp, ldp, _code(out), yp, ldy, wsp, wsb,
           _zc._stream(stream))
     return out
@@ -186,7 +191,7 @@ def linear_dgrad(dy, w, preact=None, act="none", residual=None, out=None, out_dt
         zp, ldz, _, _ = _matrix(preact, "preact", _BF, dev, m, k)
     if residual is not None:
         rp, ldr, _, _ = _matrix(residual, "residual", _BF, dev, m, k)
-    ws, wsp, wsb = _pack_space(_zc.lib(), dp, m, n, ldd, wp, n, k, ldw, workspace, stream)
+    ws, wsp, wsb = _pack_space(dp, m, n, ldd, wp, n, k, ldw, workspace, stream)
     _call("linear_dgrad", m, n, k, dp, ldd, wp, ldw, a, zp, ldz, rp, ldr, _code(out), op, ldo, wsp, wsb,
           _zc._stream(stream))
     return out
@@ -202,7 +207,7 @@ def linear_wgrad(dy, x, out, bias_grad=None, accumulate: bool = False, workspace
     xp, ldx, _, k = _matrix(x, "x", _BF, dev, m, None)
     op, ldo, _, _ = _matrix(out, "out", _OK, dev, n, k)
     bp = 0 if bias_grad is None else _vector(bias_grad, "bias_grad", _OK[1:], dev, n)
-    ws, wsp, wsb = _pack_space(_zc.lib(), dp, m, n, ldd, xp, m, k, ldx, workspace, stream)
+    ws, wsp, wsb = _pack_space(dp, m, n, ldd, xp, m, k, ldx, workspace, stream)
     _call("linear_wgrad", m, n, k, dp, ldd, xp, ldx, 1 if accumulate else 0, _code(out), op, ldo, bp, wsp, wsb,
           _zc._stream(stream))
     return out
