@@ -498,7 +498,8 @@ int dpred_accumulator_restore(int32_t world, int64_t n, float* acc, const float*
  *       bias_grad [n] fp32 or NULL.
  *
  * An empty reduction (k = 0, or n = 0 in dgrad, m = 0 in wgrad) gives the
- * epilogue of zero.  gelu is the tanh form.  residual may be the output itself
+ * epilogue of zero.  gelu is the tanh form.  Sums added to an fp32 dw may
+ * flush results below 2^-126 to zero.  residual may be the output itself
  * (same type and stride); no output may otherwise overlap an input.
  * workspace (device, 16-byte aligned): dpred_linear_workspace_bytes() of the
  * two operands (x and w; dy and w; dy and x), usually 0; it may be reused as
@@ -541,9 +542,9 @@ int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t 
  *     with X as above.  Weights are bf16 or fp32 (w_dtype), gradients bf16 or
  *     fp32 (g_dtype), momenta fp32; momentum and weight are updated in place.
  *
- * The products run on 16-bit operands (fp16, with the dominant parts kept in
- * fp32): X is within about 1e-3 (2-norm, relative) of the exact iteration, so
- * an fp32 out carries that accuracy too.  Norms, sums and accumulators are
+ * The products run on 16-bit operands (fp16, with the dominant parts kept
+ * apart in more bits): X is within about 1e-3 (2-norm, relative) of the exact
+ * iteration, so an fp32 out carries that accuracy too.  Norms, sums and accumulators are
  * fp32: |G|_F must be below about 1e19.  A matrix with a NaN or an infinity
  * gives an update of NaNs; other matrices of the call are not affected.  A
  * zero matrix gives zero.  The order of every sum is fixed by the sizes and

@@ -1037,19 +1037,25 @@ constexpr int kPromoteBlocks = 8;
 // pre-activation) comes in as a box the same way, requested before the
 // accumulator is waited for.  fp32 accumulation is a bulk copy that adds.
 // Against writing global memory from the registers by way of an fp32 block
-// (block_epilogue, which remains for unaligned matrices), a tile of 256 x 256
-// with bias, gelu and stored pre-activation went from 15,000 cycles to less
-// than its reduction of 1024 takes (9,000).
+// (block_epilogue, which remains for unaligned matrices), a plain tile's
+// epilogue went from 7,000 cycles to 2,800.  Beyond a reduction of about 1024
+// (9,500 cycles) the tile is bound by its operands: 512 KB a CTA at the 64 bytes
+// a cycle that reach an SM, which the output and what the epilogue reads share.
+
+//
+// One box per warp: the reduction's pipeline needs the rest of the shared
+// memory more (8192 x 8192 x 1024 with relu: 4 stages and three boxes 92 us,
+// 6 stages and one box 84 us).
 
 template <int BN>
 __host__ __device__ constexpr int tile_stages() {
-    return BN == 256 ? 5 : 6;
+    return BN == 256 ? 6 : 8;
 }
-constexpr uint32_t kBoxBytes = 32 * 128;         // one box
-constexpr uint32_t kWarpBytes = 2 * kBoxBytes;   // two per epilogue warp
+constexpr uint32_t kBoxBytes = 32 * 128;
+static_assert(kBoxBytes == kBlockBytes, "a warp's box and its block share memory");
 template <int BN>
 __host__ __device__ constexpr int tile_smem() {
-    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 8 * (int)kWarpBytes + 1024;
+    return tile_stages<BN>() * (128 * 128 + BN / 2 * 128) + 8 * (int)kBoxBytes + 1024;
 }
 
 #define DPRED_EACH32(expr) _Pragma("unroll") for (int x = 0; x < 32; ++x) expr
@@ -1141,7 +1147,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t kCols = 2 * BN;
     constexpr int kHalf = BN / 2;  // columns per epilogue warp
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], in_full[8][2];
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], in_full[8];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1160,8 +1166,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int a = 0; a < 2; ++a) {
             tma::mbar_init(&acc_full[a], 1);
             tma::mbar_init(&acc_empty[a], 16);  // eight epilogue warps of each CTA
-            for (int w = 0; w < 8; ++w) tma::mbar_init(&in_full[w][a], 1);
         }
+        for (int w = 0; w < 8; ++w) tma::mbar_init(&in_full[w], 1);
         tma::fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<2>(tma::smem_addr(&tmem_slot), kCols);
@@ -1257,10 +1263,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp >= kEpilogueWarp0) {
         const int q = warp & 3, half = (warp - kEpilogueWarp0) / 4;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * kHalf;
-        const uint32_t block = base + S * kStage + (warp - kEpilogueWarp0) * kWarpBytes;  // two boxes, or one block
-        uint64_t* in_bar = in_full[warp - kEpilogueWarp0];
-        uint32_t in_parity = 0;  // one bit per box
-        int used = 0;            // boxes written so far: they alternate, and at most the latest copy is still reading
+        const uint32_t box = base + S * kStage + (warp - kEpilogueWarp0) * kBoxBytes;
+        uint64_t* in_bar = &in_full[warp - kEpilogueWarp0];
+        uint32_t in_parity = 0;
         const uint32_t drained0 = map_rank(tma::smem_addr(&acc_empty[0]), 0), drained1 = map_rank(tma::smem_addr(&acc_empty[1]), 0);
         int fill = 0;
         bool ok = true;
@@ -1297,8 +1302,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int c = 0; c < kHalf / 32; ++c) {
                         if (j + c * 32 >= g.n) break;
                         if (tp.stream) {
-                            const uint32_t box = block + (used++ & 1) * kBoxBytes;
-                            if (lane == 0) tma::bulk_wait_read<1>();  // the copy that last used this box
+                            if (lane == 0) tma::bulk_wait_read<0>();  // the copy that last used the box
                             __syncwarp();
                             if (e.bias) {
                                 float bias[32];
@@ -1317,79 +1321,101 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             }
                         } else {
                             __syncwarp();
-                            block_put_row(block, lane, sum[c]);
+                            block_put_row(box, lane, sum[c]);
                             __syncwarp();
-                            block_epilogue<KIND>(e, g, batch, i, j + c * 32, block, lane, false, Ahead<KIND>());
+                            block_epilogue<KIND>(e, g, batch, i, j + c * 32, box, lane, false, Ahead<KIND>());
                         }
                     }
                 }
             } else {
                 const int a = fill & 1;
-                const bool pre = KIND == KIND_ACT && e.pre_out;                   // box 0 holds z, box 1 y
+                const bool stream = KIND != KIND_LINEAR && tp.stream;
+                const bool pre = KIND == KIND_ACT && e.pre_out;
                 const bool in = KIND == KIND_GRAD || (KIND != KIND_LINEAR && e.res);
-                auto request = [&](int c, int b) {  // lane 0: what the epilogue of columns j + 64 c reads, into its box
-                    tma::mbar_arrive_expect_tx(&in_bar[b], kBoxBytes);
-                    load_box(block + b * kBoxBytes, &tp.in, tma::smem_addr(&in_bar[b]), j + 64 * c, i, 0);
+                auto request = [&](int col) {  // lane 0: what the epilogue of 64 columns from here reads, into the box
+                    tma::mbar_arrive_expect_tx(in_bar, kBoxBytes);
+                    load_box(box, &tp.in, tma::smem_addr(in_bar), col, i, 0);
                 };
-                if (KIND != KIND_LINEAR && tp.stream && in && lane == 0 && i < g.m) {
-                    tma::bulk_wait_read<0>();
-                    for (int c = 0; c < (pre ? 1 : kHalf / 64); ++c)
-                        if (j + 64 * c < g.n) request(c, pre ? 1 : (used + c) & 1);
+                auto arrived = [&]() {
+                    ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(in_bar, in_parity)) && ok;
+                    in_parity ^= 1;
+                };
+                auto send = [&](const CUtensorMap* map, int col) {  // the box, complete, to its matrix
+                    tma::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store_box(map, box, col, i, 0);
+                        tma::bulk_commit();
+                    }
+                };
+                auto box_free = [&]() {  // the copies sent have read the box
+                    if (lane == 0) tma::bulk_wait_read<0>();
+                    __syncwarp();
+                };
+                if (stream && in && !pre && i < g.m && j < g.n) {
+                    box_free();
+                    if (lane == 0) request(j);
                 }
                 ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&acc_full[a], (fill / 2) & 1));
                 if (!ok) break;
                 ++fill;
                 fence_after();
+                if (stream) {
 #pragma unroll 1
-                for (int c = 0; c < kHalf; c += 32) {
-                    float v[32], bias[32];
-                    __syncwarp();
-                    if (KIND != KIND_LINEAR && tp.stream) load_bias(e, g.n, min(j + c, g.n - 1), bias);
-                    tmem_ld32(lanes + a * BN + c, v);
-                    tmem_wait_ld();
-                    if (c + 32 == kHalf) {  // the accumulator is in registers: the next tile may overwrite it
-                        fence_before();
+                    for (int c = 0; c < kHalf; c += 64) {
+                        const int col = j + c;
+                        const bool live = i < g.m && col < g.n;  // the same in the whole warp
+                        float v[2][32], bias[32];
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
+                        if (live) load_bias(e, g.n, col, bias);
+                        tmem_ld32(lanes + a * BN + c, v[0]);
+                        tmem_ld32(lanes + a * BN + c + 32, v[1]);
+                        tmem_wait_ld();
+                        if (c + 64 == kHalf) {  // the accumulator is in registers: the next tile may overwrite it
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
+                        }
+                        if (!live) continue;
+                        DPRED_EACH32(v[0][x] += bias[x];)
+                        load_bias(e, g.n, min(col + 32, g.n - 1), bias);
+                        DPRED_EACH32(v[1][x] += bias[x];)
+                        if (pre) {
+                            box_free();
+                            box_put(box, lane, 0, v[0]);
+                            box_put(box, lane, 1, v[1]);
+                            send(&tp.pre, col);
+                        }
+                        box_activate<KIND>(e, v[0]);
+                        box_activate<KIND>(e, v[1]);
+                        if (!in || pre || c) box_free();  // (a box requested before the accumulator is not in use)
+                        if (in) {
+                            if ((pre || c) && lane == 0) request(col);
+                            arrived();
+                            box_combine<KIND>(e, box, lane, 0, v[0]);
+                            box_combine<KIND>(e, box, lane, 1, v[1]);
+                        }
+                        box_put(box, lane, 0, v[0]);
+                        box_put(box, lane, 1, v[1]);
+                        send(&tp.out, col);
                     }
-                    if (KIND != KIND_LINEAR && tp.stream) {
-                        const int c64 = c / 64, h = c / 32 % 2, b = pre ? 1 : used & 1;
-                        const uint32_t box = block + b * kBoxBytes;
-                        if (i >= g.m || j + 64 * c64 >= g.n) continue;
-                        if (h == 0) {
-                            if (lane == 0) {
-                                // the boxes' earlier copies have read them (a requested box was checked before)
-                                if (pre)
-                                    tma::bulk_wait_read<0>();
-                                else if (!in)
-                                    tma::bulk_wait_read<1>();
-                                if (in && pre && c64) request(c64, 1);
-                            }
-                            __syncwarp();
-                            if (in) {
-                                ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&in_bar[b], (in_parity >> b) & 1)) && ok;
-                                in_parity ^= 1u << b;
-                            }
-                        }
-                        DPRED_EACH32(v[x] += bias[x];)
-                        if (pre) box_put(block, lane, h, v);
-                        box_activate<KIND>(e, v);
-                        if (in) box_combine<KIND>(e, box, lane, h, v);
-                        box_put(box, lane, h, v);
-                        if (h == 1) {
-                            ++used;
-                            tma::fence_proxy_async_shared();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (pre) store_box(&tp.pre, block, j + 64 * c64, i, 0);
-                                store_box(&tp.out, box, j + 64 * c64, i, 0);
-                                tma::bulk_commit();
-                            }
-                        }
-                    } else if (i < g.m && j + c < g.n) {
-                        block_put_row(block, lane, v);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kHalf; c += 32) {
+                        float v[32];
                         __syncwarp();
-                        block_epilogue<KIND>(e, g, batch, i, j + c, block, lane, false, Ahead<KIND>());
+                        tmem_ld32(lanes + a * BN + c, v);
+                        tmem_wait_ld();
+                        if (c + 32 == kHalf) {
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(a ? drained1 : drained0);
+                        }
+                        if (i < g.m && j + c < g.n) {
+                            block_put_row(box, lane, v);
+                            __syncwarp();
+                            block_epilogue<KIND>(e, g, batch, i, j + c, box, lane, false, Ahead<KIND>());
+                        }
                     }
                 }
             }

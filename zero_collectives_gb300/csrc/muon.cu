@@ -769,6 +769,7 @@ extern "C" int dpred_muon_step(const dpred_muon_matrix* mats, int32_t n, int32_t
                 (rc = check_matrix(m.momentum, m.rows, m.cols, m.ldm, 4, "momentum")) != DPRED_OK ||
                 (rc = check_matrix(m.grad, m.rows, m.cols, m.ldg, gs, "grad")) != DPRED_OK)
                 return rc;
+            if (m.reserved != 0) return set_error(DPRED_E_INVAL, "a matrix's reserved field is not 0");
             if (!std::isfinite(m.scale)) return set_error(DPRED_E_INVAL, "a matrix's scale is not finite");
             Item& it = items[k];
             it.in = {m.grad, m.momentum, m.ldg, m.ldm, 0, 0, 0};

@@ -9,8 +9,8 @@
 //           band of rows in rank order and sending the result to all;
 //   poly    every CTA computes the whole 128 x 128 polynomial;
 //   apply   every CTA updates its own columns in place.
-// The arithmetic is that of the general path (muon.cu), except that X is kept
-// in fp32: a thread owns the same row and columns in every step, so X stays in
+// The arithmetic is that of the general path (muon.cu), except that X's second
+// term is the rest of it in fp32: a thread owns the same row and columns in every step, so X stays in
 // its registers and only the fp16 operand goes through shared memory.
 // Operand tiles lie in the 128-byte swizzle, 64 columns wide: the same bytes
 // serve the Gram product as K-major rows and the apply product as an MN-major
