@@ -233,6 +233,28 @@ def test_streams_and_graph():
     assert torch.equal(out, zc.linear(x, w, act="gelu"))
 
 
+def test_packed_operands_from_several_threads_and_streams():
+    """Unaligned operands are packed into memory that no other thread or stream uses at the same time."""
+    import threading
+    m, n, k = 300, 200, 777
+    cases = [(randn(m + i, k, seed=10 + i), randn(n, k, seed=20 + i)) for i in range(4)]
+    want = [zc.linear(x, w) for x, w in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+
+    def work(i):
+        x, w = cases[i]
+        for _ in range(20):
+            got[i].append(zc.linear(x, w, stream=streams[i % 2]))  # two threads share a stream
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(len(cases)) for y in got[i])
+
+
 def test_output_offsets_beyond_32_bits():
     m, n, k = 22000, 98304, 64   # 2.16e9 outputs
     x, w = randn(m, k, seed=1), randn(n, k, seed=2)

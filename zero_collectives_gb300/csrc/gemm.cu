@@ -111,23 +111,24 @@ int resident_pairs(const void* kernel, int threads, int smem) {
 // kernels: a start, then waves of tiles, each reduction block costing what its
 // copies and matrix instructions take and each tile its epilogue (which the
 // tile kernel hides behind the next tile's reduction).  The constants were
-// fitted to 1000 timings of every kernel on 95 shapes from 1 to 16384 rows and
-// 256 to 8192 columns (forward, dgrad, wgrad; bf16 and fp32 results); the
-// choice by these estimates is 4% slower on average than the best kernel of each.
+// fitted to the timings of every kernel on 122 shapes from 1 to 16384 rows and
+// 256 to 32768 columns (forward, dgrad, wgrad; bf16 and fp32 results); on those
+// the choice by these estimates is 1.2% slower on average than the best kernel
+// of each, 18% at most (1024 x 1024 x 1024: 9.0 us against 7.8).
 static double split_time(const Args& a, int bn, int split, int sms) {
     const double start = bn == 32 ? 0.6 : bn == 64 ? 2.0 : 1.2;
-    const double block = bn == 32 ? 0.23 : bn == 64 ? 0.25 : 0.335, epilogue = bn == 32 ? 2.3 : bn == 64 ? 2.6 : 5.1;
+    const double block = bn == 32 ? 0.23 : bn == 64 ? 0.289 : 0.375, epilogue = bn == 32 ? 2.26 : bn == 64 ? 2.44 : 5.1;
     const double ctas = (double)tiles_of(a, 128, bn) * a.batch * split;
     const double per_wave = split_alone(ctas, split, sms) ? sms : 2 * sms;
     double load = (ctas < 2 * sms ? ctas : 2 * sms) / sms;  // CTAs per SM, sharing its bandwidth and issue slots
     if (load < 1) load = 1;
-    const double join = split == 1 ? 0.0 : split < 8 ? 1.75 : 2.9;
+    const double join = split == 1 ? 0.0 : split < 8 ? 1.85 : 2.9;
     return 0.6 + start + std::ceil(ctas / per_wave) * (a.kblocks / (double)split * block * std::pow(load, 0.23) + epilogue * load) + join;
 }
 
 static double tile_time(const Args& a, int bn, bool fp32, int pairs) {
-    const double start = bn == 128 ? 3.3 : 2.9, block = bn == 128 ? 0.262 : 0.313;
-    const double epilogue = (bn == 128 ? 1.1 : 3.3) * (fp32 ? 2.5 : 1.0), reduction = a.kblocks * block;
+    const double start = bn == 128 ? 3.6 : 2.9, block = bn == 128 ? 0.248 : 0.313;
+    const double epilogue = (bn == 128 ? 1.6 : 2.42) * (fp32 ? 2.5 : 1.0), reduction = a.kblocks * block;
     const double waves = std::ceil((double)tiles_of(a, 256, bn) * a.batch / pairs);
     return start + (waves - 1) * (reduction > epilogue ? reduction : epilogue) + reduction + epilogue;
 }

@@ -1021,9 +1021,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 // elements).  Here an accumulator takes kPromoteBlocks reduction blocks (512
 // elements, 6e-7) and the epilogue threads add it to fp32 registers.
 
-// Twelve warps: producer, issuer (two more idle), eight of the epilogue.  The
-// epilogue holds up to 128 accumulators a thread: the control warps hand their
-// registers over (168 each at launch: 128 * 56 + 256 * 224 = 384 * 168).
+// Twelve warps: producer, issuer (two more idle), eight of the epilogue.
 constexpr int kTileThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 constexpr int kPromoteBlocks = 8;

@@ -94,16 +94,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Registers per thread of this warpgroup from here on: up from, or down to
-// less than, the launch's share.  Executed by all of its warps.
-template <int N, bool UP>
-__device__ __forceinline__ void set_registers() {
-    if constexpr (UP)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ------------------------------------------------------------- tensor maps --
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
