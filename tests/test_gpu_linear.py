@@ -152,6 +152,26 @@ def test_linear_wgrad(m, n, k, dtype, accumulate):
     assert zc.device_status() == 0
 
 
+@pytest.mark.parametrize("m,n,k", [(1500, 700, 1000), (700, 4000, 1100), (640, 72, 5000), (333, 333, 2100), (6000, 1024, 1024), (64, 2048, 4096)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad,accumulate", [(0, False), (3, True)])
+def test_bias_gradient_beside_many_tiles(m, n, k, dtype, pad, accumulate):
+    """Every column of dy counts once, whatever kernel sums it, and a repeated call has the same bits."""
+    dy, x = randn(m, n, seed=1, pad=pad), randn(m, k, seed=2)
+    dw0, db0 = randn(n, k, seed=3, dtype=dtype), randn(1, n, seed=4, dtype=torch.float32)[0]
+    got = []
+    for want_db in (True, True, False):
+        dw, db = dw0.clone(), db0.clone()
+        zc.linear_wgrad(dy, x, dw, bias_grad=db if want_db else None, accumulate=accumulate)
+        got.append((dw, db))
+    close(got[0][1], dy.double().sum(0) + db0.double() * accumulate, dy.double().abs().sum(0) + db0.double().abs() * accumulate, m)
+    for dw, _ in got:
+        close(dw, dy.double().T @ x.double() + dw0.double() * accumulate,
+              dy.double().abs().T @ x.double().abs() + dw0.double().abs() * accumulate, m)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]) and torch.equal(got[2][1], db0)
+    assert zc.device_status() == 0
+
+
 def test_wgrad_into_gradient_rows():
     """Gradients land in the [W, n] row a flush reads, at an odd offset, and nothing else is touched."""
     m, n, k, off = 300, 40, 56, 13

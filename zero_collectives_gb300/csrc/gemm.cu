@@ -137,12 +137,14 @@ bool split_alone(double ctas, int split, int sms) { return ctas <= (split < 8 ? 
 
 static Shape choose(const Args& a, bool fp32, double& t) {
     const int sms = sm_count();
+    // the launch that forms the row sums beside a split product: 3 us and A at 4.8 TB/s
+    const double apart = a.row_sums ? 3.0 + (double)a.m * a.kblocks * mma::kBlockK * 2 / 4.8e6 : 0.0;
     Shape best = {};
     t = 1e30;
     for (int bn = 32; bn <= 128; bn *= 2) {
         if (bn == 32 && a.b_mn) continue;  // MN-major copies are 64 columns wide
         for (int split = 1; split <= 8 && (split == 1 || split <= a.kblocks); split *= 2) {
-            const double u = split_time(a, bn, split, sms);
+            const double u = split_time(a, bn, split, sms) + apart;
             if (u < t) {
                 t = u;
                 best = {false, bn, split, tiles_of(a, 128, bn) * a.batch};

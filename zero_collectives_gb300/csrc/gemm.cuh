@@ -60,8 +60,12 @@ struct LinearEpi {
 struct TileParams {
     LinearEpi e;
     int stream;
+    float* row_sum;    // sums of A's rows over the reduction (a bias gradient), null: not wanted
+    int row_sum_add;   // added to what is there
     CUtensorMap out, pre, in;
 };
+// The kinds a weight gradient takes, whose tile kernels can sum A's rows as well.
+__host__ __device__ constexpr bool sums_rows(int kind) { return kind == KIND_LINEAR || kind == KIND_PLAIN || kind == KIND_F32; }
 
 // One matrix of a Newton-Schulz batch as its last product writes it.
 struct FinalOut {
@@ -111,6 +115,7 @@ struct Args {
     int symmetric;       // only elements i <= j are needed (the epilogue mirrors them)
     int a_mn, b_mn;      // operand majors
     int split_only;    // split kernel only (a swapped epilogue, a Newton-Schulz product)
+    int row_sums;      // the sums of A's rows are wanted too: the tile kernel forms them, else a launch of its own
     int split;           // CTAs of a cluster that share the reduction
     int stages;          // split kernel: pipeline stages
     int regions;         // split kernel: accumulators that share a CTA's part of the reduction
@@ -1021,7 +1026,21 @@ __global__ void __launch_bounds__(kSplitThreads)
 // elements).  Here an accumulator takes kPromoteBlocks reduction blocks (512
 // elements, 6e-7) and the epilogue threads add it to fp32 registers.
 
-// Twelve warps: producer, issuer (two more idle), eight of the epilogue.
+// Twelve warps: producer, issuer, two that sum A's rows, eight of the epilogue.
+//
+// Row sums (the bias gradient beside a weight gradient, whose A is dy): the two
+// warps read each stage of A beside the matrix instructions, one 64-row box
+// each, in the tiles of the first tile column; a stage is free once they have
+// arrived as well.  A lane adds 8 rows of A over 16 reduction elements a stage
+// and the stage's sums to its total, so a sum has one fixed order.  Only the even
+// CTA sees the copies land (its barrier counts both CTAs' bytes): it passes
+// that on to the odd one, by an arrival that releases nothing of its own (the
+// bytes are in the odd CTA's memory before the barrier counts them; a releasing
+// one took longer than the stage's products: 250 us for the call below).
+// Unpacked to fp32 and added, the sums took 830 cycles a stage against the
+// products' 600; with adds that take the bf16 half as it is they keep up:
+// [16384, 4096] x [16384, 1024] into fp32 81 us, 90 with the row sums (111
+// unpacked, 109 with the sums in a launch of their own).
 constexpr int kTileThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 constexpr int kPromoteBlocks = 8;
@@ -1145,11 +1164,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t kCols = 2 * BN;
     constexpr int kHalf = BN / 2;  // columns per epilogue warp
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], in_full[8];
+    __shared__ __align__(8) uint64_t full[S], empty[S], landed[S], acc_full[2], acc_empty[2], in_full[8];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
+    const bool row_sums = sums_rows(KIND) && tp.row_sum != nullptr;
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int total = g.tiles_per_batch * g.batch;
     const int chunk = PROMOTE ? kPromoteBlocks : g.kblocks;
@@ -1159,7 +1179,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         prefetch_map(&mb);
         for (int s = 0; s < S; ++s) {
             tma::mbar_init(&full[s], 1);   // the even CTA's expected bytes (both CTAs' copies)
-            tma::mbar_init(&empty[s], 1);  // the issuing thread's commit
+            tma::mbar_init(&empty[s], row_sums ? 3 : 1);  // the issuing thread's commit, the summing warps
+            tma::mbar_init(&landed[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             tma::mbar_init(&acc_full[a], 1);
@@ -1258,7 +1279,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= kEpilogueWarp0) {
+    } else if (warp < kEpilogueWarp0) {
+        if (row_sums) {
+            const int red_group = lane / 8, piece_of = lane % 8;
+            const uint32_t peer = map_rank(tma::smem_addr(&landed[0]), 1);
+            int s = 0, round = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok; tile += pairs) {
+                int tm, tn;
+                tile_at(g, tile, 256, BN, tm, tn);
+                const int i = tm * 256 + (int)rank * 128 + (warp - 2) * 64;
+                const bool mine = tn == 0 && i < g.m;
+                float sum[8] = {};
+                for (int kb = 0; kb < g.kblocks; ++kb) {
+                    ok = __all_sync(0xFFFFFFFFu, rank == 0 ? tma::mbar_wait(&full[s], round & 1)
+                                                           : mbar_wait_cluster(&landed[s], round & 1));
+                    if (!ok) break;
+                    if (rank == 0 && warp == 2 && lane == 0) mbar_arrive_cluster(peer + s * 8);
+                    if (mine) {
+                        const uint32_t box = base + s * kStage + (warp - 2) * 8192;
+                        uint4 v[16];
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) v[r] = box_get(box, r * 4 + red_group, piece_of);
+                        float part[8] = {};
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            add_bf16x2(part[0], part[1], v[r].x);
+                            add_bf16x2(part[2], part[3], v[r].y);
+                            add_bf16x2(part[4], part[5], v[r].z);
+                            add_bf16x2(part[6], part[7], v[r].w);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {  // formed here: no read is under way when the stage is given back
+                            sum[c] += part[c];
+                            asm volatile("" : "+f"(sum[c])::"memory");
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) tma::mbar_arrive(&empty[s]);
+                    if (++s == S) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+                if (ok && mine) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        sum[c] += __shfl_xor_sync(0xFFFFFFFFu, sum[c], 8);
+                        sum[c] += __shfl_xor_sync(0xFFFFFFFFu, sum[c], 16);
+                        const int row = i + piece_of * 8 + c;
+                        if (red_group == 0 && row < g.m) {
+                            float* o = tp.row_sum + row;
+                            *o = tp.row_sum_add ? *o + sum[c] : sum[c];
+                        }
+                    }
+                }
+            }
+            if (!ok && lane == 0) record_device_error(g.err, DPRED_E_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
         const int q = warp & 3, half = (warp - kEpilogueWarp0) / 4;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * kHalf;
         const uint32_t box = base + S * kStage + (warp - kEpilogueWarp0) * kBoxBytes;
@@ -1443,6 +1523,8 @@ struct Operand {
 struct Plan {
     Args args;
     Operand a, b;
+    float* row_sum;   // args.row_sums: where to (a.reduce_rows)
+    int row_sum_add;
     int fp32_result;  // the result is stored in fp32: keep the accumulators' truncation below its precision
 };
 

@@ -78,6 +78,8 @@ int launch_tiles(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_
     if (rc != DPRED_OK) return rc;
     TileParams t = {};
     t.e = e;
+    t.row_sum = p.row_sum;
+    t.row_sum_add = p.row_sum_add;
     // what the streaming epilogue covers; block_epilogue does the rest
     t.stream = e.vec && (KIND == KIND_F32 ? !e.z && !e.res && !e.pre_out && !e.act : KIND != KIND_LINEAR && !(e.res && e.z));
     if (t.stream) {
@@ -139,8 +141,9 @@ int run_tiles(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param&
 }
 
 template <int KIND>
-int run(const Plan& p, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
+int run(const Plan& p, const typename EpiOf<KIND>::Param& e, cudaStream_t s, bool* row_sums_formed = nullptr) {
     const Shape sh = choose_shape(p.args, p.fp32_result);
+    if (row_sums_formed) *row_sums_formed = p.args.row_sums && sh.pairs;
     if (sh.tiles * sh.split > 0x7FFFFFFF) return set_error(DPRED_E_SIZE, "a matrix product of too many tiles");
     if constexpr (is_linear(KIND)) {
         if (sh.pairs) return run_tiles<KIND>(p, sh, e, s);

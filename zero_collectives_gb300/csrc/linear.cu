@@ -85,7 +85,9 @@ int pack(Operand* const (&ops)[2], char* ws, cudaStream_t s) {
 
 // ------------------------------------------------------------- bias gradient --
 //
-// db[j] = sum_i dy[i][j]: bandwidth bound, each row read once.  A cluster of 8
+// db[j] = sum_i dy[i][j], where the product runs on the split kernel (the tile
+// kernel sums dy from its own stages) or there is no product: bandwidth bound,
+// each row read once.  A cluster of 8
 // CTAs shares a strip of columns; every thread sums 8 columns of every
 // ROWS-th row in fp32, the CTA adds its row groups and the cluster its 8 partial
 // rows in rank order, so the sum has one fixed order.
@@ -201,7 +203,8 @@ bool aligned_rows(const void* p, int64_t rows, int64_t ld, int esize) {
 }
 
 int launch(Operand a, Operand b, int64_t red, const LinearEpi& e, void* workspace, size_t workspace_bytes, size_t need,
-           cudaStream_t s) {
+           cudaStream_t s, float* row_sum = nullptr, int row_sum_add = 0,
+           bool* row_sum_formed = nullptr) {
     if (need > workspace_bytes || (need && !workspace))
         return set_error(DPRED_E_SIZE, "workspace of %zu bytes, %zu needed (operands whose rows are not 16-byte aligned)",
                          workspace_bytes, need);
@@ -225,7 +228,10 @@ int launch(Operand a, Operand b, int64_t red, const LinearEpi& e, void* workspac
     p.args.bf16 = 1;
     p.args.split_only = e.swapped;
     p.fp32_result = e.out_f32;
-    return run<KIND_LINEAR>(p, e, s);
+    p.args.row_sums = row_sum != nullptr;
+    p.row_sum = row_sum;
+    p.row_sum_add = row_sum_add;
+    return run<KIND_LINEAR>(p, e, s, row_sum_formed);
 }
 
 }  // namespace
@@ -327,6 +333,7 @@ extern "C" int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* d
     if (bias_grad && reinterpret_cast<uintptr_t>(bias_grad) % 4) return set_error(DPRED_E_ALIGN, "bias_grad is not aligned to 4 bytes");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Operand a = {dy, m, n, lddy, 0, true}, b = {x, m, k, ldx, 0, true};
+    bool formed = false;  // the product's kernel has formed the bias gradient
     if (n > 0 && k > 0) {
         LinearEpi e = {};
         e.out = dw;
@@ -335,9 +342,9 @@ extern "C" int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* d
         e.o_ld = lddw;
         e.vec = aligned_rows(dw, n, lddw, osize);
         const size_t need = m > 0 ? dpred_linear_workspace_bytes(dy, m, n, lddy, x, m, k, ldx) : 0;
-        if ((rc = launch(a, b, m, e, workspace, workspace_bytes, need, s)) != DPRED_OK) return rc;
+        if ((rc = launch(a, b, m, e, workspace, workspace_bytes, need, s, bias_grad, accumulate != 0, &formed)) != DPRED_OK) return rc;
     }
-    if (bias_grad && n > 0) {
+    if (bias_grad && n > 0 && !formed) {
         const int vec = aligned_rows(dy, m, lddy, 2);
         const cudaError_t e = launch_bias_grad(dy, lddy, m, n, bias_grad, accumulate != 0, vec, s);
         if (e != cudaSuccess) return cuda_error(e, "bias gradient launch");

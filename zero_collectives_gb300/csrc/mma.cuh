@@ -86,6 +86,41 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// As tma::mbar_wait, for a barrier that another CTA of the cluster arrives on.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(tma::smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_cluster(bar, parity))
+        if (clock64() - t0 > tma::kWaitBudgetCycles) return false;
+    return true;
+}
+
+// a += the low bf16 of w, b += the high one, each in fp32.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
+    asm("{\n"
+        " .reg .b16 l, h;\n"
+        " mov.b32 {l, h}, %2;\n"
+        " add.rn.f32.bf16 %0, l, %0;\n"
+        " add.rn.f32.bf16 %1, h, %1;\n"
+        "}\n"
+        : "+f"(a), "+f"(b)
+        : "r"(w));
+}
+
 // ------------------------------------------- programmatic dependent launch --
 
 // Everything before this may run before the previous kernel of the stream has
