@@ -172,6 +172,21 @@ def test_bias_gradient_beside_many_tiles(m, n, k, dtype, pad, accumulate):
     assert zc.device_status() == 0
 
 
+@pytest.mark.parametrize("m,n,k,shift", [(5000, 5000, 520, 0), (5000, 5008, 520, 8), (4999, 5024, 1000, 16), (9000, 4500, 512, 0)])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_long_reductions_over_many_ragged_tiles(m, n, k, shift, act):
+    """Every element of a ragged output is written once, and nothing around it."""
+    x, w = randn(m, k, seed=1), randn(n, k, seed=2, scale=1 / math.sqrt(k))
+    flat = torch.full((m * n + shift + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    y = zc.linear(x, w, act=act, out=flat[shift:shift + m * n].view(m, n))
+    for rows in (slice(0, 300), slice(m - 300, m)):
+        z = x[rows].double() @ w.double().T
+        mags = x[rows].double().abs() @ w.double().abs().T
+        close(y[rows], act64(z, act), mags, k, 2.0 ** -18 * mags)
+    assert bool(torch.isfinite(y.float()).all())
+    assert bool(torch.isnan(flat[:shift]).all()) and bool(torch.isnan(flat[shift + m * n:]).all())
+
+
 def test_wgrad_into_gradient_rows():
     """Gradients land in the [W, n] row a flush reads, at an odd offset, and nothing else is touched."""
     m, n, k, off = 300, 40, 56, 13

@@ -65,6 +65,8 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Par
     return err == cudaSuccess ? DPRED_OK : cuda_error(err, "matrix product launch");
 }
 
+constexpr int kDirectBlocks = 8;
+
 template <int KIND, int BN, bool PROMOTE>
 int launch_tiles(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_t s) {
     static bool attr[64] = {};
@@ -98,6 +100,13 @@ int launch_tiles(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_
     g.regions = 1;
     const int pairs = resident_pairs(reinterpret_cast<const void*>(kernel), kTileThreads, tile_smem<BN>());
     if (pairs < 1) return set_error(DPRED_E_CUDA, "no CTA pair fits on this device");
+    // A plain result without a residual leaves straight from the registers where
+    // the next tile's reduction is long enough to hide its partly filled lines:
+    // 8192 x 8192 outputs of reductions of 256 / 512 / 1024 take 40 / 50 / 80 us
+    // so and 33 / 52 / 85 us as boxes, whose copies queue with the operands'.  With
+    // few tiles nothing hides it (4096 x 1024 x 1024: 11.1 us so, 10.5 as boxes).
+    t.direct = KIND == KIND_PLAIN && t.stream && !e.res && p.args.kblocks >= kDirectBlocks && sh.tiles >= 4 * pairs &&
+               e.o_ld % 16 == 0 && reinterpret_cast<uintptr_t>(e.out) % 32 == 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (sh.tiles < pairs ? sh.tiles : pairs)));
     cfg.blockDim = dim3(kTileThreads);
