@@ -128,6 +128,84 @@ __device__ __forceinline__ bool tile_epilogue(const NsEpi& e, const Args& g, int
     return true;
 }
 
+// 32 bytes, past the first-level cache (other SMs wrote them earlier in this launch).
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// tile_epilogue<KIND_APPLY> where X's rows are whole 32-column chunks: a lane
+// keeps the row that it has in tensor memory, and both terms of X come and go
+// in 32-byte pieces (whole sectors) without a pass through shared memory.
+struct XChunk {
+    uint32_t h[2][8], l[8];
+};
+
+__device__ __forceinline__ bool apply_rows(const NsEpi& e, const Args& g, int batch, int i, int j, uint32_t acc, int lane,
+                                           uint64_t* full, uint32_t parity, uint32_t drained) {
+    const int row = i + lane;
+    const bool live = row < g.m;
+    const int64_t at = ((int64_t)batch * g.m + row) * e.ldc + j;
+    XChunk ahead = {};
+    auto load = [&](int c) {
+        if (live && j + c < g.n) {
+            load32(e.hi_in + at + c, ahead.h[0]);
+            load32(e.hi_in + at + c + 16, ahead.h[1]);
+            load32(e.lo + at + c, ahead.l);
+        }
+    };
+    load(0);
+    const float k = live ? __ldcg(e.coef + (int64_t)batch * e.ldr + row) : 0.0f;
+    if (!__all_sync(0xFFFFFFFFu, tma::mbar_wait(full, parity))) return false;
+    mma::fence_after();
+#pragma unroll 1
+    for (int c = 0; c < kBN / 2; c += 32) {
+        float v[32];
+        __syncwarp();
+        mma::tmem_ld32(acc + c, v);
+        mma::tmem_wait_ld();
+        if (c + 32 == kBN / 2) {  // the accumulator is in registers: the next tile may overwrite it
+            mma::fence_before();
+            __syncwarp();
+            if (lane == 0) mma::mbar_arrive_cluster(drained);
+        }
+        XChunk now = ahead;
+        if (c + 32 < kBN / 2) load(c + 32);
+        if (live && j + c < g.n) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                uint32_t(&hw)[8] = now.h[p / 2];
+                const int o = p % 2 * 4;
+                float x[8];
+                join8(make_uint4(hw[o], hw[o + 1], hw[o + 2], hw[o + 3]), make_uint2(now.l[2 * p], now.l[2 * p + 1]), x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[q] = fmaf(k, x[q], v[8 * p + q]);
+                uint4 h;
+                uint2 l;
+                split8(x, h, l);
+                hw[o] = h.x;
+                hw[o + 1] = h.y;
+                hw[o + 2] = h.z;
+                hw[o + 3] = h.w;
+                now.l[2 * p] = l.x;
+                now.l[2 * p + 1] = l.y;
+            }
+            store32(e.hi + at + c, now.h[0]);
+            store32(e.hi + at + c + 16, now.h[1]);
+            store32(e.lo + at + c, now.l);
+        }
+    }
+    return true;
+}
+
 __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_constant__ ChainArgs a) {
     using namespace mma;
     extern __shared__ uint8_t raw[];
@@ -281,7 +359,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                 case CHAIN_GRAM: ok = tile_epilogue<KIND_GRAM>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
                 case CHAIN_POLY: ok = tile_epilogue<KIND_POLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
                 case CHAIN_MUL: ok = tile_epilogue<KIND_MUL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
-                case CHAIN_APPLY: ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
+                case CHAIN_APPLY:
+                    if (g.c % 32 == 0) {
+                        ok = apply_rows(e, d, at.batch, i, j, from, lane, &acc_full[acc], parity, drained);
+                        break;
+                    }
+                    ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
                 default: ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
             }
             fence_proxy_async();  // these stores will be read by other SMs' copies
