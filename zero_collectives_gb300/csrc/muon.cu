@@ -39,7 +39,20 @@ namespace {
 
 constexpr int kMaxSteps = 32;
 constexpr int kNormBlocks = 256;  // partial sums of squares per matrix (at most)
-constexpr int kTile = 64;         // the element-wise passes work on 64 x 64 tiles
+constexpr int kTile = 64;         // the element-wise passes transpose tiles of 64 x 64
+
+// How a block of the element-wise passes covers a tile of 4096 elements: a
+// thread has 4 columns of every `step`-th row, four times.
+struct Pass {
+    int r, c, step, width;
+    __device__ __forceinline__ explicit Pass(bool square) {
+        const int shift = square ? 4 : 6;  // 64 x 64, or 16 x 256: whole kilobytes of a row
+        r = threadIdx.x >> shift;
+        c = (threadIdx.x & ((1 << shift) - 1)) * 4;
+        step = 256 >> shift;
+        width = 4 << shift;
+    }
+};
 
 // One matrix of a launch as the element-wise passes see it.
 struct MatIn {
@@ -108,17 +121,17 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
     const MatIn& in = a.in[blockIdx.y];
     const Tg* g = static_cast<const Tg*>(in.g);
     const int64_t rows = in.transposed ? a.c : a.r, cols = in.transposed ? a.r : a.c;
-    const int64_t tr = (rows + kTile - 1) / kTile, tc = (cols + kTile - 1) / kTile;
-    const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
+    const Pass p(false);
+    const int64_t tr = (rows + 4 * p.step - 1) / (4 * p.step), tc = (cols + p.width - 1) / p.width;
     float sum = 0.0f;
     for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
-        const int64_t i0 = t / tc * kTile, j = t % tc * kTile + c;
+        const int64_t i0 = t / tc * 4 * p.step + p.r, j = t % tc * p.width + p.c;
         const int valid = (int)(cols - j);
         if (valid <= 0) continue;
         float gv[4][4], mv[4][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + r + 16 * u;
+            const int64_t i = i0 + p.step * u;
             if (i < rows) {
                 load4(g + i * in.ldg + j, valid, in.g_vec, gv[u]);
                 if (in.mom) load4(in.mom + i * in.ldm + j, valid, in.m_vec, mv[u]);
@@ -126,7 +139,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + r + 16 * u;
+            const int64_t i = i0 + p.step * u;
             if (i >= rows) continue;
             if (in.mom) {
 #pragma unroll
@@ -167,17 +180,18 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
     const float total = block_sum(threadIdx.x < a.blocks ? a.partial[blockIdx.y * kNormBlocks + threadIdx.x] : 0.0f);
     const float f = a.scale / (sqrtf(total) + a.eps);
     const int64_t rows = in.transposed ? a.c : a.r, cols = in.transposed ? a.r : a.c;
-    const int64_t tr = (rows + kTile - 1) / kTile, tc = (cols + kTile - 1) / kTile;
+    const Pass p(in.transposed);
+    const int64_t tr = (rows + 4 * p.step - 1) / (4 * p.step), tc = (cols + p.width - 1) / p.width;
     const int64_t xr = a.r, xc = a.c;
     __half* hi = a.hi + (int64_t)blockIdx.y * xr * a.ldc;
     uint8_t* lo = a.lo + (int64_t)blockIdx.y * xr * a.ldc;
-    const int r = threadIdx.x / 16, c = threadIdx.x % 16 * 4;
+    const int r = p.r, c = p.c;
     for (int64_t t = blockIdx.x; t < tr * tc; t += gridDim.x) {
-        const int64_t i0 = t / tc * kTile, j0 = t % tc * kTile;
+        const int64_t i0 = t / tc * 4 * p.step, j0 = t % tc * p.width;
         float x[4][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + r + 16 * u;
+            const int64_t i = i0 + r + p.step * u;
             const int valid = (int)(cols - j0 - c);
             if (i < rows && valid > 0) {
                 float m[4];
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Norm
         const int64_t xi0 = in.transposed ? j0 : i0, xj = (in.transposed ? i0 : j0) + c;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t i = xi0 + r + 16 * u;
+            const int64_t i = xi0 + r + p.step * u;
             if (i >= xr || xj >= xc) continue;  // rows are padded to 8 columns, so a group of 4 always fits
             const float t[8] = {x[u][0], x[u][1], x[u][2], x[u][3]};
             uint4 h;
@@ -320,14 +334,19 @@ int start_group(const Group& g, const Params& q, cudaStream_t s) {
     n.blocks = (int)std::min<int64_t>(tiles, kNormBlocks);
     const dim3 grid1((unsigned)n.blocks, (unsigned)g.count);
     const dim3 grid2((unsigned)std::min<int64_t>(tiles, 512), (unsigned)g.count);
-    if (q.g_dtype == DPRED_F32) {
-        norm_kernel<float><<<grid1, 256, 0, s>>>(n);
-        scale_kernel<float><<<grid2, 256, 0, s>>>(n);
-    } else {
-        norm_kernel<__nv_bfloat16><<<grid1, 256, 0, s>>>(n);
-        scale_kernel<__nv_bfloat16><<<grid2, 256, 0, s>>>(n);
-    }
-    const cudaError_t err = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid1;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const bool f32 = q.g_dtype == DPRED_F32;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, f32 ? norm_kernel<float> : norm_kernel<__nv_bfloat16>, n);
+    cfg.gridDim = grid2;
+    if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, f32 ? scale_kernel<float> : scale_kernel<__nv_bfloat16>, n);
     return err == cudaSuccess ? DPRED_OK : cuda_error(err, "orthogonalised update launch");
 }
 
