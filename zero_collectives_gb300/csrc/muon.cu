@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormA
 // X = scale * U / (|U| + eps) on its wide side, as two terms (see split8).  The
 // partial sums are added in one fixed order by every block.
 template <typename Tg>
-__global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(256, 8) scale_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float tile[kTile][kTile + 1];
     mma::grid_launch_dependents();
     mma::grid_wait();
@@ -331,9 +331,11 @@ int start_group(const Group& g, const Params& q, cudaStream_t s) {
         in.m_vec = reinterpret_cast<uintptr_t>(in.mom) % 16 == 0 && (g.items[k]->rows <= 1 || in.ldm % 4 == 0);
     }
     const int64_t tiles = ((l.r + kTile - 1) / kTile) * ((l.c + kTile - 1) / kTile);
-    n.blocks = (int)std::min<int64_t>(tiles, kNormBlocks);
+    // the norm's blocks are resident at once (four to an SM); the scaling's, of a tile each, follow one another
+    const int64_t resident = std::max<int64_t>(1, 4 * sm_count() / g.count);
+    n.blocks = (int)std::min<int64_t>(std::min<int64_t>(tiles, kNormBlocks), resident);
     const dim3 grid1((unsigned)n.blocks, (unsigned)g.count);
-    const dim3 grid2((unsigned)std::min<int64_t>(tiles, 512), (unsigned)g.count);
+    const dim3 grid2((unsigned)std::min<int64_t>(tiles, 65536), (unsigned)g.count);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid1;
     cfg.blockDim = dim3(256);
