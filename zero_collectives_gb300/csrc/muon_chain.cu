@@ -209,7 +209,7 @@ __device__ __forceinline__ bool apply_rows(const NsEpi& e, const Args& g, int ba
 __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_constant__ ChainArgs a) {
     using namespace mma;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], stored[2], taken[2];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -224,6 +224,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             tma::mbar_init(&acc_full[i], 1);
             tma::mbar_init(&acc_empty[i], 16);
+            tma::mbar_init(&stored[i], 8);  // the CTA's epilogue warps
+            tma::mbar_init(&taken[i], 1);   // the releasing thread
         }
         tma::fence_barrier_init();
     }
@@ -321,6 +323,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
             }
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // Makes finished tiles known to the other SMs.  The release waits until the CTA's stores have
+        // reached L2, about 4000 cycles, which the epilogue's warps spend on their next tile.
+        if (elect_one()) {
+            int fill = 0;
+            for (Cursor at(pair); at.settle(a); at.offset += pairs, ++fill) {
+                const int acc = fill & 1;
+                // a tile's epilogue may wait for its operands and for its accumulators first
+                if (!tma::mbar_wait(&stored[acc], (fill / 2) & 1, 3 * tma::kWaitBudgetCycles)) {
+                    record_device_error(a.err, DPRED_E_TIMEOUT);
+                    break;
+                }
+                tma::mbar_arrive(&taken[acc]);
+                fence_proxy_async();  // these stores will be read by other SMs' copies
+                asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(a.counter + a.g[at.group].first + at.batch), "r"(8u)
+                             : "memory");
+            }
+        }
+        __syncwarp();
     } else if (warp >= kEpilogueWarp0) {
         const int q = warp & 3, half = (warp - kEpilogueWarp0) / 4;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * (kBN / 2);
@@ -330,7 +351,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
         bool ok = true;
         for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
             const ChainGroup& g = a.g[at.group];
-            unsigned* counter = a.counter + g.first + at.batch;
+            const unsigned* counter = a.counter + g.first + at.batch;
             const int acc = fill & 1;
             const ChainOp op = at.op;
             if (op.kind != CHAIN_GRAM) {  // the epilogue reads what earlier products stored
@@ -367,9 +388,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
                     ok = tile_epilogue<KIND_APPLY>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
                 default: ok = tile_epilogue<KIND_FINAL>(e, d, at.batch, i, j, from, block, lane, &acc_full[acc], parity, drained); break;
             }
-            fence_proxy_async();  // these stores will be read by other SMs' copies
             __syncwarp();
-            if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(counter), "r"(1u) : "memory");
+            if (lane == 0 && ok) {
+                if (fill >= 2) ok = tma::mbar_wait(&taken[acc], (fill / 2 - 1) & 1);
+                if (ok) tma::mbar_arrive(&stored[acc]);
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
         if (!ok && lane == 0) record_device_error(a.err, DPRED_E_TIMEOUT);
         __syncwarp();
