@@ -6,8 +6,8 @@
 // pairs, twice as long as 76.  Here the pairs walk one list of tiles in the order
 // (product, matrix): the first matrices' next product starts while the
 // last ones' current product is still running.  What a tile needs is its own
-// matrix's previous product, complete: a counter per matrix says so (every
-// epilogue warp adds one when its part of a tile is in memory), and since the
+// matrix's previous product, complete: a counter per matrix says so (it counts
+// the epilogue warps whose part of a tile is in memory), and since the
 // list is in dependency order and all pairs are resident (a cooperative
 // launch), every wait ends.  Waits are bounded all the same.
 //
@@ -24,6 +24,9 @@ namespace {
 
 constexpr int kBN = 256;
 constexpr int kStages = 6;
+// The producer is at most this many tiles ahead of the epilogue: two accumulators, a tile in every stage.
+constexpr int kReady = 16;
+static_assert(kReady > 2 + kStages + 1, "a tile's barrier is reused before it was waited for");
 constexpr uint32_t kStageBytes = 2 * 128 * 128;
 constexpr int kSmem = kStages * (int)kStageBytes + 8 * (int)kBlockBytes + 1024;
 
@@ -144,7 +147,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 
 // tile_epilogue<KIND_APPLY> where X's rows are whole 32-column chunks: a lane
 // keeps the row that it has in tensor memory, and both terms of X come and go
-// in 32-byte pieces (whole sectors) without a pass through shared memory.
+// in 32-byte pieces (whole sectors) without a pass through shared memory.  All
+// of X that the tile reads is requested before its accumulators are waited for.
 struct XChunk {
     uint32_t h[2][8], l[8];
 };
@@ -154,19 +158,20 @@ __device__ __forceinline__ bool apply_rows(const NsEpi& e, const Args& g, int ba
     const int row = i + lane;
     const bool live = row < g.m;
     const int64_t at = ((int64_t)batch * g.m + row) * e.ldc + j;
-    XChunk ahead = {};
-    auto load = [&](int c) {
+    XChunk ahead[kBN / 64] = {};
+    auto load = [&](int c, XChunk& x) {
         if (live && j + c < g.n) {
-            load32(e.hi_in + at + c, ahead.h[0]);
-            load32(e.hi_in + at + c + 16, ahead.h[1]);
-            load32(e.lo + at + c, ahead.l);
+            load32(e.hi_in + at + c, x.h[0]);
+            load32(e.hi_in + at + c + 16, x.h[1]);
+            load32(e.lo + at + c, x.l);
         }
     };
-    load(0);
+#pragma unroll
+    for (int c = 0; c < kBN / 2; c += 32) load(c, ahead[c / 32]);
     const float k = live ? __ldcg(e.coef + (int64_t)batch * e.ldr + row) : 0.0f;
     if (!__all_sync(0xFFFFFFFFu, tma::mbar_wait(full, parity))) return false;
     mma::fence_after();
-#pragma unroll 1
+#pragma unroll
     for (int c = 0; c < kBN / 2; c += 32) {
         float v[32];
         __syncwarp();
@@ -177,8 +182,7 @@ __device__ __forceinline__ bool apply_rows(const NsEpi& e, const Args& g, int ba
             __syncwarp();
             if (lane == 0) mma::mbar_arrive_cluster(drained);
         }
-        XChunk now = ahead;
-        if (c + 32 < kBN / 2) load(c + 32);
+        XChunk& now = ahead[c / 32];
         if (live && j + c < g.n) {
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -209,7 +213,7 @@ __device__ __forceinline__ bool apply_rows(const NsEpi& e, const Args& g, int ba
 __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_constant__ ChainArgs a) {
     using namespace mma;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], stored[2], taken[2];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], stored[2], taken[2], ready[kReady];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -227,6 +231,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
             tma::mbar_init(&stored[i], 8);  // the CTA's epilogue warps
             tma::mbar_init(&taken[i], 1);   // the releasing thread
         }
+        for (int i = 0; i < kReady; ++i) tma::mbar_init(&ready[i], 1);
         tma::fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<2>(tma::smem_addr(&tmem_slot), 512);
@@ -237,15 +242,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
 
     if (warp == 0) {
         if (elect_one()) {
-            int s = 0, round = 0;
+            int s = 0, round = 0, fill = 0;
             bool ok = true;
-            for (Cursor at(pair); ok && at.settle(a); at.offset += pairs) {
+            for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
                 const ChainGroup& g = a.g[at.group];
                 if (!wait_counter(a.counter + g.first + at.batch, at.needed(g))) {
                     record_device_error(a.err, DPRED_E_TIMEOUT);
                     ok = false;
                     break;
                 }
+                tma::mbar_arrive(&ready[fill % kReady]);
                 fence_proxy_async();  // what other SMs stored is about to be read by copies
                 const ChainOp op = at.op;
                 const CUtensorMap* ma = op.kind == CHAIN_GRAM ? &g.x[op.x] : g.square[op.a];
@@ -351,12 +357,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) chain_kernel(const __grid_con
         bool ok = true;
         for (Cursor at(pair); ok && at.settle(a); at.offset += pairs, ++fill) {
             const ChainGroup& g = a.g[at.group];
-            const unsigned* counter = a.counter + g.first + at.batch;
             const int acc = fill & 1;
             const ChainOp op = at.op;
-            if (op.kind != CHAIN_GRAM) {  // the epilogue reads what earlier products stored
-                if (lane == 0) ok = wait_counter(counter, at.needed(g));
-                ok = __all_sync(0xFFFFFFFFu, ok);
+            if (op.kind != CHAIN_GRAM) {  // the epilogue reads what earlier products stored, as the producer has seen
+                ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&ready[fill % kReady], (fill / kReady) & 1, 2 * tma::kWaitBudgetCycles));
                 if (!ok) break;
             }
             NsEpi e = g.e;
