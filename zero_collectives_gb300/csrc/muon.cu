@@ -459,8 +459,8 @@ int chain_program(ChainOp* op, int steps, bool pairs) {
 }
 
 // Double steps pay where the products with X are much the longer ones (plain
-// -> double): 6 of 1024 x 4096 513 -> 454 us, 24 of 512 x 2048 440 -> 399; 6 of
-// 1024 x 2048 305 -> 322, 8 of 1024 x 1024 241 -> 275.
+// -> double): 6 of 1024 x 4096 437 -> 393 us, 6 of 300 x 3000 241 -> 221, 12 of
+// 512 x 2048 233 -> 237; 4 of 1024 x 2048 234 -> 251, 8 of 1024 x 1024 223 -> 252.
 bool double_steps(const Layout& l) { return l.c >= 3 * l.r; }
 
 int run_chained(const std::vector<Group>& groups, const Params& q, cudaStream_t s) {
@@ -510,20 +510,22 @@ int run_chained(const std::vector<Group>& groups, const Params& q, cudaStream_t 
     return run_chain(a, s);
 }
 
-// Estimated times (us) of the two ways, fitted to batches of 1 to 16 matrices
-// from 256 x 256 to 2048 x 4096 (within 12%).  The chained kernel is bound by
-// one matrix's chain of products (a tile costs 0.3 a reduction block and 7 to
+// Estimated times (us) of the two ways, fitted to batches of 1 to 12 matrices
+// from 160 x 2500 to 2048 x 4096 (most within 12%).  The chained kernel is bound
+// by one matrix's chain of products (a tile costs 0.3 a reduction block and 5.5 to
 // start, drain and hand over) and by its tiles' total over the CTA pairs.
+// Either side, chained against one by one: 1 of 1024 x 1024 171 and 126 us, 3 of
+// them 175 and 189, 12 of them 263 and 550.
 double chained_time(const std::vector<Group>& groups, int steps) {
     double work = 0, chain = 0;
     for (const Group& g : groups) {
         const double tr = (double)((g.l.r + 255) / 256), tc = (double)((g.l.c + 255) / 256), sym = tr * (tr + 1) / 2;
         const double kc = 0.3 * blocks_of(g.l.c), kr = 0.3 * blocks_of(g.l.r);
         const int twos = double_steps(g.l) ? steps / 2 : 0, passes = steps - twos, squares = steps + 3 * twos;
-        work += g.count * (passes * (sym * std::max(kc, 6.5) + tr * tc * std::max(kr, 6.5)) + squares * sym * std::max(kr, 6.5));
-        chain = std::max(chain, passes * (kc + kr + 2 * 7.0) + squares * (kr + 7.0));
+        work += g.count * (passes * (sym * std::max(kc, 7.6) + tr * tc * std::max(kr, 7.6)) + squares * sym * std::max(kr, 7.6));
+        chain = std::max(chain, passes * (kc + kr + 2 * 5.5) + squares * (kr + 5.5));
     }
-    return 12 + std::hypot(0.93 * chain, 1.45 * work / (sm_count() / 2));
+    return 2.5 + std::hypot(1.1 * chain, 1.1 * work / (sm_count() / 2));
 }
 
 double products_time(const Group& g, int steps) {
