@@ -209,3 +209,14 @@ def test_many_large_matrices(shapes):
     zc.muon_step(again, [torch.zeros(s, device="cuda") for s in shapes], gs, lr=0.1, scale=1.0)
     assert all(torch.equal(x, y) for x, y in zip(again, ws)), "two runs differ"
     assert zc.device_status() == 0
+
+
+@pytest.mark.parametrize("shapes", [[(40, 4096)] * 48 + [(1500, 1500)] * 4, [(992, 1248)] * 10, [(130, 2080)] * 20 + [(2080, 600)] * 6])
+def test_chained_tiles_of_short_reductions_and_ragged_rows(shapes):
+    """Reductions of one to three blocks, whose tiles follow one another closely, and row tails beside whole 32-column chunks."""
+    gs = [gradient(*s, seed=200 + i) for i, s in enumerate(shapes)]
+    ws, ms = [torch.zeros_like(g) for g in gs], [torch.zeros_like(g) for g in gs]
+    zc.muon_step(ws, ms, gs, lr=1.0, scale=1.0)
+    for w, g in zip(ws, gs):
+        assert rel(-w, ns64(g)) <= TOL
+    assert zc.device_status() == 0
