@@ -229,10 +229,14 @@ size_t dpred_flush_workspace_bytes(int32_t world, int32_t n_tasks);
  *  - DPRED_FLUSH_OVERLAP is the caller's promise that this flush shares no
  *    byte with the work enqueued on `stream` just before it (normally the
  *    previous bucket's flush): neither reads what that work writes nor
- *    writes what it reads or writes.  The flush may then start on the SMs
- *    that the previous flush's last wave leaves idle (programmatic dependent
- *    launch); it still completes after that flush, so the stream's order of
- *    completion is unchanged.  Plans that do not fit inside the launch
+ *    writes what it reads or writes.  After a flush that carries the bit
+ *    itself, this goes for the flushes before that one too, back to the last
+ *    flush without the bit.  Other earlier calls need no promise: only a flush
+ *    lets the next call start before it is done itself, so whatever a product
+ *    or an update wrote is there, whichever call lies between.  The flush may
+ *    then start on the SMs that the previous flush's last wave leaves idle
+ *    (programmatic dependent launch); it still completes after that flush, so
+ *    the stream's order of completion is unchanged.  Plans that do not fit inside the launch
  *    (dpred_flush_workspace_bytes() > 0) ignore the bit.  A promise that
  *    does not hold makes the results undefined.
  * probe (host, may be NULL) receives the counters of dpred_flush_probe.

@@ -121,6 +121,7 @@ struct Args {
     int stages;          // split kernel: pipeline stages
     int regions;         // split kernel: accumulators that share a CTA's part of the reduction
     int bf16;
+    int release;         // a later launch of the same call follows (see grid_launch_dependents)
     int* err;
 };
 
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    grid_launch_dependents();
+    if (g.release) grid_launch_dependents();
     grid_wait();
 
     bool ok = true;
@@ -1205,7 +1206,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     cluster_sync();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    grid_launch_dependents();
+    if (g.release) grid_launch_dependents();
     grid_wait();
 
     if (warp == 0) {

@@ -47,6 +47,7 @@ int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Par
     const bool deep = split_alone((double)sh.tiles * sh.split, sh.split, sm_count());
     g.stages = split_stages<BN>(deep);
     g.regions = p.fp32_result ? 256 / BN : 1;
+    if (g.row_sums) g.release = 1;  // formed by a launch of their own, right after this one
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sh.tiles * sh.split));
     cfg.blockDim = dim3(kSplitThreads);

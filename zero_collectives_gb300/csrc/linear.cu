@@ -101,7 +101,6 @@ __global__ void __cluster_dims__(kBiasCluster, 1, 1) __launch_bounds__(256, 2)
     constexpr int STRIP = kBiasStrip, kGroups = STRIP / 8, ROWS = 256 / kGroups, kUnroll = 8;
     __shared__ float part[ROWS][STRIP + 1];
     __shared__ float mine[STRIP];
-    mma::grid_launch_dependents();
     mma::grid_wait();
     const int rank = (int)mma::cluster_rank();
     const int64_t j0 = (int64_t)(blockIdx.x / kBiasCluster) * STRIP;

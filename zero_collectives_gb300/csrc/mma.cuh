@@ -127,6 +127,11 @@ __device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
 // finished; nothing that kernel writes (or reads and this one writes) may be
 // touched before it.  A no-op in a launch without the attribute.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the stream's next launch start while this one runs.  Only where that
+// launch belongs to the same call and waits before it touches memory: the next
+// call may be a bucket flush that overlaps (it reads its bucket at once and
+// waits at its end), which may rely on everything before this call being done.
+// The last launch of a call therefore never does it, and its end is the signal.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------- tensor maps --

@@ -403,19 +403,25 @@ Plan product_plan(const Group& g, int product, int buffer) {
 }
 
 // One launch per product: the matrices of a group that are too small, or too few, for the chained kernel.
-int run_products(const Group& g, const Params& q, cudaStream_t s) {
+// last: nothing of the call follows this group.
+int run_products(const Group& g, const Params& q, bool last, cudaStream_t s) {
     NsParams n = {};
     NsEpi& e = n.e;
     e = epilogue_of_group(g, q);
     for (int k = 0; k < g.count; ++k) n.table[k] = output_of(g, k, q);
     for (int step = 0; step < q.steps; ++step) {
-        int rc = run<KIND_GRAM>(product_plan(g, 0, step & 1), n, s);
+        Plan p = product_plan(g, 0, step & 1);
+        p.args.release = 1;
+        int rc = run<KIND_GRAM>(p, n, s);
         if (rc != DPRED_OK) return rc;
-        rc = run<KIND_POLY>(product_plan(g, 1, step & 1), n, s);
+        p = product_plan(g, 1, step & 1);
+        p.args.release = 1;
+        rc = run<KIND_POLY>(p, n, s);
         if (rc != DPRED_OK) return rc;
         e.hi_in = g.hi[step & 1];
         e.hi = g.hi[(step + 1) & 1];
-        const Plan p = product_plan(g, 2, step & 1);
+        p = product_plan(g, 2, step & 1);
+        p.args.release = !last || step + 1 < q.steps;
         rc = step + 1 < q.steps ? run<KIND_APPLY>(p, n, s) : run<KIND_FINAL>(p, n, s);
         if (rc != DPRED_OK) return rc;
     }
@@ -548,7 +554,7 @@ std::vector<const Item*> take_small(std::vector<const Item*>& v) {
     return small;
 }
 
-int run_small_items(std::vector<const Item*>& v, const Params& q, cudaStream_t s) {
+int run_small_items(std::vector<const Item*>& v, const Params& q, bool last, cudaStream_t s) {
     std::stable_sort(v.begin(), v.end(),
                      [](const Item* x, const Item* y) { return small_split(x->rows, x->cols) < small_split(y->rows, y->cols); });
     SmallArgs a = {};
@@ -569,6 +575,7 @@ int run_small_items(std::vector<const Item*>& v, const Params& q, cudaStream_t s
             const Item& it = *v[i];
             a.m[a.count++] = {it.in.g, it.in.mom, it.out, it.in.ldg, it.in.ldm, it.ldo, (int)it.rows, (int)it.cols, it.step};
         }
+        a.release = !last || i < v.size();
         const int rc = run_small(a, s);
         if (rc != DPRED_OK) return rc;
     }
@@ -625,7 +632,7 @@ int run_items(std::vector<Item>& items, const Params& q, void* workspace, size_t
         return set_error(DPRED_E_SIZE, "workspace of %zu bytes, %lld needed", workspace ? workspace_bytes : (size_t)0, (long long)need);
     if (need && reinterpret_cast<uintptr_t>(workspace) % 256)
         return set_error(DPRED_E_ALIGN, "workspace is not 256-byte aligned");
-    int rc = run_small_items(small, q, s);
+    int rc = run_small_items(small, q, launches.empty(), s);
     for (size_t i = 0; i < launches.size() && rc == DPRED_OK; ++i) {
         std::vector<Group>& groups = launches[i];
         char* ws = static_cast<char*>(workspace);
@@ -642,7 +649,8 @@ int run_items(std::vector<Item>& items, const Params& q, void* workspace, size_t
         if (chained_time(groups, q.steps) < separate) {
             rc = run_chained(groups, q, s);
         } else {
-            for (size_t k = 0; k < groups.size() && rc == DPRED_OK; ++k) rc = run_products(groups[k], q, s);
+            for (size_t k = 0; k < groups.size() && rc == DPRED_OK; ++k)
+                rc = run_products(groups[k], q, i + 1 == launches.size() && k + 1 == groups.size(), s);
         }
     }
     return rc;

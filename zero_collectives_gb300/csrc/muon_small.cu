@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         tma::fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<1>(tma::smem_addr(&tmem_slot), 512);
-    grid_launch_dependents();
+    if (a.release) grid_launch_dependents();
     grid_wait();
 
     // U to shared memory as fp32 (rows and columns past the matrix as zeros), and its sum of squares

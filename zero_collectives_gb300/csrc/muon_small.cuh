@@ -24,6 +24,7 @@ struct SmallArgs {
     int count;
     int split;           // CTAs of a cluster, each holding a run of X's columns
     int steps, nesterov, g_f32, out_f32;
+    int release;         // a later launch of the same call follows
     float mu, eps, a, b, c, keep;
     int* err;
 };
