@@ -502,7 +502,8 @@ int dpred_accumulator_restore(int32_t world, int64_t n, float* acc, const float*
  *       bias_grad [n] fp32 or NULL.
  *
  * An empty reduction (k = 0, or n = 0 in dgrad, m = 0 in wgrad) gives the
- * epilogue of zero.  gelu is the tanh form.  Sums added to an fp32 dw may
+ * epilogue of zero.  gelu is the tanh form.  A NaN in z gives a NaN in act(z)
+ * and in act'(z), relu included; relu'(0) is 0.  Sums added to an fp32 dw may
  * flush results below 2^-126 to zero.  residual may be the output itself
  * (same type and stride); no output may otherwise overlap an input.
  * workspace (device, 16-byte aligned): dpred_linear_workspace_bytes() of the

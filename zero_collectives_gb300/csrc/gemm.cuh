@@ -156,9 +156,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluQ = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 
+// A NaN stays one, in the activations and their gradients.
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-    if constexpr (ACT == ACT_RELU) return z > 0.0f ? z : 0.0f;
+    if constexpr (ACT == ACT_RELU) return z <= 0.0f ? 0.0f : z;
     if constexpr (ACT == ACT_GELU) return z * logistic2(z * fmaf(-kLog2e * kGeluQ * kGeluC, z * z, -kLog2e * kGeluQ));
     if constexpr (ACT == ACT_SILU) return z * logistic2(-kLog2e * z);
     return z;
@@ -166,7 +167,7 @@ __device__ __forceinline__ float activate(float z) {
 
 template <int ACT>
 __device__ __forceinline__ float activate_grad(float z) {
-    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
     if constexpr (ACT == ACT_GELU) {
         // beyond |z| = 1000 the logistic is 0 or 1 exactly; the clamp keeps z^2 finite there
         const float z2 = fminf(z * z, 1e6f);

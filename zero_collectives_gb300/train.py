@@ -150,7 +150,8 @@ def linear(x, w, bias=None, act="none", residual=None, preact=None, out=None, ou
     bf16 or fp32 [n]; residual: bf16 [m, n]; preact: bf16 [m, n], receives
     x w^T + bias (what linear_dgrad of the next layer down needs).  out: bf16
     or fp32 [m, n] (allocated on the call's stream when None).  Rows may be
-    strided; m may be 1 (a single token)."""
+    strided; m may be 1 (a single token).  A NaN before the activation stays
+    one after it, relu included."""
     dev = _device()
     xp, ldx, m, k = _matrix(x, "x", _BF, dev)
     wp, ldw, n, _ = _matrix(w, "w", _BF, dev, None, k)
