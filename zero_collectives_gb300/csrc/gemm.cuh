@@ -772,15 +772,22 @@ __device__ __forceinline__ void tile_at(const Args& g, int t, int bm, int bn, in
 // over up to 8 times as many SMs.
 //
 // fp32 results (regions = 256 / BN) give each part of a CTA's reduction its own
-// accumulator in tensor memory, added in fp32 registers at the end: the tensor
+// accumulator in tensor memory, added in fp32 registers: the tensor
 // cores' accumulators truncate, about 1.9e-8 of the sum per 16-element step.
-
+// A part is at most kPromoteBlocks blocks (512 elements, 6e-7).  Where there are
+// no more parts than accumulators they are added at the end; a longer reduction
+// goes round the accumulators, and the epilogue warps empty one while the
+// issuing thread fills the next (reduction of 98304 into 1024 x 2048: 2.8e-5 off
+// and 341 us from two accumulators, 5.0e-7 and 344 us so; of 1048576 into
+// 256 x 256: 3.8e-5 and 533 us, 5.6e-7 and 533 us).  The sums take up to 128 registers
+// a thread, hence the bound on registers for BN = 128: two CTAs still share an SM.
 //
 // Stages: a copy takes about 1500 cycles from its issue until its stage is free
 // again, so a CTA that has an SM to itself takes all the shared memory (`deep`:
 // a reduction of 640 elements at BN = 32 is in flight at once); launches of
 // more CTAs than SMs use half of it and run two CTAs per SM.
 
+constexpr int kPromoteBlocks = 8;
 constexpr int kSplitThreads = 192;  // producer warp, issuing warp, four epilogue warps
 constexpr int kMaxStages = 10;
 
@@ -823,7 +830,7 @@ __device__ __forceinline__ void cluster_get(uint32_t at, int split, float* t) {
 }
 
 template <int KIND, int BN>
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 128 ? 2 : 0)
     split_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::Param ep) {
     using namespace mma;
@@ -832,7 +839,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     constexpr uint32_t kA = 128 * 128, kStage = kA + BN * 128;
     constexpr uint32_t kCols = 256;  // two CTAs per SM together allocate all 512
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
+    constexpr int R = 256 / BN;  // accumulators
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], filled[R], drained[R], done;
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -843,7 +851,10 @@ __global__ void __launch_bounds__(kSplitThreads)
     tile_at(g, tile - batch * g.tiles_per_batch, 128, BN, tm, tn);
     const int kb0 = (int)((int64_t)g.kblocks * rank / g.split), kb1 = (int)((int64_t)g.kblocks * (rank + 1) / g.split);
     const int nkb = kb1 - kb0;
+    // parts of the reduction: one, or (fp32 results) one per accumulator, or more
     const int regions = min(g.regions, nkb);
+    const int parts = g.regions > 1 ? max(regions, (nkb + kPromoteBlocks - 1) / kPromoteBlocks) : regions;
+    const bool drain = KIND == KIND_LINEAR && parts > regions;
     const bool mirror = g.symmetric && tn * BN >= (tm + 1) * 128;
 
     if (threadIdx.x == 0) {
@@ -854,6 +865,10 @@ __global__ void __launch_bounds__(kSplitThreads)
         for (int s = 0; s < S; ++s) {
             tma::mbar_init(&full[s], 1);
             tma::mbar_init(&empty[s], 1);
+        }
+        for (int r = 0; r < R; ++r) {
+            tma::mbar_init(&filled[r], 1);
+            tma::mbar_init(&drained[r], 4);  // the epilogue warps
         }
         tma::mbar_init(&done, 1);
         tma::fence_barrier_init();
@@ -907,12 +922,20 @@ __global__ void __launch_bounds__(kSplitThreads)
             const uint64_t da0 = operand_desc(base, g.a_mn), db0 = operand_desc(base + kA, g.b_mn);
             const uint32_t sa = g.a_mn ? 128 : 2, sb = g.b_mn ? 128 : 2;  // 16 reduction elements, in 16-byte units
             const uint32_t idesc = instr_desc(128, BN, g.bf16, g.a_mn, g.b_mn);
-            int region = 0, s = 0, round = 0;
-            for (int it = 0; it < nkb; ++it) {
+            int part = 0, region = 0, s = 0, round = 0;
+            for (int it = 0, next = (int)((int64_t)nkb / max(parts, 1)); it < nkb; ++it) {
                 bool first = it == 0;
-                if (region + 1 < regions && it >= nkb * (region + 1) / regions) {
-                    ++region;
+                if (part + 1 < parts && it >= next) {
+                    if (drain) commit<1>(tma::smem_addr(&filled[region]));
+                    ++part;
+                    region = part % R;
+                    next = (int)((int64_t)nkb * (part + 1) / parts);
                     first = true;
+                    if (part >= R && !tma::mbar_wait(&drained[region], (part / R - 1) & 1)) {
+                        record_device_error(g.err, DPRED_E_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
                 }
                 if (!tma::mbar_wait(&full[s], round & 1)) {
                     record_device_error(g.err, DPRED_E_TIMEOUT);
@@ -930,12 +953,37 @@ __global__ void __launch_bounds__(kSplitThreads)
                     ++round;
                 }
             }
-            if (ok && nkb) commit<1>(tma::smem_addr(&done));
+            if (ok && nkb) commit<1>(tma::smem_addr(drain ? &filled[region] : &done));
         }
         __syncwarp();
     } else {
         const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31 belong to this warp
-        if (nkb && !tma::mbar_wait(&done, 0)) {
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        float sum[BN / 32][32];
+        if (drain) {
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+                for (int x = 0; x < 32; ++x) sum[c][x] = 0.0f;
+            for (int part = 0; part < parts; ++part) {
+                const int r = part % R;
+                ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&filled[r], (part / R) & 1));
+                if (!ok) break;
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < BN / 16; ++c) {  // 16 columns: the sums take most of the registers
+                    float v[16];
+                    tmem_ld16(lanes + r * BN + c * 16, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) sum[c / 2][c % 2 * 16 + x] += v[x];
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) tma::mbar_arrive(&drained[r]);
+            }
+            if (!ok) record_device_error(g.err, DPRED_E_TIMEOUT);
+        } else if (nkb && !tma::mbar_wait(&done, 0)) {
             record_device_error(g.err, DPRED_E_TIMEOUT);
             ok = false;
         }
@@ -947,14 +995,22 @@ __global__ void __launch_bounds__(kSplitThreads)
         for (int c0 = 0; c0 < BN; c0 += 32) {
             float v[32];
             __syncwarp();
-            read_regions<BN>(tmem + ((uint32_t)(q * 32) << 16) + c0, ok ? regions : 0, v);
-            const uint32_t block = base + (c0 / 32 * 4 + q) * kBlockBytes;
-            block_put_row(block, lane, v);
-            if (g.split == 1) {
-                __syncwarp();
+            if (drain) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) v[x] = sum[c0 / 32][x];
+            } else {
+                read_regions<BN>(lanes + c0, ok ? regions : 0, v);
+            }
+            block_put_row(base + (c0 / 32 * 4 + q) * kBlockBytes, lane, v);
+        }
+        if (g.split == 1 && ok) {
+            __syncwarp();
+#pragma unroll
+            for (int c0 = 0; c0 < BN; c0 += 32) {
                 Ahead<KIND> ahead;
                 load_ahead<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, lane, ahead);
-                if (ok) block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, block, lane, mirror, ahead);
+                block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, base + (c0 / 32 * 4 + q) * kBlockBytes, lane, mirror,
+                                     ahead);
             }
         }
         fence_before();
@@ -1046,7 +1102,6 @@ __global__ void __launch_bounds__(kSplitThreads)
 // unpacked, 109 with the sums in a launch of their own).
 constexpr int kTileThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
-constexpr int kPromoteBlocks = 8;
 
 //
 // Streaming epilogue (16-byte aligned matrices).  A warp owns 32 rows; a thread
