@@ -1088,18 +1088,23 @@ __global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 12
 // Twelve warps: producer, issuer, two that sum A's rows, eight of the epilogue.
 //
 // Row sums (the bias gradient beside a weight gradient, whose A is dy): the two
-// warps read each stage of A beside the matrix instructions, one 64-row box
+// warps read each stage of A, one 64-row box
 // each, in the tiles of the first tile column; a stage is free once they have
 // arrived as well.  A lane adds 8 rows of A over 16 reduction elements a stage
 // and the stage's sums to its total, so a sum has one fixed order.  Only the even
-// CTA sees the copies land (its barrier counts both CTAs' bytes): it passes
-// that on to the odd one, by an arrival that releases nothing of its own (the
-// bytes are in the odd CTA's memory before the barrier counts them; a releasing
-// one took longer than the stage's products: 250 us for the call below).
+// CTA sees the copies land (its barrier counts both CTAs' bytes), and its warps
+// read beside the matrix instructions.  The odd one's wait for the commit of
+// the stage's products, which arrives in both CTAs: those products were issued
+// by the thread that saw the bytes land, and have read them.  That holds a
+// stage a little longer and costs nothing measurable.  (Passing the even CTA's
+// observation on by an arrival of its own needs a releasing one, which took
+// longer than the stage's products: 250 us for the call below.  A fence over
+// all proxies before the reads, instead of the one over this CTA's shared
+// memory: 205 us.)
 // Unpacked to fp32 and added, the sums took 830 cycles a stage against the
 // products' 600; with adds that take the bf16 half as it is they keep up:
-// [16384, 4096] x [16384, 1024] into fp32 81 us, 90 with the row sums (111
-// unpacked, 109 with the sums in a launch of their own).
+// [16384, 4096] x [16384, 1024] into fp32, cache flushed, 88 us and 98 with the
+// row sums (in a launch of their own they add 28).
 constexpr int kTileThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 
@@ -1232,7 +1237,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t kCols = 2 * BN;
     constexpr int kHalf = BN / 2;  // columns per epilogue warp
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], landed[S], acc_full[2], acc_empty[2], in_full[8];
+    __shared__ __align__(8) uint64_t full[S], empty[S], summed[S], acc_full[2], acc_empty[2], in_full[8];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1247,8 +1252,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         prefetch_map(&mb);
         for (int s = 0; s < S; ++s) {
             tma::mbar_init(&full[s], 1);   // the even CTA's expected bytes (both CTAs' copies)
-            tma::mbar_init(&empty[s], row_sums ? 3 : 1);  // the issuing thread's commit, the summing warps
-            tma::mbar_init(&landed[s], 1);
+            tma::mbar_init(&empty[s], 1);  // the issuing thread's commit
+            tma::mbar_init(&summed[s], 2);  // this CTA's summing warps
         }
         for (int a = 0; a < 2; ++a) {
             tma::mbar_init(&acc_full[a], 1);
@@ -1275,7 +1280,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
                 const int i0 = tm * 256 + (int)rank * 128, j0 = tn * BN + (int)rank * (BN / 2);
                 for (int kb = 0; kb < g.kblocks; ++kb) {
-                    if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
+                    if (round && !(tma::mbar_wait(&empty[s], (round - 1) & 1) &&
+                                   (!row_sums || tma::mbar_wait(&summed[s], (round - 1) & 1)))) {
                         record_device_error(g.err, DPRED_E_TIMEOUT);
                         ok = false;
                         break;
@@ -1350,7 +1356,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp < kEpilogueWarp0) {
         if (row_sums) {
             const int red_group = lane / 8, piece_of = lane % 8;
-            const uint32_t peer = map_rank(tma::smem_addr(&landed[0]), 1);
             int s = 0, round = 0;
             bool ok = true;
             for (int tile = pair; tile < total && ok; tile += pairs) {
@@ -1361,9 +1366,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 float sum[8] = {};
                 for (int kb = 0; kb < g.kblocks; ++kb) {
                     ok = __all_sync(0xFFFFFFFFu, rank == 0 ? tma::mbar_wait(&full[s], round & 1)
-                                                           : mbar_wait_cluster(&landed[s], round & 1));
+                                                           : mbar_wait_cluster(&empty[s], round & 1));
                     if (!ok) break;
-                    if (rank == 0 && warp == 2 && lane == 0) mbar_arrive_cluster(peer + s * 8);
+                    if (rank != 0) {
+                        fence_after();
+                        tma::fence_proxy_async_shared();  // copies wrote what is read next
+                    }
                     if (mine) {
                         const uint32_t box = base + s * kStage + (warp - 2) * 8192;
                         uint4 v[16];
@@ -1384,7 +1392,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) tma::mbar_arrive(&empty[s]);
+                    if (lane == 0) tma::mbar_arrive(&summed[s]);
                     if (++s == S) {
                         s = 0;
                         ++round;
