@@ -550,9 +550,10 @@ int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t 
  * The products run on 16-bit operands (fp16, with the dominant parts kept
  * apart in more bits): X is within about 1e-3 (2-norm, relative) of the exact
  * iteration, so an fp32 out carries that accuracy too.  Norms, sums and accumulators are
- * fp32: |G|_F must be below about 1e19.  A matrix with a NaN or an infinity
+ * fp32: |G|_F must be below about 1e19 (and, with eps = 0, above about 1e-16
+ * unless it is 0).  A matrix with a NaN or an infinity
  * gives an update of NaNs; other matrices of the call are not affected.  A
- * zero matrix gives zero.  The order of every sum is fixed by the sizes and
+ * zero matrix gives zero, with eps = 0 too.  The order of every sum is fixed by the sizes and
  * the number of matrices of a shape, so a call's results are reproducible.
  *
  * Row strides in elements (at least the columns), any size from 0 (long side

@@ -139,6 +139,12 @@ inline int linear_kind(const LinearEpi& e) {
     return e.act || e.pre_out ? KIND_ACT : KIND_PLAIN;
 }
 
+// Factor that brings U to X = scale U / (|U| + eps), from the sum of U's squares.
+// A zero matrix stays zero with eps = 0 too; a NaN in the sum stays one.
+__device__ __forceinline__ float norm_factor(float scale, float squares, float eps) {
+    return squares == 0.0f ? 0.0f : scale / (sqrtf(squares) + eps);
+}
+
 // ------------------------------------------------------------- activations --
 
 // The logistic function of -x / log2(e), 1 / (1 + 2^x), from the hardware's

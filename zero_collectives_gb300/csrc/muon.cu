@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256, 8) scale_kernel(const __grid_constant__ N
     const MatIn& in = a.in[blockIdx.y];
     const Tg* g = static_cast<const Tg*>(in.g);
     const float total = block_sum(threadIdx.x < a.blocks ? a.partial[blockIdx.y * kNormBlocks + threadIdx.x] : 0.0f);
-    const float f = a.scale / (sqrtf(total) + a.eps);
+    const float f = norm_factor(a.scale, total, a.eps);
     const int64_t rows = in.transposed ? a.c : a.r, cols = in.transposed ? a.r : a.c;
     const Pass p(in.transposed);
     const int64_t tr = (rows + 4 * p.step - 1) / (4 * p.step), tc = (cols + p.width - 1) / p.width;

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     }
     // entries of X near 1 (see muon.cu); a power of two
     const float scale = exp2f(rintf(0.5f * log2f((float)c)));
-    const float f = scale / (sqrtf(norm) + a.eps);
+    const float f = norm_factor(scale, norm, a.eps);
 
     // Every thread owns a row (its tensor-memory lane) and columns quarter * 32 + 128 h + 0..31, h = 0, 1.
     const int row = (warp & 3) * 32 + lane, quarter = warp >> 2;
