@@ -558,7 +558,8 @@ int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t 
  *
  * Row strides in elements (at least the columns), any size from 0 (long side
  * up to 2^20, short side up to 65536), any alignment to the element size.
- * `in` and `out` must not overlap; matrices of one dpred_muon_step call must
+ * `in` and `out` must not overlap, nor the matrices of `out` one another (one
+ * after another or side by side in wider rows; else DPRED_E_SIZE); matrices of one dpred_muon_step call must
  * not overlap one another.  Matrices of one shape share launches.  mats: host
  * array, read during the call only.  workspace (device, 256-byte aligned):
  * dpred_newton_schulz_workspace_bytes() / dpred_muon_workspace_bytes() (only

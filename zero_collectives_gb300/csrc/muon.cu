@@ -677,6 +677,20 @@ int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int esiz
     return DPRED_OK;
 }
 
+// Whether two of `batch` matrices that start `stride` elements apart share an
+// element: any layout without one is accepted, side by side in wider rows as
+// well as one after another.
+bool matrices_overlap(int batch, int64_t rows, int64_t cols, int64_t ld, int64_t stride) {
+    if (batch > 1 && stride < cols) return true;
+    if (rows == 1) ld = cols;  // it has no row stride
+    const int64_t last = (rows - 1) * ld;
+    for (int64_t k = 1, d = stride; k < batch && d < last + cols; ++k, d += stride) {
+        const int64_t shift = d / ld, column = d % ld;  // the later matrix against the rows of the earlier one
+        if ((shift < rows && column < cols) || (shift + 1 < rows && ld - column < cols)) return true;
+    }
+    return false;
+}
+
 int check_params(int steps, const float* coeffs, float eps) {
     if (steps < 1 || steps > kMaxSteps) return set_error(DPRED_E_INVAL, "steps %d outside 1..%d", steps, kMaxSteps);
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return set_error(DPRED_E_INVAL, "eps must be finite and not negative");
@@ -730,7 +744,7 @@ extern "C" int dpred_newton_schulz(int32_t batch, int64_t rows, int64_t cols, in
         if ((rc = check_matrix(in, rows, cols, ld, is, "in")) != DPRED_OK || (rc = check_matrix(out, rows, cols, ldo, os, "out")) != DPRED_OK)
             return rc;
         if (batch > 1 && batch_stride < 0) return set_error(DPRED_E_SIZE, "a negative batch stride");
-        if (batch > 1 && out_batch_stride < (rows - 1) * ldo + cols && out_batch_stride < cols)
+        if (matrices_overlap(batch, rows, cols, ldo, out_batch_stride))
             return set_error(DPRED_E_SIZE, "output matrices overlap (batch stride %lld)", (long long)out_batch_stride);
         Params q = {};
         q.g_dtype = in_dtype;
