@@ -99,6 +99,8 @@ def _empty(shape, dtype, stream):
 
 def _workspace(need: int, given, stream):
     if given is not None:
+        if given.get_device() != _device() or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if not need:
         return None, 0, 0
