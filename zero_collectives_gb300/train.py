@@ -217,7 +217,12 @@ def linear_wgrad(dy, x, out, bias_grad=None, accumulate: bool = False, workspace
 
 
 def _coeffs(coeffs):
-    return None if coeffs is None else (ctypes.c_float * 3)(*coeffs)
+    if coeffs is None:
+        return None
+    c = [float(x) for x in coeffs]
+    if len(c) != 3:
+        raise ValueError("coeffs must be (a, b, c)")
+    return (ctypes.c_float * 3)(*c)
 
 
 def newton_schulz(g, out=None, steps: int = 5, eps: float = 1e-7, coeffs=None, workspace=None, stream=None):
