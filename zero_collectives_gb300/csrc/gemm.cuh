@@ -1512,12 +1512,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (lane == 0) tma::bulk_wait_read<0>();
                     __syncwarp();
                 };
-                if (stream && in && !pre && i < g.m && j < g.n) {
+                const bool early = stream && in && !pre && i < g.m && j < g.n;
+                if (early) {
                     box_free();
                     if (lane == 0) request(j);
                 }
                 ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(&acc_full[a], (fill / 2) & 1));
-                if (!ok) break;
+                if (!ok) {
+                    if (early) tma::mbar_wait(in_bar, in_parity);  // no copy may land after this CTA has left
+                    break;
+                }
                 ++fill;
                 fence_after();
                 if (stream) {
@@ -1552,6 +1556,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         if (in) {
                             if ((pre || c) && lane == 0) request(col);
                             arrived();
+                            if (!ok) break;
                             box_combine<KIND>(e, box, lane, 0, v[0]);
                             box_combine<KIND>(e, box, lane, 1, v[1]);
                         }
