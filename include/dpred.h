@@ -479,12 +479,19 @@ int dpred_accumulator_restore(int32_t world, int64_t n, float* acc, const float*
 
 /*
  * Linear-layer products (no counterpart in the pages): what makes the
- * gradients that the calls above reduce.  Operands are bf16; products are
- * exact, sums are fp32 in an order fixed by the sizes alone, and every result
- * is rounded once.  Matrices are row-major with a row stride in elements (at
- * least the number of columns; ignored where there is one row).  Any size from
- * 0 (up to 2^30 - 1) and any alignment to the element size is accepted;
- * operands whose base and row stride are not multiples of 16 bytes are first
+ * gradients that the calls above reduce.  Operands are bf16 and their products
+ * exact.  Sums run in the tensor cores' fp32 accumulators, which truncate
+ * (about 2e-8 of a sum per 16 elements).  An fp32 result adds runs of at most
+ * 512 elements in fp32 (about 5e-7 in the 2-norm, at any length); a bf16 one
+ * keeps one run, which stays below its own rounding up to some 10^6 elements.
+ * The epilogue is fp32, and what is stored is rounded once (a sum that is
+ * added to an output once before).  The order of a sum depends on the device
+ * and on the whole call, its sizes, types and optional arguments (dw's on
+ * whether bias_grad is asked for); the same call gives the same bits.
+ *
+ * Matrices are row-major with a row stride in elements (at least the number of
+ * columns; ignored where there is one row).  Any size from 0 (up to 2^30 - 1)
+ * and any alignment to the element size is accepted; operands whose base and row stride are not multiples of 16 bytes are first
  * copied into `workspace`.
  *
  *   dpred_linear:       z = x w^T + bias;  y = act(z) + residual
@@ -547,26 +554,29 @@ int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t 
  *     with X as above.  Weights are bf16 or fp32 (w_dtype), gradients bf16 or
  *     fp32 (g_dtype), momenta fp32; momentum and weight are updated in place.
  *
- * The products run on 16-bit operands (fp16, with the dominant parts kept
- * apart in more bits): X is within about 1e-3 (2-norm, relative) of the exact
- * iteration, so an fp32 out carries that accuracy too.  Norms, sums and accumulators are
+ * The products run on 16-bit operands (fp16, with the dominant parts kept apart
+ * in more bits).  After five steps X is 2e-4 to 1e-3 (2-norm, relative) off the
+ * exact iteration on gradients as they occur, and at most 2.8e-3 |X|_F + 3e-5
+ * sqrt(short side), whose second term shows only where |G|_F is far below eps;
+ * an fp32 out is no more accurate than that.  Norms, sums and accumulators are
  * fp32: |G|_F must be below about 1e19 (and, with eps = 0, above about 1e-16
- * unless it is 0).  A matrix with a NaN or an infinity
- * gives an update of NaNs; other matrices of the call are not affected.  A
- * zero matrix gives zero, with eps = 0 too.  The order of every sum is fixed by the sizes and
- * the number of matrices of a shape, so a call's results are reproducible.
+ * unless it is 0).  A matrix with a NaN or an infinity gives an update of NaNs;
+ * other matrices of the call are not affected.  A zero matrix gives zero, with
+ * eps = 0 too.  The order of a matrix's sums depends on the device and on the
+ * shapes of all the call's matrices (they decide whether its products run one
+ * by one or chained with the others'); the same call gives the same bits.
  *
- * Row strides in elements (at least the columns), any size from 0 (long side
- * up to 2^20, short side up to 65536), any alignment to the element size.
- * `in` and `out` must not overlap, nor the matrices of `out` one another (one
- * after another or side by side in wider rows; else DPRED_E_SIZE); matrices of one dpred_muon_step call must
- * not overlap one another.  Matrices of one shape share launches.  mats: host
- * array, read during the call only.  workspace (device, 256-byte aligned):
- * dpred_newton_schulz_workspace_bytes() / dpred_muon_workspace_bytes() (only
- * the shapes matter).  Asynchronous on `stream`; may be captured into a CUDA
- * graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN, DPRED_E_SIZE, DPRED_E_CUDA; a
- * bounded device-side wait that gives up records DPRED_E_TIMEOUT in the device
- * error word.
+ * Row strides in elements (at least the columns), any size from 0 (long side up
+ * to 2^20, short side up to 65536), any alignment to the element size. `in` and
+ * `out` must not overlap, nor the matrices of `out` one another (one after
+ * another or side by side in wider rows; else DPRED_E_SIZE); matrices of one
+ * dpred_muon_step call must not overlap one another.  Matrices of one shape
+ * share launches.  mats: host array, read during the call only.  workspace
+ * (device, 256-byte aligned): dpred_newton_schulz_workspace_bytes() /
+ * dpred_muon_workspace_bytes() (only the shapes matter).  Asynchronous on
+ * `stream`; may be captured into a CUDA graph.  Errors: DPRED_E_INVAL,
+ * DPRED_E_ALIGN, DPRED_E_SIZE, DPRED_E_CUDA; a bounded device-side wait that
+ * gives up records DPRED_E_TIMEOUT in the device error word.
  */
 typedef struct {
     int64_t rows, cols;
