@@ -491,8 +491,8 @@ int dpred_accumulator_restore(int32_t world, int64_t n, float* acc, const float*
  *
  * Matrices are row-major with a row stride in elements (at least the number of
  * columns; ignored where there is one row).  Any size from 0 (up to 2^30 - 1)
- * and any alignment to the element size is accepted; operands whose base and row stride are not multiples of 16 bytes are first
- * copied into `workspace`.
+ * and any alignment to the element size is accepted; operands whose base and
+ * row stride are not multiples of 16 bytes are first copied into `workspace`.
  *
  *   dpred_linear:       z = x w^T + bias;  y = act(z) + residual
  *       x [m, k], w [n, k], y [m, n] of out_dtype; bias [n] of bias_dtype,
@@ -510,7 +510,8 @@ int dpred_accumulator_restore(int32_t world, int64_t n, float* acc, const float*
  *
  * An empty reduction (k = 0, or n = 0 in dgrad, m = 0 in wgrad) gives the
  * epilogue of zero.  gelu is the tanh form.  A NaN in z gives a NaN in act(z)
- * and in act'(z), relu included; relu'(0) is 0.  Sums added to an fp32 dw may
+ * and in act'(z), relu included; relu'(0) is 0, and 0 times an
+ * infinity is NaN here as well.  Sums added to an fp32 dw may
  * flush results below 2^-126 to zero.  residual may be the output itself
  * (same type and stride); no output may otherwise overlap an input.
  * workspace (device, 16-byte aligned): dpred_linear_workspace_bytes() of the
