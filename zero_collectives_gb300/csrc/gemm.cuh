@@ -1123,7 +1123,7 @@ constexpr int kEpilogueWarp0 = 4;
 // computes one row, 32 columns at a time, straight from the tensor-memory load,
 // and packs it into a 32-row x 128-byte box of shared memory (128-byte swizzle:
 // no bank conflicts), which one bulk tensor copy writes; the copies' bounds
-// checks take care of ragged edges.  What is read per element (residual, stored
+// checks take care of ragged edges but for a last part of 16 bytes (box_tail).  What is read per element (residual, stored
 // pre-activation) comes in as a box the same way, requested before the
 // accumulator is waited for.  fp32 accumulation is a bulk copy that adds.
 // Against writing global memory from the registers by way of an fp32 block
@@ -1202,6 +1202,36 @@ __device__ __forceinline__ uint4 box_get(uint32_t box, int lane, int c) {
                  : "r"(piece(box, lane, c))
                  : "memory");
     return q;
+}
+
+// A bulk tensor copy writes whole groups of 16 bytes: where a matrix's rows end
+// inside one, it would write past them (zeros, or with an adding copy sums with
+// them).  The maps of the matrices that are written therefore end at the last
+// whole group, column `whole_columns`, and a lane stores (or adds) the up to 7
+// elements behind it from its row of the box that is about to be sent.
+template <typename T>
+__host__ __device__ __forceinline__ constexpr int whole_columns(int cols) {
+    return cols & ~(16 / (int)sizeof(T) - 1);
+}
+
+template <typename T>
+__device__ __forceinline__ void box_tail(T* out, int64_t ld, int rows, int cols, uint32_t box, int lane, int i, int col, bool add) {
+    constexpr int kGroup = 16 / sizeof(T), kBox = 128 / sizeof(T);
+    const int whole = whole_columns<T>(cols);
+    if (whole == cols || col + kBox <= whole || i + lane >= rows) return;
+    const uint4 q = box_get(box, lane, (whole - col) / kGroup);
+    T* p = out + (int64_t)(i + lane) * ld + whole;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < kGroup - 1; ++k) {
+        if (whole + k >= cols) break;
+        if constexpr (sizeof(T) == 4) {
+            const float x = __uint_as_float(w[k]);
+            p[k] = add ? p[k] + x : x;
+        } else {
+            reinterpret_cast<uint16_t*>(p)[k] = (uint16_t)(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
+        }
+    }
 }
 
 template <int KIND>
@@ -1474,9 +1504,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 DPRED_EACH32(sum[c][x] += bias[x];)
                             }
                             block_put_row(box, lane, sum[c]);
+                            box_tail(static_cast<float*>(e.out), e.o_ld, g.m, g.n, box, lane, i, j + c * 32, e.accumulate);
                             tma::fence_proxy_async_shared();
                             __syncwarp();
-                            if (lane == 0) {
+                            if (lane == 0 && j + c * 32 < whole_columns<float>(g.n)) {
                                 if (e.accumulate)
                                     add_box(&tp.out, box, j + c * 32, i, 0);
                                 else
@@ -1504,10 +1535,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     ok = __all_sync(0xFFFFFFFFu, tma::mbar_wait(in_bar, in_parity)) && ok;
                     in_parity ^= 1;
                 };
-                auto send = [&](const CUtensorMap* map, int col) {  // the box, complete, to its matrix
+                auto send = [&](const CUtensorMap* map, void* to, int64_t ld, int col) {  // the box, complete, to its matrix
+                    box_tail(static_cast<__nv_bfloat16*>(to), ld, g.m, g.n, box, lane, i, col, false);
                     tma::fence_proxy_async_shared();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (lane == 0 && col < whole_columns<__nv_bfloat16>(g.n)) {
                         store_box(map, box, col, i, 0);
                         tma::bulk_commit();
                     }
@@ -1552,7 +1584,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             box_free();
                             box_put(box, lane, 0, v[0]);
                             box_put(box, lane, 1, v[1]);
-                            send(&tp.pre, col);
+                            send(&tp.pre, e.pre_out, e.p_ld, col);
                         }
                         box_activate<KIND>(e, v[0]);
                         box_activate<KIND>(e, v[1]);
@@ -1576,7 +1608,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         }
                         box_put(box, lane, 0, v[0]);
                         box_put(box, lane, 1, v[1]);
-                        send(&tp.out, col);
+                        send(&tp.out, e.out, e.o_ld, col);
                     }
                 } else {
 #pragma unroll 1

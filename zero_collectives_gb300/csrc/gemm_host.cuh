@@ -85,9 +85,11 @@ int launch_tiles(const Plan& p, const Shape& sh, const LinearEpi& e, cudaStream_
     t.row_sum_add = p.row_sum_add;
     // what the streaming epilogue covers; block_epilogue does the rest
     t.stream = e.vec && (KIND == KIND_F32 ? !e.z && !e.res && !e.pre_out && !e.act : KIND != KIND_LINEAR && !(e.res && e.z));
+    const int whole = e.out_f32 ? whole_columns<float>(p.args.n) : whole_columns<__nv_bfloat16>(p.args.n);
+    t.stream = t.stream && whole > 0;
     if (t.stream) {
-        rc = make_box_map(e.out, p.args.m, p.args.n, e.o_ld, e.out_f32, &t.out);
-        if (rc == DPRED_OK && e.pre_out) rc = make_box_map(e.pre_out, p.args.m, p.args.n, e.p_ld, false, &t.pre);
+        rc = make_box_map(e.out, p.args.m, whole, e.o_ld, e.out_f32, &t.out);
+        if (rc == DPRED_OK && e.pre_out) rc = make_box_map(e.pre_out, p.args.m, whole, e.p_ld, false, &t.pre);
         if (rc == DPRED_OK && (e.res || e.z))
             rc = e.z ? make_box_map(e.z, p.args.m, p.args.n, e.z_ld, false, &t.in)
                      : make_box_map(e.res, p.args.m, p.args.n, e.r_ld, false, &t.in);
