@@ -1,5 +1,5 @@
 """What the header says about the accuracy of orthogonalised updates: five steps are off by at most 2.8e-3 of
-the result (tests/test_gpu_muon.py derives it) plus an absolute part that shows where |G|_F is far below eps.
+the result (tests/test_gpu_muon.py derives it; for short sides from 16 on) plus an absolute part that shows where |G|_F is far below eps.
 
 The absolute part: X's entries are stored times a power of two s >= sqrt(c / 2) (c the long side) in terms no finer than
 fp16's subnormal spacing, so each of the five stored X is off by at most 2^-25 / s an entry, sqrt(r c) 2^-25 / s <=
