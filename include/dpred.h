@@ -559,9 +559,9 @@ int dpred_linear_wgrad(int64_t m, int64_t n, int64_t k, const void* dy, int64_t 
  * in more bits).  After five steps X is 2e-4 to 1e-3 (2-norm, relative) off the
  * exact iteration on gradients as they occur, and at most 2.8e-3 |X|_F + 3e-5
  * sqrt(short side), whose second term shows only where |G|_F is far below eps.
- * A short side below 16 has too few singular values to average the error, which
- * the iteration can amplify: up to 1e-2 |X|_F there (median 1e-3).  An fp32 out
- * is no more accurate than that.  Norms, sums and accumulators are
+ * A short side or a rank below 16 has too few singular values to average the
+ * error, which the iteration can amplify: up to 1e-2 |X|_F there (median 1e-3).
+ * An fp32 out is no more accurate than that.  Norms, sums and accumulators are
  * fp32: |G|_F must be below about 1e19 (and, with eps = 0, above about 1e-16
  * unless it is 0).  A matrix with a NaN or an infinity gives an update of NaNs;
  * other matrices of the call are not affected.  A zero matrix gives zero, with
