@@ -233,7 +233,9 @@ size_t dpred_flush_workspace_bytes(int32_t world, int32_t n_tasks);
  *    itself, this goes for the flushes before that one too, back to the last
  *    flush without the bit.  Other earlier calls need no promise: only a flush
  *    lets the next call start before it is done itself, so whatever a product
- *    or an update wrote is there, whichever call lies between.  The flush may
+ *    or an update wrote is there, whichever call lies between.  (A kernel of
+ *    another library that releases its dependents early counts as such a
+ *    flush.)  The flush may
  *    then start on the SMs that the previous flush's last wave leaves idle
  *    (programmatic dependent launch); it still completes after that flush, so
  *    the stream's order of completion is unchanged.  Plans that do not fit inside the launch

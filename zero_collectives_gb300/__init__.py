@@ -338,8 +338,8 @@ def flush_bucket(grads, tasks: np.ndarray, owner, dst: DstTable | None, out_dtyp
     """grads: CUDA tensor [W, m] (row stride = ld, e.g. a column slice of the
     whole [W, n] gradient); tasks: TASK_DTYPE array; owner: int32 per param or
     None; dst: DstTable or None (in place).  overlap=True promises that this
-    flush shares no byte with the work just before it on the stream
-    (DPRED_FLUSH_OVERLAP).  Returns a Probe when probe=True."""
+    flush shares no byte with the work just before it on the stream, nor with
+    overlapping flushes right before that (DPRED_FLUSH_OVERLAP).  Returns a Probe when probe=True."""
     shape, strides = grads.shape, grads.stride()
     if len(shape) != 2 or strides[1] != 1:
         raise ValueError("grads must be a 2-D CUDA tensor with unit column stride")
