@@ -786,7 +786,7 @@ __device__ __forceinline__ void tile_at(const Args& g, int t, int bm, int bn, in
 // cores' accumulators truncate, about 1.9e-8 of the sum per 16-element step.
 // A part is at most kPromoteBlocks blocks (512 elements, 6e-7).  Where there are
 // no more parts than accumulators they are added at the end; a longer reduction
-// goes round the accumulators, and the epilogue warps empty one while the
+// (DRAIN: a kernel of its own, its code costs short calls 0.3 us) goes round the accumulators, and the epilogue warps empty one while the
 // issuing thread fills the next (reduction of 98304 into 1024 x 2048: 2.8e-5 off
 // and 341 us from two accumulators, 5.0e-7 and 344 us so; of 1048576 into
 // 256 x 256: 3.8e-5 and 533 us, 5.6e-7 and 533 us).  The sums take up to 128 registers
@@ -839,8 +839,8 @@ __device__ __forceinline__ void cluster_get(uint32_t at, int split, float* t) {
     }
 }
 
-template <int KIND, int BN>
-__global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 128 ? 2 : 0)
+template <int KIND, int BN, bool DRAIN>
+__global__ void __launch_bounds__(kSplitThreads, DRAIN && BN == 128 ? 2 : 0)
     split_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const __grid_constant__ Args g, const __grid_constant__ typename EpiOf<KIND>::Param ep) {
     using namespace mma;
@@ -861,10 +861,9 @@ __global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 12
     tile_at(g, tile - batch * g.tiles_per_batch, 128, BN, tm, tn);
     const int kb0 = (int)((int64_t)g.kblocks * rank / g.split), kb1 = (int)((int64_t)g.kblocks * (rank + 1) / g.split);
     const int nkb = kb1 - kb0;
-    // parts of the reduction: one, or (fp32 results) one per accumulator, or more
+    // parts of the reduction: one, or (fp32 results) one per accumulator, or (DRAIN) more
     const int regions = min(g.regions, nkb);
-    const int parts = g.regions > 1 ? max(regions, (nkb + kPromoteBlocks - 1) / kPromoteBlocks) : regions;
-    const bool drain = KIND == KIND_LINEAR && parts > regions;
+    const int parts = DRAIN ? max(regions, (nkb + kPromoteBlocks - 1) / kPromoteBlocks) : regions;
     const bool mirror = g.symmetric && tn * BN >= (tm + 1) * 128;
 
     if (threadIdx.x == 0) {
@@ -876,10 +875,11 @@ __global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 12
             tma::mbar_init(&full[s], 1);
             tma::mbar_init(&empty[s], 1);
         }
-        for (int r = 0; r < R; ++r) {
-            tma::mbar_init(&filled[r], 1);
-            tma::mbar_init(&drained[r], 4);  // the epilogue warps
-        }
+        if (DRAIN)
+            for (int r = 0; r < R; ++r) {
+                tma::mbar_init(&filled[r], 1);
+                tma::mbar_init(&drained[r], 4);  // the epilogue warps
+            }
         tma::mbar_init(&done, 1);
         tma::fence_barrier_init();
     }
@@ -933,15 +933,15 @@ __global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 12
             const uint32_t sa = g.a_mn ? 128 : 2, sb = g.b_mn ? 128 : 2;  // 16 reduction elements, in 16-byte units
             const uint32_t idesc = instr_desc(128, BN, g.bf16, g.a_mn, g.b_mn);
             int part = 0, region = 0, s = 0, round = 0;
-            for (int it = 0, next = (int)((int64_t)nkb / max(parts, 1)); it < nkb; ++it) {
+            for (int it = 0, next = parts > 1 ? nkb / parts : nkb; it < nkb; ++it) {
                 bool first = it == 0;
-                if (part + 1 < parts && it >= next) {
-                    if (drain) commit<1>(tma::smem_addr(&filled[region]));
+                if (it >= next) {
+                    if (DRAIN) commit<1>(tma::smem_addr(&filled[region]));
                     ++part;
                     region = part % R;
-                    next = (int)((int64_t)nkb * (part + 1) / parts);
+                    next = DRAIN ? (int)((int64_t)nkb * (part + 1) / parts) : nkb * (part + 1) / parts;
                     first = true;
-                    if (part >= R && !tma::mbar_wait(&drained[region], (part / R - 1) & 1)) {
+                    if (DRAIN && part >= R && !tma::mbar_wait(&drained[region], (part / R - 1) & 1)) {
                         record_device_error(g.err, DPRED_E_TIMEOUT);
                         ok = false;
                         break;
@@ -963,14 +963,14 @@ __global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 12
                     ++round;
                 }
             }
-            if (ok && nkb) commit<1>(tma::smem_addr(drain ? &filled[region] : &done));
+            if (ok && nkb) commit<1>(tma::smem_addr(DRAIN ? &filled[region] : &done));
         }
         __syncwarp();
     } else {
         const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31 belong to this warp
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-        float sum[BN / 32][32];
-        if (drain) {
+        float sum[DRAIN ? BN / 32 : 1][32];
+        if constexpr (DRAIN) {
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c)
 #pragma unroll
@@ -1005,23 +1005,27 @@ __global__ void __launch_bounds__(kSplitThreads, KIND == KIND_LINEAR && BN == 12
         for (int c0 = 0; c0 < BN; c0 += 32) {
             float v[32];
             __syncwarp();
-            if (drain) {
+            if constexpr (DRAIN) {
 #pragma unroll
                 for (int x = 0; x < 32; ++x) v[x] = sum[c0 / 32][x];
             } else {
                 read_regions<BN>(lanes + c0, ok ? regions : 0, v);
             }
-            block_put_row(base + (c0 / 32 * 4 + q) * kBlockBytes, lane, v);
-        }
-        if (g.split == 1 && ok) {
-            __syncwarp();
-#pragma unroll
-            for (int c0 = 0; c0 < BN; c0 += 32) {
+            const uint32_t block = base + (c0 / 32 * 4 + q) * kBlockBytes;
+            block_put_row(block, lane, v);
+            if (!DRAIN && g.split == 1) {
+                __syncwarp();
                 Ahead<KIND> ahead;
                 load_ahead<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, lane, ahead);
-                block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, base + (c0 / 32 * 4 + q) * kBlockBytes, lane, mirror,
-                                     ahead);
+                if (ok) block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, block, lane, mirror, ahead);
             }
+        }
+        if (DRAIN && g.split == 1 && ok) {  // after all of them: the sums and an epilogue together take too many registers
+            __syncwarp();
+#pragma unroll
+            for (int c0 = 0; c0 < BN; c0 += 32)
+                block_epilogue<KIND>(e, g, batch, tm * 128 + q * 32, tn * BN + c0, base + (c0 / 32 * 4 + q) * kBlockBytes, lane, mirror,
+                                     Ahead<KIND>());
         }
         fence_before();
     }

@@ -26,10 +26,14 @@ double estimate(const Args& a, bool fp32);  // time of the chosen shape, us
 // Whether a split launch gives every CTA an SM of its own (eight-CTA clusters do not fit every SM of a GPC).
 bool split_alone(double ctas, int split, int sms);
 
-template <int KIND, int BN>
+template <int KIND, int BN, bool DRAIN = false>
 int launch_split(const Plan& p, const Shape& sh, const typename EpiOf<KIND>::Param& e, cudaStream_t s) {
+    if constexpr (is_linear(KIND) && !DRAIN) {  // fp32 results of more parts than a CTA has accumulators
+        if (p.fp32_result && (p.args.kblocks + sh.split - 1) / sh.split > kPromoteBlocks * (256 / BN))
+            return launch_split<KIND, BN, true>(p, sh, e, s);
+    }
     static bool attr[64] = {};
-    auto kernel = split_kernel<KIND, BN>;
+    auto kernel = split_kernel<KIND, BN, DRAIN>;
     cudaError_t err = ensure_smem_attr(kernel, split_smem<BN>(true), attr);
     if (err != cudaSuccess) return cuda_error(err, "shared-memory limit of a matrix product");
     CUtensorMap ma = {}, mb = {};
