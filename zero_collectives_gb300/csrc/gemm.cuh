@@ -1102,23 +1102,24 @@ __global__ void __launch_bounds__(kSplitThreads, DRAIN && BN == 128 ? 2 : 0)
 // Twelve warps: producer, issuer, two that sum A's rows, eight of the epilogue.
 //
 // Row sums (the bias gradient beside a weight gradient, whose A is dy): the two
-// warps read each stage of A, one 64-row box
-// each, in the tiles of the first tile column; a stage is free once they have
-// arrived as well.  A lane adds 8 rows of A over 16 reduction elements a stage
-// and the stage's sums to its total, so a sum has one fixed order.  Only the even
-// CTA sees the copies land (its barrier counts both CTAs' bytes), and its warps
-// read beside the matrix instructions.  The odd one's wait for the commit of
-// the stage's products, which arrives in both CTAs: those products were issued
-// by the thread that saw the bytes land, and have read them.  That holds a
-// stage a little longer and costs nothing measurable.  (Passing the even CTA's
+// warps read each stage of A, one 64-row box each, in the tiles of the first
+// tile column; a stage is free once they have arrived as well.  A lane adds 8
+// rows of A over 16 reduction elements a stage and the stage's sums to its
+// total, so a sum has one fixed order.  Only the even CTA sees the copies land
+// (its barrier counts both CTAs' bytes), and its warps read beside the matrix
+// instructions.  The odd one's wait for a commit of the stage's products, which
+// arrives in both CTAs on a barrier of its own: those products were issued by
+// the thread that saw the bytes land, and have read them.  That holds a stage a
+// little longer and costs nothing measurable.  (Passing the even CTA's
 // observation on by an arrival of its own needs a releasing one, which took
 // longer than the stage's products: 250 us for the call below.  A fence over
 // all proxies before the reads, instead of the one over this CTA's shared
-// memory: 205 us.)
+// memory: 205 us.  A second wait in the producer, instead of the second commit:
+// 3-5% on short products without row sums.)
 // Unpacked to fp32 and added, the sums took 830 cycles a stage against the
 // products' 600; with adds that take the bf16 half as it is they keep up:
-// [16384, 4096] x [16384, 1024] into fp32, cache flushed, 88 us and 98 with the
-// row sums (in a launch of their own they add 28).
+// [16384, 4096] x [16384, 1024] into fp32, cache flushed, 84-88 us and 98 with
+// the row sums (in a launch of their own they add 28).
 constexpr int kTileThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 
@@ -1223,17 +1224,17 @@ __device__ __forceinline__ void box_tail(T* out, int64_t ld, int rows, int cols,
     constexpr int kGroup = 16 / sizeof(T), kBox = 128 / sizeof(T);
     const int whole = whole_columns<T>(cols);
     if (whole == cols || col + kBox <= whole || i + lane >= rows) return;
-    const uint4 q = box_get(box, lane, (whole - col) / kGroup);
-    T* p = out + (int64_t)(i + lane) * ld + whole;
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < kGroup - 1; ++k) {
-        if (whole + k >= cols) break;
+    T* p = out + (int64_t)(i + lane) * ld;
+#pragma unroll 1  // seldom run: short code matters more
+    for (int c = whole; c < cols; ++c) {
+        const uint32_t at = piece(box, lane, (c - col) / kGroup) + (c - col) % kGroup * (int)sizeof(T);
         if constexpr (sizeof(T) == 4) {
-            const float x = __uint_as_float(w[k]);
-            p[k] = add ? p[k] + x : x;
+            const float x = lds1(at);
+            p[c] = add ? p[c] + x : x;
         } else {
-            reinterpret_cast<uint16_t*>(p)[k] = (uint16_t)(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+            reinterpret_cast<uint16_t*>(p)[c] = x;
         }
     }
 }
@@ -1281,7 +1282,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t kCols = 2 * BN;
     constexpr int kHalf = BN / 2;  // columns per epilogue warp
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], summed[S], acc_full[2], acc_empty[2], in_full[8];
+    __shared__ __align__(8) uint64_t full[S], empty[S], consumed[S], acc_full[2], acc_empty[2], in_full[8];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1296,8 +1297,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         prefetch_map(&mb);
         for (int s = 0; s < S; ++s) {
             tma::mbar_init(&full[s], 1);   // the even CTA's expected bytes (both CTAs' copies)
-            tma::mbar_init(&empty[s], 1);  // the issuing thread's commit
-            tma::mbar_init(&summed[s], 2);  // this CTA's summing warps
+            tma::mbar_init(&empty[s], row_sums ? 3 : 1);  // the issuing thread's commit, this CTA's summing warps
+            tma::mbar_init(&consumed[s], 1);  // another commit of the same products, for the odd CTA's summing warps
         }
         for (int a = 0; a < 2; ++a) {
             tma::mbar_init(&acc_full[a], 1);
@@ -1324,8 +1325,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tile_at(g, tile - batch * g.tiles_per_batch, 256, BN, tm, tn);
                 const int i0 = tm * 256 + (int)rank * 128, j0 = tn * BN + (int)rank * (BN / 2);
                 for (int kb = 0; kb < g.kblocks; ++kb) {
-                    if (round && !(tma::mbar_wait(&empty[s], (round - 1) & 1) &&
-                                   (!row_sums || tma::mbar_wait(&summed[s], (round - 1) & 1)))) {
+                    if (round && !tma::mbar_wait(&empty[s], (round - 1) & 1)) {
                         record_device_error(g.err, DPRED_E_TIMEOUT);
                         ok = false;
                         break;
@@ -1387,6 +1387,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for (int k = 0; k < kBlockK / 16; ++k)
                             issue<2>(tmem + a * BN, da + k * sa, db + k * sb, idesc, kb != first || k != 0);
                         commit<2>(tma::smem_addr(&empty[s]));
+                        if (row_sums) commit<2>(tma::smem_addr(&consumed[s]));
                         if (++s == S) {
                             s = 0;
                             ++round;
@@ -1410,7 +1411,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 float sum[8] = {};
                 for (int kb = 0; kb < g.kblocks; ++kb) {
                     ok = __all_sync(0xFFFFFFFFu, rank == 0 ? tma::mbar_wait(&full[s], round & 1)
-                                                           : mbar_wait_cluster(&empty[s], round & 1));
+                                                           : mbar_wait_cluster(&consumed[s], round & 1));
                     if (!ok) break;
                     if (rank != 0) {
                         fence_after();
@@ -1436,7 +1437,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) tma::mbar_arrive(&summed[s]);
+                    if (lane == 0) tma::mbar_arrive(&empty[s]);
                     if (++s == S) {
                         s = 0;
                         ++round;
