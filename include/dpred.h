@@ -58,8 +58,8 @@ extern "C" {
 #define DPRED_E_MISMATCH (-4) /* checked mode: destinations disagree with the owner map */
 #define DPRED_E_CUDA (-5)     /* a CUDA runtime call failed */
 #define DPRED_E_TIMEOUT (-6)  /* a device-side bounded wait gave up (reported by dpred_device_status) */
-#define DPRED_E_BOUNDS (-7)   /* checked build: a kernel access failed its bounds test and was skipped
-                                 (reported by dpred_device_status) */
+#define DPRED_E_BOUNDS (-7)   /* a token id outside the embedding, or (checked build) a kernel access that failed its
+                                 bounds test; either access was skipped (reported by dpred_device_status) */
 
 /* element types */
 #define DPRED_BF16 0
@@ -603,6 +603,124 @@ size_t dpred_muon_workspace_bytes(const dpred_muon_matrix* mats, int32_t n);
 int dpred_muon_step(const dpred_muon_matrix* mats, int32_t n, int32_t w_dtype, int32_t g_dtype, float lr,
                     float momentum, int32_t nesterov, float weight_decay, int32_t steps, const float* coeffs,
                     float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Token embedding (no counterpart in the pages): the first operator of a
+ * training step, and the largest gradient that a flush reduces.
+ *
+ *   dpred_embedding:      y[t] = scale w[id(t)]
+ *       ids [t] of id_bytes bytes (4 or 8, signed), w [v, d] of w_dtype, y [t, d]
+ *       of out_dtype.
+ *   dpred_embedding_grad: dw[k] = scale * (sum of dy[t] over the t with id(t) = k)
+ *       for every row k (zeros where no token is); with accumulate != 0 it is
+ *       added to what dw holds, and rows without a token are not touched.
+ *       dy [t, d] of g_dtype, dw [v, d] of out_dtype (bf16: the gradient row a
+ *       flush reads; fp32: the accumulator of the deferred reduction).  Tokens
+ *       whose id is `padding` give no gradient (-1: no such id).
+ *
+ * Rows are summed in fp32, in ascending t (in stretches of the sorted order
+ * whose sums are added in ascending order): the same call gives the same bits.
+ * What is stored is rounded once, after the scale and the value added to.  An id
+ * outside 0..v-1 (and not padding) reads and writes nothing: its row of y is
+ * zero, it gives no gradient, and DPRED_E_BOUNDS is recorded in the device error
+ * word.  Row strides in elements (at least d), any size from 0 (t and v up to
+ * 2^30 - 1, d up to 2^20), any alignment to the element size; w, dy and dw must
+ * not overlap an output.  workspace (device, 256-byte aligned):
+ * dpred_embedding_grad_workspace_bytes().  Asynchronous on `stream`; may be
+ * captured into a CUDA graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN,
+ * DPRED_E_SIZE, DPRED_E_CUDA.
+ */
+int dpred_embedding(int64_t t, int64_t v, int64_t d, int32_t id_bytes, const void* ids, int32_t w_dtype, const void* w,
+                    int64_t ldw, float scale, int32_t out_dtype, void* y, int64_t ldy, void* stream);
+size_t dpred_embedding_grad_workspace_bytes(int64_t t, int64_t v, int64_t d);
+int dpred_embedding_grad(int64_t t, int64_t v, int64_t d, int32_t id_bytes, const void* ids, int64_t padding,
+                         int32_t g_dtype, const void* dy, int64_t lddy, float scale, int32_t accumulate,
+                         int32_t out_dtype, void* dw, int64_t lddw, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Norms, gate and residual sum between two blocks (no counterpart in the
+ * pages).  With N(a, w) = w a / sqrt(mean(a^2) + eps), row by row:
+ *
+ *   dpred_block_norm:      u = N(y, post)         (y without post)
+ *                          r = scale x + gate u   (u without gate)
+ *                          h = N(r, pre)          (not formed without pre)
+ *       x, r [m, d] of r_dtype; y, h [m, d] bf16; post, pre [d] and gate
+ *       [gate_rows, d] of their types or NULL.  gate_rows divides m: row i takes
+ *       gate row i / (m / gate_rows) (1: a gate per channel; m: one per token).
+ *       y NULL: r is x and is not written, scale must be 1 and pre given.
+ *   dpred_block_norm_grad: with g = dr + (gradient of N(r, pre) to r from dh):
+ *       dx = scale g, dy = gradient of N(y, post) to y from gate g, and the
+ *       gradients of post, gate and pre, each NULL where it is not wanted; with
+ *       accumulate != 0 these three are added to what the outputs hold.
+ *       r, dr, dx [m, d] of r_dtype, dh, y, dy [m, d] bf16, the weight gradients
+ *       of grad_dtype, shaped as the weights, rows of the gate's back to back.
+ *       dr NULL: no gradient from above (then pre is needed); r and dh are read
+ *       only where pre is given, y and dy only where y is.
+ *
+ * Everything is formed in fp32 and each output rounded once; h is the norm of r
+ * before its rounding, the gradient that of the stored r.  Sums over rows have a
+ * fixed order that depends on the device and the sizes: the same call gives the
+ * same bits.  The mean of a row's squares must stay below 3e38 (elements below
+ * about 1e19); with eps = 0 a row of zeros gives NaN.  A NaN or an infinity stays in its row
+ * and in the weight gradients.  Row strides in elements (at least d), any m from
+ * 0 up to 2^31 - 1 and d up to 16384, any alignment to the element size.  An output
+ * matrix may be an input of the same type and stride; no output may otherwise
+ * overlap an input or another output.  workspace (device, 256-byte aligned):
+ * dpred_block_norm_grad_workspace_bytes() (gate_rows 0 without a gate), needed
+ * for weight gradients only.  Asynchronous on `stream`; may be captured into a
+ * CUDA graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN, DPRED_E_SIZE, DPRED_E_CUDA.
+ */
+int dpred_block_norm(int64_t m, int64_t d, int32_t r_dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                     int32_t post_dtype, const void* post, int32_t gate_dtype, const void* gate, int64_t gate_rows,
+                     float scale, int32_t pre_dtype, const void* pre, float eps, void* r, int64_t ldr, void* h,
+                     int64_t ldh, void* stream);
+size_t dpred_block_norm_grad_workspace_bytes(int64_t m, int64_t d, int64_t gate_rows);
+int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, const void* r, int64_t ldr, const void* dr,
+                          int64_t lddr, const void* dh, int64_t lddh, const void* y, int64_t ldy, int32_t post_dtype,
+                          const void* post, int32_t gate_dtype, const void* gate, int64_t gate_rows, float scale,
+                          int32_t pre_dtype, const void* pre, float eps, void* dx, int64_t lddx, void* dy,
+                          int64_t lddy, int32_t grad_dtype, void* post_grad, void* gate_grad, void* pre_grad,
+                          int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Global gradient norm and clipping (no counterpart in the pages): between the
+ * reduction and the update.
+ *
+ *   dpred_grad_norm:  norm[0] = sqrt(sum of g^2 over the counted gradients)
+ *   dpred_clip_grads: result[0] = that norm, result[1] = c =
+ *       min(1, max_norm / (norm + eps)), and every gradient, counted or not, is
+ *       replaced by c g (where c is 1 none is written).
+ *
+ * counted: 1, or 0 for a further copy of a gradient, such as those that the
+ * holders of a straddling parameter have: it is scaled and does not enter the
+ * norm.  Types may be mixed.  The sum takes squares over the whole range of the
+ * types (no overflow or underflow below the norm's own) and is within 1e-6 of
+ * the norm; its order depends on the device and the shapes; the same call gives the same
+ * bits.  An infinity among the counted gradients gives the norm infinity and
+ * c = 0 (finite values become 0, infinities NaN), a NaN gives NaN everywhere.
+ * No counted gradient: norm 0, c = 1.
+ *
+ * grads: host array, read during the call only; row strides in elements (at least
+ * cols), any size from 0 (rows up to 2^31 - 1, cols up to 2^40), any alignment to
+ * the element size; what lies between rows is not touched.  dpred_clip_grads
+ * refuses gradients that share memory (DPRED_E_SIZE; matrices side by side in
+ * wider rows do not).  norm, result: device, fp32.  workspace (device, 256-byte
+ * aligned): dpred_clip_workspace_bytes(n).  Asynchronous on `stream`; may be
+ * captured into a CUDA graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN,
+ * DPRED_E_SIZE, DPRED_E_CUDA.
+ */
+typedef struct {
+    void* data;      /* device, [rows, cols] of dtype */
+    int64_t rows, cols, ld;
+    int32_t dtype;
+    int32_t counted; /* 1, or 0: scaled only */
+} dpred_grad_tensor;
+size_t dpred_clip_workspace_bytes(int32_t n);
+int dpred_grad_norm(const dpred_grad_tensor* grads, int32_t n, float* norm, void* workspace, size_t workspace_bytes,
+                    void* stream);
+int dpred_clip_grads(const dpred_grad_tensor* grads, int32_t n, float max_norm, float eps, float* result,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * ReduceScatter.  [AG] "与 ReduceScatter 的对偶关系" (duality table: M

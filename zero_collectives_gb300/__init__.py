@@ -15,7 +15,9 @@ from dataclasses import dataclass
 
 import numpy as np
 
-from . import train
+from . import layers, train
+from .layers import (GradClip, block_norm, block_norm_grad, clip_grads, embedding, embedding_grad,  # noqa: F401
+                     grad_norm)
 from .train import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, Muon, linear, linear_dgrad, linear_wgrad,  # noqa: F401
                     muon_step, newton_schulz, update_scale)
 
@@ -115,6 +117,7 @@ def lib() -> ctypes.CDLL:
         L.dpred_host_mapped_pointer.argtypes = [vp, ctypes.POINTER(vp)]
         L.dpred_executor_flush_all_mapped.argtypes = L.dpred_executor_flush_all_from_host.argtypes
         train.declare(L)
+        layers.declare(L)
         _lib = L
     return _lib
 
@@ -874,6 +877,19 @@ class Zero1Executor:
         self._bind(grads)
         _check(lib().dpred_executor_flush(self._native, int(bucket), None, _stream(stream)))
 
+    def grad_clip(self, eps: float = 1e-6) -> GradClip:
+        """The reduced gradients of a step, to be clipped together: every parameter
+        of the buckets counts once, and all delivered buffers are scaled."""
+        grads, copies = [], []
+        for _, tasks in self.buckets:
+            for p in tasks["param_id"]:
+                o, lo, hi = int(self.omap.owner[p]), int(self.omap.holder_lo[p]), int(self.omap.holder_hi[p])
+                held = [self.grad.view(r, int(p)) for r in ([o] if o >= 0 else range(lo, hi + 1))]
+                held = [g for g in held if g is not None]
+                grads += held[:1]
+                copies += held[1:]
+        return GradClip(grads, copies, eps)
+
     def flush_all_from_host(self, host_grads, host_bufs, grads, stream=None, probe: bool = False):
         """One step with host buffers: host_grads (pinned [W, n]) is copied into
         grads bucket by bucket, every bucket is flushed, and each rank's
@@ -957,6 +973,19 @@ class InPlaceExecutor(Zero1Executor):
     def _regions(self):
         raise DpredError(-1, "host-buffer steps need destination buffers (in-place executor)")
 
+    def grad_clip(self, grads, eps: float = 1e-6) -> GradClip:
+        """The reduced gradients in the rows of grads ([W, n]), to be clipped
+        together: an owned parameter's in its owner's row, another's in every row,
+        counted once."""
+        counted, copies = [], []
+        for start, tasks in self.buckets:
+            for t in tasks:
+                at, o = start + int(t["offset"]), int(self.omap.owner[t["param_id"]])
+                held = [grads[r, at:at + int(t["numel"])] for r in ([o] if o >= 0 else range(self.world))]
+                counted += held[:1]
+                copies += held[1:]
+        return GradClip(counted, copies, eps)
+
 
 class PartitionedExecutor(Zero1Executor):
     """The executor over partitioned flushes (dpred_executor_create_partitioned):
@@ -983,6 +1012,7 @@ class PartitionedExecutor(Zero1Executor):
             [torch.empty(self.part_size, dtype=dtype, device="cuda") for _ in range(world)]
         if len(self.parts) != world or any(p.numel() < self.part_size for p in self.parts):
             raise ValueError(f"one partition buffer of {self.part_size} elements per rank")
+        self.total = total
         self.buckets = [(int(s), np.ascontiguousarray(t, dtype=TASK_DTYPE)) for s, t in buckets]
         self.sizes = [int((t["offset"] + t["numel"]).max()) if len(t) else 0 for _, t in self.buckets]
         self.probe_log = probe_log
@@ -1004,3 +1034,9 @@ class PartitionedExecutor(Zero1Executor):
 
     def _regions(self):
         return self.parts
+
+    def grad_clip(self, eps: float = 1e-6) -> GradClip:
+        """The partitions, to be clipped together (the buckets must cover every
+        parameter; what lies behind the last one stays as it is)."""
+        sizes = [min(self.part_size, max(0, self.total - r * self.part_size)) for r in range(self.world)]
+        return GradClip([p[:n] for p, n in zip(self.parts, sizes)], (), eps)

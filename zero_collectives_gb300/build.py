@@ -26,7 +26,7 @@ LINEAR_UNITS = [f"linear_{k}.cu" for k in ("any", "plain", "act", "grad", "f32")
 SOURCES = ["abi.cu", "flush_dispatch.cu", *FLUSH_UNITS, "accumulate.cu", "allgather.cu", "noalloc.cu", "selftest.cu",
            "relayout.cu", "schedule.cu", "owner_map.cu", "executor.cu", "ceiling.cu", "gemm.cu", "linear.cu",
            *LINEAR_UNITS, "muon.cu", "muon_small.cu",
-           "muon_chain.cu"]
+           "muon_chain.cu", "clip.cu", "embedding.cu", "block_norm.cu", "block_norm_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", *ARCH, "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-I", CSRC]

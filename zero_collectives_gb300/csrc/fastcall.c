@@ -8,7 +8,8 @@
  * a capsule, and flush() passes them on together with the per-call stream and
  * probe.  call() makes one unprepared call from plain integers, for the
  * binding's flush_bucket; linear(), linear_dgrad() and linear_wgrad() do the
- * same for the linear-layer products.  The function called is the library's own dpred_flush_bucket, whose
+ * same for the linear-layer products, embedding() and the others below them for the
+ * rest of a training step.  The function called is the library's own dpred_flush_bucket, whose
  * address the Python binding hands over (the library is loaded once, by the
  * binding, so the plan cache and the error state are the ones every other
  * call uses).  This module adds no arithmetic: argument marshalling only.
@@ -269,7 +270,127 @@ static PyObject* linear_wgrad(PyObject* self, PyObject* const* args, Py_ssize_t 
     return PyLong_FromLong(rc);
 }
 
+/* As integers(), for entry points with floating arguments: bit i of `reals` says
+ * that argument i is one (it goes to r[i]). */
+#define DPRED_MAX_ARGS 36
+static int numbers(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want, unsigned long long reals, long long* v, double* r) {
+    if (nargs != want) {
+        PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", want, nargs);
+        return -1;
+    }
+    for (Py_ssize_t i = 0; i < want; ++i) {
+        if (reals >> i & 1) {
+            r[i] = PyFloat_AsDouble(args[i]);
+            if (r[i] == -1.0 && PyErr_Occurred()) return -1;
+        } else {
+            v[i] = PyLong_AsLongLong(args[i]);
+            if (v[i] == -1 && PyErr_Occurred()) return -1;
+        }
+    }
+    if (!v[0]) {
+        PyErr_SetString(PyExc_ValueError, "null function address");
+        return -1;
+    }
+    return 0;
+}
+#define DPRED_F32(i) ((float)r[i])
+
+static PyObject* embedding(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_ARGS];
+    double r[DPRED_MAX_ARGS];
+    if (numbers(args, nargs, 14, 1ull << 9, v, r)) return NULL;
+    int (*fn)(int64_t, int64_t, int64_t, int32_t, const void*, int32_t, const void*, int64_t, float, int32_t, void*, int64_t,
+              void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], v[3], DPRED_I32(4), DPRED_PTR(5), DPRED_I32(6), DPRED_PTR(7), v[8], DPRED_F32(9), DPRED_I32(10),
+            DPRED_PTR(11), v[12], DPRED_PTR(13));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* embedding_grad(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_ARGS];
+    double r[DPRED_MAX_ARGS];
+    if (numbers(args, nargs, 18, 1ull << 10, v, r)) return NULL;
+    int (*fn)(int64_t, int64_t, int64_t, int32_t, const void*, int64_t, int32_t, const void*, int64_t, float, int32_t, int32_t, void*,
+              int64_t, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], v[3], DPRED_I32(4), DPRED_PTR(5), v[6], DPRED_I32(7), DPRED_PTR(8), v[9], DPRED_F32(10), DPRED_I32(11),
+            DPRED_I32(12), DPRED_PTR(13), v[14], DPRED_PTR(15), (size_t)v[16], DPRED_PTR(17));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* block_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_ARGS];
+    double r[DPRED_MAX_ARGS];
+    if (numbers(args, nargs, 22, 1ull << 13 | 1ull << 16, v, r)) return NULL;
+    int (*fn)(int64_t, int64_t, int32_t, const void*, int64_t, const void*, int64_t, int32_t, const void*, int32_t, const void*, int64_t,
+              float, int32_t, const void*, float, void*, int64_t, void*, int64_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], DPRED_I32(3), DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_I32(8), DPRED_PTR(9), DPRED_I32(10), DPRED_PTR(11),
+            v[12], DPRED_F32(13), DPRED_I32(14), DPRED_PTR(15), DPRED_F32(16), DPRED_PTR(17), v[18], DPRED_PTR(19), v[20], DPRED_PTR(21));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* block_norm_grad(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_ARGS];
+    double r[DPRED_MAX_ARGS];
+    if (numbers(args, nargs, 33, 1ull << 17 | 1ull << 20, v, r)) return NULL;
+    int (*fn)(int64_t, int64_t, int32_t, const void*, int64_t, const void*, int64_t, const void*, int64_t, const void*, int64_t, int32_t,
+              const void*, int32_t, const void*, int64_t, float, int32_t, const void*, float, void*, int64_t, void*, int64_t, int32_t,
+              void*, void*, void*, int32_t, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(v[1], v[2], DPRED_I32(3), DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_PTR(8), v[9], DPRED_PTR(10), v[11], DPRED_I32(12),
+            DPRED_PTR(13), DPRED_I32(14), DPRED_PTR(15), v[16], DPRED_F32(17), DPRED_I32(18), DPRED_PTR(19), DPRED_F32(20), DPRED_PTR(21),
+            v[22], DPRED_PTR(23), v[24], DPRED_I32(25), DPRED_PTR(26), DPRED_PTR(27), DPRED_PTR(28), DPRED_I32(29), DPRED_PTR(30),
+            (size_t)v[31], DPRED_PTR(32));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* grad_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_ARGS];
+    double r[DPRED_MAX_ARGS];
+    if (numbers(args, nargs, 7, 0, v, r)) return NULL;
+    int (*fn)(const dpred_grad_tensor*, int32_t, float*, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(DPRED_PTR(1), DPRED_I32(2), DPRED_PTR(3), DPRED_PTR(4), (size_t)v[5], DPRED_PTR(6));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+static PyObject* clip_grads(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    long long v[DPRED_MAX_ARGS];
+    double r[DPRED_MAX_ARGS];
+    if (numbers(args, nargs, 9, 1ull << 3 | 1ull << 4, v, r)) return NULL;
+    int (*fn)(const dpred_grad_tensor*, int32_t, float, float, float*, void*, size_t, void*) = DPRED_PTR(0);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(DPRED_PTR(1), DPRED_I32(2), DPRED_F32(3), DPRED_F32(4), DPRED_PTR(5), DPRED_PTR(6), (size_t)v[7], DPRED_PTR(8));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 static PyMethodDef kMethods[] = {
+    {"embedding", (PyCFunction)(void (*)(void))embedding, METH_FASTCALL, "One dpred_embedding call from numbers."},
+    {"embedding_grad", (PyCFunction)(void (*)(void))embedding_grad, METH_FASTCALL, "One dpred_embedding_grad call from numbers."},
+    {"block_norm", (PyCFunction)(void (*)(void))block_norm, METH_FASTCALL, "One dpred_block_norm call from numbers."},
+    {"block_norm_grad", (PyCFunction)(void (*)(void))block_norm_grad, METH_FASTCALL, "One dpred_block_norm_grad call from numbers."},
+    {"grad_norm", (PyCFunction)(void (*)(void))grad_norm, METH_FASTCALL, "One dpred_grad_norm call from numbers."},
+    {"clip_grads", (PyCFunction)(void (*)(void))clip_grads, METH_FASTCALL, "One dpred_clip_grads call from numbers."},
     {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, "One dpred_linear call from integers."},
     {"linear_dgrad", (PyCFunction)(void (*)(void))linear_dgrad, METH_FASTCALL, "One dpred_linear_dgrad call from integers."},
     {"linear_wgrad", (PyCFunction)(void (*)(void))linear_wgrad, METH_FASTCALL, "One dpred_linear_wgrad call from integers."},
