@@ -23,10 +23,11 @@ LIB_CHECKED = os.path.join(HERE, "libdpred_checked.so")
 OBJDIR_CHECKED = os.path.join(HERE, "_build_checked")
 FLUSH_UNITS = [f"flush_w{w}.cu" for w in (*(str(w) for w in range(2, 17)), "gen", "gen32", "genx")]
 LINEAR_UNITS = [f"linear_{k}.cu" for k in ("any", "plain", "act", "grad", "f32")]
+NORM_GRAD_UNITS = [f"block_norm_grad_{t}_{k}.cu" for t in ("bf16", "f32") for k in ("whole", "part")]
 SOURCES = ["abi.cu", "flush_dispatch.cu", *FLUSH_UNITS, "accumulate.cu", "allgather.cu", "noalloc.cu", "selftest.cu",
            "relayout.cu", "schedule.cu", "owner_map.cu", "executor.cu", "ceiling.cu", "gemm.cu", "linear.cu",
            *LINEAR_UNITS, "muon.cu", "muon_small.cu",
-           "muon_chain.cu", "clip.cu", "embedding.cu", "block_norm.cu", "block_norm_grad.cu"]
+           "muon_chain.cu", "clip.cu", "embedding.cu", "block_norm.cu", "block_norm_grad.cu", *NORM_GRAD_UNITS]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", *ARCH, "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-I", CSRC]

@@ -27,6 +27,8 @@ struct ForwardArgs {
     float scale, eps;
 };
 
+// Few rows, or rows without 16-byte alignment: a row group loads its row itself,
+// up to 8 columns a thread where they are enough.
 template <typename T, bool VEC, int VPT>
 __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ ForwardArgs a, int lanes) {
     mma::grid_wait();
@@ -36,79 +38,211 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
     for (int64_t row = (int64_t)blockIdx.x * groups + group; row < a.m; row += (int64_t)gridDim.x * groups) {
         Cols<T, VEC> x[VPT];
         Cols<__nv_bfloat16, VEC> y[VPT];
+        F8 gate, pre;
+        const int64_t gate_row = a.per_gate == a.m ? 0 : a.per_gate == 1 ? row : (uint32_t)row / (uint32_t)a.per_gate;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) x[v].load(static_cast<const T*>(a.x) + row * a.ldx, first<VEC>(v, id, lanes), lanes, a.d);
-        float r[VPT][8];
+        for (int v = 0; v < VPT; ++v) {
+            const int c0 = first<VEC>(v, id, lanes);
+            if (a.y) y[v].load(a.y + row * a.ldy, c0, lanes, a.d);
+            x[v].load(static_cast<const T*>(a.x) + row * a.ldx, c0, lanes, a.d);
+            if (VPT == 1 && a.gate.p) gate = a.gate.load<VEC>(gate_row, c0, lanes, a.d);
+            if (VPT == 1 && a.post.p) {
+                const F8 post = a.post.load<VEC>(0, c0, lanes, a.d);
+                gate = a.gate.p ? post * gate : post;
+            }
+            if (VPT == 1 && a.pre.p) pre = a.pre.load<VEC>(0, c0, lanes, a.d);
+        }
+        F8 r[VPT];
         if (a.y) {
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) y[v].load(a.y + row * a.ldy, first<VEC>(v, id, lanes), lanes, a.d);
             float iy = 1.0f;
             if (a.post.p) {
-                float s[1] = {};
+                float2 t = {};
 #pragma unroll
-                for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) s[0] = fmaf(y[v][k], y[v][k], s[0]);
+                for (int v = 0; v < VPT; ++v) {
+                    const F8 f = widen(y[v]);
+                    t = dot8(f, f, t);
+                }
+                float s[1] = {t.x + t.y};
                 sum(s);
                 iy = rsqrtf(fmaf(s[0], inv_d, a.eps));
             }
-            const int64_t gate_row = a.per_gate == a.m ? 0 : a.per_gate == 1 ? row : row / a.per_gate;
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int c0 = first<VEC>(v, id, lanes);
-                float w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[v][k] = y[v][k] * iy;
-                if (a.post.p) {
-                    a.post.load<VEC>(0, c0, lanes, a.d, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) r[v][k] *= w[k];
+                F8 u = widen(y[v]) * splat(iy);
+                if (VPT == 1) {
+                    if (a.post.p || a.gate.p) u = u * gate;
+                } else {
+                    if (a.post.p) u = u * a.post.load<VEC>(0, c0, lanes, a.d);
+                    if (a.gate.p) u = u * a.gate.load<VEC>(gate_row, c0, lanes, a.d);
                 }
-                if (a.gate.p) {
-                    a.gate.load<VEC>(gate_row, c0, lanes, a.d, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) r[v][k] *= w[k];
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[v][k] = fmaf(a.scale, x[v][k], r[v][k]);
+                r[v] = fma8(splat(a.scale), widen(x[v]), u);
                 store_cols<VEC>(static_cast<T*>(a.r) + row * a.ldr, c0, lanes, a.d, r[v]);
             }
         } else {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[v][k] = x[v][k];
+            for (int v = 0; v < VPT; ++v) r[v] = widen(x[v]);
         }
-        if (a.pre.p) {
-            float s[1] = {};
+        if (!a.pre.p) continue;
+        float2 t = {};
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
+        for (int v = 0; v < VPT; ++v) t = dot8(r[v], r[v], t);
+        float s[1] = {t.x + t.y};
+        sum(s);
+        const float ir = rsqrtf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    s[0] = fmaf(r[v][k], r[v][k], s[0]);
-            sum(s);
-            const float ir = rsqrtf(fmaf(s[0], inv_d, a.eps));
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int c0 = first<VEC>(v, id, lanes);
-                float w[8];
-                a.pre.load<VEC>(0, c0, lanes, a.d, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] *= r[v][k] * ir;
-                store_cols<VEC>(a.h + row * a.ldh, c0, lanes, a.d, w);
-            }
+        for (int v = 0; v < VPT; ++v) {
+            const int c0 = first<VEC>(v, id, lanes);
+            if (VPT > 1) pre = a.pre.load<VEC>(0, c0, lanes, a.d);
+            store_cols<VEC>(a.h + row * a.ldh, c0, lanes, a.d, r[v] * splat(ir) * pre);
         }
     }
 }
 
+// Many aligned rows: a block for each SM has a stretch of them, and they come
+// through a ring of bulk copies while rows before them are worked on.  The weights
+// lie in shared memory, post and a gate that all rows share as one product.  What
+// bounds it next to HBM is issue: LANES known to the compiler turns addresses into
+// immediates, and WHOLE (y, post and pre are there, and all rows share a gate)
+// spares the loop its tests.
+template <typename T, int VPT, int LANES, bool WHOLE>
+__global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_constant__ ForwardArgs a, const __grid_constant__ Rows in) {
+    extern __shared__ __align__(128) char smem[];
+    constexpr int lanes = LANES;
+    const bool has_y = WHOLE || a.y, has_post = WHOLE || a.post.p, has_pre = WHOLE || a.pre.p, own_gate = !WHOLE && in.seg[2].p;
+    const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
+    const int64_t row0 = a.m * blockIdx.x / gridDim.x + group, row1 = a.m * (blockIdx.x + 1) / gridDim.x;
+    Ring ring(in, smem, group);
+    ring.start(id);
+    mma::grid_wait();
+    int64_t ahead = row0;
+    auto request = [&]() {
+        if (id == 0 && ahead < row1) ring.request(in.seg, ahead);
+        ahead += groups;
+    };
+    for (int k = 0; k < in.stages; ++k) request();
+    float* weights = reinterpret_cast<float*>(smem + kBarrierBytes + groups * in.stages * in.slot_bytes);
+    Staged<true, VPT> post = {weights, lanes}, pre = {weights + staged_floats(lanes, VPT), lanes};
+    if (has_y) post.fill(a.d, [&](int c) { return a.post.at(0, c) * (own_gate ? 1.0f : a.gate.at(0, c)); });
+    if (has_pre) pre.fill(a.d, [&](int c) { return a.pre.at(0, c); });
+    __syncthreads();
+    RowSum sum(lanes, group);
+    const float inv_d = 1.0f / (float)a.d;
+    const F8 scale = splat(a.scale);
+    for (int64_t row = row0; row < row1; row += groups) {
+        const char* slot = ring.take();
+        F8 r[VPT];
+        if (has_y) {
+            Eight<__nv_bfloat16> y[VPT];
+            float iy = 1.0f;
+            float2 t = {};
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c0 = first<true>(v, id, lanes);
+                y[v] = {};
+                if (c0 < a.d) y[v].load(reinterpret_cast<const __nv_bfloat16*>(slot + in.seg[1].at) + c0);
+                const F8 f = widen(y[v]);
+                t = dot8(f, f, t);
+            }
+            if (has_post) {
+                float s[1] = {t.x + t.y};
+                sum(s);
+                iy = rsqrtf(fmaf(s[0], inv_d, a.eps));
+            }
+            T* out = static_cast<T*>(a.r) + row * a.ldr;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c0 = first<true>(v, id, lanes);
+                F8 u = widen(y[v]) * splat(iy) * post.get(v, id);
+                Eight<T> x = {};
+                if (c0 < a.d) {
+                    x.load(reinterpret_cast<const T*>(slot + in.seg[0].at) + c0);
+                    if (own_gate) {
+                        const Weight g = {slot + in.seg[2].at, a.gate.f32, 0};
+                        u = u * g.load<true>(0, c0, lanes, a.d);
+                    }
+                }
+                r[v] = fma8(scale, widen(x), u);
+                if (c0 < a.d) store_cols<true>(out, c0, lanes, a.d, r[v]);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c0 = first<true>(v, id, lanes);
+                Eight<T> x = {};
+                if (c0 < a.d) x.load(reinterpret_cast<const T*>(slot + in.seg[0].at) + c0);
+                r[v] = widen(x);
+            }
+        }
+        float s[1] = {};
+        if (has_pre) {
+            float2 t = {};
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) t = dot8(r[v], r[v], t);
+            s[0] = t.x + t.y;
+            sum(s);
+        }
+        // the row is in registers: its slot takes another
+        if (lanes == 32 || !has_pre) group_sync(group, lanes);
+        request();
+        if (!has_pre) continue;
+        const F8 ir = splat(rsqrtf(fmaf(s[0], inv_d, a.eps)));
+        __nv_bfloat16* out = a.h + row * a.ldh;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c0 = first<true>(v, id, lanes);
+            if (c0 < a.d) store_cols<true>(out, c0, lanes, a.d, r[v] * ir * pre.get(v, id));
+        }
+    }
+}
+
+template <typename T, int VPT, int LANES, bool WHOLE>
+cudaError_t launch_ring(const ForwardArgs& a, const Rows& in, int groups, cudaStream_t s) {
+    static bool done[64];
+    const cudaError_t e = ensure_smem_attr(ring_forward_kernel<T, VPT, LANES, WHOLE>, kRoom, done);
+    if (e != cudaSuccess) return e;
+    const size_t smem = kBarrierBytes + (size_t)groups * in.stages * in.slot_bytes + 2 * 4 * staged_floats(LANES, VPT);
+    return launch(ring_forward_kernel<T, VPT, LANES, WHOLE>, dim3((unsigned)sm_count()), groups * LANES, smem, s, a, in);
+}
+
+template <typename T, bool WHOLE>
+cudaError_t launch_ring(const ForwardArgs& a, const RowShape& q, const Rows& in, int groups, cudaStream_t s) {
+    if (q.vecs == 1) return launch_ring<T, 1, 32, WHOLE>(a, in, groups, s);
+    if (q.vecs == 2) return launch_ring<T, 2, 32, WHOLE>(a, in, groups, s);
+    if (q.lanes == 32) return launch_ring<T, 4, 32, WHOLE>(a, in, groups, s);
+    if (q.lanes == 64) return launch_ring<T, 4, 64, WHOLE>(a, in, groups, s);
+    if (q.lanes == 128) return launch_ring<T, 4, 128, WHOLE>(a, in, groups, s);
+    if (q.lanes == 256) return launch_ring<T, 4, 256, WHOLE>(a, in, groups, s);
+    return launch_ring<T, 4, 512, WHOLE>(a, in, groups, s);
+}
+
+template <typename T, bool VEC, int VPT>
+cudaError_t launch_kernel(const ForwardArgs& a, const RowShape& q, cudaStream_t s) {
+    const int64_t groups = q.threads / q.lanes;
+    return launch(forward_kernel<T, VEC, VPT>, dim3((unsigned)((a.m + groups - 1) / groups)), q.threads, 0, s, a, q.lanes);
+}
+
 template <typename T, bool VEC>
 cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
-    const RowShape q = shape_of(a.d);
-    const int64_t groups = q.threads / q.lanes, blocks = (a.m + groups - 1) / groups;
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, 0x7FFFFFFF));
-    if (q.vecs == 1) return launch(forward_kernel<T, VEC, 1>, grid, q.threads, 0, s, a, q.lanes);
-    if (q.vecs == 2) return launch(forward_kernel<T, VEC, 2>, grid, q.threads, 0, s, a, q.lanes);
-    return launch(forward_kernel<T, VEC, 4>, grid, q.threads, 0, s, a, q.lanes);
+    if constexpr (VEC) {
+        const RowShape q = shape_of(a.d, 4);
+        Rows in = {};
+        in.add(0, a.x, a.ldx, a.d, sizeof(T));
+        if (a.y) in.add(1, a.y, a.ldy, a.d, 2);
+        if (a.gate.p && a.per_gate != a.m) in.add(2, a.gate.p, a.gate.ld, a.d, a.gate.f32 ? 4 : 2, a.per_gate);
+        in.slot_bytes = in.slot();
+        in.err = device_error_word();
+        const int room = kRoom - 2 * 4 * staged_floats(q.lanes, q.vecs), groups = ring_groups(q, in.slot_bytes, room, 512);
+        // a ring is worth its start where a row group has several rows
+        if (groups > 0 && a.m > 2 * (int64_t)groups * sm_count()) {
+            in.stages = ring_stages(groups, in.slot_bytes, room);
+            return a.y && a.post.p && a.pre.p && !in.seg[2].p ? launch_ring<T, true>(a, q, in, groups, s) : launch_ring<T, false>(a, q, in, groups, s);
+        }
+    }
+    const RowShape q = shape_of(a.d, 1);
+    if (q.vecs == 1) return launch_kernel<T, VEC, 1>(a, q, s);
+    if (q.vecs == 2) return launch_kernel<T, VEC, 2>(a, q, s);
+    return launch_kernel<T, VEC, 4>(a, q, s);
 }
 
 }  // namespace

@@ -12,15 +12,18 @@ namespace layers {
 constexpr int kMaxWidth = 16384;
 
 // `lanes` threads (a power of two, whole warps) hold a row, 8 * vecs columns each.
+// More columns a thread mean fewer instructions a row (what a row takes besides
+// its elements, some 150 for each of its warps, is most of it at 8 columns), fewer
+// columns a shorter way through a single one.
 struct RowShape {
     int lanes, vecs, threads;
 };
-inline RowShape shape_of(int64_t d) {
-    RowShape q;
-    q.lanes = 32;
-    while (q.lanes < 512 && q.lanes * 8 < d) q.lanes *= 2;
-    q.vecs = d <= 4096 ? 1 : d <= 8192 ? 2 : 4;
-    q.threads = std::max(q.lanes, 256);
+inline RowShape shape_of(int64_t d, int most_vecs) {
+    RowShape q = {32, 1, 256};
+    while (q.vecs < most_vecs && q.lanes * 8 * q.vecs < d) q.vecs *= 2;
+    while (q.lanes < 512 && q.lanes * 8 * q.vecs < d) q.lanes *= 2;
+    while (q.lanes * 8 * q.vecs < d) q.vecs *= 2;
+    q.threads = std::max(q.lanes, 256);  // of a block without a ring
     return q;
 }
 
@@ -30,6 +33,14 @@ inline RowShape shape_of(int64_t d) {
 template <bool VEC>
 __device__ __forceinline__ int first(int v, int id, int lanes) {
     return v * 8 * lanes + (VEC ? 8 * id : id);
+}
+
+// All threads of a row group.
+__device__ __forceinline__ void group_sync(int group, int lanes) {
+    if (lanes == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
 }
 
 // Sums over the threads of a row, the same in all of them.  A row of several
@@ -42,24 +53,122 @@ struct RowSum {
 
     template <int N>
     __device__ __forceinline__ void operator()(float (&s)[N]) {
-        __shared__ float warps[2][16][4];
+        __shared__ float4 warps[2][16];
         static_assert(N <= 4, "sums at once");
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+        for (int o = 16; o; o >>= 1)
 #pragma unroll
-            for (int o = 16; o; o >>= 1) s[n] += __shfl_xor_sync(0xFFFFFFFFu, s[n], o);
+            for (int n = 0; n < N; ++n) s[n] += __shfl_xor_sync(0xFFFFFFFFu, s[n], o);
         if (lanes == 32) return;
         const int warp = threadIdx.x / 32, first_warp = group * (lanes / 32);
-        if (threadIdx.x % 32 == 0)
-#pragma unroll
-            for (int n = 0; n < N; ++n) warps[turn][warp][n] = s[n];
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
-#pragma unroll
-        for (int n = 0; n < N; ++n) s[n] = 0.0f;
-        for (int w = 0; w < lanes / 32; ++w)
-#pragma unroll
-            for (int n = 0; n < N; ++n) s[n] += warps[turn][first_warp + w][n];
+        if (threadIdx.x % 32 == 0) warps[turn][warp] = make_float4(s[0], N > 1 ? s[1 % N] : 0.0f, N > 2 ? s[2 % N] : 0.0f, N > 3 ? s[3 % N] : 0.0f);
+        group_sync(group, lanes);
+        float4 t = warps[turn][first_warp];
+        for (int w = 1; w < lanes / 32; ++w) {
+            const float4 x = warps[turn][first_warp + w];
+            t.x += x.x;
+            if (N > 1) t.y += x.y;
+            if (N > 2) t.z += x.z;
+            if (N > 3) t.w += x.w;
+        }
+        s[0] = t.x;
+        if (N > 1) s[1 % N] = t.y;
+        if (N > 2) s[2 % N] = t.z;
+        if (N > 3) s[3 % N] = t.w;
         turn ^= 1;
+    }
+};
+
+#endif  // __CUDACC__
+
+constexpr int kMaxStages = 8, kMaxGroups = 16, kSegments = 5;
+// Shared memory of a block that has an SM to itself; what is left of it lets the
+// next launch's small blocks start beside it.
+constexpr int kRoom = 220 * 1024;
+constexpr int kBarrierBytes = kMaxGroups * kMaxStages * 8;
+
+// One matrix of a ring, and all of them.
+struct Segment {
+    const char* p;       // null: not there
+    int64_t pitch;       // bytes between rows
+    uint32_t bytes, at;  // of a row; where it lies in a slot
+    uint32_t div;        // rows that share one of it
+};
+struct Rows {
+    Segment seg[kSegments];
+    uint32_t used;
+    int32_t stages, slot_bytes;
+    int* err;
+    void add(int k, const void* p, int64_t ld, int64_t d, int es, int64_t div = 1) {
+        seg[k] = {static_cast<const char*>(p), ld * es, (uint32_t)(d * es), used, (uint32_t)div};
+        used += seg[k].bytes;
+    }
+    int slot() const { return (int)((used + 127) / 128 * 128); }
+};
+
+// The ring of a block that has an SM to itself, in `room` bytes: as many row groups
+// as may have two slots each (up to `most` threads), then as many slots.  0: not
+// even one group may.
+inline int ring_groups(const RowShape& q, int slot_bytes, int room, int most) {
+    return std::min({kMaxGroups, most / q.lanes, (room - kBarrierBytes) / (2 * slot_bytes)});
+}
+inline int ring_stages(int groups, int slot_bytes, int room) { return std::min(kMaxStages, (room - kBarrierBytes) / (groups * slot_bytes)); }
+
+#ifdef __CUDACC__
+
+// Rows on their way from global to shared memory by bulk copies: each row group
+// of a block has a ring of `stages` slots, and its first thread asks for rows
+// ahead of the one that the group works on.  A slot holds one row of up to five
+// matrices.  Rows are 16-byte aligned and a multiple of 16 bytes.
+struct Ring {
+    uint64_t* full;
+    char* slots;
+    int stages, slot_bytes;
+    int to = 0, from = 0;  // the slot that the next request fills, that the next row comes from
+    uint32_t phase = 0;
+    int* err;
+    long long budget = tma::kWaitBudgetCycles;
+
+    __device__ __forceinline__ Ring(const Rows& in, char* smem, int group)
+        : full(reinterpret_cast<uint64_t*>(smem) + group * kMaxStages),
+          slots(smem + kBarrierBytes + group * in.stages * in.slot_bytes),
+          stages(in.stages), slot_bytes(in.slot_bytes), err(in.err) {}
+
+    // All threads of the block.
+    __device__ __forceinline__ void start(int id) {
+        if (id == 0) {
+            for (int k = 0; k < stages; ++k) tma::mbar_init(full + k, 1);
+            tma::fence_barrier_init();
+        }
+        __syncthreads();
+    }
+
+    // Called by the group's first thread, for rows in the order in which take() is called.
+    __device__ __forceinline__ void request(const Segment (&seg)[kSegments], int64_t row) {
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int k = 0; k < kSegments; ++k)
+            if (seg[k].p) bytes += seg[k].bytes;
+        tma::mbar_arrive_expect_tx(full + to, bytes);
+#pragma unroll
+        for (int k = 0; k < kSegments; ++k)
+            if (seg[k].p) tma::bulk_load(slots + to * slot_bytes + seg[k].at, seg[k].p + (seg[k].div == 1 ? row : row / seg[k].div) * seg[k].pitch, seg[k].bytes, full + to);
+        to = to + 1 == stages ? 0 : to + 1;
+    }
+
+    // The slot of the next row, once it is there.  A wait that gives up is
+    // reported, and the ones after it give up at once: the block still ends.
+    __device__ __forceinline__ const char* take() {
+        if (!tma::mbar_wait(full + from, phase, budget)) {
+            record_device_error(err, DPRED_E_TIMEOUT);
+            budget = 1000;
+        }
+        const char* slot = slots + from * slot_bytes;
+        if (++from == stages) {
+            from = 0;
+            phase ^= 1;
+        }
+        return slot;
     }
 };
 
@@ -71,22 +180,67 @@ struct Weight {
     int32_t f32;
     int64_t ld;
 #ifdef __CUDACC__
+    // One element; 1 where there is no weight.
+    __device__ __forceinline__ float at(int64_t row, int c) const {
+        if (!p) return 1.0f;
+        return f32 ? static_cast<const float*>(p)[row * ld + c] : load1(static_cast<const __nv_bfloat16*>(p) + row * ld + c);
+    }
     template <bool VEC>
-    __device__ __forceinline__ void load(int64_t row, int c0, int step, int d, float (&f)[8]) const {
+    __device__ __forceinline__ F8 load(int64_t row, int c0, int step, int d) const {
         if (f32) {
             Cols<float, VEC> q;
             q.load(static_cast<const float*>(p) + row * ld, c0, step, d);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = q[k];
-        } else {
-            Cols<__nv_bfloat16, VEC> q;
-            q.load(static_cast<const __nv_bfloat16*>(p) + row * ld, c0, step, d);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = q[k];
+            return widen(q);
         }
+        Cols<__nv_bfloat16, VEC> q;
+        q.load(static_cast<const __nv_bfloat16*>(p) + row * ld, c0, step, d);
+        return widen(q);
     }
 #endif
 };
+
+#ifdef __CUDACC__
+
+// Weights of a row in shared memory, in fp32 and in the order in which threads
+// take them, so that the loop over rows has no flags, types or bank conflicts: a
+// thread's columns lie together, their 16-byte pieces exchanged among themselves
+// so that eight threads in a row read eight different bank groups (VEC), or
+// column by column.  Columns from d on are 0.
+template <bool VEC, int VPT>
+struct Staged {
+    float* at;
+    int lanes;
+    // Where thread id has column k of its v-th eight.
+    __device__ __forceinline__ int place(int v, int id, int k) const {
+        if (!VEC) return (v * 8 + k) * lanes + id;
+        constexpr int kPieces = 2 * VPT;  // of 4 columns
+        const int turn = id / (8 / kPieces) & (kPieces - 1);
+        return (id * kPieces + ((v * 2 + k / 4) ^ turn)) * 4 + k % 4;
+    }
+    // All threads of the block: f(column) of every column.
+    template <typename F>
+    __device__ __forceinline__ void fill(int d, F f) {
+        for (int i = threadIdx.x; i < VPT * 8 * lanes; i += blockDim.x) {
+            const int k = VEC ? i % 8 : i / lanes % 8, id = VEC ? i / 8 % lanes : i % lanes, v = i / (8 * lanes);
+            const int c = column<VEC>(first<VEC>(v, id, lanes), lanes, k);
+            at[place(v, id, k)] = c < d ? f(c) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ F8 get(int v, int id) const {
+        F8 f;
+        if constexpr (VEC) {
+            const float4 a = *reinterpret_cast<const float4*>(at + place(v, id, 0)), b = *reinterpret_cast<const float4*>(at + place(v, id, 4));
+            f.p[0] = make_float2(a.x, a.y); f.p[1] = make_float2(a.z, a.w); f.p[2] = make_float2(b.x, b.y); f.p[3] = make_float2(b.z, b.w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f.p[i] = make_float2(at[place(v, id, 2 * i)], at[place(v, id, 2 * i + 1)]);
+        }
+        return f;
+    }
+};
+inline __host__ __device__ int staged_floats(int lanes, int vecs) { return 8 * lanes * vecs; }
+
+#endif  // __CUDACC__
 
 // The arguments that both directions have.
 struct NormShape {

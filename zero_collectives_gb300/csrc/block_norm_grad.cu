@@ -19,214 +19,15 @@
 // Bandwidth bound: r, y, dr and dh are read, dx and dy written once.
 #include <algorithm>
 
-#include "block_norm.cuh"
+#include "block_norm_grad.cuh"
 
 namespace dpred {
 namespace layers {
 namespace {
 
-// A weight gradient: where it goes and how.
-struct Target {
-    void* p;
-    int64_t ld;
-    int32_t f32, add;
-#ifdef __CUDACC__
-    __device__ __forceinline__ void put(int64_t row, int c, float v) const {
-        if (f32) {
-            float* o = static_cast<float*>(p) + row * ld + c;
-            *o = add ? *o + v : v;
-        } else {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p) + row * ld + c;
-            store1(o, add ? load1(o) + v : v);
-        }
-    }
-#endif
-};
-
-struct BackwardArgs {
-    const void* r;
-    const void* dr;           // null: 0
-    const __nv_bfloat16* dh;  // null: no norm above
-    const __nv_bfloat16* y;   // null: no block below
-    Weight post, gate, pre;
-    void* dx;
-    __nv_bfloat16* dy;
-    Target dpost, dgate, dpre;  // p null: not wanted
-    float* partial;             // rows of d: dpost and dpre of each block, dgate of each unit
-    int64_t ldr, lddr, lddh, ldy, lddx, lddy;
-    int64_t sections;  // consecutive rows that share a gate row (the whole when each row has its own)
-    int64_t per;       // rows of a section
-    int32_t parts;     // units of a section
-    int32_t each;      // every row has a gate row of its own
-    int32_t d;
-    int32_t release;   // another launch of the call follows
-    float scale, eps;
-};
-
-constexpr int kCombine = 2048;  // columns of a block's row groups where there are several: 256 threads of 8
-
-// Adds the threads' sums of a column over the block's row groups, in order.
-template <bool VEC, int VPT, typename F>
-__device__ __forceinline__ void combine(float (&s)[VPT][8], int id, int group, int groups, int lanes, int d, float* buf, F put) {
-    if (groups == 1) {
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = column<VEC>(first<VEC>(v, id, lanes), lanes, k);
-                if (c < d) put(c, s[v][k]);
-            }
-        return;
-    }
-    // several groups hold a row in one vector a thread
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) buf[(group * 8 + k) * lanes + id] = s[0][k];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 8 * lanes; i += blockDim.x) {
-        const int k = i / lanes, t = i % lanes, c = column<VEC>(first<VEC>(0, t, lanes), lanes, k);
-        if (c >= d) continue;
-        float v = 0.0f;
-        for (int g = 0; g < groups; ++g) v += buf[(g * 8 + k) * lanes + t];
-        put(c, v);
-    }
-}
-
-template <typename T, bool VEC, int VPT>
-__global__ void __launch_bounds__(512) backward_kernel(const __grid_constant__ BackwardArgs a, int lanes) {
-    __shared__ float buf[kCombine];
-    if (a.release) mma::grid_launch_dependents();
-    mma::grid_wait();
-    const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
-    RowSum sum(lanes, group);
-    const float inv_d = 1.0f / (float)a.d;
-    float dpost[VPT][8] = {}, dpre[VPT][8] = {};
-    const int64_t units = a.sections * a.parts;
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t section = unit / a.parts, part = unit - section * a.parts;
-        const int64_t row0 = section * a.per + a.per * part / a.parts, row1 = section * a.per + a.per * (part + 1) / a.parts;
-        float dgate[VPT][8] = {};
-        for (int64_t row = row0 + group; row < row1; row += groups) {
-            Cols<T, VEC> r[VPT], dr[VPT];
-            Cols<__nv_bfloat16, VEC> dh[VPT], y[VPT];
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int c0 = first<VEC>(v, id, lanes);
-                if (a.dh) {
-                    r[v].load(static_cast<const T*>(a.r) + row * a.ldr, c0, lanes, a.d);
-                    dh[v].load(a.dh + row * a.lddh, c0, lanes, a.d);
-                }
-                if (a.y) y[v].load(a.y + row * a.ldy, c0, lanes, a.d);
-                if (a.dr) dr[v].load(static_cast<const T*>(a.dr) + row * a.lddr, c0, lanes, a.d);
-            }
-            float s[3] = {};  // r^2, dh pre r, y^2
-            float w[8];
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                if (a.dh) {
-                    a.pre.load<VEC>(0, first<VEC>(v, id, lanes), lanes, a.d, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        s[0] = fmaf(r[v][k], r[v][k], s[0]);
-                        s[1] = fmaf(dh[v][k] * w[k], r[v][k], s[1]);
-                    }
-                }
-                if (a.post.p)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) s[2] = fmaf(y[v][k], y[v][k], s[2]);
-            }
-            if (a.dh || a.post.p) sum(s);
-            const float ir = rsqrtf(fmaf(s[0], inv_d, a.eps)), iy = a.post.p ? rsqrtf(fmaf(s[2], inv_d, a.eps)) : 1.0f;
-            const float mean_r = s[1] * inv_d * ir;  // of v n_r
-            float q[1] = {};                         // w y
-            float g[VPT][8];
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int c0 = first<VEC>(v, id, lanes);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) g[v][k] = a.dr ? dr[v][k] : 0.0f;
-                if (a.dh) {
-                    a.pre.load<VEC>(0, c0, lanes, a.d, w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float n = r[v][k] * ir;
-                        g[v][k] = fmaf(ir, fmaf(-n, mean_r, dh[v][k] * w[k]), g[v][k]);
-                        dpre[v][k] = fmaf(dh[v][k], n, dpre[v][k]);
-                    }
-                }
-                float o[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = a.scale * g[v][k];
-                store_cols<VEC>(static_cast<T*>(a.dx) + row * a.lddx, c0, lanes, a.d, o);
-                if (!a.y) continue;
-                float post[8];
-                if (a.post.p) a.post.load<VEC>(0, c0, lanes, a.d, post);
-                if (a.gate.p) {
-                    a.gate.load<VEC>(a.each ? row : section, c0, lanes, a.d, w);
-                    if (a.dgate.p) {
-                        float u[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] = a.post.p ? y[v][k] * iy * post[k] : y[v][k];
-                        if (a.each) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int c = column<VEC>(c0, lanes, k);
-                                if (c < a.d) a.dgate.put(row, c, g[v][k] * u[k]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) dgate[v][k] = fmaf(g[v][k], u[k], dgate[v][k]);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) g[v][k] *= w[k];
-                }
-                if (a.post.p) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        dpost[v][k] = fmaf(g[v][k], y[v][k] * iy, dpost[v][k]);
-                        g[v][k] *= post[k];
-                        q[0] = fmaf(g[v][k], y[v][k], q[0]);
-                    }
-                }
-            }
-            if (!a.y) continue;
-            if (a.post.p) sum(q);
-            const float mean_y = q[0] * inv_d * iy;  // of w n_y
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                if (a.post.p)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) g[v][k] = iy * fmaf(-(y[v][k] * iy), mean_y, g[v][k]);
-                store_cols<VEC>(a.dy + row * a.lddy, first<VEC>(v, id, lanes), lanes, a.d, g[v]);
-            }
-        }
-        if (a.dgate.p && !a.each)
-            combine<VEC>(dgate, id, group, groups, lanes, a.d, buf, [&](int c, float v) {
-                if (a.parts == 1)
-                    a.dgate.put(section, c, v);
-                else
-                    a.partial[(2 * (int64_t)gridDim.x + unit) * a.d + c] = v;
-            });
-    }
-    if (a.dpost.p)
-        combine<VEC>(dpost, id, group, groups, lanes, a.d, buf, [&](int c, float v) {
-            if (gridDim.x == 1)
-                a.dpost.put(0, c, v);
-            else
-                a.partial[(int64_t)blockIdx.x * a.d + c] = v;
-        });
-    if (a.dpre.p)
-        combine<VEC>(dpre, id, group, groups, lanes, a.d, buf, [&](int c, float v) {
-            if (gridDim.x == 1)
-                a.dpre.put(0, c, v);
-            else
-                a.partial[((int64_t)gridDim.x + blockIdx.x) * a.d + c] = v;
-        });
-}
-
-// Adds the partial rows of one weight gradient: 32 columns a block, 32 shares of
+// Adds the partial rows of one weight gradient: 32 columns a block, 16 shares of
 // the rows, added in order.
+constexpr int kShares = 16;
 struct Job {
     const float* src;
     int64_t rows;
@@ -237,8 +38,8 @@ struct FinishArgs {
     int32_t d;
 };
 
-__global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ FinishArgs a) {
-    __shared__ float part[32][33];
+__global__ void __launch_bounds__(kShares * 32) finish_kernel(const __grid_constant__ FinishArgs a) {
+    __shared__ float part[kShares][32];
     mma::grid_wait();
     int at = blockIdx.y;
     int64_t out_row = 0;
@@ -253,7 +54,7 @@ __global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ Fi
     }
     const float* src = j->src + out_row * j->rows * a.d;
     const int lane = threadIdx.x % 32, share = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
-    const int64_t r0 = j->rows * share / 32, r1 = j->rows * (share + 1) / 32;
+    const int64_t r0 = j->rows * share / kShares, r1 = j->rows * (share + 1) / kShares;
     float v = 0.0f;
     if (c < a.d) {
 #pragma unroll 8
@@ -263,29 +64,21 @@ __global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ Fi
     __syncthreads();
     if (share || c >= a.d) return;
     v = 0.0f;
-    for (int w = 0; w < 32; ++w) v += part[w][lane];
+    for (int w = 0; w < kShares; ++w) v += part[w][lane];
     j->to.put(out_row, c, v);
 }
 
 // --------------------------------------------------------------------- host --
 
-constexpr int kBlocksPerSm = 2;
-
-struct Grid {
-    RowShape q;
-    int64_t sections, per, blocks;
-    int32_t parts;
-};
-
-// Sections are cut into as many units as there are resident blocks, or dealt
+// Sections are cut into as many units as there are blocks (one to an SM), or dealt
 // out whole where there are more of them.
 Grid grid_of(int64_t m, int64_t d, int64_t gate_rows) {
     Grid g;
-    g.q = shape_of(d);
+    g.q = shape_of(d, 2);
     g.sections = gate_rows <= 1 || gate_rows == m ? 1 : gate_rows;
     g.per = m / g.sections;
-    const int64_t groups = g.q.threads / g.q.lanes, most = (int64_t)kBlocksPerSm * sm_count();
-    const int64_t parts = std::min((g.per + groups - 1) / groups, std::max<int64_t>(1, most / g.sections));
+    g.groups = std::max(1, kThreads / g.q.lanes);
+    const int64_t most = sm_count(), parts = std::min((g.per + g.groups - 1) / g.groups, std::max<int64_t>(1, most / g.sections));
     g.parts = (int32_t)std::max<int64_t>(1, parts);
     g.blocks = std::min(most, g.sections * g.parts);
     return g;
@@ -293,12 +86,30 @@ Grid grid_of(int64_t m, int64_t d, int64_t gate_rows) {
 
 size_t partial_bytes(const Grid& g, int64_t d) { return (size_t)((2 * g.blocks + (g.parts > 1 ? g.sections * g.parts : 0)) * d) * 4; }
 
-template <typename T, bool VEC>
-cudaError_t launch_backward(const BackwardArgs& a, const Grid& g, cudaStream_t s) {
-    const dim3 grid((unsigned)g.blocks);
-    if (g.q.vecs == 1) return launch(backward_kernel<T, VEC, 1>, grid, g.q.threads, 0, s, a, g.q.lanes);
-    if (g.q.vecs == 2) return launch(backward_kernel<T, VEC, 2>, grid, g.q.threads, 0, s, a, g.q.lanes);
-    return launch(backward_kernel<T, VEC, 4>, grid, g.q.threads, 0, s, a, g.q.lanes);
+template <typename T>
+cudaError_t launch_plain(const BackwardArgs& a, const Rows& in, const Grid& g, cudaStream_t s) {
+    if (g.q.vecs == 1) return launch_kernel<T, false, 1, 0, false>(a, in, g, g.groups, s);
+    if (g.q.lanes == 512) return g.q.vecs == 2 ? launch_kernel<T, false, 2, 512, false>(a, in, g, g.groups, s) : launch_kernel<T, false, 4, 512, false>(a, in, g, g.groups, s);
+    return launch_kernel<T, false, 2, 0, false>(a, in, g, g.groups, s);
+}
+
+template <typename T>
+cudaError_t launch_backward(const BackwardArgs& a, const Grid& g, bool vec, cudaStream_t s) {
+    Rows in = {};
+    const int es = (int)sizeof(T), gs = a.gate.f32 ? 4 : 2;
+    const struct { const void* p; int64_t ld; int es; } parts[kSegments] = {
+        {a.dh ? a.r : nullptr, a.ldr, es}, {a.dr, a.lddr, es}, {a.dh, a.lddh, 2}, {a.y, a.ldy, 2}, {a.each ? a.gate.p : nullptr, a.gate.ld, gs}};
+    for (int k = 0; k < kSegments; ++k)
+        if (parts[k].p) in.add(k, parts[k].p, parts[k].ld, a.d, parts[k].es);
+    in.slot_bytes = in.slot();
+    in.err = device_error_word();
+    const int room = kRoom - 4 * (2 * staged_floats(g.q.lanes, g.q.vecs) + 8 * g.q.lanes * g.groups);
+    int groups = vec ? ring_groups(g.q, in.slot_bytes, room, g.groups * g.q.lanes) : 0;
+    if (vec && groups == 0 && in.slot_bytes + kBarrierBytes <= room) groups = 1;  // a single slot
+    if (groups == 0) return launch_plain<T>(a, in, g, s);
+    in.stages = ring_stages(groups, in.slot_bytes, room);
+    const bool whole = a.dr && a.dh && a.y && a.post.p && !a.each;
+    return whole ? launch_ring<T, true>(a, in, g, groups, s) : launch_ring<T, false>(a, in, g, groups, s);
 }
 
 }  // namespace
@@ -375,20 +186,17 @@ extern "C" int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, cons
     a.scale = scale;
     a.eps = eps;
     const bool vec = weights_aligned(n) && (!pre || (aligned_rows(r, m, ldr, es) && aligned_rows(dh, m, lddh, 2))) && (!dr || aligned_rows(dr, m, lddr, es)) &&
-                     aligned_rows(dx, m, lddx, es) && (!y || (aligned_rows(y, m, ldy, 2) && aligned_rows(dy, m, lddy, 2)));
+                     aligned_rows(dx, m, lddx, es) && (!each || reinterpret_cast<uintptr_t>(gate_grad) % 16 == 0) && (!y || (aligned_rows(y, m, ldy, 2) && aligned_rows(dy, m, lddy, 2)));
     FinishArgs f = {};
     f.d = (int32_t)d;
-    if (g.blocks > 1) {
-        if (post_grad) f.dpost = {a.partial, g.blocks, a.dpost};
-        if (pre_grad) f.dpre = {a.partial + g.blocks * d, g.blocks, a.dpre};
-    }
+    if (post_grad && g.sections * g.parts > 1) f.dpost = {a.partial, g.blocks, a.dpost};
+    if (pre_grad && g.blocks > 1) f.dpre = {a.partial + g.blocks * d, g.blocks, a.dpre};
     if (gate_sums && g.parts > 1) f.dgate = {a.partial + 2 * g.blocks * d, g.parts, a.dgate};
     const int64_t jobs = (f.dpost.to.p != nullptr) + (f.dpre.to.p != nullptr) + (f.dgate.to.p ? g.sections : 0);
     a.release = jobs > 0;
-    cudaError_t e = r_dtype == DPRED_F32 ? (vec ? launch_backward<float, true>(a, g, s) : launch_backward<float, false>(a, g, s))
-                                         : (vec ? launch_backward<__nv_bfloat16, true>(a, g, s) : launch_backward<__nv_bfloat16, false>(a, g, s));
+    cudaError_t e = r_dtype == DPRED_F32 ? launch_backward<float>(a, g, vec, s) : launch_backward<__nv_bfloat16>(a, g, vec, s);
     if (e != cudaSuccess) return cuda_error(e, "block norm gradient launch");
     if (jobs == 0) return DPRED_OK;
-    e = launch(finish_kernel, dim3((unsigned)((d + 31) / 32), (unsigned)jobs), 1024, 0, s, f);
+    e = launch(finish_kernel, dim3((unsigned)((d + 31) / 32), (unsigned)jobs), kShares * 32, 0, s, f);
     return e == cudaSuccess ? DPRED_OK : cuda_error(e, "block norm gradient launch");
 }

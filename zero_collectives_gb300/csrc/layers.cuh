@@ -95,6 +95,64 @@ __device__ __forceinline__ void store_cols(T* p, int c0, int step, int d, const 
     }
 }
 
+// Eight values in fp32, as four pairs: one instruction works on a pair (each half
+// rounded as by itself), which is what keeps the norms from being bound by issue.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+
+struct F8 {
+    float2 p[4];
+    __device__ __forceinline__ float get(int k) const { return k & 1 ? p[k / 2].y : p[k / 2].x; }
+};
+__device__ __forceinline__ F8 splat(float v) {
+    F8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.p[i] = make_float2(v, v);
+    return f;
+}
+__device__ __forceinline__ F8 operator*(const F8& a, const F8& b) {
+    F8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.p[i] = mul2(a.p[i], b.p[i]);
+    return f;
+}
+__device__ __forceinline__ F8 fma8(const F8& a, const F8& b, const F8& c) {
+    F8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.p[i] = fma2(a.p[i], b.p[i], c.p[i]);
+    return f;
+}
+// s + a . b, by halves.
+__device__ __forceinline__ float2 dot8(const F8& a, const F8& b, float2 s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fma2(a.p[i], b.p[i], s);
+    return s;
+}
+template <typename C>
+__device__ __forceinline__ F8 widen(const C& c) {
+    F8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.p[i] = make_float2(c[2 * i], c[2 * i + 1]);
+    return f;
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_cols(T* p, int c0, int step, int d, const F8& f) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = f.get(k);
+    store_cols<VEC>(p, c0, step, d, v);
+}
+
 #endif  // __CUDACC__
 
 // -------------------------------------------------------------------- host --
