@@ -2,7 +2,7 @@
 
 Tolerances.  Lookup: w * scale is one rounding in fp32 (2^-24) and one to the
 output's type.  Gradient: a row of n tokens is summed in fp32 with at most n +
-n / 32 + 9 additions (runs of 32 positions, then 8 shares of their sums), each
+n / 32 + 9 additions (runs of up to 32 positions, then 8 shares of their sums), each
 off by at most 2^-24 of the terms' magnitudes; the scale and the value added to
 are one or two roundings more; one rounding to the output's type."""
 import pytest

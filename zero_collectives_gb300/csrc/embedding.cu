@@ -6,21 +6,21 @@
 //
 // The embedding is the largest task of a bucket flush (98304 x 1024 of the
 // 402.8M parameters).  Its gradient is summed in fp32 in one fixed order: the
-// tokens of a row in ascending t, in runs of kRun positions of the sorted order
+// tokens of a row in ascending t, in runs of 4 to 32 positions of the sorted order
 // whose sums are then added in ascending order.  Three launches:
 //
-//  sort   Every CTA owns a range of ids and reads all ids: it counts those below
-//         its range (where its tokens start in the sorted order) and those of
-//         each of its rows, per warp, then places its tokens.  The order is
-//         stable and no CTA waits for another.  Reading T ids per SM from L2
-//         costs T / 30000 us, a ninth at most of what T rows of 2 KB take from
-//         HBM.
-//  sum    A warp takes kRun sorted positions and 256 columns, eight rows in
-//         flight.  Rows whose tokens lie inside its positions are written;
-//         what continues from or into other positions is left as a partial sum.
-//         Work is the same whatever the ids are: one row with all tokens is cut
-//         like any other.  Where the whole table is stored, other blocks write
-//         the rows without a token.
+//  sort   Tokens are ordered by the low bits of their id, then by the rest, then
+//         by t.  Every block owns the ids with its low bits (frequent ids lie next
+//         to each other, so this spreads them) and reads all ids: it counts those
+//         with lower low bits (where its tokens start in the order) and those of
+//         each of its rows, per warp, then places its tokens.  No block waits for
+//         another.  Reading T ids per SM from L2 costs T / 30000 us, a ninth at
+//         most of what T rows of 2 KB take from HBM.
+//  sum    A warp takes a run of positions and 256 columns, eight rows in flight.
+//         Rows whose tokens lie inside the run are written; what continues from or
+//         into other runs is left as a partial sum.  Work is the same whatever the
+//         ids are: one row with all tokens is cut like any other.  Where the whole
+//         table is stored, other blocks write the rows without a token.
 //  join   Adds the partial sums of the rows that were cut.
 //
 // Bandwidth bound: dy is read once and each row of dW written once (read and
@@ -33,14 +33,9 @@ namespace dpred {
 namespace layers {
 namespace {
 
-template <typename I>
-__device__ __forceinline__ int64_t id_at(const I* ids, int64_t t) {
-    return (int64_t)ids[t];
-}
-
 // ------------------------------------------------------------------- lookup --
 
-constexpr int kLookThreads = 256, kLookRows = 4;
+constexpr int kLookThreads = 256;
 
 struct LookArgs {
     const void* ids;
@@ -52,52 +47,75 @@ struct LookArgs {
     int* err;
 };
 
-// `lanes` threads cover a row in steps, kLookRows rows at a time.
-template <typename TW, typename TY, bool VEC>
+// The id of token t, -1 where it is outside the table or t behind the last token.
+__device__ __forceinline__ int64_t checked_id(const LookArgs& a, int64_t t, bool report) {
+    if (t >= a.t) return -1;
+    const int64_t id = a.id64 ? static_cast<const int64_t*>(a.ids)[t] : static_cast<const int32_t*>(a.ids)[t];
+    if (id >= 0 && id < a.v) return id;
+    if (report) record_device_error(a.err, DPRED_E_BOUNDS);
+    return -1;
+}
+
+// `lanes` threads of a warp cover a row, CH vectors of 8 columns each at a time; a
+// thread has 8 vectors in flight, of 8 / CH rows, and asks for the ids of its next
+// rows meanwhile.
+template <typename TW, typename TY, int CH>
 __global__ void __launch_bounds__(kLookThreads) lookup_kernel(const __grid_constant__ LookArgs a, int lanes) {
+    constexpr int R = 8 / CH;
     mma::grid_wait();
-    const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = kLookThreads / lanes;
-    const TW* w = static_cast<const TW*>(a.w);
-    TY* y = static_cast<TY*>(a.y);
-    const int64_t step = (int64_t)gridDim.x * groups;
-    for (int64_t t0 = (int64_t)blockIdx.x * groups + group; t0 < a.t; t0 += step * kLookRows) {
-        int64_t id[kLookRows];
+    const int lane = threadIdx.x & (lanes - 1), sub = 32 / lanes, part = threadIdx.x % 32 / lanes;
+    const int64_t step = (int64_t)gridDim.x * (kLookThreads / 32) * sub * R;
+    int64_t t0 = ((int64_t)blockIdx.x * (kLookThreads / 32) + threadIdx.x / 32) * sub * R + part;
+    int64_t id[R];
 #pragma unroll
-        for (int u = 0; u < kLookRows; ++u) {
-            const int64_t t = t0 + u * step;
-            id[u] = -1;
-            if (t < a.t) {
-                id[u] = a.id64 ? id_at(static_cast<const int64_t*>(a.ids), t) : id_at(static_cast<const int32_t*>(a.ids), t);
-                if (id[u] < 0 || id[u] >= a.v) {
-                    id[u] = -1;
-                    if (lane == 0) record_device_error(a.err, DPRED_E_BOUNDS);
+    for (int u = 0; u < R; ++u) id[u] = checked_id(a, t0 + u * sub, lane == 0);
+    for (; t0 < a.t; t0 += step) {
+        int64_t next[R];
+        for (int c0 = 0; c0 < a.d; c0 += CH * lanes * 8) {
+            Eight<TW> q[R][CH];
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int c = c0 + (k * lanes + lane) * 8;
+                    if (id[u] >= 0 && c < a.d)
+                        q[u][k].load(static_cast<const TW*>(a.w) + id[u] * a.ldw + c);
+                    else
+                        q[u][k] = {};
+                }
+            if (c0 == 0)
+#pragma unroll
+                for (int u = 0; u < R; ++u) next[u] = checked_id(a, t0 + step + u * sub, lane == 0);
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                const int64_t t = t0 + u * sub;
+                if (t >= a.t) continue;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int c = c0 + (k * lanes + lane) * 8;
+                    if (c < a.d) store_cols<true>(static_cast<TY*>(a.y) + t * a.ldy, c, 0, a.d, widen(q[u][k]) * splat(a.scale));
                 }
             }
         }
-        if constexpr (VEC) {
-            for (int c = lane * 8; c < a.d; c += lanes * 8) {
-                Eight<TW> q[kLookRows];
 #pragma unroll
-                for (int u = 0; u < kLookRows; ++u)
-                    if (id[u] >= 0) q[u].load(w + id[u] * a.ldw + c);
+        for (int u = 0; u < R; ++u) id[u] = next[u];
+    }
+}
+
+// Rows without 16-byte alignment: a warp per row, element by element.
+template <typename TW, typename TY>
+__global__ void __launch_bounds__(kLookThreads) lookup_any_kernel(const __grid_constant__ LookArgs a) {
+    mma::grid_wait();
+    const int lane = threadIdx.x % 32;
+    for (int64_t t = (int64_t)blockIdx.x * (kLookThreads / 32) + threadIdx.x / 32; t < a.t; t += (int64_t)gridDim.x * (kLookThreads / 32)) {
+        const int64_t id = checked_id(a, t, lane == 0);
+        const TW* w = static_cast<const TW*>(a.w) + (id < 0 ? 0 : id * a.ldw);
+        TY* y = static_cast<TY*>(a.y) + t * a.ldy;
+        for (int c0 = lane; c0 < a.d; c0 += 256) {
+            float f[8];
 #pragma unroll
-                for (int u = 0; u < kLookRows; ++u) {
-                    if (t0 + u * step >= a.t) continue;
-                    float f[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = id[u] >= 0 ? q[u][k] * a.scale : 0.0f;
-                    store8(y + (t0 + u * step) * a.ldy + c, f);
-                }
-            }
-        } else {
-            for (int c = lane; c < a.d; c += lanes) {
-                float f[kLookRows];
-#pragma unroll
-                for (int u = 0; u < kLookRows; ++u) f[u] = id[u] >= 0 ? load1(w + id[u] * a.ldw + c) * a.scale : 0.0f;
-#pragma unroll
-                for (int u = 0; u < kLookRows; ++u)
-                    if (t0 + u * step < a.t) store1(y + (t0 + u * step) * a.ldy + c, f[u]);
-            }
+            for (int k = 0; k < 8; ++k) f[k] = id >= 0 && c0 + 32 * k < a.d ? load1(w + c0 + 32 * k) * a.scale : 0.0f;
+            store_cols<false>(y, c0, 32, a.d, f);
         }
     }
 }
@@ -105,21 +123,24 @@ __global__ void __launch_bounds__(kLookThreads) lookup_kernel(const __grid_const
 // --------------------------------------------------------------------- sort --
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxRange = 1024;  // ids of a CTA: a counter for each and every warp, 128 KB
-constexpr int kRun = 32;         // sorted positions of a warp in the sums
+constexpr int kMaxRows = 4096;            // of a block
+constexpr int kCounters = 192 * 1024;     // bytes: one for each of its rows and warps
+constexpr int kHeld = 16;                 // ids that a thread keeps between counting and placing
 
 struct SortArgs {
     const void* ids;
-    int64_t padding;  // this id's tokens give no gradient; INT64_MIN: none
-    int64_t t, v;
-    int32_t range;    // ids of a CTA, a multiple of 32
-    int32_t warps;    // warps that share the tokens
-    int32_t* key;     // [t] id of a sorted position
-    int32_t* order;   // [t] its token
-    uint32_t* met;    // a bit per id: it has a token (null: not wanted)
-    int32_t* count;   // sorted positions in all
+    int64_t t;
+    uint32_t v, padding;  // this id's tokens give no gradient; kNoId: none
+    int32_t shift;        // the low bits of an id say which block has it
+    int32_t rows;         // rows of a block, a multiple of 32
+    int32_t warps;        // warps that share the tokens
+    int32_t* key;         // [t] id of a sorted position
+    int32_t* order;       // [t] its token
+    uint32_t* met;        // [blocks][rows / 32] bits: rows with a token (null: not wanted)
+    int32_t* count;       // sorted positions in all
     int* err;
 };
+constexpr uint32_t kNoId = 0xFFFFFFFFu;
 
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
@@ -127,51 +148,68 @@ __device__ __forceinline__ int warp_sum(int v) {
     return v;
 }
 
+// An id, or kNoId where it gives no gradient.
 template <typename I>
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a) {
-    extern __shared__ int counts[];  // [warps][range]: tokens of a row that a warp has met, then where its next one goes
+__device__ __forceinline__ uint32_t usable_id(const SortArgs& a, int64_t t, bool& outside) {
+    const I id = static_cast<const I*>(a.ids)[t];
+    if constexpr (sizeof(I) == 8) {
+        if (static_cast<uint64_t>(id) >= a.v) {
+            outside = true;
+            return kNoId;
+        }
+    } else if (static_cast<uint32_t>(id) >= a.v) {
+        outside = true;
+        return kNoId;
+    }
+    return static_cast<uint32_t>(id) == a.padding ? kNoId : static_cast<uint32_t>(id);
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
+    extern __shared__ int counts[];  // [warps][rows]: tokens of a row that a warp has met, then where its next one goes
     __shared__ int below[kSortWarps], sums[kSortWarps];
+    __shared__ uint32_t bits[kMaxRows / 32];
     mma::grid_launch_dependents();
-    mma::grid_wait();
-    const I* ids = static_cast<const I*>(a.ids);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t lo = (int64_t)blockIdx.x * a.range;
-    const int rows = (int)min((int64_t)a.range, a.v - lo);
-    for (int i = threadIdx.x; i < a.warps * a.range; i += kSortThreads) counts[i] = 0;
+    const uint32_t mask = (1u << a.shift) - 1, me = blockIdx.x, rows = a.rows;
+    for (int i = threadIdx.x * 4; i < a.warps * a.rows; i += kSortThreads * 4) *reinterpret_cast<int4*>(counts + i) = make_int4(0, 0, 0, 0);
+    if (threadIdx.x < kMaxRows / 32) bits[threadIdx.x] = 0;
     __syncthreads();
+    mma::grid_wait();
     // each warp has one stretch of the tokens, a multiple of 32
     const int64_t per = (a.t + a.warps * 32 - 1) / (a.warps * 32) * 32;
     const int64_t t0 = warp * per, t1 = warp < a.warps ? min(a.t, t0 + per) : 0;
-    int* mine = counts + warp * a.range;
+    int* mine = counts + warp * a.rows;
     int less = 0;
     bool outside = false;
-    constexpr int U = 8;
-    for (int64_t t = t0 + lane; t < t1; t += 32 * U) {
-        int64_t id[U];
+    uint32_t held[kHeld];
+    for (int64_t base = t0; base < t1; base += 32 * kHeld) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = t + 32 * u < t1 ? id_at(ids, t + 32 * u) : a.v;
+        for (int u = 0; u < kHeld; ++u) {
+            const int64_t t = base + 32 * u + lane;
+            held[u] = t < t1 ? usable_id<I>(a, t, outside) : kNoId;
+        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + 32 * u >= t1) continue;
-            const bool good = id[u] >= 0 && id[u] < a.v;
-            outside |= !good && id[u] != a.padding;
-            if (!good || id[u] == a.padding) continue;
-            less += id[u] < lo;
-            const int64_t r = id[u] - lo;
-            if (r >= 0 && r < rows) atomicAdd(mine + r, 1);
+        for (int u = 0; u < kHeld; ++u) {
+            // kNoId has the highest low bits and no row
+            less += (held[u] & mask) < me;
+            if ((held[u] & mask) == me && (held[u] >> a.shift) < rows) atomicAdd(mine + (held[u] >> a.shift), 1);
         }
     }
     if (outside && blockIdx.x == 0) record_device_error(a.err, DPRED_E_BOUNDS);
     less = warp_sum(less);
     if (lane == 0) below[warp] = less;
     __syncthreads();
-    // the rows' tokens in all; an exclusive sum over rows, then over the warps of a row
+    // the rows' tokens in all (a thread has up to 4 rows next to each other); an
+    // exclusive sum over rows, then over the warps of a row
+    const int each = (a.rows + kSortThreads - 1) / kSortThreads, r0 = threadIdx.x * each, r1 = min(r0 + each, a.rows);
     int total = 0;
-    if ((int)threadIdx.x < rows)
-        for (int w = 0; w < a.warps; ++w) total += counts[w * a.range + threadIdx.x];
-    if (a.met) {
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, total != 0);
-        if (lane == 0 && warp * 32 < rows) a.met[lo / 32 + warp] = bits;
+    for (int r = r0; r < r1; ++r) {
+        int n = 0;
+#pragma unroll 8
+        for (int w = 0; w < a.warps; ++w) n += counts[w * a.rows + r];
+        if (n && a.met) atomicOr(bits + r / 32, 1u << r % 32);
+        total += n;
     }
     int before = total;
 #pragma unroll
@@ -182,41 +220,47 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     if (lane == 31) sums[warp] = before;
     before -= total;
     __syncthreads();
-    int start = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-        start += below[w];
-        if (w < warp) before += sums[w];
-    }
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == kSortThreads - 1) *a.count = start + before + total;
-    if ((int)threadIdx.x < rows) {
-        int at = start + before;
+    int start = below[lane], ahead = lane < warp ? sums[lane] : 0;
+    start = warp_sum(start);
+    before += warp_sum(ahead) + start;
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == kSortThreads - 1) *a.count = before + total;
+    if (a.met && threadIdx.x < a.rows / 32) a.met[(int64_t)blockIdx.x * (a.rows / 32) + threadIdx.x] = bits[threadIdx.x];
+    for (int r = r0; r < r1; ++r) {
+#pragma unroll 8
         for (int w = 0; w < a.warps; ++w) {
-            int& c = counts[w * a.range + threadIdx.x];
+            int& c = counts[w * a.rows + r];
             const int n = c;
-            c = at;
-            at += n;
+            c = before;
+            before += n;
         }
     }
     __syncthreads();
-    for (int64_t t = t0 + lane; t - lane < t1; t += 32 * U) {
-        int64_t id[U];
+    for (int64_t base = t0; base < t1; base += 32 * kHeld) {
+        if (per > 32 * kHeld) {  // else the ids are still there
 #pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = t + 32 * u < t1 ? id_at(ids, t + 32 * u) : -1;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = id[u] - lo;
-            const bool here = id[u] >= 0 && r >= 0 && r < rows && id[u] != a.padding;
-            if (!__any_sync(0xFFFFFFFFu, here)) continue;
-            const unsigned same = __match_any_sync(0xFFFFFFFFu, here ? (int)r : -1 - lane);
-            if (here) {
-                const int rank = __popc(same & ((1u << lane) - 1));
-                const int at = mine[r] + rank;
-                a.key[at] = (int32_t)id[u];
-                a.order[at] = (int32_t)(t + 32 * u);
+            for (int u = 0; u < kHeld; ++u) {
+                const int64_t t = base + 32 * u + lane;
+                held[u] = t < t1 ? usable_id<I>(a, t, outside) : kNoId;
             }
-            __syncwarp();
-            if (here && lane == __ffs(same) - 1) mine[r] += __popc(same);
-            __syncwarp();
+        }
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            const uint32_t r = held[u] >> a.shift;
+            const bool here = (held[u] & mask) == me && r < rows;
+            unsigned left = __ballot_sync(0xFFFFFFFFu, here);
+            while (left) {  // row by row, the tokens of one in ascending t
+                const uint32_t row = __shfl_sync(0xFFFFFFFFu, r, __ffs(left) - 1);
+                const unsigned same = __ballot_sync(0xFFFFFFFFu, here && r == row);
+                left &= ~same;
+                const int at = mine[row] + __popc(same & ((1u << lane) - 1));
+                __syncwarp();
+                if (same >> lane & 1) {
+                    a.key[at] = (int32_t)held[u];
+                    a.order[at] = (int32_t)(base + 32 * u + lane);
+                    if ((same >> lane) == 1u) mine[row] = at + 1;  // the last of them
+                }
+                __syncwarp();
+            }
         }
     }
 }
@@ -226,6 +270,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
 constexpr int kSlab = 256;      // columns of a warp
 constexpr int kFillRows = 8;    // rows of a warp that writes zeros
+constexpr int kMostRun = 32;    // positions of a run
 
 struct SumArgs {
     const void* dy;
@@ -234,10 +279,10 @@ struct SumArgs {
     const uint32_t* met;   // null: rows without a token stay as they are
     float *head, *tail;    // [runs][d] partial sums: of the row that began before the run, of the one that goes on behind it
     int64_t ldy, ldw, v;
-    int32_t d, slabs;
+    int32_t d, slabs, run;  // run: positions, a power of two
+    int32_t shift, rows;    // as in SortArgs
     int64_t runs, sum_blocks;
     float scale;
-    int32_t accumulate;
 };
 
 // A lane's first column of a slab.
@@ -246,104 +291,87 @@ __device__ __forceinline__ int first_column(int base, int lane) {
     return VEC ? base + lane * 8 : base + lane;
 }
 
-// A finished row into the gradient.
-template <bool VEC, typename T>
-__device__ __forceinline__ void leave(T* p, int c0, int d, const float (&sum)[8], float scale, bool add) {
-    float f[8];
-    if (add) {
-        Cols<T, VEC> old;
-        old.load(p, c0, 32, d);
+__device__ __forceinline__ F8 plus(const F8& a, const F8& b) {
+    F8 f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = fmaf(sum[k], scale, old[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = sum[k] * scale;
-    }
-    store_cols<VEC>(p, c0, 32, d, f);
+    for (int i = 0; i < 4; ++i) f.p[i] = make_float2(a.p[i].x + b.p[i].x, a.p[i].y + b.p[i].y);
+    return f;
 }
 
-template <typename TG, typename TW, bool VEC>
+// ADD: the sums are added to rows of dw, which are asked for with the last of
+// their tokens' rows.
+template <typename TG, typename TW, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumArgs a) {
     if (a.runs > 1) mma::grid_launch_dependents();  // another launch of the call follows
     mma::grid_wait();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     TW* dw = static_cast<TW*>(a.dw);
     if (blockIdx.x >= a.sum_blocks) {  // zeros for the rows without a token
-        const int64_t r0 = ((blockIdx.x - a.sum_blocks) * kSumWarps + warp) * kFillRows;
-        const float zero[8] = {};
-        if (r0 >= a.v) return;
-        const uint32_t bits = a.met[r0 / 32] >> (r0 % 32);
-        for (int r = 0; r < kFillRows && r0 + r < a.v; ++r) {
-            if (bits >> r & 1) continue;
-            for (int base = 0; base < a.d; base += kSlab) store_cols<VEC>(dw + (r0 + r) * a.ldw, first_column<VEC>(base, lane), 32, a.d, zero);
+        const int64_t v0 = ((blockIdx.x - a.sum_blocks) * kSumWarps + warp) * kFillRows, id = v0 + lane;
+        bool met = true;
+        if (lane < kFillRows && id < a.v) {
+            const int64_t block = id & ((1 << a.shift) - 1), r = id >> a.shift;
+            met = a.met[block * (a.rows / 32) + r / 32] >> (r % 32) & 1;
         }
+        const unsigned without = __ballot_sync(0xFFFFFFFFu, !met);
+        const F8 zero = splat(0.0f);
+#pragma unroll
+        for (int r = 0; r < kFillRows; ++r)
+            if (without >> r & 1)
+                for (int base = 0; base < a.d; base += kSlab) store_cols<VEC>(dw + (v0 + r) * a.ldw, first_column<VEC>(base, lane), 32, a.d, zero);
         return;
     }
     const int64_t item = (int64_t)blockIdx.x * kSumWarps + warp, run = item / a.slabs;
     const int c0 = first_column<VEC>((int)(item % a.slabs) * kSlab, lane);
-    const int64_t n = *a.count, p0 = run * kRun;
+    const int64_t n = *a.count, p0 = run * a.run;
     if (p0 >= n) return;
-    const int len = (int)min((int64_t)kRun, n - p0);
+    const int len = (int)min((int64_t)a.run, n - p0);
     const int32_t key = lane < len ? a.key[p0 + lane] : -1, token = lane < len ? a.order[p0 + lane] : 0;
-    const bool goes_on = p0 + len < n && a.key[p0 + len] == __shfl_sync(0xFFFFFFFFu, key, len - 1);
-    bool began_before = p0 > 0 && a.key[p0 - 1] == __shfl_sync(0xFFFFFFFFu, key, 0);
+    const int32_t after = p0 + len < n ? a.key[p0 + len] : -1, ahead = p0 > 0 ? a.key[p0 - 1] : -1;
+    const int32_t next = __shfl_down_sync(0xFFFFFFFFu, key, 1);
+    // positions that end a row's share of this run; the row that began before, and the one that goes on behind it
+    const unsigned ends = __ballot_sync(0xFFFFFFFFu, lane < len && (lane == len - 1 || key != next));
+    const unsigned head = __shfl_sync(0xFFFFFFFFu, key, 0) == ahead ? ends & (0u - ends) : 0u;
+    const unsigned tail = __shfl_sync(0xFFFFFFFFu, key, len - 1) == after ? (1u << (len - 1)) & ~head : 0u;
+    const unsigned whole = ends & ~head & ~tail;
     const TG* dy = static_cast<const TG*>(a.dy);
-    float sum[8] = {};
-    constexpr int U = 8;
+    const F8 scale = splat(a.scale);
+    F8 sum = splat(0.0f);
+    constexpr int U = ADD ? 4 : 8;
     for (int i = 0; i < len; i += U) {
         Cols<TG, VEC> q[U];
+        Cols<TW, VEC> old[ADD ? U : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t t = __shfl_sync(0xFFFFFFFFu, token, i + u);
+            const int64_t t = __shfl_sync(0xFFFFFFFFu, token, (i + u) % 32), row = __shfl_sync(0xFFFFFFFFu, key, (i + u) % 32);
             if (i + u < len) q[u].load(dy + t * a.ldy, c0, 32, a.d);
+            if (ADD && (whole >> (i + u) & 1)) old[ADD ? u : 0].load(dw + row * a.ldw, c0, 32, a.d);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t now = __shfl_sync(0xFFFFFFFFu, key, i + u), next = __shfl_sync(0xFFFFFFFFu, key, (i + u + 1) % 32);
+            const int64_t row = __shfl_sync(0xFFFFFFFFu, key, (i + u) % 32);
             if (i + u >= len) continue;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += q[u][k];
-            const bool last = i + u + 1 == len;
-            if (!last && now == next) continue;
-            if (began_before)
+            sum = plus(sum, widen(q[u]));
+            if (!(ends >> (i + u) & 1)) continue;
+            if (head >> (i + u) & 1)
                 store_cols<VEC>(a.head + run * a.d, c0, 32, a.d, sum);
-            else if (last && goes_on)
+            else if (tail >> (i + u) & 1)
                 store_cols<VEC>(a.tail + run * a.d, c0, 32, a.d, sum);
             else
-                leave<VEC>(dw + now * a.ldw, c0, a.d, sum, a.scale, a.accumulate);
-            began_before = false;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+                store_cols<VEC>(dw + row * a.ldw, c0, 32, a.d, ADD ? fma8(sum, scale, widen(old[ADD ? u : 0])) : sum * scale);
+            sum = splat(0.0f);
         }
     }
 }
 
-// The row that begins in this run and goes on behind it: its tail here and the
-// heads of the runs that follow.  The block's warps share them, and the shares
-// are added in order.
-template <typename TW, bool VEC>
-__global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant__ SumArgs a) {
-    __shared__ float part[kSumWarps][kSlab];
-    mma::grid_wait();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t run = blockIdx.x / a.slabs, n = *a.count, p0 = run * kRun;
-    const int c0 = first_column<VEC>((int)(blockIdx.x % a.slabs) * kSlab, lane);
-    if (p0 + kRun >= n) return;
-    const int32_t row = a.key[p0 + kRun - 1];
-    if (a.key[p0 + kRun] != row) return;
-    if (a.key[p0] == row && p0 > 0 && a.key[p0 - 1] == row) return;  // it began before
-    // runs behind this one that begin with the row
-    const int64_t runs = (n + kRun - 1) / kRun;
-    int64_t more = 1;
-    for (;;) {
-        const int64_t r = run + 1 + more + lane;
-        const unsigned same = __ballot_sync(0xFFFFFFFFu, r < runs && a.key[r * kRun] == row);
-        const int k = same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
-        more += k;
-        if (k < 32) break;
-    }
-    const int64_t q0 = run + 1 + more * warp / kSumWarps, q1 = run + 1 + more * (warp + 1) / kSumWarps;
-    float sum[8] = {};
+// The rows that begin in a run and go on behind it: the tail there and the heads of
+// the runs that follow.  A warp looks at one run; it adds a few heads itself, and
+// leaves a longer row to all warps of the block, whose shares are added in order.
+constexpr int kFewHeads = 8;
+
+template <bool VEC>
+__device__ __forceinline__ F8 sum_heads(const SumArgs& a, int64_t q0, int64_t q1, int c0) {
+    F8 sum = splat(0.0f);
     constexpr int U = 4;
     for (int64_t q = q0; q < q1; q += U) {
         Cols<float, VEC> f[U];
@@ -352,28 +380,99 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant
             if (q + u < q1) f[u].load(a.head + (q + u) * a.d, c0, 32, a.d);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + u < q1)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum[k] += f[u][k];
+            if (q + u < q1) sum = plus(sum, widen(f[u]));
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) part[warp][k * 32 + lane] = sum[k];
+    return sum;
+}
+
+template <bool VEC, bool ADD, typename TW>
+__device__ __forceinline__ void leave(TW* p, int c0, int d, const F8& sum, float scale) {
+    if (ADD) {
+        Cols<TW, VEC> old;
+        old.load(p, c0, 32, d);
+        store_cols<VEC>(p, c0, 32, d, fma8(sum, splat(scale), widen(old)));
+    } else {
+        store_cols<VEC>(p, c0, 32, d, sum * splat(scale));
+    }
+}
+
+template <typename TW, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant__ SumArgs a) {
+    __shared__ float part[kSumWarps][kSlab];
+    __shared__ int64_t heads[kSumWarps];
+    mma::grid_wait();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int c0 = first_column<VEC>((int)(blockIdx.x % a.slabs) * kSlab, lane);
+    const int64_t run0 = (int64_t)(blockIdx.x / a.slabs) * kSumWarps, run = run0 + warp, n = *a.count, p0 = run * a.run;
+    TW* dw = static_cast<TW*>(a.dw);
+    int64_t more = 0;  // runs behind this one that begin with the row that begins here
+    if (p0 + a.run < n) {
+        const int32_t row = a.key[p0 + a.run - 1], after = a.key[p0 + a.run], first = a.key[p0], ahead = p0 > 0 ? a.key[p0 - 1] : -1;
+        if (after == row && !(first == row && ahead == row)) {
+            const int64_t runs = (n + a.run - 1) / a.run;
+            for (;;) {
+                const int64_t r = run + 1 + more + lane;
+                const unsigned same = __ballot_sync(0xFFFFFFFFu, r < runs && a.key[min(r, runs - 1) * a.run] == row);
+                const int k = same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
+                more += k;
+                if (k < 32) break;
+            }
+            if (more <= kFewHeads) {
+                Cols<float, VEC> first_part;
+                first_part.load(a.tail + run * a.d, c0, 32, a.d);
+                leave<VEC, ADD>(dw + (int64_t)row * a.ldw, c0, a.d, plus(widen(first_part), sum_heads<VEC>(a, run + 1, run + 1 + more, c0)), a.scale);
+            }
+        }
+    }
+    if (lane == 0) heads[warp] = more;
     __syncthreads();
-    if (warp) return;
-    Cols<float, VEC> first;
-    first.load(a.tail + run * a.d, c0, 32, a.d);
+    for (int w = 0; w < kSumWarps; ++w) {
+        const int64_t k = heads[w], q0 = run0 + w + 1;
+        if (k <= kFewHeads) continue;
+        const F8 mine = sum_heads<VEC>(a, q0 + k * warp / kSumWarps, q0 + k * (warp + 1) / kSumWarps, c0);
+        __syncthreads();  // the row before is done with part
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        sum[k] = first[k];
-        for (int w = 0; w < kSumWarps; ++w) sum[k] += part[w][k * 32 + lane];
+        for (int i = 0; i < 8; ++i) part[warp][i * 32 + lane] = mine.get(i);
+        __syncthreads();
+        if (warp) continue;
+        Cols<float, VEC> first_part;
+        first_part.load(a.tail + (q0 - 1) * a.d, c0, 32, a.d);
+        F8 sum = widen(first_part);
+        for (int x = 0; x < kSumWarps; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum.p[i].x += part[x][2 * i * 32 + lane];
+                sum.p[i].y += part[x][(2 * i + 1) * 32 + lane];
+            }
+        leave<VEC, ADD>(dw + (int64_t)a.key[q0 * a.run] * a.ldw, c0, a.d, sum, a.scale);
     }
-    leave<VEC>(static_cast<TW*>(a.dw) + row * a.ldw, c0, a.d, sum, a.scale, a.accumulate);
 }
 
 // --------------------------------------------------------------------- host --
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
-int64_t runs_of(int64_t t) { return (t + kRun - 1) / kRun; }
+int64_t slabs_of(int64_t d) { return (d + kSlab - 1) / kSlab; }
+
+// Positions of a run: 32 where that leaves 4096 warps (27 to an SM) or more, fewer
+// where there are fewer tokens, so that they keep the SMs busy too.
+int run_of(int64_t t, int64_t d) {
+    int run = kMostRun;
+    while (run > 4 && t * slabs_of(d) < (int64_t)4096 * run) run /= 2;
+    return run;
+}
+int64_t runs_of(int64_t t, int64_t d) { return (t + run_of(t, d) - 1) / run_of(t, d); }
+
+// How the ids are dealt out: to 128 blocks, or to more where a block would have
+// more than kMaxRows rows.
+struct Deal {
+    int shift, rows;
+};
+Deal deal_of(int64_t v) {
+    Deal q = {7, 0};
+    while (((v - 1) >> q.shift) + 1 > kMaxRows) ++q.shift;
+    q.rows = (int)((((v - 1) >> q.shift) + 1 + 31) / 32 * 32);
+    return q;
+}
 
 struct Space {
     int64_t key, order, met, count, head, tail, bytes;
@@ -386,12 +485,13 @@ Space space_of(int64_t t, int64_t v, int64_t d) {
         at += align256(n);
         return p;
     };
+    const Deal q = deal_of(v);
     s.key = take(t * 4);
     s.order = take(t * 4);
-    s.met = take((v + 31) / 32 * 4);
+    s.met = take(((int64_t)q.rows << q.shift) / 8);
     s.count = take(4);
-    s.head = take(runs_of(t) * d * 4);
-    s.tail = take(runs_of(t) * d * 4);
+    s.head = take(runs_of(t, d) * d * 4);
+    s.tail = take(runs_of(t, d) * d * 4);
     s.bytes = at;
     return s;
 }
@@ -410,24 +510,36 @@ int check_ids(const void* ids, int64_t t, int32_t id_bytes) {
     return DPRED_OK;
 }
 
+template <typename TW, typename TY, int CH>
+cudaError_t launch_rows(const LookArgs& a, int lanes, cudaStream_t s) {
+    const int64_t per = (int64_t)(kLookThreads / 32) * (32 / lanes) * (8 / CH), blocks = (a.t + per - 1) / per;
+    // two turns for each warp where that leaves every SM two blocks
+    const int64_t grid = std::max((blocks + 1) / 2, std::min<int64_t>(blocks, 2 * sm_count()));
+    return launch(lookup_kernel<TW, TY, CH>, dim3((unsigned)std::min<int64_t>(grid, 1 << 20)), kLookThreads, 0, s, a, lanes);
+}
+
 template <typename TW, typename TY>
 cudaError_t launch_lookup(const LookArgs& a, bool vec, cudaStream_t s) {
-    const int items = vec ? (a.d + 7) / 8 : a.d;
+    if (!vec) return launch(lookup_any_kernel<TW, TY>, dim3((unsigned)std::min<int64_t>((a.t + 7) / 8, 1 << 20)), kLookThreads, 0, s, a);
     int lanes = 1;
-    while (lanes < items && lanes < kLookThreads) lanes *= 2;
-    const int64_t groups = kLookThreads / lanes;
-    // a row at a time while that gives every SM its blocks, then kLookRows at once
-    const int64_t blocks = std::min<int64_t>((a.t + groups - 1) / groups, std::max<int64_t>((a.t + groups * kLookRows - 1) / (groups * kLookRows), 8 * sm_count()));
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 20));
-    return vec ? launch(lookup_kernel<TW, TY, true>, grid, kLookThreads, 0, s, a, lanes) : launch(lookup_kernel<TW, TY, false>, grid, kLookThreads, 0, s, a, lanes);
+    while (lanes < 32 && lanes * 8 < a.d) lanes *= 2;
+    if (a.d <= 256) return launch_rows<TW, TY, 1>(a, lanes, s);
+    if (a.d <= 512) return launch_rows<TW, TY, 2>(a, lanes, s);
+    if (a.d <= 1024) return launch_rows<TW, TY, 4>(a, lanes, s);
+    return launch_rows<TW, TY, 8>(a, lanes, s);
+}
+
+template <typename TG, typename TW, bool VEC, bool ADD>
+cudaError_t launch_sums(const SumArgs& a, unsigned blocks, cudaStream_t s) {
+    const cudaError_t e = launch(sum_kernel<TG, TW, VEC, ADD>, dim3(blocks), kSumThreads, 0, s, a);
+    if (e != cudaSuccess || a.runs <= 1) return e;
+    return launch(join_kernel<TW, VEC, ADD>, dim3((unsigned)((a.runs - 1 + kSumWarps - 1) / kSumWarps * a.slabs)), kSumThreads, 0, s, a);
 }
 
 template <typename TG, typename TW>
-cudaError_t launch_sums(const SumArgs& a, bool vec, unsigned blocks, cudaStream_t s) {
-    cudaError_t e = vec ? launch(sum_kernel<TG, TW, true>, dim3(blocks), kSumThreads, 0, s, a) : launch(sum_kernel<TG, TW, false>, dim3(blocks), kSumThreads, 0, s, a);
-    if (e != cudaSuccess || a.runs <= 1) return e;
-    const dim3 grid((unsigned)((a.runs - 1) * a.slabs));
-    return vec ? launch(join_kernel<TW, true>, grid, kSumThreads, 0, s, a) : launch(join_kernel<TW, false>, grid, kSumThreads, 0, s, a);
+cudaError_t launch_sums(const SumArgs& a, bool vec, bool add, unsigned blocks, cudaStream_t s) {
+    if (vec) return add ? launch_sums<TG, TW, true, true>(a, blocks, s) : launch_sums<TG, TW, true, false>(a, blocks, s);
+    return add ? launch_sums<TG, TW, false, true>(a, blocks, s) : launch_sums<TG, TW, false, false>(a, blocks, s);
 }
 
 }  // namespace
@@ -473,33 +585,35 @@ extern "C" int dpred_embedding_grad(int64_t t, int64_t v, int64_t d, int32_t id_
         (rc = check_matrix(dw, v, d, lddw, ws, "dw")) != DPRED_OK)
         return rc;
     if (t == 0 && accumulate) return DPRED_OK;
-    const int64_t slabs = (d + kSlab - 1) / kSlab, sum_blocks = (runs_of(t) * slabs + kSumWarps - 1) / kSumWarps;
+    const int64_t slabs = slabs_of(d), runs = runs_of(t, d), sum_blocks = (runs * slabs + kSumWarps - 1) / kSumWarps;
     const int64_t blocks = sum_blocks + (accumulate ? 0 : (v + kSumWarps * kFillRows - 1) / (kSumWarps * kFillRows));
-    if (blocks > 0x7FFFFFFF || runs_of(t) * slabs > 0x7FFFFFFF)
+    if (blocks > 0x7FFFFFFF || runs * slabs > 0x7FFFFFFF)
         return set_error(DPRED_E_SIZE, "%lld tokens of %lld columns are too many", (long long)t, (long long)d);
     const Space sp = space_of(t, v, d);
     if ((rc = check_workspace(workspace, workspace_bytes, (size_t)sp.bytes)) != DPRED_OK) return rc;
     char* base = static_cast<char*>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Deal deal = deal_of(v);
 
     SortArgs q = {};
     q.ids = ids;
-    q.padding = padding < 0 ? INT64_MIN : padding;
     q.t = t;
-    q.v = v;
-    // one CTA per SM where its counters fit; a counter row for each 128 tokens, so that few tokens clear few counters
-    q.range = (int32_t)std::min<int64_t>(kMaxRange, ((v + sm_count() - 1) / sm_count() + 31) / 32 * 32);
-    q.warps = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kSortWarps, t / 128));
+    q.v = (uint32_t)v;
+    q.padding = padding < 0 ? kNoId : (uint32_t)padding;
+    q.shift = deal.shift;
+    q.rows = deal.rows;
+    // a set of counters for each 128 tokens, so that few tokens clear few, as far as there is room
+    q.warps = (int32_t)std::max<int64_t>(1, std::min<int64_t>({kSortWarps, t / 128, kCounters / (deal.rows * 4)}));
     q.key = reinterpret_cast<int32_t*>(base + sp.key);
     q.order = reinterpret_cast<int32_t*>(base + sp.order);
     q.met = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + sp.met);
     q.count = reinterpret_cast<int32_t*>(base + sp.count);
     q.err = device_error_word();
-    const int smem = q.warps * q.range * 4;
+    const int smem = q.warps * q.rows * 4;
     static bool done32[64], done64[64];
-    cudaError_t e = id_bytes == 8 ? ensure_smem_attr(sort_kernel<int64_t>, kSortWarps * kMaxRange * 4, done64) : ensure_smem_attr(sort_kernel<int32_t>, kSortWarps * kMaxRange * 4, done32);
+    cudaError_t e = id_bytes == 8 ? ensure_smem_attr(sort_kernel<int64_t>, kCounters, done64) : ensure_smem_attr(sort_kernel<int32_t>, kCounters, done32);
     if (e != cudaSuccess) return cuda_error(e, "embedding gradient set-up");
-    const dim3 grid((unsigned)((v + q.range - 1) / q.range));
+    const dim3 grid(1u << deal.shift);
     e = id_bytes == 8 ? launch(sort_kernel<int64_t>, grid, kSortThreads, smem, s, q) : launch(sort_kernel<int32_t>, grid, kSortThreads, smem, s, q);
     if (e != cudaSuccess) return cuda_error(e, "embedding gradient launch");
 
@@ -517,12 +631,14 @@ extern "C" int dpred_embedding_grad(int64_t t, int64_t v, int64_t d, int32_t id_
     a.v = v;
     a.d = (int32_t)d;
     a.slabs = (int32_t)slabs;
-    a.runs = runs_of(t);
+    a.run = run_of(t, d);
+    a.shift = deal.shift;
+    a.rows = deal.rows;
+    a.runs = runs;
     a.sum_blocks = sum_blocks;
     a.scale = scale;
-    a.accumulate = accumulate != 0;
-        const bool vec = d % 8 == 0 && aligned_rows(dy, t, lddy, gs) && aligned_rows(dw, v, lddw, ws);
-    e = g_dtype == DPRED_F32 ? (out_dtype == DPRED_F32 ? launch_sums<float, float>(a, vec, (unsigned)blocks, s) : launch_sums<float, __nv_bfloat16>(a, vec, (unsigned)blocks, s))
-                             : (out_dtype == DPRED_F32 ? launch_sums<__nv_bfloat16, float>(a, vec, (unsigned)blocks, s) : launch_sums<__nv_bfloat16, __nv_bfloat16>(a, vec, (unsigned)blocks, s));
+    const bool vec = d % 8 == 0 && aligned_rows(dy, t, lddy, gs) && aligned_rows(dw, v, lddw, ws), add = accumulate != 0;
+    e = g_dtype == DPRED_F32 ? (out_dtype == DPRED_F32 ? launch_sums<float, float>(a, vec, add, (unsigned)blocks, s) : launch_sums<float, __nv_bfloat16>(a, vec, add, (unsigned)blocks, s))
+                             : (out_dtype == DPRED_F32 ? launch_sums<__nv_bfloat16, float>(a, vec, add, (unsigned)blocks, s) : launch_sums<__nv_bfloat16, __nv_bfloat16>(a, vec, add, (unsigned)blocks, s));
     return e == cudaSuccess ? DPRED_OK : cuda_error(e, "embedding gradient launch");
 }
