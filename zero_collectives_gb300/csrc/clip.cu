@@ -9,11 +9,12 @@
 //
 // One launch sums squares, a second forms n and c from its partial sums and
 // scales; where c is 1 it reads and writes nothing more.  Both walk the same
-// table of units of 16 KB; it travels inside the launch.
+// table of units of 16 KB; it travels inside the launch.  Few units are done by
+// one cluster in one launch.
 //
-// Bandwidth bound: each gradient is read, then read and written.  The second
-// launch takes the units in the opposite order, so that what the first read last
-// is still in L2.
+// Bandwidth bound: each gradient is read, then read and written.  Every block has
+// the same stretch in both launches and takes it in the opposite order in the
+// second, so that what the first read last is still in L2.
 #include <algorithm>
 #include <vector>
 
@@ -26,6 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnit = 16384;         // bytes of a unit: four 16-byte vectors a thread
 constexpr int kNarrow = 512;         // rows below this many bytes are taken element by element
+constexpr int kBlocksPerSm = 3;      // each with up to 32 KB of loads in flight, in 80 registers a thread
 constexpr int kMaxBlocks = 2048;     // partial sums a launch can leave
 constexpr int kSmallTable = 32, kMidTable = 256, kTable = 768;  // pieces that travel in a launch (1, 10 and 31 KB)
 constexpr int kMaxUnits = 0x3FFFFFFF;  // of a launch
@@ -47,6 +49,38 @@ struct Table {
 };
 static_assert(sizeof(Table<kTable>) < 32000, "a launch's arguments");
 
+// Four 16-byte vectors of a type, widened piece by piece.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ float2 pair(const uint4& q, int i) {
+        const uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+        return make_float2(bf16_lo(w), bf16_hi(w));
+    }
+    static __device__ __forceinline__ uint4 scaled(const uint4& q, float c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = mul2(pair(q, i), make_float2(c, c));
+            w[i] = pack_bf16x2(f.x, f.y);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ float2 pair(const uint4& q, int i) {
+        return i == 0 ? make_float2(__uint_as_float(q.x), __uint_as_float(q.y)) : make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+    static __device__ __forceinline__ uint4 scaled(const uint4& q, float c) {
+        const float2 a = mul2(pair(q, 0), make_float2(c, c)), b = mul2(pair(q, 1), make_float2(c, c));
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+};
+
 // A sum of squares over the whole range of the type.  A chunk of up to 32
 // squares is added in fp32; chunks between 2^-90 and 2^80 go to a compensated
 // pair of fp32 (its error stays near 2^-24 of the sum however many there are;
@@ -56,26 +90,46 @@ struct Squares {
     float hi = 0.0f, lo = 0.0f;
     double far = 0.0;
 
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N]) {
-        float q[4] = {};
+    template <typename T>
+    __device__ __forceinline__ void add(const uint4 (&q)[4]) {
+        float2 t[2] = {};
 #pragma unroll
-        for (int k = 0; k < N; ++k) q[k & 3] = fmaf(x[k], x[k], q[k & 3]);
-        const float c = (q[0] + q[1]) + (q[2] + q[3]);
-        if (c >= 0x1p-90f && c <= 0x1p80f) {
-            const float s = hi + c, t = s - hi;
-            lo += (hi - (s - t)) + (c - t);
-            hi = s;
-            return;
-        }
-        const bool small = c < 0x1p-90f;  // zeros most of the time
-        const float f = small ? 0x1p100f : 0x1p-70f;
-        float d = 0.0f;
+        for (int v = 0; v < 4; ++v)
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const float y = x[k] * f;
-            d = fmaf(y, y, d);
+            for (int i = 0; i < Vec<T>::N / 2; ++i) {
+                const float2 f = Vec<T>::pair(q[v], i);
+                t[v & 1] = fma2(f, f, t[v & 1]);
+            }
+        const float c = (t[0].x + t[0].y) + (t[1].x + t[1].y);
+        if (!near(c)) {
+            const bool small = c < 0x1p-90f;  // zeros most of the time
+            const float f = small ? 0x1p100f : 0x1p-70f;
+            float d = 0.0f;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int i = 0; i < Vec<T>::N / 2; ++i) {
+                    const float2 x = Vec<T>::pair(q[v], i);
+                    d = fmaf(x.x * f, x.x * f, d);
+                    d = fmaf(x.y * f, x.y * f, d);
+                }
+            apart(d, small);
         }
+    }
+    __device__ __forceinline__ void add(float x) {
+        if (near(x * x)) return;
+        const bool small = x * x < 0x1p-90f;
+        const float y = x * (small ? 0x1p100f : 0x1p-70f);
+        apart(y * y, small);
+    }
+    __device__ __forceinline__ bool near(float c) {
+        if (!(c >= 0x1p-90f && c <= 0x1p80f)) return false;
+        const float s = hi + c, t = s - hi;
+        lo += (hi - (s - t)) + (c - t);
+        hi = s;
+        return true;
+    }
+    __device__ __forceinline__ void apart(float d, bool small) {
         if (d != 0.0f) far += (double)d * (small ? 0x1p-200 : 0x1p140);
     }
     __device__ __forceinline__ double total() const { return far + ((double)hi + (double)lo); }
@@ -92,118 +146,173 @@ __device__ __forceinline__ double block_sum(double v) {
     return v;
 }
 
-// The 16-byte vectors of a type.
-template <typename T>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void widen(const uint4& q, float* f) {
-        f[0] = bf16_lo(q.x); f[1] = bf16_hi(q.x); f[2] = bf16_lo(q.y); f[3] = bf16_hi(q.y);
-        f[4] = bf16_lo(q.z); f[5] = bf16_hi(q.z); f[6] = bf16_lo(q.w); f[7] = bf16_hi(q.w);
-    }
-    static __device__ __forceinline__ uint4 scaled(const uint4& q, float c) {
-        return make_uint4(pack_bf16x2(bf16_lo(q.x) * c, bf16_hi(q.x) * c), pack_bf16x2(bf16_lo(q.y) * c, bf16_hi(q.y) * c),
-                          pack_bf16x2(bf16_lo(q.z) * c, bf16_hi(q.z) * c), pack_bf16x2(bf16_lo(q.w) * c, bf16_hi(q.w) * c));
-    }
-};
-template <>
-struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void widen(const uint4& q, float* f) {
-        f[0] = __uint_as_float(q.x); f[1] = __uint_as_float(q.y); f[2] = __uint_as_float(q.z); f[3] = __uint_as_float(q.w);
-    }
-    static __device__ __forceinline__ uint4 scaled(const uint4& q, float c) {
-        return make_uint4(__float_as_uint(__uint_as_float(q.x) * c), __float_as_uint(__uint_as_float(q.y) * c),
-                          __float_as_uint(__uint_as_float(q.z) * c), __float_as_uint(__uint_as_float(q.w) * c));
-    }
-};
-
 template <bool SCALE, typename T>
 __device__ __forceinline__ void one(T* p, Squares& s, float c) {
-    const float x[1] = {load1(p)};
+    const float x = load1(p);
     if constexpr (SCALE)
-        store1(p, x[0] * c);
+        store1(p, x * c);
     else
         s.add(x);
 }
 
-// Vectors [v0, v1) of the n elements at p, counted from the first 16-byte
-// boundary, with the elements before it and after the last whole vector; by
-// threads id, id + step, ...
-template <bool SCALE, typename T>
-__device__ __forceinline__ void span(T* p, int64_t n, int64_t v0, int64_t v1, bool first, bool last, int id, int step, Squares& s, float c) {
-    constexpr int N = Vec<T>::N;
-    const int64_t head = min(n, (int64_t)((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T)));
-    const int64_t whole = (n - head) / N, tail = head + whole * N;
-    uint4* v = reinterpret_cast<uint4*>(p + head);
-    if (v1 > whole) v1 = whole;
-    for (int64_t i = v0 + id; i < v1; i += 4 * step) {
-        uint4 q[4];
-        if (i + 3 * step < v1) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) q[u] = v[i + u * step];
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) q[u] = i + u * step < v1 ? v[i + u * step] : make_uint4(0, 0, 0, 0);
-        }
-        if constexpr (SCALE) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i + u * step < v1) v[i + u * step] = Vec<T>::scaled(q[u], c);
-        } else {
-            float x[4 * N];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) Vec<T>::widen(q[u], x + u * N);
-            s.add(x);
-        }
+// A row's elements before the first 16-byte boundary, its whole vectors, and what
+// is left behind them.
+template <typename T>
+struct Row {
+    T* p;
+    int64_t n, head, whole;
+    __device__ __forceinline__ Row(T* p, int64_t n) : p(p), n(n) {
+        head = min(n, (int64_t)((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T)));
+        whole = (n - head) / Vec<T>::N;
     }
-    if (first)
-        for (int64_t i = id; i < head; i += step) one<SCALE>(p + i, s, c);
-    if (last)
-        for (int64_t i = tail + id; i < n; i += step) one<SCALE>(p + i, s, c);
+    __device__ __forceinline__ uint4* vectors() const { return reinterpret_cast<uint4*>(p + head); }
+    template <bool SCALE>
+    __device__ __forceinline__ void edges(bool first, bool last, int id, int step, Squares& s, float c) const {
+        if (first)
+            for (int64_t i = id; i < head; i += step) one<SCALE>(p + i, s, c);
+        if (last)
+            for (int64_t i = head + whole * Vec<T>::N + id; i < n; i += step) one<SCALE>(p + i, s, c);
+    }
+};
+
+// Past L1: nothing is read twice by one SM (the norm of 402.8M: 133 -> 121 us).
+__device__ __forceinline__ void load_four(uint4 (&q)[4], const uint4* v, int i, int n, int step) {
+    if (n >= 4 * step) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) q[u] = __ldcg(v + i + u * step);
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q[u] = i + u * step < n ? v[i + u * step] : make_uint4(0, 0, 0, 0);
 }
 
 template <bool SCALE, typename T>
-__device__ __forceinline__ void unit_of(const Piece& pc, int k, Squares& s, float c) {
+__device__ __forceinline__ void take_four(const uint4 (&q)[4], uint4* v, int i, int n, int step, Squares& s, float c) {
+    if constexpr (SCALE) {
+        if (n >= 4 * step) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[i + u * step] = Vec<T>::scaled(q[u], c);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * step < n) v[i + u * step] = Vec<T>::scaled(q[u], c);
+    } else {
+        s.add<T>(q);
+    }
+}
+
+// What a block has in flight of a unit: the vectors of a stretch of one row.
+struct Stretch {
+    uint4* v;
+    int n;  // vectors, at most 4 for each thread
+    int f32;
+};
+
+constexpr int kVecs = kUnit / 16;
+static_assert(kVecs == 4 * kThreads, "four vectors a thread");
+
+// The units of a row between its first and last that are full: nothing has to be
+// worked out for them.
+struct Inside {
+    int lo = 0, hi = 0;  // units
+    uint4* v = nullptr;  // of lo
+    int f32 = 0;
+};
+
+// A unit of whole rows, or the edges of a stretch; the stretch itself is returned.
+template <bool SCALE, typename T>
+__device__ __forceinline__ Stretch begin_unit(const Piece& pc, int unit, Squares& s, float c, Inside& in) {
     T* p = reinterpret_cast<T*>(pc.p);
+    const int k = unit - pc.unit0;
     if (pc.per < 0) {  // part of one row
-        const int row = k / -pc.per, part = k % -pc.per;
-        constexpr int64_t kVecs = kUnit / 16;
-        span<SCALE>(p + row * pc.ld, pc.cols, part * kVecs, (part + 1) * kVecs, part == 0, part == -pc.per - 1, threadIdx.x, kThreads, s, c);
-        return;
+        const int row = pc.per == -1 ? k : k / -pc.per, part = pc.per == -1 ? 0 : k % -pc.per, last = -pc.per - 1;
+        const Row<T> r(p + row * pc.ld, pc.cols);
+        r.template edges<SCALE>(part == 0, part == last, threadIdx.x, kThreads, s, c);
+        in = {unit - part + 1, unit - part + (int)min(r.whole / kVecs, (int64_t)last), r.vectors() + kVecs, sizeof(T) == 4};
+        const int64_t left = r.whole - (int64_t)part * kVecs;
+        return {r.vectors() + (int64_t)part * kVecs, (int)max((int64_t)0, min(left, (int64_t)kVecs)), sizeof(T) == 4};
     }
     const int64_t r0 = (int64_t)k * pc.per, r1 = min(r0 + pc.per, (int64_t)pc.rows);
     if (pc.cols * (int)sizeof(T) >= kNarrow) {  // a warp per row
-        for (int64_t r = r0 + threadIdx.x / 32; r < r1; r += kThreads / 32)
-            span<SCALE>(p + r * pc.ld, pc.cols, 0, pc.cols, true, true, threadIdx.x % 32, 32, s, c);
-        return;
+        const int lane = threadIdx.x % 32;
+        for (int64_t i = r0 + threadIdx.x / 32; i < r1; i += kThreads / 32) {
+            const Row<T> r(p + i * pc.ld, pc.cols);
+            uint4* v = r.vectors();
+            const int n = (int)r.whole;  // the row is within a unit
+            for (int j = 0; j < n; j += 128) {
+                uint4 q[4];
+                load_four(q, v + j, lane, n - j, 32);
+                take_four<SCALE, T>(q, v + j, lane, n - j, 32, s, c);
+            }
+            r.template edges<SCALE>(true, true, lane, 32, s, c);
+        }
+    } else {
+        const uint32_t cols = (uint32_t)pc.cols, total = (uint32_t)(r1 - r0) * cols;
+        for (uint32_t i = threadIdx.x; i < total; i += kThreads) one<SCALE>(p + (r0 + i / cols) * pc.ld + i % cols, s, c);
     }
-    const uint32_t cols = (uint32_t)pc.cols, total = (uint32_t)(r1 - r0) * cols;
-    for (uint32_t i = threadIdx.x; i < total; i += kThreads) one<SCALE>(p + (r0 + i / cols) * pc.ld + i % cols, s, c);
+    return {nullptr, 0, 0};
 }
 
+// The piece that unit lies in.
+template <typename A>
+__device__ __forceinline__ int piece_of(const A& t, int unit) {
+    int lo = 0, hi = t.n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (t.piece[mid].unit0 <= unit)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Block `block` of `blocks` has a stretch of the units and loads the next one while
+// it works on the one before.  Squares go up, scaling goes down.  (Units dealt out
+// in turn cost a search of the table each: the norm of 402.8M took 146 us.)
 template <bool SCALE, typename A>
-__device__ __forceinline__ void do_unit(const A& t, int unit, int& at, Squares& s, float c) {
-    // units come in order: the piece of one lies near that of the one before
-    if constexpr (SCALE)
-        while (t.piece[at].unit0 > unit) --at;
-    else
-        while (at + 1 < t.n && t.piece[at + 1].unit0 <= unit) ++at;
-    const Piece& pc = t.piece[at];
-    if (pc.f32)
-        unit_of<SCALE, float>(pc, unit - pc.unit0, s, c);
-    else
-        unit_of<SCALE, __nv_bfloat16>(pc, unit - pc.unit0, s, c);
+__device__ __forceinline__ void walk(const A& t, int block, int blocks, Squares& s, float c) {
+    const int u0 = (int)((int64_t)t.units * block / blocks), u1 = (int)((int64_t)t.units * (block + 1) / blocks);
+    const int first = SCALE ? u1 - 1 : u0, step = SCALE ? -1 : 1;
+    int at = piece_of(t, first);
+    Inside in;
+    auto begin = [&](int unit) -> Stretch {
+        if (SCALE ? unit < u0 : unit >= u1) return {nullptr, 0, 0};
+        if (unit >= in.lo && unit < in.hi) return {in.v + (int64_t)(unit - in.lo) * kVecs, kVecs, in.f32};
+        if constexpr (SCALE)
+            while (t.piece[at].unit0 > unit) --at;
+        else
+            while (at + 1 < t.n && t.piece[at + 1].unit0 <= unit) ++at;
+        const Piece& pc = t.piece[at];
+        return pc.f32 ? begin_unit<SCALE, float>(pc, unit, s, c, in) : begin_unit<SCALE, __nv_bfloat16>(pc, unit, s, c, in);
+    };
+    auto take = [&](const uint4 (&q)[4], const Stretch& u) {
+        if (u.n <= 0) return;
+        if (u.f32)
+            take_four<SCALE, float>(q, u.v, threadIdx.x, u.n, kThreads, s, c);
+        else
+            take_four<SCALE, __nv_bfloat16>(q, u.v, threadIdx.x, u.n, kThreads, s, c);
+    };
+    uint4 qa[4], qb[4];
+    Stretch a = begin(first);
+    load_four(qa, a.v, threadIdx.x, a.n, kThreads);
+    for (int unit = first; SCALE ? unit >= u0 : unit < u1; unit += 2 * step) {
+        const Stretch b = begin(unit + step);
+        load_four(qb, b.v, threadIdx.x, b.n, kThreads);
+        take(qa, a);
+        a = begin(unit + 2 * step);
+        load_four(qa, a.v, threadIdx.x, a.n, kThreads);
+        take(qb, b);
+    }
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<CAP> t, double* __restrict__ partial) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) squares_kernel(const __grid_constant__ Table<CAP> t, double* __restrict__ partial) {
     mma::grid_launch_dependents();
     mma::grid_wait();
     Squares s;
-    int at = 0;
-    for (int u = blockIdx.x; u < t.units; u += gridDim.x) do_unit<false>(t, u, at, s, 0.0f);
+    walk<false>(t, blockIdx.x, gridDim.x, s, 0.0f);
     const double v = block_sum(s.total());
     if (threadIdx.x == 0) partial[blockIdx.x] = v;
 }
@@ -215,6 +324,13 @@ __device__ __forceinline__ double total_of(const double* partial, int n) {
     return block_sum(v);
 }
 
+// The factor of the gradients; a NaN stays one.
+__device__ __forceinline__ float factor(double norm, float max_norm, float eps) {
+    const double down = norm + (double)eps;
+    const double q = down == 0.0 ? 1.0 : (double)max_norm / down;
+    return q >= 1.0 ? 1.0f : (float)q;
+}
+
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ out) {
     mma::grid_wait();
     const double v = total_of(partial, n);
@@ -222,27 +338,61 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* __restrict
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<CAP> t, const double* __restrict__ partial, int n,
-                                                         float max_norm, float eps, float* __restrict__ out) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __grid_constant__ Table<CAP> t, const double* __restrict__ partial, int n,
+                                                                       float max_norm, float eps, float* __restrict__ out) {
     __shared__ float coefficient;
     mma::grid_wait();
     const double sum = total_of(partial, n);
     if (threadIdx.x == 0) {
-        const double norm = sqrt(sum), down = norm + (double)eps;
-        const double q = down == 0.0 ? 1.0 : (double)max_norm / down;
-        const float c = q >= 1.0 ? 1.0f : (float)q;  // a NaN stays one
-        coefficient = c;
+        const double norm = sqrt(sum);
+        coefficient = factor(norm, max_norm, eps);
         if (blockIdx.x == 0 && out) {
             out[0] = (float)norm;
-            out[1] = c;
+            out[1] = coefficient;
         }
     }
     __syncthreads();
     const float c = coefficient;
     if (c == 1.0f) return;
     Squares s;
-    int at = t.n - 1;
-    for (int u = t.units - 1 - (int)blockIdx.x; u >= 0; u -= gridDim.x) do_unit<true>(t, u, at, s, c);
+    walk<true>(t, blockIdx.x, gridDim.x, s, c);
+}
+
+// Few units in one launch: the blocks of a cluster exchange their sums through
+// distributed shared memory.  Two launches take 2 us more on the device and 2 us
+// more of the host's time.
+constexpr int kCluster = 8;
+constexpr int kFewUnits = 8 * kCluster;
+
+template <bool SCALE>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    cluster_kernel(const __grid_constant__ Table<kSmallTable> t, int counted, float max_norm, float eps, float* __restrict__ out) {
+    __shared__ double mine;
+    mma::grid_wait();
+    const int rank = (int)mma::cluster_rank();
+    Squares s;
+    struct {  // the counted pieces come first
+        int32_t n, units;
+        const Piece* piece;
+    } const part = {counted, counted < t.n ? t.piece[counted].unit0 : t.units, t.piece};
+    walk<false>(part, rank, kCluster, s, 0.0f);
+    const double v = block_sum(s.total());
+    if (threadIdx.x == 0) mine = v;
+    mma::cluster_sync();
+    double sum = 0.0;
+    for (int k = 0; k < kCluster; ++k) {
+        const uint32_t at = mma::map_rank(tma::smem_addr(&mine), k);
+        const float lo = mma::ld_cluster(at), hi = mma::ld_cluster(at + 4);
+        sum += __hiloint2double(__float_as_int(hi), __float_as_int(lo));
+    }
+    mma::cluster_sync();  // no block leaves while its sum is read
+    const double norm = sqrt(sum);
+    const float c = SCALE ? factor(norm, max_norm, eps) : 1.0f;
+    if (rank == 0 && threadIdx.x == 0) {
+        out[0] = (float)norm;
+        if (SCALE) out[1] = c;
+    }
+    if (SCALE && c != 1.0f) walk<true>(t, rank, kCluster, s, c);
 }
 
 // -------------------------------------------------------------------- host --
@@ -306,11 +456,12 @@ bool any_overlap(const dpred_grad_tensor* g, int n) {
     return false;
 }
 
-// The launches over the gradients (the counted ones, or all).
+// The launches over the counted gradients, or over the others too, behind them.
 int plan(const dpred_grad_tensor* g, int n, bool counted_only, std::vector<Chunk>& out) {
-    for (int k = 0; k < n; ++k) {
+    for (int i = 0; i < (counted_only ? n : 2 * n); ++i) {
+        const int k = i < n ? i : i - n;
         const dpred_grad_tensor& t = g[k];
-        if (t.rows == 0 || t.cols == 0 || (counted_only && !t.counted)) continue;
+        if (t.rows == 0 || t.cols == 0 || t.counted != (i < n)) continue;
         const int es = esize(t.dtype);
         const bool flat = t.rows == 1 || t.ld == t.cols;
         Piece p = {};
@@ -338,8 +489,7 @@ int plan(const dpred_grad_tensor* g, int n, bool counted_only, std::vector<Chunk
     return DPRED_OK;
 }
 
-// Eight blocks of an SM hold 128 KB of loads in flight.
-int blocks_of(const Chunk& c) { return std::max(1, std::min({c.units, 8 * sm_count(), kMaxBlocks})); }
+int blocks_of(const Chunk& c) { return std::max(1, std::min({c.units, kBlocksPerSm * sm_count(), kMaxBlocks})); }
 
 template <int CAP>
 Table<CAP> table_of(const Chunk& c) {
@@ -382,6 +532,18 @@ int run_squares(const std::vector<Chunk>& chunks, double* partial, int& n, cudaS
     return DPRED_OK;
 }
 
+bool few(const std::vector<Chunk>& c) {
+    return c.empty() || (c.size() == 1 && c[0].units <= kFewUnits && (int)c[0].pieces.size() <= kSmallTable);
+}
+
+// counted: how many of the pieces, from the first on, enter the norm.
+template <bool SCALE>
+int run_cluster(const std::vector<Chunk>& chunks, int counted, float max_norm, float eps, float* out, cudaStream_t s) {
+    const Chunk c = chunks.empty() ? Chunk() : chunks[0];
+    const cudaError_t e = launch(cluster_kernel<SCALE>, dim3(kCluster), kThreads, 0, s, table_of<kSmallTable>(c), std::min(counted, (int)c.pieces.size()), max_norm, eps, out);
+    return e == cudaSuccess ? DPRED_OK : cuda_error(e, "gradient norm launch");
+}
+
 }  // namespace
 }  // namespace layers
 }  // namespace dpred
@@ -403,6 +565,7 @@ extern "C" int dpred_grad_norm(const dpred_grad_tensor* grads, int32_t n, float*
         if ((rc = plan(grads, n, true, chunks)) != DPRED_OK) return rc;
         double* partial = static_cast<double*>(workspace);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (few(chunks)) return run_cluster<false>(chunks, n, 0.0f, 0.0f, norm, s);
         int sums = 0;
         if ((rc = run_squares(chunks, partial, sums, s)) != DPRED_OK) return rc;
         const cudaError_t e = launch(norm_kernel, dim3(1), kThreads, 0, s, partial, sums, norm);
@@ -423,9 +586,9 @@ extern "C" int dpred_clip_grads(const dpred_grad_tensor* grads, int32_t n, float
         if (any_overlap(grads, n)) return set_error(DPRED_E_SIZE, "two gradients share memory: each would be scaled more than once");
         std::vector<Chunk> counted, all;
         if ((rc = plan(grads, n, true, counted)) != DPRED_OK || (rc = plan(grads, n, false, all)) != DPRED_OK) return rc;
-        if (all.empty()) all.emplace_back();  // no gradient: norm 0
         double* partial = static_cast<double*>(workspace);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (few(all)) return run_cluster<true>(all, counted.empty() ? 0 : (int)counted[0].pieces.size(), max_norm, eps, result, s);
         int sums = 0;
         if ((rc = run_squares(counted, partial, sums, s)) != DPRED_OK) return rc;
         for (size_t k = 0; k < all.size(); ++k) {

@@ -70,7 +70,11 @@ def embedding(ids, w, scale: float = 1.0, out=None, out_dtype=None, stream=None)
     wp, ldw, v, d = _matrix(w, "w", _t._OK, dev)
     if out is None:
         out = _empty((*ids.shape, d), out_dtype or w.dtype, stream)
-    yp, ldy = _rows_of(out, "out", _t._OK, dev, t, d)
+        if out.dtype not in _t._OK:
+            raise TypeError(f"out_dtype: unsupported dtype {out.dtype}")
+        yp, ldy = out.data_ptr(), d
+    else:
+        yp, ldy = _rows_of(out, "out", _t._OK, dev, t, d)
     _call("embedding", t, v, d, ib, ip, _code(w), wp, ldw, float(scale), _code(out), yp, ldy, _t._zc._stream(stream))
     return out
 
@@ -122,16 +126,24 @@ def block_norm(x, y=None, post=None, gate=None, residual_scale: float = 1.0, pre
     r, h = x, None
     if y is not None:
         yp, ldy, _, _ = _matrix(y, "y", _t._BF, dev, m, d)
-        r = _empty((m, d), x.dtype, stream) if out is None else out
-        rp, ldr, _, _ = _matrix(r, "out", (x.dtype,), dev, m, d)
+        if out is None:
+            r = _empty((m, d), x.dtype, stream)
+            rp, ldr = r.data_ptr(), d
+        else:
+            r = out
+            rp, ldr, _, _ = _matrix(r, "out", (x.dtype,), dev, m, d)
     if post is not None:
         pp, pdt = _vector(post, "post", _t._OK, dev, d), _code(post)
     if gate is not None:
         (gp, gr), gdt = _gate(gate, "gate", _t._OK, dev, m, d), _code(gate)
     if pre is not None:
         wp, wdt = _vector(pre, "pre", _t._OK, dev, d), _code(pre)
-        h = _empty((m, d), _t._BF[0], stream) if out_norm is None else out_norm
-        hp, ldh, _, _ = _matrix(h, "out_norm", _t._BF, dev, m, d)
+        if out_norm is None:
+            h = _empty((m, d), _t._BF[0], stream)
+            hp, ldh = h.data_ptr(), d
+        else:
+            h = out_norm
+            hp, ldh, _, _ = _matrix(h, "out_norm", _t._BF, dev, m, d)
     if m and d:
         _call("block_norm", m, d, _code(x), xp, ldx, yp, ldy, pdt, pp, gdt, gp, gr, float(residual_scale), wdt, wp, float(eps), rp, ldr,
               hp, ldh, _t._zc._stream(stream))
@@ -156,12 +168,16 @@ def block_norm_grad(r, dr=None, dh=None, y=None, post=None, gate=None, residual_
         drp, lddr, _, _ = _matrix(dr, "dr", (r.dtype,), dev, m, d)
     if dx is None:
         dx = _empty((m, d), r.dtype, stream)
-    dxp, lddx, _, _ = _matrix(dx, "dx", (r.dtype,), dev, m, d)
+        dxp, lddx = dx.data_ptr(), d
+    else:
+        dxp, lddx, _, _ = _matrix(dx, "dx", (r.dtype,), dev, m, d)
     if y is not None:
         yp, ldy, _, _ = _matrix(y, "y", _t._BF, dev, m, d)
         if dy is None:
             dy = _empty((m, d), _t._BF[0], stream)
-        dyp, lddy, _, _ = _matrix(dy, "dy", _t._BF, dev, m, d)
+            dyp, lddy = dy.data_ptr(), d
+        else:
+            dyp, lddy, _, _ = _matrix(dy, "dy", _t._BF, dev, m, d)
     elif dy is not None:
         raise ValueError("dy needs y")
     kinds = {g.dtype for g in (post_grad, gate_grad, pre_grad) if g is not None}
@@ -229,43 +245,48 @@ class GradClip:
         self.grads, self.copies, self.eps = list(grads), list(copies), float(eps)
         self._table, self._n = _grad_table(self.grads, self.copies)
         self.workspace = _t.torch.empty(_t._zc.lib().dpred_clip_workspace_bytes(self._n), dtype=_t.torch.uint8, device="cuda")
+        self._args = ctypes.addressof(self._table), self._n
+        self._space = self.workspace.data_ptr(), self.workspace.numel()
 
     def norm(self, out=None, stream=None):
         """The norm: fp32 [1], on the device."""
-        return _norm(self._table, self._n, out, self.workspace, stream)
+        return _norm(self._args, self._space, out, stream)
 
     def clip(self, max_norm: float, out=None, stream=None):
         """Scales the gradients; returns fp32 [2] on the device: the norm before
         and the factor."""
-        return _clip(self._table, self._n, max_norm, self.eps, out, self.workspace, stream)
+        return _clip(self._args, self._space, max_norm, self.eps, out, stream)
 
 
 def _result(out, n: int, stream):
+    dev = _device()
     if out is None:
-        out = _empty((n,), _t._OK[1], stream)
-    return out, _vector(out, "out", _t._OK[1:], _device(), n)
+        out = _empty(n, _t._OK[1], stream)
+        return out, out.data_ptr()
+    return out, _vector(out, "out", _t._OK[1:], dev, n)
 
 
-def _norm(table, n, out, workspace, stream):
+def _norm(args, space, out, stream):
     out, p = _result(out, 1, stream)
-    ws, wsp, wsb = _workspace(0, workspace, stream)
-    _call("grad_norm", ctypes.addressof(table), n, p, wsp, wsb, _t._zc._stream(stream))
+    _call("grad_norm", *args, p, *space, _t._zc._stream(stream))
     return out
 
 
-def _clip(table, n, max_norm, eps, out, workspace, stream):
+def _clip(args, space, max_norm, eps, out, stream):
     out, p = _result(out, 2, stream)
-    ws, wsp, wsb = _workspace(0, workspace, stream)
-    _call("clip_grads", ctypes.addressof(table), n, float(max_norm), float(eps), p, wsp, wsb, _t._zc._stream(stream))
+    _call("clip_grads", *args, float(max_norm), eps, p, *space, _t._zc._stream(stream))
     return out
+
+
+def _clip_space(n: int, workspace, stream):
+    return _workspace(_t._zc.lib().dpred_clip_workspace_bytes(n) if workspace is None else 0, workspace, stream)
 
 
 def grad_norm(grads, out=None, workspace=None, stream=None):
     """The 2-norm of all gradients together (see GradClip): fp32 [1] on the device."""
     table, n = _grad_table(list(grads), ())
-    if workspace is None:
-        workspace = _empty(_t._zc.lib().dpred_clip_workspace_bytes(n), _t.torch.uint8, stream)
-    return _norm(table, n, out, workspace, stream)
+    ws, *space = _clip_space(n, workspace, stream)
+    return _norm((ctypes.addressof(table), n), space, out, stream)
 
 
 def clip_grads(grads, max_norm: float, copies=(), eps: float = 1e-6, out=None, workspace=None, stream=None):
@@ -273,6 +294,5 @@ def clip_grads(grads, max_norm: float, copies=(), eps: float = 1e-6, out=None, w
     2-norm together; returns fp32 [2] on the device: norm and factor (see GradClip,
     which keeps the table of a step's gradients)."""
     table, n = _grad_table(list(grads), list(copies))
-    if workspace is None:
-        workspace = _empty(_t._zc.lib().dpred_clip_workspace_bytes(n), _t.torch.uint8, stream)
-    return _clip(table, n, max_norm, eps, out, workspace, stream)
+    ws, *space = _clip_space(n, workspace, stream)
+    return _clip((ctypes.addressof(table), n), space, max_norm, float(eps), out, stream)
