@@ -124,6 +124,13 @@ def test_embedding_grad(t, v, d, kind, gdt, odt, accumulate):
     check_grad(ids, dy, dw, 0.3, v - 1 if t % 3 == 0 else None, accumulate)
 
 
+@pytest.mark.parametrize("t,v", [(70001, 500), (65536, 40000), (65535, 3), (200000, 7)])
+@pytest.mark.parametrize("kind", ["uniform", "skewed", "one"])
+def test_many_tokens(t, v, kind):
+    """Either side of what fits counters of 16 bits, and more tokens of a row than those hold."""
+    check_grad(ids_of(t, v, 9, kind), randn(t, 8, seed=1), randn(v, 8, seed=2, dtype=torch.float32), 1.0, None, False)
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (8, 8), (1, 0), (0, 1), (3, 5)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_embedding_grad_strides(pad, shift, accumulate):

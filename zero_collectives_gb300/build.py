@@ -23,7 +23,7 @@ LIB_CHECKED = os.path.join(HERE, "libdpred_checked.so")
 OBJDIR_CHECKED = os.path.join(HERE, "_build_checked")
 FLUSH_UNITS = [f"flush_w{w}.cu" for w in (*(str(w) for w in range(2, 17)), "gen", "gen32", "genx")]
 LINEAR_UNITS = [f"linear_{k}.cu" for k in ("any", "plain", "act", "grad", "f32")]
-NORM_GRAD_UNITS = [f"block_norm_grad_{t}_{k}.cu" for t in ("bf16", "f32") for k in ("whole", "part")]
+NORM_GRAD_UNITS = [f"block_norm_grad_{t}_{k}.cu" for t in ("bf16", "f32") for k in ("whole", "part", "any")]
 SOURCES = ["abi.cu", "flush_dispatch.cu", *FLUSH_UNITS, "accumulate.cu", "allgather.cu", "noalloc.cu", "selftest.cu",
            "relayout.cu", "schedule.cu", "owner_map.cu", "executor.cu", "ceiling.cu", "gemm.cu", "linear.cu",
            *LINEAR_UNITS, "muon.cu", "muon_small.cu",

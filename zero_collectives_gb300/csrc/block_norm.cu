@@ -122,9 +122,12 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
     };
     for (int k = 0; k < in.stages; ++k) request();
     float* weights = reinterpret_cast<float*>(smem + kBarrierBytes + groups * in.stages * in.slot_bytes);
-    Staged<true, VPT> post = {weights, lanes}, pre = {weights + staged_floats(lanes, VPT), lanes};
-    if (has_y) post.fill(a.d, [&](int c) { return a.post.at(0, c) * (own_gate ? 1.0f : a.gate.at(0, c)); });
-    if (has_pre) pre.fill(a.d, [&](int c) { return a.pre.at(0, c); });
+    const Staged<true, VPT> post = {weights, lanes}, pre = {weights + staged_floats(lanes, VPT), lanes};
+    fill<true, VPT>(lanes, a.d, [&](int c, bool in_row, int at) {
+        const float w = has_pre && in_row ? a.pre.at(0, c) : 0.0f, p = has_y && in_row ? a.post.at(0, c) : 0.0f, q = has_y && in_row && !own_gate ? a.gate.at(0, c) : 1.0f;
+        if (has_pre) pre.at[at] = w;
+        if (has_y) post.at[at] = p * q;
+    });
     __syncthreads();
     RowSum sum(lanes, group);
     const float inv_d = 1.0f / (float)a.d;

@@ -217,15 +217,6 @@ struct Staged {
         const int turn = id / (8 / kPieces) & (kPieces - 1);
         return (id * kPieces + ((v * 2 + k / 4) ^ turn)) * 4 + k % 4;
     }
-    // All threads of the block: f(column) of every column.
-    template <typename F>
-    __device__ __forceinline__ void fill(int d, F f) {
-        for (int i = threadIdx.x; i < VPT * 8 * lanes; i += blockDim.x) {
-            const int k = VEC ? i % 8 : i / lanes % 8, id = VEC ? i / 8 % lanes : i % lanes, v = i / (8 * lanes);
-            const int c = column<VEC>(first<VEC>(v, id, lanes), lanes, k);
-            at[place(v, id, k)] = c < d ? f(c) : 0.0f;
-        }
-    }
     __device__ __forceinline__ F8 get(int v, int id) const {
         F8 f;
         if constexpr (VEC) {
@@ -238,6 +229,18 @@ struct Staged {
         return f;
     }
 };
+
+// All threads of a block: f(column, it is one, place) for every column that their
+// vectors cover; f is to load its weights before it writes any, and 0 behind the row.
+template <bool VEC, int VPT, typename F>
+__device__ __forceinline__ void fill(int lanes, int d, F f) {
+    const Staged<VEC, VPT> s = {nullptr, lanes};
+    for (int i = threadIdx.x; i < VPT * 8 * lanes; i += blockDim.x) {
+        const int k = VEC ? i % 8 : i / lanes % 8, id = VEC ? i / 8 % lanes : i % lanes, v = i / (8 * lanes);
+        const int c = column<VEC>(first<VEC>(v, id, lanes), lanes, k);
+        f(c, c < d, s.place(v, id, k));
+    }
+}
 inline __host__ __device__ int staged_floats(int lanes, int vecs) { return 8 * lanes * vecs; }
 
 #endif  // __CUDACC__

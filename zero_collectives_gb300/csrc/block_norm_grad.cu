@@ -87,13 +87,6 @@ Grid grid_of(int64_t m, int64_t d, int64_t gate_rows) {
 size_t partial_bytes(const Grid& g, int64_t d) { return (size_t)((2 * g.blocks + (g.parts > 1 ? g.sections * g.parts : 0)) * d) * 4; }
 
 template <typename T>
-cudaError_t launch_plain(const BackwardArgs& a, const Rows& in, const Grid& g, cudaStream_t s) {
-    if (g.q.vecs == 1) return launch_kernel<T, false, 1, 0, false>(a, in, g, g.groups, s);
-    if (g.q.lanes == 512) return g.q.vecs == 2 ? launch_kernel<T, false, 2, 512, false>(a, in, g, g.groups, s) : launch_kernel<T, false, 4, 512, false>(a, in, g, g.groups, s);
-    return launch_kernel<T, false, 2, 0, false>(a, in, g, g.groups, s);
-}
-
-template <typename T>
 cudaError_t launch_backward(const BackwardArgs& a, const Grid& g, bool vec, cudaStream_t s) {
     Rows in = {};
     const int es = (int)sizeof(T), gs = a.gate.f32 ? 4 : 2;
@@ -103,13 +96,13 @@ cudaError_t launch_backward(const BackwardArgs& a, const Grid& g, bool vec, cuda
         if (parts[k].p) in.add(k, parts[k].p, parts[k].ld, a.d, parts[k].es);
     in.slot_bytes = in.slot();
     in.err = device_error_word();
-    const int room = kRoom - 4 * (2 * staged_floats(g.q.lanes, g.q.vecs) + 8 * g.q.lanes * g.groups);
+    const int room = kRoom - 4 * staged_space(g.q.lanes, g.q.vecs, g.groups);
     int groups = vec ? ring_groups(g.q, in.slot_bytes, room, g.groups * g.q.lanes) : 0;
     if (vec && groups == 0 && in.slot_bytes + kBarrierBytes <= room) groups = 1;  // a single slot
-    if (groups == 0) return launch_plain<T>(a, in, g, s);
+    if (groups == 0) return launch_rows<T, false, false>(a, in, g, g.groups, s);
     in.stages = ring_stages(groups, in.slot_bytes, room);
     const bool whole = a.dr && a.dh && a.y && a.post.p && !a.each;
-    return whole ? launch_ring<T, true>(a, in, g, groups, s) : launch_ring<T, false>(a, in, g, groups, s);
+    return whole ? launch_rows<T, true, true>(a, in, g, groups, s) : launch_rows<T, true, false>(a, in, g, groups, s);
 }
 
 }  // namespace

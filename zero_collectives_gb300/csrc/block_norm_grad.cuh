@@ -77,19 +77,18 @@ __device__ __forceinline__ void combine(const F8 (&s)[VPT], int id, int group, i
             }
         return;
     }
+    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        __syncthreads();
+    for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) buf[(group * 8 + k) * lanes + id] = s[v].get(k);
-        __syncthreads();
-        for (int i = threadIdx.x; i < 8 * lanes; i += blockDim.x) {
-            const int k = i / lanes, t = i % lanes, c = column<VEC>(first<VEC>(v, t, lanes), lanes, k);
-            if (c >= d) continue;
-            float x = 0.0f;
-            for (int g = 0; g < groups; ++g) x += buf[(g * 8 + k) * lanes + t];
-            put(c, x);
-        }
+        for (int k = 0; k < 8; ++k) buf[((group * VPT + v) * 8 + k) * lanes + id] = s[v].get(k);
+    __syncthreads();
+    for (int i = threadIdx.x; i < VPT * 8 * lanes; i += blockDim.x) {
+        const int v = i / (8 * lanes), k = i / lanes % 8, t = i % lanes, c = column<VEC>(first<VEC>(v, t, lanes), lanes, k);
+        if (c >= d) continue;
+        float x = 0.0f;
+        for (int g = 0; g < groups; ++g) x += buf[g * VPT * 8 * lanes + i];
+        put(c, x);
     }
 }
 
@@ -131,10 +130,10 @@ struct Walk {
 // row: what a step has in the middle of the model) spares the loop its tests.
 template <typename T, bool VEC, int VPT, int LANES, bool WHOLE>
 __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
-    backward_kernel(const __grid_constant__ BackwardArgs a, const __grid_constant__ Rows in, int lanes_arg) {
+    backward_kernel(const __grid_constant__ BackwardArgs a, const __grid_constant__ Rows in) {
     extern __shared__ __align__(128) char smem[];
     if (a.release) mma::grid_launch_dependents();
-    const int lanes = LANES ? LANES : lanes_arg;
+    constexpr int lanes = LANES;
     const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
     const bool has_dr = WHOLE || a.dr, has_dh = WHOLE || a.dh, has_y = WHOLE || a.y, has_post = WHOLE || a.post.p, each = !WHOLE && a.each;
     Ring ring(in, smem, group);
@@ -153,9 +152,8 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
 
     float* weights = reinterpret_cast<float*>(smem + kBarrierBytes + groups * in.stages * in.slot_bytes);
     const int width = staged_floats(lanes, VPT);
-    Staged<VEC, VPT> post = {weights, lanes}, pre = {weights + width, lanes};  // post: with the unit's gate
+    const Staged<VEC, VPT> post = {weights, lanes}, pre = {weights + width, lanes};  // post: with the unit's gate
     float* buf = weights + 2 * width;
-    if (has_dh) pre.fill(a.d, [&](int c) { return a.pre.at(0, c); });
     RowSum sum(lanes, group);
     const float inv_d = 1.0f / (float)a.d;
     const F8 zero = splat(0.0f), scale = splat(a.scale);
@@ -169,8 +167,14 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
         const int64_t section = unit / a.parts, part = unit - section * a.parts;
         const int64_t row0 = section * a.per + a.per * part / a.parts, row1 = section * a.per + a.per * (part + 1) / a.parts;
         if (unit == blockIdx.x || a.sections > 1) {
-            __syncthreads();
-            if (has_y) post.fill(a.d, [&](int c) { return a.post.at(0, c) * (each ? 1.0f : a.gate.at(section, c)); });
+            const bool begin = unit == blockIdx.x;
+            if (!begin) __syncthreads();
+            fill<VEC, VPT>(lanes, a.d, [&](int c, bool in_row, int at) {
+                const float w = has_dh && begin && in_row ? a.pre.at(0, c) : 0.0f, p = has_y && in_row ? a.post.at(0, c) : 0.0f,
+                            q = has_y && in_row && !each ? a.gate.at(section, c) : 1.0f;
+                if (has_dh && begin) pre.at[at] = w;
+                if (has_y) post.at[at] = p * q;
+            });
             __syncthreads();
         }
         F8 dyn[VPT];  // sums of g n_y (times the gate where every row has its own)
@@ -307,31 +311,38 @@ struct Grid {
     int32_t parts, groups;
 };
 
+// Floats of the weights and of combine().
+inline int staged_space(int lanes, int vecs, int groups) { return staged_floats(lanes, vecs) * (2 + (groups > 1 ? groups : 0)); }
+
 template <typename T, bool VEC, int VPT, int LANES, bool WHOLE>
 cudaError_t launch_kernel(const BackwardArgs& a, const Rows& in, const Grid& g, int groups, cudaStream_t s) {
     static bool done[64];
     const cudaError_t e = ensure_smem_attr(backward_kernel<T, VEC, VPT, LANES, WHOLE>, kRoom, done);
     if (e != cudaSuccess) return e;
-    const size_t smem = kBarrierBytes + (size_t)groups * in.stages * in.slot_bytes + 4 * (2 * staged_floats(g.q.lanes, VPT) + 8 * g.q.lanes * groups);
-    return launch(backward_kernel<T, VEC, VPT, LANES, WHOLE>, dim3((unsigned)g.blocks), groups * g.q.lanes, smem, s, a, in, g.q.lanes);
+    const size_t smem = kBarrierBytes + (size_t)groups * in.stages * in.slot_bytes + 4 * (int)staged_space(g.q.lanes, VPT, groups);
+    return launch(backward_kernel<T, VEC, VPT, LANES, WHOLE>, dim3((unsigned)g.blocks), groups * g.q.lanes, smem, s, a, in);
 }
 
-// Aligned rows.  Each form has a unit of its own.
-template <typename T, bool WHOLE>
-cudaError_t launch_ring(const BackwardArgs& a, const Rows& in, const Grid& g, int groups, cudaStream_t s) {
-    if (g.q.vecs == 1) return launch_kernel<T, true, 1, 32, WHOLE>(a, in, g, groups, s);
-    if (g.q.vecs == 4) return launch_kernel<T, true, 4, 512, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 32) return launch_kernel<T, true, 2, 32, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 64) return launch_kernel<T, true, 2, 64, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 128) return launch_kernel<T, true, 2, 128, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 256) return launch_kernel<T, true, 2, 256, WHOLE>(a, in, g, groups, s);
-    return launch_kernel<T, true, 2, 512, WHOLE>(a, in, g, groups, s);
+// Each form has units of its own: aligned rows, and rows of any alignment.
+template <typename T, bool VEC, bool WHOLE>
+cudaError_t launch_rows(const BackwardArgs& a, const Rows& in, const Grid& g, int groups, cudaStream_t s) {
+    if (g.q.vecs == 1) return launch_kernel<T, VEC, 1, 32, WHOLE>(a, in, g, groups, s);
+    if (g.q.vecs == 4) return launch_kernel<T, VEC, 4, 512, WHOLE>(a, in, g, groups, s);
+    if (g.q.lanes == 32) return launch_kernel<T, VEC, 2, 32, WHOLE>(a, in, g, groups, s);
+    if (g.q.lanes == 64) return launch_kernel<T, VEC, 2, 64, WHOLE>(a, in, g, groups, s);
+    if (g.q.lanes == 128) return launch_kernel<T, VEC, 2, 128, WHOLE>(a, in, g, groups, s);
+    if (g.q.lanes == 256) return launch_kernel<T, VEC, 2, 256, WHOLE>(a, in, g, groups, s);
+    return launch_kernel<T, VEC, 2, 512, WHOLE>(a, in, g, groups, s);
 }
 
-extern template cudaError_t launch_ring<__nv_bfloat16, true>(const BackwardArgs&, const Rows&, const Grid&, int, cudaStream_t);
-extern template cudaError_t launch_ring<__nv_bfloat16, false>(const BackwardArgs&, const Rows&, const Grid&, int, cudaStream_t);
-extern template cudaError_t launch_ring<float, true>(const BackwardArgs&, const Rows&, const Grid&, int, cudaStream_t);
-extern template cudaError_t launch_ring<float, false>(const BackwardArgs&, const Rows&, const Grid&, int, cudaStream_t);
+#define DPRED_NORM_GRAD_FORM(T, VEC, WHOLE) \
+    template cudaError_t launch_rows<T, VEC, WHOLE>(const BackwardArgs&, const Rows&, const Grid&, int, cudaStream_t)
+extern DPRED_NORM_GRAD_FORM(__nv_bfloat16, true, true);
+extern DPRED_NORM_GRAD_FORM(__nv_bfloat16, true, false);
+extern DPRED_NORM_GRAD_FORM(__nv_bfloat16, false, false);
+extern DPRED_NORM_GRAD_FORM(float, true, true);
+extern DPRED_NORM_GRAD_FORM(float, true, false);
+extern DPRED_NORM_GRAD_FORM(float, false, false);
 
 }  // namespace layers
 }  // namespace dpred

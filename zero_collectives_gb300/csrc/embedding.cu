@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(kLookThreads) lookup_any_kernel(const __grid_c
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kMaxRows = 4096;            // of a block
-constexpr int kCounters = 192 * 1024;     // bytes: one for each of its rows and warps
-constexpr int kHeld = 16;                 // ids that a thread keeps between counting and placing
+constexpr int kCounters = 160 * 1024;     // bytes: one for each of its rows and warps
+constexpr int kHeld = 16;                 // ids that a thread has in flight
+constexpr int kList = 96;                 // tokens of the block that a warp lists
 
 struct SortArgs {
     const void* ids;
@@ -164,53 +165,85 @@ __device__ __forceinline__ uint32_t usable_id(const SortArgs& a, int64_t t, bool
     return static_cast<uint32_t>(id) == a.padding ? kNoId : static_cast<uint32_t>(id);
 }
 
-template <typename I>
+// How many tokens of a row a warp has met, then how many of the row come before
+// its next one; two rows in a word where no count passes 16 bits (HALF).
+template <bool HALF>
+struct Counters {
+    uint32_t* w;
+    __device__ __forceinline__ uint32_t* word(int row) const { return w + (HALF ? row / 2 : row); }
+    __device__ __forceinline__ uint32_t one(int row) const { return HALF && (row & 1) ? 0x10000u : 1u; }
+    __device__ __forceinline__ int get(int row) const { return HALF ? (*word(row) >> (row & 1) * 16) & 0xFFFF : *word(row); }
+};
+
+template <typename I, bool HALF>
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
-    extern __shared__ int counts[];  // [warps][rows]: tokens of a row that a warp has met, then where its next one goes
-    __shared__ int below[kSortWarps], sums[kSortWarps];
+    extern __shared__ uint32_t counters[];  // [warps][words]
+    __shared__ int below[kSortWarps], sums[kSortWarps], starts[kMaxRows];
     __shared__ uint32_t bits[kMaxRows / 32];
+    __shared__ int2 lists[kSortWarps][kList];  // row and token, in order
     mma::grid_launch_dependents();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint32_t mask = (1u << a.shift) - 1, me = blockIdx.x, rows = a.rows;
-    for (int i = threadIdx.x * 4; i < a.warps * a.rows; i += kSortThreads * 4) *reinterpret_cast<int4*>(counts + i) = make_int4(0, 0, 0, 0);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, words = HALF ? a.rows / 2 : a.rows;
+    const uint32_t mask = (1u << a.shift) - 1, me = blockIdx.x, rows = a.rows, before_me = (1u << lane) - 1;
+    for (int i = threadIdx.x * 4; i < a.warps * words; i += kSortThreads * 4) *reinterpret_cast<int4*>(counters + i) = make_int4(0, 0, 0, 0);
     if (threadIdx.x < kMaxRows / 32) bits[threadIdx.x] = 0;
     __syncthreads();
     mma::grid_wait();
     // each warp has one stretch of the tokens, a multiple of 32
     const int64_t per = (a.t + a.warps * 32 - 1) / (a.warps * 32) * 32;
     const int64_t t0 = warp * per, t1 = warp < a.warps ? min(a.t, t0 + per) : 0;
-    int* mine = counts + warp * a.rows;
-    int less = 0;
+    const Counters<HALF> mine = {counters + warp * words};
+    int2* list = lists[warp];
+    int less = 0, listed = 0;
     bool outside = false;
-    uint32_t held[kHeld];
     for (int64_t base = t0; base < t1; base += 32 * kHeld) {
+        uint32_t id[kHeld];
 #pragma unroll
         for (int u = 0; u < kHeld; ++u) {
             const int64_t t = base + 32 * u + lane;
-            held[u] = t < t1 ? usable_id<I>(a, t, outside) : kNoId;
+            id[u] = t < t1 ? usable_id<I>(a, t, outside) : kNoId;
         }
 #pragma unroll
         for (int u = 0; u < kHeld; ++u) {
             // kNoId has the highest low bits and no row
-            less += (held[u] & mask) < me;
-            if ((held[u] & mask) == me && (held[u] >> a.shift) < rows) atomicAdd(mine + (held[u] >> a.shift), 1);
+            less += (id[u] & mask) < me;
+            const uint32_t row = id[u] >> a.shift;
+            const bool here = (id[u] & mask) == me && row < rows;
+            const unsigned met = __ballot_sync(0xFFFFFFFFu, here);
+            if (here) {
+                const int at = listed + __popc(met & before_me);
+                if (at < kList) list[at] = make_int2((int)row, (int)(base + 32 * u + lane));
+                atomicAdd(mine.word(row), mine.one(row));
+            }
+            listed += __popc(met);
         }
     }
     if (outside && blockIdx.x == 0) record_device_error(a.err, DPRED_E_BOUNDS);
     less = warp_sum(less);
     if (lane == 0) below[warp] = less;
     __syncthreads();
-    // the rows' tokens in all (a thread has up to 4 rows next to each other); an
-    // exclusive sum over rows, then over the warps of a row
-    const int each = (a.rows + kSortThreads - 1) / kSortThreads, r0 = threadIdx.x * each, r1 = min(r0 + each, a.rows);
+    // over the warps, what comes before each one's tokens of a row; a thread has up
+    // to 4 rows next to each other
+    constexpr int kPer = HALF ? 2 : 1;  // rows of a word
+    const int each = (words + kSortThreads - 1) / kSortThreads, w0 = min((int)threadIdx.x * each, words), w1 = min(w0 + each, words);
     int total = 0;
-    for (int r = r0; r < r1; ++r) {
-        int n = 0;
+    uint32_t sum[kMaxRows / kSortThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kSortThreads; ++i) {
+        sum[i] = 0;
+        if (w0 + i >= w1) continue;
 #pragma unroll 8
-        for (int w = 0; w < a.warps; ++w) n += counts[w * a.rows + r];
-        if (n && a.met) atomicOr(bits + r / 32, 1u << r % 32);
-        total += n;
+        for (int w = 0; w < a.warps; ++w) {
+            uint32_t& c = counters[w * words + w0 + i];
+            const uint32_t n = c;
+            c = sum[i];
+            sum[i] += n;
+        }
+        const int r = (w0 + i) * kPer;
+        const uint32_t some = HALF ? ((sum[i] & 0xFFFF) != 0) | ((sum[i] >> 16 != 0) << 1) : sum[i] != 0;
+        if (some && a.met) atomicOr(bits + r / 32, some << r % 32);
+        total += HALF ? (sum[i] & 0xFFFF) + (sum[i] >> 16) : sum[i];
     }
+    // where each row starts in the order
     int before = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -220,48 +253,55 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     if (lane == 31) sums[warp] = before;
     before -= total;
     __syncthreads();
-    int start = below[lane], ahead = lane < warp ? sums[lane] : 0;
-    start = warp_sum(start);
-    before += warp_sum(ahead) + start;
+    before += warp_sum(lane < warp ? sums[lane] : 0) + warp_sum(below[lane]);
     if (blockIdx.x == gridDim.x - 1 && threadIdx.x == kSortThreads - 1) *a.count = before + total;
     if (a.met && threadIdx.x < a.rows / 32) a.met[(int64_t)blockIdx.x * (a.rows / 32) + threadIdx.x] = bits[threadIdx.x];
-    for (int r = r0; r < r1; ++r) {
-#pragma unroll 8
-        for (int w = 0; w < a.warps; ++w) {
-            int& c = counts[w * a.rows + r];
-            const int n = c;
-            c = before;
-            before += n;
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kSortThreads; ++i) {
+        if (w0 + i >= w1) continue;
+        starts[(w0 + i) * kPer] = before;
+        if (HALF) {
+            before += sum[i] & 0xFFFF;
+            starts[(w0 + i) * 2 + 1] = before;
+            before += sum[i] >> 16;
+        } else {
+            before += sum[i];
         }
     }
     __syncthreads();
-    for (int64_t base = t0; base < t1; base += 32 * kHeld) {
-        if (per > 32 * kHeld) {  // else the ids are still there
-#pragma unroll
-            for (int u = 0; u < kHeld; ++u) {
-                const int64_t t = base + 32 * u + lane;
-                held[u] = t < t1 ? usable_id<I>(a, t, outside) : kNoId;
+    // up to 32 tokens in ascending order, row by row
+    auto place = [&](bool here, uint32_t row, int token) {
+        unsigned left = __ballot_sync(0xFFFFFFFFu, here);
+        while (left) {
+            const uint32_t r = __shfl_sync(0xFFFFFFFFu, row, __ffs(left) - 1);
+            const unsigned same = __ballot_sync(0xFFFFFFFFu, here && row == r);
+            left &= ~same;
+            const int at = starts[r] + mine.get(r) + __popc(same & before_me);
+            __syncwarp();
+            if (same >> lane & 1) {
+                a.key[at] = (int32_t)(r << a.shift | me);
+                a.order[at] = token;
+                if ((same >> lane) == 1u) *mine.word(r) += mine.one(r) * __popc(same);  // the last of them
             }
+            __syncwarp();
         }
+    };
+    if (listed <= kList) {
+        for (int i = 0; i < listed; i += 32) {
+            const int2 e = list[min(i + lane, kList - 1)];
+            place(i + lane < listed, e.x, e.y);
+        }
+        return;
+    }
+    for (int64_t base = t0; base < t1; base += 32 * kHeld) {
+        uint32_t id[kHeld];
 #pragma unroll
         for (int u = 0; u < kHeld; ++u) {
-            const uint32_t r = held[u] >> a.shift;
-            const bool here = (held[u] & mask) == me && r < rows;
-            unsigned left = __ballot_sync(0xFFFFFFFFu, here);
-            while (left) {  // row by row, the tokens of one in ascending t
-                const uint32_t row = __shfl_sync(0xFFFFFFFFu, r, __ffs(left) - 1);
-                const unsigned same = __ballot_sync(0xFFFFFFFFu, here && r == row);
-                left &= ~same;
-                const int at = mine[row] + __popc(same & ((1u << lane) - 1));
-                __syncwarp();
-                if (same >> lane & 1) {
-                    a.key[at] = (int32_t)held[u];
-                    a.order[at] = (int32_t)(base + 32 * u + lane);
-                    if ((same >> lane) == 1u) mine[row] = at + 1;  // the last of them
-                }
-                __syncwarp();
-            }
+            const int64_t t = base + 32 * u + lane;
+            id[u] = t < t1 ? usable_id<I>(a, t, outside) : kNoId;
         }
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) place((id[u] & mask) == me && (id[u] >> a.shift) < rows, id[u] >> a.shift, (int)(base + 32 * u + lane));
     }
 }
 
@@ -529,6 +569,13 @@ cudaError_t launch_lookup(const LookArgs& a, bool vec, cudaStream_t s) {
     return launch_rows<TW, TY, 8>(a, lanes, s);
 }
 
+template <typename I, bool HALF>
+cudaError_t launch_sort(const SortArgs& q, unsigned blocks, int per_warp, cudaStream_t s) {
+    static bool done[64];
+    const cudaError_t e = ensure_smem_attr(sort_kernel<I, HALF>, kCounters, done);
+    return e == cudaSuccess ? launch(sort_kernel<I, HALF>, dim3(blocks), kSortThreads, (size_t)q.warps * per_warp, s, q) : e;
+}
+
 template <typename TG, typename TW, bool VEC, bool ADD>
 cudaError_t launch_sums(const SumArgs& a, unsigned blocks, cudaStream_t s) {
     const cudaError_t e = launch(sum_kernel<TG, TW, VEC, ADD>, dim3(blocks), kSumThreads, 0, s, a);
@@ -603,18 +650,17 @@ extern "C" int dpred_embedding_grad(int64_t t, int64_t v, int64_t d, int32_t id_
     q.shift = deal.shift;
     q.rows = deal.rows;
     // a set of counters for each 128 tokens, so that few tokens clear few, as far as there is room
-    q.warps = (int32_t)std::max<int64_t>(1, std::min<int64_t>({kSortWarps, t / 128, kCounters / (deal.rows * 4)}));
+    const bool half = t <= 0xFFFF;
+    const int per_warp = deal.rows * (half ? 2 : 4);
+    q.warps = (int32_t)std::max<int64_t>(1, std::min<int64_t>({kSortWarps, t / 128, kCounters / per_warp}));
     q.key = reinterpret_cast<int32_t*>(base + sp.key);
     q.order = reinterpret_cast<int32_t*>(base + sp.order);
     q.met = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + sp.met);
     q.count = reinterpret_cast<int32_t*>(base + sp.count);
     q.err = device_error_word();
-    const int smem = q.warps * q.rows * 4;
-    static bool done32[64], done64[64];
-    cudaError_t e = id_bytes == 8 ? ensure_smem_attr(sort_kernel<int64_t>, kCounters, done64) : ensure_smem_attr(sort_kernel<int32_t>, kCounters, done32);
-    if (e != cudaSuccess) return cuda_error(e, "embedding gradient set-up");
-    const dim3 grid(1u << deal.shift);
-    e = id_bytes == 8 ? launch(sort_kernel<int64_t>, grid, kSortThreads, smem, s, q) : launch(sort_kernel<int32_t>, grid, kSortThreads, smem, s, q);
+    const unsigned grid = 1u << deal.shift;
+    cudaError_t e = id_bytes == 8 ? (half ? launch_sort<int64_t, true>(q, grid, per_warp, s) : launch_sort<int64_t, false>(q, grid, per_warp, s))
+                                  : (half ? launch_sort<int32_t, true>(q, grid, per_warp, s) : launch_sort<int32_t, false>(q, grid, per_warp, s));
     if (e != cudaSuccess) return cuda_error(e, "embedding gradient launch");
 
     SumArgs a = {};
