@@ -397,9 +397,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 
 // -------------------------------------------------------------------- host --
 
-struct Chunk {  // the pieces of one launch
-    std::vector<Piece> pieces;
-    int units = 0;
+// The pieces of one launch, the counted ones first.
+struct Chunk {
+    Table<kTable> t;
+    int counted, counted_units;
 };
 
 int check_grads(const dpred_grad_tensor* g, int n) {
@@ -431,15 +432,27 @@ bool overlap(const Range& a, const Range& b) {  // a.lo <= b.lo < a.hi
     return column < a.row || step - column < b.row;
 }
 
+Range range_of(const dpred_grad_tensor& g) {
+    const int64_t es = esize(g.dtype), row = g.cols * es, step = g.rows > 1 ? g.ld * es : row;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(g.data);
+    return {lo, lo + (uintptr_t)((g.rows - 1) * step + row), row, step, g.rows};
+}
+
 bool any_overlap(const dpred_grad_tensor* g, int n) {
+    // one after another in memory, as views of a buffer are: nothing to sort
+    bool apart = true;
+    uintptr_t end = 0;
+    for (int k = 0; k < n && apart; ++k) {
+        if (g[k].rows == 0 || g[k].cols == 0) continue;
+        const Range r = range_of(g[k]);
+        apart = r.lo >= end;
+        end = r.hi;
+    }
+    if (apart) return false;
     std::vector<Range> v;
     v.reserve(n);
-    for (int k = 0; k < n; ++k) {
-        if (g[k].rows == 0 || g[k].cols == 0) continue;
-        const int64_t es = esize(g[k].dtype), row = g[k].cols * es, step = g[k].rows > 1 ? g[k].ld * es : row;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(g[k].data);
-        v.push_back({lo, lo + (uintptr_t)((g[k].rows - 1) * step + row), row, step, g[k].rows});
-    }
+    for (int k = 0; k < n; ++k)
+        if (g[k].rows > 0 && g[k].cols > 0) v.push_back(range_of(g[k]));
     if (!std::is_sorted(v.begin(), v.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; }))
         std::sort(v.begin(), v.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     std::vector<Range> open;  // ranges that reach past the present start
@@ -456,7 +469,7 @@ bool any_overlap(const dpred_grad_tensor* g, int n) {
     return false;
 }
 
-// The launches over the counted gradients, or over the others too, behind them.
+// The launches over the counted gradients and, behind them, over the others.
 int plan(const dpred_grad_tensor* g, int n, bool counted_only, std::vector<Chunk>& out) {
     for (int i = 0; i < (counted_only ? n : 2 * n); ++i) {
         const int k = i < n ? i : i - n;
@@ -480,40 +493,49 @@ int plan(const dpred_grad_tensor* g, int n, bool counted_only, std::vector<Chunk
             p.per = (int32_t)std::max<int64_t>(1, kUnit / bytes);
             units = (p.rows + p.per - 1) / p.per;
         }
-        if (out.empty() || (int)out.back().pieces.size() == kTable) out.emplace_back();
-        if (units > kMaxUnits - (int64_t)out.back().units) return set_error(DPRED_E_SIZE, "gradient %d is too large", k);
-        p.unit0 = out.back().units;
-        out.back().units += (int)units;
-        out.back().pieces.push_back(p);
+        if (out.empty() || out.back().t.n == kTable) {
+            out.emplace_back();
+            out.back().t.n = out.back().t.units = out.back().counted = out.back().counted_units = 0;
+        }
+        Chunk& c = out.back();
+        if (units > kMaxUnits - (int64_t)c.t.units) return set_error(DPRED_E_SIZE, "gradient %d is too large", k);
+        p.unit0 = c.t.units;
+        c.t.units += (int)units;
+        c.t.piece[c.t.n++] = p;
+        if (i < n) {
+            c.counted = c.t.n;
+            c.counted_units = c.t.units;
+        }
     }
     return DPRED_OK;
 }
 
-int blocks_of(const Chunk& c) { return std::max(1, std::min({c.units, kBlocksPerSm * sm_count(), kMaxBlocks})); }
+int blocks_of(int units) { return std::max(1, std::min({units, kBlocksPerSm * sm_count(), kMaxBlocks})); }
 
+// The first n pieces, in a table of no more than needed.
 template <int CAP>
-Table<CAP> table_of(const Chunk& c) {
+Table<CAP> table_of(const Chunk& c, int n, int units) {
     Table<CAP> t;
-    t.n = (int)c.pieces.size();
-    t.units = c.units;
-    std::copy(c.pieces.begin(), c.pieces.end(), t.piece);
+    t.n = n;
+    t.units = units;
+    std::copy(c.t.piece, c.t.piece + n, t.piece);
     return t;
 }
 
 cudaError_t launch_squares(const Chunk& c, double* partial, cudaStream_t s) {
-    if (c.pieces.size() <= kSmallTable)
-        return launch(squares_kernel<kSmallTable>, dim3(blocks_of(c)), kThreads, 0, s, table_of<kSmallTable>(c), partial);
-    if (c.pieces.size() <= kMidTable)
-        return launch(squares_kernel<kMidTable>, dim3(blocks_of(c)), kThreads, 0, s, table_of<kMidTable>(c), partial);
-    return launch(squares_kernel<kTable>, dim3(blocks_of(c)), kThreads, 0, s, table_of<kTable>(c), partial);
+    const int n = c.counted, u = c.counted_units;
+    const dim3 grid(blocks_of(u));
+    if (n <= kSmallTable) return launch(squares_kernel<kSmallTable>, grid, kThreads, 0, s, table_of<kSmallTable>(c, n, u), partial);
+    if (n <= kMidTable) return launch(squares_kernel<kMidTable>, grid, kThreads, 0, s, table_of<kMidTable>(c, n, u), partial);
+    return launch(squares_kernel<kTable>, grid, kThreads, 0, s, table_of<kTable>(c, n, u), partial);
 }
 
-cudaError_t launch_scale(const Chunk& c, const double* partial, int n, float max_norm, float eps, float* out, cudaStream_t s) {
-    if (c.pieces.size() <= kSmallTable)
-        return launch(scale_kernel<kSmallTable>, dim3(blocks_of(c)), kThreads, 0, s, table_of<kSmallTable>(c), partial, n, max_norm, eps, out);
-    if (c.pieces.size() <= kMidTable)
-        return launch(scale_kernel<kMidTable>, dim3(blocks_of(c)), kThreads, 0, s, table_of<kMidTable>(c), partial, n, max_norm, eps, out);
-    return launch(scale_kernel<kTable>, dim3(blocks_of(c)), kThreads, 0, s, table_of<kTable>(c), partial, n, max_norm, eps, out);
+cudaError_t launch_scale(const Chunk& c, const double* partial, int sums, float max_norm, float eps, float* out, cudaStream_t s) {
+    const int n = c.t.n, u = c.t.units;
+    const dim3 grid(blocks_of(u));
+    if (n <= kSmallTable) return launch(scale_kernel<kSmallTable>, grid, kThreads, 0, s, table_of<kSmallTable>(c, n, u), partial, sums, max_norm, eps, out);
+    if (n <= kMidTable) return launch(scale_kernel<kMidTable>, grid, kThreads, 0, s, table_of<kMidTable>(c, n, u), partial, sums, max_norm, eps, out);
+    return launch(scale_kernel<kTable>, grid, kThreads, 0, s, c.t, partial, sums, max_norm, eps, out);
 }
 
 // A partial sum per block and launch; calls that count nothing launch one block.
@@ -522,25 +544,26 @@ size_t workspace_of(int64_t n) {
     return (size_t)launches * kMaxBlocks * sizeof(double);
 }
 
-int run_squares(const std::vector<Chunk>& chunks, double* partial, int& n, cudaStream_t s) {
-    n = 0;
+int run_squares(const std::vector<Chunk>& chunks, double* partial, int& sums, cudaStream_t s) {
+    sums = 0;
     for (const Chunk& c : chunks) {
-        const cudaError_t e = launch_squares(c, partial + n, s);
+        if (c.counted == 0) continue;
+        const cudaError_t e = launch_squares(c, partial + sums, s);
         if (e != cudaSuccess) return cuda_error(e, "gradient norm launch");
-        n += blocks_of(c);
+        sums += blocks_of(c.counted_units);
     }
     return DPRED_OK;
 }
 
-bool few(const std::vector<Chunk>& c) {
-    return c.empty() || (c.size() == 1 && c[0].units <= kFewUnits && (int)c[0].pieces.size() <= kSmallTable);
-}
+bool few(const std::vector<Chunk>& c) { return c.empty() || (c.size() == 1 && c[0].t.units <= kFewUnits && c[0].t.n <= kSmallTable); }
 
-// counted: how many of the pieces, from the first on, enter the norm.
 template <bool SCALE>
-int run_cluster(const std::vector<Chunk>& chunks, int counted, float max_norm, float eps, float* out, cudaStream_t s) {
-    const Chunk c = chunks.empty() ? Chunk() : chunks[0];
-    const cudaError_t e = launch(cluster_kernel<SCALE>, dim3(kCluster), kThreads, 0, s, table_of<kSmallTable>(c), std::min(counted, (int)c.pieces.size()), max_norm, eps, out);
+int run_cluster(const std::vector<Chunk>& chunks, float max_norm, float eps, float* out, cudaStream_t s) {
+    Table<kSmallTable> t;
+    t.n = t.units = 0;
+    if (!chunks.empty()) t = table_of<kSmallTable>(chunks[0], chunks[0].t.n, chunks[0].t.units);
+    const int counted = chunks.empty() ? 0 : chunks[0].counted;
+    const cudaError_t e = launch(cluster_kernel<SCALE>, dim3(kCluster), kThreads, 0, s, t, counted, max_norm, eps, out);
     return e == cudaSuccess ? DPRED_OK : cuda_error(e, "gradient norm launch");
 }
 
@@ -565,7 +588,7 @@ extern "C" int dpred_grad_norm(const dpred_grad_tensor* grads, int32_t n, float*
         if ((rc = plan(grads, n, true, chunks)) != DPRED_OK) return rc;
         double* partial = static_cast<double*>(workspace);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (few(chunks)) return run_cluster<false>(chunks, n, 0.0f, 0.0f, norm, s);
+        if (few(chunks)) return run_cluster<false>(chunks, 0.0f, 0.0f, norm, s);
         int sums = 0;
         if ((rc = run_squares(chunks, partial, sums, s)) != DPRED_OK) return rc;
         const cudaError_t e = launch(norm_kernel, dim3(1), kThreads, 0, s, partial, sums, norm);
@@ -584,13 +607,13 @@ extern "C" int dpred_clip_grads(const dpred_grad_tensor* grads, int32_t n, float
         if (reinterpret_cast<uintptr_t>(result) % 4) return set_error(DPRED_E_ALIGN, "result is not aligned to 4 bytes");
         if ((rc = check_workspace(workspace, workspace_bytes, workspace_of(n))) != DPRED_OK) return rc;
         if (any_overlap(grads, n)) return set_error(DPRED_E_SIZE, "two gradients share memory: each would be scaled more than once");
-        std::vector<Chunk> counted, all;
-        if ((rc = plan(grads, n, true, counted)) != DPRED_OK || (rc = plan(grads, n, false, all)) != DPRED_OK) return rc;
+        std::vector<Chunk> all;
+        if ((rc = plan(grads, n, false, all)) != DPRED_OK) return rc;
         double* partial = static_cast<double*>(workspace);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (few(all)) return run_cluster<true>(all, counted.empty() ? 0 : (int)counted[0].pieces.size(), max_norm, eps, result, s);
+        if (few(all)) return run_cluster<true>(all, max_norm, eps, result, s);
         int sums = 0;
-        if ((rc = run_squares(counted, partial, sums, s)) != DPRED_OK) return rc;
+        if ((rc = run_squares(all, partial, sums, s)) != DPRED_OK) return rc;
         for (size_t k = 0; k < all.size(); ++k) {
             const cudaError_t e = launch_scale(all[k], partial, sums, max_norm, eps, k == 0 ? result : nullptr, s);
             if (e != cudaSuccess) return cuda_error(e, "clipping launch");

@@ -35,6 +35,13 @@ def declare(L) -> None:
     L.dpred_clip_grads.argtypes = [vp, i32, f32, f32, vp, vp, sz, vp]
 
 
+def _like(t, stream):
+    """Contiguous device memory of t's shape and type that belongs to the stream of the call."""
+    if stream is None and t.is_contiguous():
+        return _t.torch.empty_like(t)
+    return _empty(tuple(t.shape), t.dtype, stream)
+
+
 def _ids(ids, device: int):
     """(data pointer, bytes of an id, tokens) of a contiguous integer tensor."""
     if ids.dtype is not _t.torch.int64 and ids.dtype is not _t.torch.int32:
@@ -127,7 +134,7 @@ def block_norm(x, y=None, post=None, gate=None, residual_scale: float = 1.0, pre
     if y is not None:
         yp, ldy, _, _ = _matrix(y, "y", _t._BF, dev, m, d)
         if out is None:
-            r = _empty((m, d), x.dtype, stream)
+            r = _like(x, stream)
             rp, ldr = r.data_ptr(), d
         else:
             r = out
@@ -139,7 +146,7 @@ def block_norm(x, y=None, post=None, gate=None, residual_scale: float = 1.0, pre
     if pre is not None:
         wp, wdt = _vector(pre, "pre", _t._OK, dev, d), _code(pre)
         if out_norm is None:
-            h = _empty((m, d), _t._BF[0], stream)
+            h = _like(y, stream) if y is not None else _empty((m, d), _t._BF[0], stream)
             hp, ldh = h.data_ptr(), d
         else:
             h = out_norm
@@ -167,14 +174,14 @@ def block_norm_grad(r, dr=None, dh=None, y=None, post=None, gate=None, residual_
     if dr is not None:
         drp, lddr, _, _ = _matrix(dr, "dr", (r.dtype,), dev, m, d)
     if dx is None:
-        dx = _empty((m, d), r.dtype, stream)
+        dx = _like(r, stream)
         dxp, lddx = dx.data_ptr(), d
     else:
         dxp, lddx, _, _ = _matrix(dx, "dx", (r.dtype,), dev, m, d)
     if y is not None:
         yp, ldy, _, _ = _matrix(y, "y", _t._BF, dev, m, d)
         if dy is None:
-            dy = _empty((m, d), _t._BF[0], stream)
+            dy = _like(y, stream)
             dyp, lddy = dy.data_ptr(), d
         else:
             dyp, lddy, _, _ = _matrix(dy, "dy", _t._BF, dev, m, d)
@@ -243,6 +250,7 @@ class GradClip:
 
     def __init__(self, grads, copies=(), eps: float = 1e-6):
         self.grads, self.copies, self.eps = list(grads), list(copies), float(eps)
+        self._device = _device()
         self._table, self._n = _grad_table(self.grads, self.copies)
         self.workspace = _t.torch.empty(_t._zc.lib().dpred_clip_workspace_bytes(self._n), dtype=_t.torch.uint8, device="cuda")
         self._args = ctypes.addressof(self._table), self._n
@@ -250,11 +258,17 @@ class GradClip:
 
     def norm(self, out=None, stream=None):
         """The norm: fp32 [1], on the device."""
+        self._check()
         return _norm(self._args, self._space, out, stream)
+
+    def _check(self) -> None:
+        if _device() != self._device:
+            raise ValueError(f"the gradients are on CUDA device {self._device}, not the current one")
 
     def clip(self, max_norm: float, out=None, stream=None):
         """Scales the gradients; returns fp32 [2] on the device: the norm before
         and the factor."""
+        self._check()
         return _clip(self._args, self._space, max_norm, self.eps, out, stream)
 
 
