@@ -27,8 +27,8 @@ struct ForwardArgs {
     float scale, eps;
 };
 
-// Few rows, or rows without 16-byte alignment: a row group loads its row itself,
-// up to 8 columns a thread where they are enough.
+// Few rows: a row group loads its row itself, up to 8 columns a thread where they
+// are enough.
 template <typename T, bool VEC, int VPT>
 __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ ForwardArgs a, int lanes) {
     mma::grid_wait();
@@ -99,20 +99,19 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
     }
 }
 
-// Many aligned rows: a block for each SM has a stretch of them, and they come
-// through a ring of bulk copies while rows before them are worked on.  The weights
+// Many rows: a block for each SM has a stretch of them, and they come through a ring of bulk copies while rows before them are worked on.  The weights
 // lie in shared memory, post and a gate that all rows share as one product.  What
 // bounds it next to HBM is issue: LANES known to the compiler turns addresses into
 // immediates, and WHOLE (y, post and pre are there, and all rows share a gate)
 // spares the loop its tests.
-template <typename T, int VPT, int LANES, bool WHOLE>
+template <typename T, bool VEC, int VPT, int LANES, bool WHOLE>
 __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_constant__ ForwardArgs a, const __grid_constant__ Rows in) {
     extern __shared__ __align__(128) char smem[];
     constexpr int lanes = LANES;
     const bool has_y = WHOLE || a.y, has_post = WHOLE || a.post.p, has_pre = WHOLE || a.pre.p, own_gate = !WHOLE && in.seg[2].p;
     const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
     const int64_t row0 = a.m * blockIdx.x / gridDim.x + group, row1 = a.m * (blockIdx.x + 1) / gridDim.x;
-    Ring ring(in, smem, group);
+    Ring<VEC> ring(in, smem, group);
     ring.start(id);
     mma::grid_wait();
     int64_t ahead = row0;
@@ -122,8 +121,8 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
     };
     for (int k = 0; k < in.stages; ++k) request();
     float* weights = reinterpret_cast<float*>(smem + kBarrierBytes + groups * in.stages * in.slot_bytes);
-    const Staged<true, VPT> post = {weights, lanes}, pre = {weights + staged_floats(lanes, VPT), lanes};
-    fill<true, VPT>(lanes, a.d, [&](int c, bool in_row, int at) {
+    const Staged<VEC, VPT> post = {weights, lanes}, pre = {weights + staged_floats(lanes, VPT), lanes};
+    fill<VEC, VPT>(lanes, a.d, [&](int c, bool in_row, int at) {
         const float w = has_pre && in_row ? a.pre.at(0, c) : 0.0f, p = has_y && in_row ? a.post.at(0, c) : 0.0f, q = has_y && in_row && !own_gate ? a.gate.at(0, c) : 1.0f;
         if (has_pre) pre.at[at] = w;
         if (has_y) post.at[at] = p * q;
@@ -134,16 +133,16 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
     const F8 scale = splat(a.scale);
     for (int64_t row = row0; row < row1; row += groups) {
         const char* slot = ring.take();
+        const T* in_x = ring.in(slot, in.seg[0], static_cast<const T*>(a.x) + row * a.ldx);
         F8 r[VPT];
         if (has_y) {
-            Eight<__nv_bfloat16> y[VPT];
+            Cols<__nv_bfloat16, VEC> y[VPT];
+            const __nv_bfloat16* in_y = ring.in(slot, in.seg[1], a.y + row * a.ldy);
             float iy = 1.0f;
             float2 t = {};
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const int c0 = first<true>(v, id, lanes);
-                y[v] = {};
-                if (c0 < a.d) y[v].load(reinterpret_cast<const __nv_bfloat16*>(slot + in.seg[1].at) + c0);
+                y[v].load(in_y, first<VEC>(v, id, lanes), lanes, a.d);
                 const F8 f = widen(y[v]);
                 t = dot8(f, f, t);
             }
@@ -155,25 +154,23 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
             T* out = static_cast<T*>(a.r) + row * a.ldr;
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const int c0 = first<true>(v, id, lanes);
+                const int c0 = first<VEC>(v, id, lanes);
                 F8 u = widen(y[v]) * splat(iy) * post.get(v, id);
-                Eight<T> x = {};
-                if (c0 < a.d) {
-                    x.load(reinterpret_cast<const T*>(slot + in.seg[0].at) + c0);
-                    if (own_gate) {
-                        const Weight g = {slot + in.seg[2].at, a.gate.f32, 0};
-                        u = u * g.load<true>(0, c0, lanes, a.d);
-                    }
+                Cols<T, VEC> x;
+                x.load(in_x, c0, lanes, a.d);
+                if (own_gate) {
+                    const char* p = in.seg[2].p + (in.seg[2].div == 1 ? row : row / in.seg[2].div) * in.seg[2].pitch;
+                    const Weight g = {slot + in.seg[2].at + (VEC ? 0 : reinterpret_cast<uintptr_t>(p) % 16), a.gate.f32, 0};
+                    u = u * g.load<VEC>(0, c0, lanes, a.d);
                 }
                 r[v] = fma8(scale, widen(x), u);
-                if (c0 < a.d) store_cols<true>(out, c0, lanes, a.d, r[v]);
+                store_cols<VEC>(out, c0, lanes, a.d, r[v]);
             }
         } else {
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const int c0 = first<true>(v, id, lanes);
-                Eight<T> x = {};
-                if (c0 < a.d) x.load(reinterpret_cast<const T*>(slot + in.seg[0].at) + c0);
+                Cols<T, VEC> x;
+                x.load(in_x, first<VEC>(v, id, lanes), lanes, a.d);
                 r[v] = widen(x);
             }
         }
@@ -193,30 +190,30 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
         __nv_bfloat16* out = a.h + row * a.ldh;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int c0 = first<true>(v, id, lanes);
-            if (c0 < a.d) store_cols<true>(out, c0, lanes, a.d, r[v] * ir * pre.get(v, id));
+            const int c0 = first<VEC>(v, id, lanes);
+            store_cols<VEC>(out, c0, lanes, a.d, r[v] * ir * pre.get(v, id));
         }
     }
 }
 
-template <typename T, int VPT, int LANES, bool WHOLE>
+template <typename T, bool VEC, int VPT, int LANES, bool WHOLE>
 cudaError_t launch_ring(const ForwardArgs& a, const Rows& in, int groups, cudaStream_t s) {
     static bool done[64];
-    const cudaError_t e = ensure_smem_attr(ring_forward_kernel<T, VPT, LANES, WHOLE>, kRoom, done);
+    const cudaError_t e = ensure_smem_attr(ring_forward_kernel<T, VEC, VPT, LANES, WHOLE>, kRoom, done);
     if (e != cudaSuccess) return e;
     const size_t smem = kBarrierBytes + (size_t)groups * in.stages * in.slot_bytes + 2 * 4 * staged_floats(LANES, VPT);
-    return launch(ring_forward_kernel<T, VPT, LANES, WHOLE>, dim3((unsigned)sm_count()), groups * LANES, smem, s, a, in);
+    return launch(ring_forward_kernel<T, VEC, VPT, LANES, WHOLE>, dim3((unsigned)sm_count()), groups * LANES, smem, s, a, in);
 }
 
-template <typename T, bool WHOLE>
+template <typename T, bool VEC, bool WHOLE>
 cudaError_t launch_ring(const ForwardArgs& a, const RowShape& q, const Rows& in, int groups, cudaStream_t s) {
-    if (q.vecs == 1) return launch_ring<T, 1, 32, WHOLE>(a, in, groups, s);
-    if (q.vecs == 2) return launch_ring<T, 2, 32, WHOLE>(a, in, groups, s);
-    if (q.lanes == 32) return launch_ring<T, 4, 32, WHOLE>(a, in, groups, s);
-    if (q.lanes == 64) return launch_ring<T, 4, 64, WHOLE>(a, in, groups, s);
-    if (q.lanes == 128) return launch_ring<T, 4, 128, WHOLE>(a, in, groups, s);
-    if (q.lanes == 256) return launch_ring<T, 4, 256, WHOLE>(a, in, groups, s);
-    return launch_ring<T, 4, 512, WHOLE>(a, in, groups, s);
+    if (q.vecs == 1) return launch_ring<T, VEC, 1, 32, WHOLE>(a, in, groups, s);
+    if (q.vecs == 2) return launch_ring<T, VEC, 2, 32, WHOLE>(a, in, groups, s);
+    if (q.lanes == 32) return launch_ring<T, VEC, 4, 32, WHOLE>(a, in, groups, s);
+    if (q.lanes == 64) return launch_ring<T, VEC, 4, 64, WHOLE>(a, in, groups, s);
+    if (q.lanes == 128) return launch_ring<T, VEC, 4, 128, WHOLE>(a, in, groups, s);
+    if (q.lanes == 256) return launch_ring<T, VEC, 4, 256, WHOLE>(a, in, groups, s);
+    return launch_ring<T, VEC, 4, 512, WHOLE>(a, in, groups, s);
 }
 
 template <typename T, bool VEC, int VPT>
@@ -227,19 +224,20 @@ cudaError_t launch_kernel(const ForwardArgs& a, const RowShape& q, cudaStream_t 
 
 template <typename T, bool VEC>
 cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
-    if constexpr (VEC) {
+    {
         const RowShape q = shape_of(a.d, 4);
         Rows in = {};
-        in.add(0, a.x, a.ldx, a.d, sizeof(T));
-        if (a.y) in.add(1, a.y, a.ldy, a.d, 2);
-        if (a.gate.p && a.per_gate != a.m) in.add(2, a.gate.p, a.gate.ld, a.d, a.gate.f32 ? 4 : 2, a.per_gate);
+        in.add(0, VEC, a.x, a.m, a.ldx, a.d, sizeof(T));
+        if (a.y) in.add(1, VEC, a.y, a.m, a.ldy, a.d, 2);
+        if (a.gate.p && a.per_gate != a.m) in.add(2, VEC, a.gate.p, a.m, a.gate.ld, a.d, a.gate.f32 ? 4 : 2, a.per_gate);
         in.slot_bytes = in.slot();
         in.err = device_error_word();
         const int room = kRoom - 2 * 4 * staged_floats(q.lanes, q.vecs), groups = ring_groups(q, in.slot_bytes, room, 512);
         // a ring is worth its start where a row group has several rows
         if (groups > 0 && a.m > 2 * (int64_t)groups * sm_count()) {
             in.stages = ring_stages(groups, in.slot_bytes, room);
-            return a.y && a.post.p && a.pre.p && !in.seg[2].p ? launch_ring<T, true>(a, q, in, groups, s) : launch_ring<T, false>(a, q, in, groups, s);
+            if (VEC && a.y && a.post.p && a.pre.p && !in.seg[2].p) return launch_ring<T, VEC, VEC>(a, q, in, groups, s);
+            return launch_ring<T, VEC, false>(a, q, in, groups, s);
         }
     }
     const RowShape q = shape_of(a.d, 1);

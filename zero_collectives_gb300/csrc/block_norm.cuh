@@ -92,16 +92,22 @@ struct Segment {
     const char* p;       // null: not there
     int64_t pitch;       // bytes between rows
     uint32_t bytes, at;  // of a row; where it lies in a slot
-    uint32_t div;        // rows that share one of it
+    uint32_t div, last;  // rows of the stream that share one of it; its last row
 };
 struct Rows {
     Segment seg[kSegments];
     uint32_t used;
     int32_t stages, slot_bytes;
     int* err;
-    void add(int k, const void* p, int64_t ld, int64_t d, int es, int64_t div = 1) {
-        seg[k] = {static_cast<const char*>(p), ld * es, (uint32_t)(d * es), used, (uint32_t)div};
-        used += seg[k].bytes;
+    // vec: rows of whole 16-byte pieces; other rows take a piece more than they fill.
+    void add(int k, bool vec, const void* p, int64_t m, int64_t ld, int64_t d, int es, int64_t div = 1) {
+        const uint32_t bytes = (uint32_t)(d * es);
+        seg[k] = {static_cast<const char*>(p), ld * es, bytes, used, (uint32_t)div, (uint32_t)(m / div - 1)};
+        used += vec ? bytes : (bytes + 15) / 16 * 16 + 16;
+    }
+    void drop(int k) {  // the one added last
+        used = seg[k].at;
+        seg[k] = {};
     }
     int slot() const { return (int)((used + 127) / 128 * 128); }
 };
@@ -119,7 +125,14 @@ inline int ring_stages(int groups, int slot_bytes, int room) { return std::min(k
 // Rows on their way from global to shared memory by bulk copies: each row group
 // of a block has a ring of `stages` slots, and its first thread asks for rows
 // ahead of the one that the group works on.  A slot holds one row of up to five
-// matrices.  Rows are 16-byte aligned and a multiple of 16 bytes.
+// matrices.
+//
+// Bulk copies move whole 16-byte pieces.  A row that does not fill its first and
+// last piece (VEC false) comes with its neighbours' share of them, which nobody
+// looks at, and lies in the slot as far behind a 16-byte boundary as in memory.
+// Nothing is read before the matrix or behind it: elements that lie in such a piece
+// are copied one by one.
+template <bool VEC>
 struct Ring {
     uint64_t* full;
     char* slots;
@@ -143,17 +156,64 @@ struct Ring {
         __syncthreads();
     }
 
+    static __device__ __forceinline__ uintptr_t down(uintptr_t x) { return x & ~(uintptr_t)15; }
+    static __device__ __forceinline__ uintptr_t up(uintptr_t x) { return (x + 15) & ~(uintptr_t)15; }
+
     // Called by the group's first thread, for rows in the order in which take() is called.
     __device__ __forceinline__ void request(const Segment (&seg)[kSegments], int64_t row) {
-        uint32_t bytes = 0;
+        char* slot = slots + to * slot_bytes;
+        uint32_t all = 0;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < kSegments; ++k)
-            if (seg[k].p) bytes += seg[k].bytes;
-        tma::mbar_arrive_expect_tx(full + to, bytes);
+            for (int k = 0; k < kSegments; ++k)
+                if (seg[k].p) all += seg[k].bytes;
+            tma::mbar_arrive_expect_tx(full + to, all);
 #pragma unroll
-        for (int k = 0; k < kSegments; ++k)
-            if (seg[k].p) tma::bulk_load(slots + to * slot_bytes + seg[k].at, seg[k].p + (seg[k].div == 1 ? row : row / seg[k].div) * seg[k].pitch, seg[k].bytes, full + to);
+            for (int k = 0; k < kSegments; ++k)
+                if (seg[k].p) tma::bulk_load(slot + seg[k].at, row_of(seg[k], row), seg[k].bytes, full + to);
+        } else {
+            for (int k = 0; k < kSegments; ++k)
+                if (seg[k].p) {
+                    const Pieces x(seg[k], row_of(seg[k], row));
+                    all += x.bytes();
+                    x.copy_rest(slot + seg[k].at);
+                }
+            tma::mbar_arrive_expect_tx(full + to, all);
+            for (int k = 0; k < kSegments; ++k)
+                if (seg[k].p) {
+                    const Pieces x(seg[k], row_of(seg[k], row));
+                    if (x.bytes()) tma::bulk_load(slot + seg[k].at + (x.lo - down(x.s)), reinterpret_cast<const void*>(x.lo), x.bytes(), full + to);
+                }
+        }
         to = to + 1 == stages ? 0 : to + 1;
+    }
+
+    static __device__ __forceinline__ const char* row_of(const Segment& seg, int64_t row) { return seg.p + (seg.div == 1 ? row : row / seg.div) * seg.pitch; }
+
+    // A row [s, e) and the pieces [lo, hi) that may be copied for it.
+    struct Pieces {
+        uintptr_t s, e, lo, hi;
+        __device__ __forceinline__ Pieces(const Segment& seg, const char* row) {
+            const uintptr_t start = reinterpret_cast<uintptr_t>(seg.p), end = start + seg.last * seg.pitch + seg.bytes;
+            s = reinterpret_cast<uintptr_t>(row);
+            e = s + seg.bytes;
+            lo = max(down(s), up(start));
+            hi = min(up(e), down(end));
+        }
+        __device__ __forceinline__ uint32_t bytes() const { return lo < hi ? (uint32_t)(hi - lo) : 0; }
+        // What lies before and behind them, element by element.
+        __device__ __forceinline__ void copy_rest(char* place) const {
+            char* there = place - down(s);  // an address plus this is its place
+            const uintptr_t head = lo < hi ? lo : e;
+            for (uintptr_t x = s; x < head; x += 2) *reinterpret_cast<uint16_t*>(there + x) = *reinterpret_cast<const uint16_t*>(x);
+            for (uintptr_t x = max(head, hi); x < e; x += 2) *reinterpret_cast<uint16_t*>(there + x) = *reinterpret_cast<const uint16_t*>(x);
+        }
+    };
+
+    // Where a row of a matrix (at `row` in memory) lies in its slot.
+    template <typename T>
+    static __device__ __forceinline__ const T* in(const char* slot, const Segment& seg, const T* row) {
+        return reinterpret_cast<const T*>(slot + seg.at + (VEC ? 0 : reinterpret_cast<uintptr_t>(row) % 16));
     }
 
     // The slot of the next row, once it is there.  A wait that gives up is

@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(kShares * 32) finish_kernel(const __grid_const
 
 // Sections are cut into as many units as there are blocks (one to an SM), or dealt
 // out whole where there are more of them.
-Grid grid_of(int64_t m, int64_t d, int64_t gate_rows) {
+Grid grid_of(int64_t m, int64_t d, int64_t gate_rows, bool vec) {
     Grid g;
-    g.q = shape_of(d, 2);
+    g.q = shape_of(d, vec ? 2 : 1);
     g.sections = gate_rows <= 1 || gate_rows == m ? 1 : gate_rows;
     g.per = m / g.sections;
     g.groups = std::max(1, kThreads / g.q.lanes);
@@ -87,21 +87,21 @@ Grid grid_of(int64_t m, int64_t d, int64_t gate_rows) {
 size_t partial_bytes(const Grid& g, int64_t d) { return (size_t)((2 * g.blocks + (g.parts > 1 ? g.sections * g.parts : 0)) * d) * 4; }
 
 template <typename T>
-cudaError_t launch_backward(const BackwardArgs& a, const Grid& g, bool vec, cudaStream_t s) {
+cudaError_t launch_backward(const BackwardArgs& a, int64_t m, const Grid& g, bool vec, cudaStream_t s) {
     Rows in = {};
     const int es = (int)sizeof(T), gs = a.gate.f32 ? 4 : 2;
     const struct { const void* p; int64_t ld; int es; } parts[kSegments] = {
         {a.dh ? a.r : nullptr, a.ldr, es}, {a.dr, a.lddr, es}, {a.dh, a.lddh, 2}, {a.y, a.ldy, 2}, {a.each ? a.gate.p : nullptr, a.gate.ld, gs}};
     for (int k = 0; k < kSegments; ++k)
-        if (parts[k].p) in.add(k, parts[k].p, parts[k].ld, a.d, parts[k].es);
+        if (parts[k].p) in.add(k, vec, parts[k].p, m, parts[k].ld, a.d, parts[k].es);
+    const int room = kRoom - 4 * staged_space(g.q.lanes, g.q.vecs, g.groups);
+    if (in.seg[4].p && in.slot() + kBarrierBytes > room) in.drop(4);  // the gate of the widest rows is read in place
     in.slot_bytes = in.slot();
     in.err = device_error_word();
-    const int room = kRoom - 4 * staged_space(g.q.lanes, g.q.vecs, g.groups);
-    int groups = vec ? ring_groups(g.q, in.slot_bytes, room, g.groups * g.q.lanes) : 0;
-    if (vec && groups == 0 && in.slot_bytes + kBarrierBytes <= room) groups = 1;  // a single slot
-    if (groups == 0) return launch_rows<T, false, false>(a, in, g, g.groups, s);
+    const int groups = std::max(1, ring_groups(g.q, in.slot_bytes, room, g.groups * g.q.lanes));  // the widest rows have a single slot
     in.stages = ring_stages(groups, in.slot_bytes, room);
     const bool whole = a.dr && a.dh && a.y && a.post.p && !a.each;
+    if (!vec) return launch_rows<T, false, false>(a, in, g, groups, s);
     return whole ? launch_rows<T, true, true>(a, in, g, groups, s) : launch_rows<T, true, false>(a, in, g, groups, s);
 }
 
@@ -114,7 +114,7 @@ using namespace dpred::layers;
 
 extern "C" size_t dpred_block_norm_grad_workspace_bytes(int64_t m, int64_t d, int64_t gate_rows) {
     if (m <= 0 || d <= 0 || d > kMaxWidth || gate_rows < 0 || (gate_rows > 0 && m % gate_rows)) return 0;
-    return partial_bytes(grid_of(m, d, gate_rows), d);
+    return std::max(partial_bytes(grid_of(m, d, gate_rows, true), d), partial_bytes(grid_of(m, d, gate_rows, false), d));
 }
 
 extern "C" int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, const void* r, int64_t ldr, const void* dr, int64_t lddr,
@@ -146,8 +146,10 @@ extern "C" int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, cons
         }
         return DPRED_OK;
     }
-    const Grid g = grid_of(m, d, gate ? gate_rows : 0);
     const bool each = gate && gate_rows == m && m > 1;
+    const bool vec = weights_aligned(n) && (!pre || (aligned_rows(r, m, ldr, es) && aligned_rows(dh, m, lddh, 2))) && (!dr || aligned_rows(dr, m, lddr, es)) &&
+                     aligned_rows(dx, m, lddx, es) && (!each || reinterpret_cast<uintptr_t>(gate_grad) % 16 == 0) && (!y || (aligned_rows(y, m, ldy, 2) && aligned_rows(dy, m, lddy, 2)));
+    const Grid g = grid_of(m, d, gate ? gate_rows : 0, vec);
     const bool gate_sums = gate_grad && !each;
     if ((post_grad || pre_grad || gate_sums) && (rc = check_workspace(workspace, workspace_bytes, partial_bytes(g, d))) != DPRED_OK) return rc;
     BackwardArgs a = {};
@@ -178,8 +180,6 @@ extern "C" int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, cons
     a.d = (int32_t)d;
     a.scale = scale;
     a.eps = eps;
-    const bool vec = weights_aligned(n) && (!pre || (aligned_rows(r, m, ldr, es) && aligned_rows(dh, m, lddh, 2))) && (!dr || aligned_rows(dr, m, lddr, es)) &&
-                     aligned_rows(dx, m, lddx, es) && (!each || reinterpret_cast<uintptr_t>(gate_grad) % 16 == 0) && (!y || (aligned_rows(y, m, ldy, 2) && aligned_rows(dy, m, lddy, 2)));
     FinishArgs f = {};
     f.d = (int32_t)d;
     if (post_grad && g.sections * g.parts > 1) f.dpost = {a.partial, g.blocks, a.dpost};
@@ -187,7 +187,7 @@ extern "C" int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, cons
     if (gate_sums && g.parts > 1) f.dgate = {a.partial + 2 * g.blocks * d, g.parts, a.dgate};
     const int64_t jobs = (f.dpost.to.p != nullptr) + (f.dpre.to.p != nullptr) + (f.dgate.to.p ? g.sections : 0);
     a.release = jobs > 0;
-    cudaError_t e = r_dtype == DPRED_F32 ? launch_backward<float>(a, g, vec, s) : launch_backward<__nv_bfloat16>(a, g, vec, s);
+    cudaError_t e = r_dtype == DPRED_F32 ? launch_backward<float>(a, m, g, vec, s) : launch_backward<__nv_bfloat16>(a, m, g, vec, s);
     if (e != cudaSuccess) return cuda_error(e, "block norm gradient launch");
     if (jobs == 0) return DPRED_OK;
     e = launch(finish_kernel, dim3((unsigned)((d + 31) / 32), (unsigned)jobs), kShares * 32, 0, s, f);

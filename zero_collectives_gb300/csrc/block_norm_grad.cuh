@@ -116,11 +116,12 @@ struct Walk {
     }
 };
 
-// VEC: aligned rows.  They come through a ring of bulk copies while rows before
-// them are worked on; without it a row's loads and its two sums follow one another,
-// and the few row groups that an SM holds cannot hide that.  (A row that fills the
-// only slot is asked for when the one before it is done.)  Otherwise, rows without
-// 16-byte alignment or too long for a slot, elements are loaded one by one.
+// Rows come through a ring of bulk copies while rows before them are worked on;
+// without it a row's loads and its two sums follow one another, and the few row
+// groups that an SM holds cannot hide that (16384 x 1024 took 74 us).  A row that
+// fills the only slot is asked for when the one before it is done.
+// VEC: aligned rows, 8 columns next to each other a thread; otherwise every
+// LANES-th, element by element, past the copies.
 //
 // Where rows share a gate row, sum of g n_y over them gives both gradients:
 // dgate = post times it, dpost = gate times it, which is added per unit.
@@ -136,22 +137,22 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
     constexpr int lanes = LANES;
     const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
     const bool has_dr = WHOLE || a.dr, has_dh = WHOLE || a.dh, has_y = WHOLE || a.y, has_post = WHOLE || a.post.p, each = !WHOLE && a.each;
-    Ring ring(in, smem, group);
-    if (VEC) ring.start(id);
+    Ring<VEC> ring(in, smem, group);
+    ring.start(id);
     mma::grid_wait();
     Walk ahead(a, group);
-    bool more = VEC && id == 0 && ahead.any(a, group);
+    bool more = id == 0 && ahead.any(a, group);
     auto request = [&]() {
         if (!more) return;
         ring.request(in.seg, ahead.row);
         ahead.row += groups;
         more = ahead.any(a, group);
     };
-    if (VEC)
-        for (int k = 0; k < in.stages; ++k) request();
+    for (int k = 0; k < in.stages; ++k) request();
 
     float* weights = reinterpret_cast<float*>(smem + kBarrierBytes + groups * in.stages * in.slot_bytes);
-    const int width = staged_floats(lanes, VPT);
+    constexpr bool kStaged = VPT <= 2;  // the weights of wider rows would take the room of their slots
+    const int width = kStaged ? staged_floats(lanes, VPT) : 0;
     const Staged<VEC, VPT> post = {weights, lanes}, pre = {weights + width, lanes};  // post: with the unit's gate
     float* buf = weights + 2 * width;
     RowSum sum(lanes, group);
@@ -166,7 +167,15 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int64_t section = unit / a.parts, part = unit - section * a.parts;
         const int64_t row0 = section * a.per + a.per * part / a.parts, row1 = section * a.per + a.per * (part + 1) / a.parts;
-        if (unit == blockIdx.x || a.sections > 1) {
+        auto pre8 = [&](int v) { return kStaged ? pre.get(v, id) : a.pre.load<VEC>(0, first<VEC>(v, id, lanes), lanes, a.d); };
+        auto post8 = [&](int v) {
+            if (kStaged) return post.get(v, id);
+            const int c0 = first<VEC>(v, id, lanes);
+            F8 w = a.post.p ? a.post.load<VEC>(0, c0, lanes, a.d) : splat(1.0f);
+            if (a.gate.p && !each) w = w * a.gate.load<VEC>(section, c0, lanes, a.d);
+            return w;
+        };
+        if (kStaged && (unit == blockIdx.x || a.sections > 1)) {
             const bool begin = unit == blockIdx.x;
             if (!begin) __syncthreads();
             fill<VEC, VPT>(lanes, a.d, [&](int c, bool in_row, int at) {
@@ -181,11 +190,11 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
 #pragma unroll
         for (int v = 0; v < VPT; ++v) dyn[v] = zero;
         for (int64_t row = row0 + group; row < row1; row += groups) {
-            const char* slot = VEC ? ring.take() : nullptr;
-            const T* in_r = VEC ? reinterpret_cast<const T*>(slot + in.seg[0].at) : static_cast<const T*>(a.r) + row * a.ldr;
-            const T* in_dr = VEC ? reinterpret_cast<const T*>(slot + in.seg[1].at) : static_cast<const T*>(a.dr) + row * a.lddr;
-            const __nv_bfloat16* in_dh = VEC ? reinterpret_cast<const __nv_bfloat16*>(slot + in.seg[2].at) : a.dh + row * a.lddh;
-            const __nv_bfloat16* in_y = VEC ? reinterpret_cast<const __nv_bfloat16*>(slot + in.seg[3].at) : a.y + row * a.ldy;
+            const char* slot = ring.take();
+            const T* in_r = ring.in(slot, in.seg[0], static_cast<const T*>(a.r) + row * a.ldr);
+            const T* in_dr = ring.in(slot, in.seg[1], static_cast<const T*>(a.dr) + row * a.lddr);
+            const __nv_bfloat16* in_dh = ring.in(slot, in.seg[2], a.dh + row * a.lddh);
+            const __nv_bfloat16* in_y = ring.in(slot, in.seg[3], a.y + row * a.ldy);
             Cols<T, VEC> r;
             Cols<__nv_bfloat16, VEC> dh, y;
             // rows of up to two vectors a thread stay in registers, longer ones are read again
@@ -212,13 +221,13 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
                 fetch(h, first<VEC>(v, id, lanes));
                 if (has_dh) {
                     rr = dot8(r8[h], r8[h], rr);
-                    vr = dot8(dh8[h] * pre.get(v, id), r8[h], vr);
+                    vr = dot8(dh8[h] * pre8(v), r8[h], vr);
                 }
                 if (has_post) yy = dot8(y8[h], y8[h], yy);
             }
             float s[3] = {rr.x + rr.y, vr.x + vr.y, yy.x + yy.y};
             if (has_dh || has_post) sum(s);
-            if (VEC) {
+            {
                 if (lanes == 32 || !(has_dh || has_post)) group_sync(group, lanes);
                 // the row is in registers: its slot takes another; or everyone has left the row before
                 if (early || (begun && in.stages > 1)) request();
@@ -237,23 +246,27 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
                 if (has_dr) g[v] = widen(dr[h]);
                 if (has_dh) {
                     const F8 n = r8[h] * ir8;
-                    g[v] = fma8(ir8, fma8(n, mean_r, dh8[h] * pre.get(v, id)), g[v]);
+                    g[v] = fma8(ir8, fma8(n, mean_r, dh8[h] * pre8(v)), g[v]);
                     dpre[v] = fma8(dh8[h], n, dpre[v]);
                 }
                 store_cols<VEC>(dx, c0, lanes, a.d, scale * g[v]);
                 if (!has_y) continue;
-                const F8 n = y8[h] * iy8, w8 = post.get(v, id);
+                const F8 n = y8[h] * iy8, w8 = post8(v);
                 if (each) {
-                    const Weight w = {VEC ? slot + in.seg[4].at : a.gate.p, a.gate.f32, VEC ? 0 : a.gate.ld};
                     if (a.dgate.p) a.dgate.put8<VEC>(row, c0, lanes, a.d, g[v] * n * w8);
-                    g[v] = g[v] * w.load<VEC>(row, c0, lanes, a.d);
+                    if (VPT <= 2 || in.seg[4].p) {
+                        const Weight w = {slot + in.seg[4].at + (VEC ? 0 : reinterpret_cast<uintptr_t>(in.seg[4].p + row * in.seg[4].pitch) % 16), a.gate.f32, 0};
+                        g[v] = g[v] * w.load<VEC>(0, c0, lanes, a.d);
+                    } else {
+                        g[v] = g[v] * a.gate.load<VEC>(row, c0, lanes, a.d);
+                    }
                 }
                 dyn[v] = fma8(g[v], n, dyn[v]);
                 g[v] = g[v] * w8;
                 wn = dot8(g[v], n, wn);
                 if (VPT == kHeld) y8[h] = n;
             }
-            if (VEC && !early && in.stages == 1 && !has_post) {  // nothing more is read
+            if (!early && in.stages == 1 && !has_post) {  // nothing more is read
                 group_sync(group, lanes);
                 request();
             }
@@ -272,7 +285,7 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
                 if (has_post) g[v] = iy8 * fma8(y8[v % kHeld], mean_y, g[v]);
                 store_cols<VEC>(dy, c0, lanes, a.d, g[v]);
             }
-            if (VEC && !early && in.stages == 1 && has_post) {
+            if (!early && in.stages == 1 && has_post) {
                 group_sync(group, lanes);
                 request();
             }
@@ -312,7 +325,7 @@ struct Grid {
 };
 
 // Floats of the weights and of combine().
-inline int staged_space(int lanes, int vecs, int groups) { return staged_floats(lanes, vecs) * (2 + (groups > 1 ? groups : 0)); }
+inline int staged_space(int lanes, int vecs, int groups) { return vecs <= 2 ? staged_floats(lanes, vecs) * (2 + (groups > 1 ? groups : 0)) : 0; }
 
 template <typename T, bool VEC, int VPT, int LANES, bool WHOLE>
 cudaError_t launch_kernel(const BackwardArgs& a, const Rows& in, const Grid& g, int groups, cudaStream_t s) {
@@ -326,6 +339,15 @@ cudaError_t launch_kernel(const BackwardArgs& a, const Rows& in, const Grid& g, 
 // Each form has units of its own: aligned rows, and rows of any alignment.
 template <typename T, bool VEC, bool WHOLE>
 cudaError_t launch_rows(const BackwardArgs& a, const Rows& in, const Grid& g, int groups, cudaStream_t s) {
+    if constexpr (!VEC) {  // one vector a thread as far as 512 threads reach
+        if (g.q.vecs == 1 && g.q.lanes == 64) return launch_kernel<T, VEC, 1, 64, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 1 && g.q.lanes == 128) return launch_kernel<T, VEC, 1, 128, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 1 && g.q.lanes == 256) return launch_kernel<T, VEC, 1, 256, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 1 && g.q.lanes == 512) return launch_kernel<T, VEC, 1, 512, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 2) return launch_kernel<T, VEC, 2, 512, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 4) return launch_kernel<T, VEC, 4, 512, WHOLE>(a, in, g, groups, s);
+        return launch_kernel<T, VEC, 1, 32, WHOLE>(a, in, g, groups, s);
+    } else {
     if (g.q.vecs == 1) return launch_kernel<T, VEC, 1, 32, WHOLE>(a, in, g, groups, s);
     if (g.q.vecs == 4) return launch_kernel<T, VEC, 4, 512, WHOLE>(a, in, g, groups, s);
     if (g.q.lanes == 32) return launch_kernel<T, VEC, 2, 32, WHOLE>(a, in, g, groups, s);
@@ -333,6 +355,7 @@ cudaError_t launch_rows(const BackwardArgs& a, const Rows& in, const Grid& g, in
     if (g.q.lanes == 128) return launch_kernel<T, VEC, 2, 128, WHOLE>(a, in, g, groups, s);
     if (g.q.lanes == 256) return launch_kernel<T, VEC, 2, 256, WHOLE>(a, in, g, groups, s);
     return launch_kernel<T, VEC, 2, 512, WHOLE>(a, in, g, groups, s);
+    }
 }
 
 #define DPRED_NORM_GRAD_FORM(T, VEC, WHOLE) \
