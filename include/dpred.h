@@ -660,15 +660,17 @@ int dpred_embedding_grad(int64_t t, int64_t v, int64_t d, int32_t id_bytes, cons
  *
  * Everything is formed in fp32 and each output rounded once; h is the norm of r
  * before its rounding, the gradient that of the stored r.  Sums over rows have a
- * fixed order that depends on the device and the sizes: the same call gives the
- * same bits.  The mean of a row's squares must stay below 3e38 (elements below
- * about 1e19); with eps = 0 a row of zeros gives NaN.  A NaN or an infinity stays in its row
- * and in the weight gradients.  Row strides in elements (at least d), any m from
+ * fixed order that depends on the device and on the whole call, its sizes, types,
+ * alignment and optional arguments: the same call gives the same bits.  A bounded
+ * device-side wait that gives up records DPRED_E_TIMEOUT in the device error word.
+ * The mean of a row's squares must stay below 3e38 (elements below about 1e19);
+ * with eps = 0 a row of zeros gives NaN.  A NaN or an infinity stays in its row and
+ * in the weight gradients.  Row strides in elements (at least d), any m from
  * 0 up to 2^31 - 1 and d up to 16384, any alignment to the element size.  An output
  * matrix may be an input of the same type and stride; no output may otherwise
  * overlap an input or another output.  workspace (device, 256-byte aligned):
- * dpred_block_norm_grad_workspace_bytes() (gate_rows 0 without a gate), needed
- * for weight gradients only.  Asynchronous on `stream`; may be captured into a
+ * dpred_block_norm_grad_workspace_bytes() (gate_rows 0 without a gate), for the
+ * current device, needed for weight gradients only.  Asynchronous on `stream`; may be captured into a
  * CUDA graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN, DPRED_E_SIZE, DPRED_E_CUDA.
  */
 int dpred_block_norm(int64_t m, int64_t d, int32_t r_dtype, const void* x, int64_t ldx, const void* y, int64_t ldy,

@@ -160,6 +160,51 @@ def test_gates_of_sequences_and_tokens(m, d, stream, share):
     c.check_backward(dx, dy, grads, fill=-0.5)
 
 
+# rows enough for every row group to have several, at each width's way of covering a row
+MANY = [(9000, 33), (9001, 64), (9000, 250), (6000, 400), (6000, 509), (6000, 777), (5500, 1000), (3000, 1537), (3001, 2048), (1500, 3333), (1400, 4096),
+        (900, 5001), (801, 8192), (700, 8191), (500, 12288), (500, 12289), (420, 16384), (420, 16383)]
+
+
+@pytest.mark.parametrize("m,d", MANY)
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("form", [dict(), dict(gate="token"), dict(y=False), dict(post=False, gate=0, dr=False)], ids=str)
+def test_many_rows(m, d, stream, form):
+    form = dict(form)
+    if form.get("gate") == "token":
+        form["gate"] = m
+    c = Case(m, d, stream=stream, **form)
+    c.check_forward(*c.forward())
+    grads = c.grads(fill=0.125)
+    dx, dy = c.backward(grads, accumulate=True)
+    c.check_backward(dx, dy, grads, fill=0.125)
+    assert zc.device_status() == 0
+
+
+@pytest.mark.parametrize("m,d,pad,shift", [(6000, 97, 0, 1), (6000, 1, 0, 3), (6001, 3, 2, 1), (20000, 5, 0, 7), (5000, 1024, 1, 0), (5000, 1000, 3, 5), (1000, 5000, 0, 1),
+                                          (400, 16000, 7, 3)])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gate", [1, 4, 0])
+def test_many_rows_of_any_alignment(m, d, pad, shift, stream, gate):
+    """Rows that share 16-byte pieces with their neighbours, shorter than a piece, and
+    at the ends of their storage; into outputs whose gaps stay as they are."""
+    gate = gate if gate == 0 or m % gate == 0 else m
+    c = Case(m, d, stream=stream, gate=gate, pad=pad, shift=shift)
+    outs = [randn(m, d, seed=20 + i, dtype=t, pad=pad, shift=shift) for i, t in enumerate((stream, torch.bfloat16, stream, torch.bfloat16))]
+    gaps = [o.as_strided((m - 1, pad), (d + pad, 1), o.storage_offset() + d) for o in outs]
+    before = [g.clone() for g in gaps]
+    c.check_forward(*c.forward(out=outs[0], out_norm=outs[1]))
+    grads = c.grads()
+    c.check_backward(*c.backward(grads, dx=outs[2], dy=outs[3]), grads)
+    assert all(torch.equal(a, b) for a, b in zip(gaps, before)), "columns between the rows were written"
+    # in place, over the rows themselves
+    want = [o.clone() for o in outs]
+    r2, h2 = c.forward(out=c.x, out_norm=c.y)
+    assert torch.equal(r2, want[0]) and torch.equal(h2, want[1])
+    k = Case(m, d, stream=stream, gate=gate, pad=pad, shift=shift)
+    dx2, dy2 = k.backward(k.grads(), dx=k.dr, dy=k.dh)
+    assert torch.equal(dx2, want[2]) and torch.equal(dy2, want[3])
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (8, 8), (1, 0), (0, 1), (3, 5)])
 @pytest.mark.parametrize("m,d", [(50, 136), (9, 2056)])
 @pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
@@ -318,6 +363,7 @@ def test_refusals():
         lambda: zc.block_norm(c.x, post=c.post, pre=c.pre), lambda: zc.block_norm(c.x, residual_scale=0.5, pre=c.pre),
         lambda: zc.block_norm(c.x, y=c.y, gate=torch.ones(5, 64, device="cuda")), lambda: zc.block_norm(c.x, y=c.y, gate=torch.ones(0, 64, device="cuda")),
         lambda: zc.block_norm(c.x, y=c.y, gate=torch.ones(2, 128, device="cuda")[:, :64]), lambda: zc.block_norm(c.x, y=c.y, post=c.post[:63]),
+        lambda: zc.block_norm(c.x, pre=c.pre, out=torch.empty_like(c.x)), lambda: zc.block_norm(c.x, y=c.y, out_norm=torch.empty_like(c.y)),
         lambda: zc.block_norm(c.x, y=c.y, out=torch.empty(12, 64, device="cuda")), lambda: zc.block_norm(c.x, y=c.y, eps=-1.0),
         lambda: zc.block_norm(torch.zeros(2, 20000, device="cuda"), y=torch.zeros(2, 20000, device="cuda").bfloat16()),
         lambda: zc.block_norm_grad(c.x), lambda: zc.block_norm_grad(c.x, dr=c.dr, dh=c.dh), lambda: zc.block_norm_grad(c.x, dr=c.dr, pre=c.pre),

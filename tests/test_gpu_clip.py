@@ -81,11 +81,20 @@ def test_mixed_types_and_copies():
     check([grad(4, 6 * 8, 6).view(4, 6, 8)])
 
 
-def test_the_whole_range_of_values():
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_copies(dtype):
+    """Copies in launches with and without counted gradients."""
+    check([grad(300, 1000, 1, dtype=dtype)], copies=[grad(400, 5000, 2, dtype=dtype), grad(70, 33, 3, dtype=dtype, pad=5)])
+    check([grad(1, 50 + i, i, dtype=dtype) for i in range(500)], copies=[grad(1, 50 + i, i, dtype=dtype) for i in range(1200)])
+    check([grad(1, 9, 1)], copies=[grad(1, 10 + i, i, dtype=dtype) for i in range(800)])
+
+
+@pytest.mark.parametrize("n", [5000, 3_000_000])
+def test_the_whole_range_of_values(n):
     """Squares that overflow or underflow fp32, alone and beside ordinary ones."""
-    for scale in (1e-38, 1e-30, 1e-22, 1e-12, 1e10, 1e18, 1e25, 1e36):
+    for scale in (1e-38, 1e-30, 1e-22, 1e-12, 1e10, 1e18, 1e25, 1e34):
         for dtype in (torch.bfloat16, torch.float32):
-            check([(torch.randn(5000, device="cuda").clamp(-3, 3) * scale).to(dtype)], eps=0.0)
+            check([(torch.randn(n, device="cuda").clamp(-3, 3) * scale).to(dtype)], eps=0.0)
     big = torch.full((100000,), 1.5e18, device="cuda")
     assert abs(float(zc.grad_norm([big])) / (1.5e18 * 100000 ** 0.5) - 1) < 1e-6
     tiny = torch.full((33,), 1e-45, device="cuda")  # the smallest subnormal

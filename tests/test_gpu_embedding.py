@@ -39,7 +39,7 @@ def ids_of(t, v, seed, kind="uniform", dtype=torch.int64):
 
 
 @pytest.mark.parametrize("t,v,d", [(1, 1, 1), (1, 1000, 1024), (5, 7, 3), (33, 100, 64), (300, 500, 777), (1000, 40, 8), (4097, 3000, 256), (64, 50, 2056),
-                                   (20000, 11, 16)])
+                                   (20000, 11, 16), (777, 60, 264), (3000, 90, 512), (300, 40, 5000)])
 @pytest.mark.parametrize("wdt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("odt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 1)])

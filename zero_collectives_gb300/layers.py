@@ -130,6 +130,8 @@ def block_norm(x, y=None, post=None, gate=None, residual_scale: float = 1.0, pre
     dev = _device()
     xp, ldx, m, d = _matrix(x, "x", _t._OK, dev)
     yp = ldy = pp = pdt = gp = gdt = rp = ldr = wp = wdt = hp = ldh = gr = 0
+    if (out is not None and y is None) or (out_norm is not None and pre is None):
+        raise ValueError("out needs y (r is x without it), out_norm needs pre")
     r, h = x, None
     if y is not None:
         yp, ldy, _, _ = _matrix(y, "y", _t._BF, dev, m, d)
