@@ -247,8 +247,11 @@ class GradClip:
     min(1, max_norm / (norm + eps)).  grads: bf16 or fp32 tensors on the current
     device, contiguous or with strided rows; copies: further copies of some of
     them (such as those of a parameter that several ranks hold), which are scaled
-    and not counted.  Calls of one object run one after another (they share its
-    workspace): use one stream, or order the streams."""
+    and not counted.  Calls of one object scale the same gradients: use one stream,
+    or order the streams.  The workspace belongs to the stream that is current here;
+    a call on another one, or one that is captured, has memory of its own, so the
+    object may go as soon as a call has returned (a graph still needs the
+    gradients)."""
 
     def __init__(self, grads, copies=(), eps: float = 1e-6):
         self.grads, self.copies, self.eps = list(grads), list(copies), float(eps)
@@ -256,12 +259,22 @@ class GradClip:
         self._table, self._n = _grad_table(self.grads, self.copies)
         self.workspace = _t.torch.empty(_t._zc.lib().dpred_clip_workspace_bytes(self._n), dtype=_t.torch.uint8, device="cuda")
         self._args = ctypes.addressof(self._table), self._n
-        self._space = self.workspace.data_ptr(), self.workspace.numel()
+        self._own = self.workspace, self.workspace.data_ptr(), self.workspace.numel()
+        self._stream = _t._zc._stream(None)
+
+    def _space(self, stream):
+        """A workspace that belongs to the stream of the call, or to the graph that
+        captures it: the memory of another stream may still be in use there, and is
+        given to others there while this call runs."""
+        if _t._zc._stream(stream) == self._stream and not _t.torch._C._cuda_isCurrentStreamCapturing():
+            return self._own
+        return _workspace(self.workspace.numel(), None, stream)
 
     def norm(self, out=None, stream=None):
         """The norm: fp32 [1], on the device."""
         self._check()
-        return _norm(self._args, self._space, out, stream)
+        ws, *space = self._space(stream)
+        return _norm(self._args, space, out, stream)
 
     def _check(self) -> None:
         if _device() != self._device:
@@ -271,7 +284,8 @@ class GradClip:
         """Scales the gradients; returns fp32 [2] on the device: the norm before
         and the factor."""
         self._check()
-        return _clip(self._args, self._space, max_norm, self.eps, out, stream)
+        ws, *space = self._space(stream)
+        return _clip(self._args, space, max_norm, self.eps, out, stream)
 
 
 def _result(out, n: int, stream):
