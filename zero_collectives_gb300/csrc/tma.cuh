@@ -91,7 +91,7 @@ __device__ __forceinline__ void bulk_wait() {
     asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Order generic-proxy shared-memory writes before a later bulk store reads them.
+// Order generic-proxy shared-memory writes before what a later bulk copy does there.
 __device__ __forceinline__ void fence_proxy_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
