@@ -176,8 +176,10 @@ struct Ring {
                 if (seg[k].p) {
                     const Pieces x(seg[k], row_of(seg[k], row));
                     all += x.bytes();
-                    // bulk copies write these bytes when the slot takes another row
-                    if (x.copy_rest(slot + seg[k].at)) tma::fence_proxy_async_shared();
+                    if (!x.whole()) {
+                        x.copy_rest(slot + seg[k].at);
+                        tma::fence_proxy_async_shared();  // bulk copies write these bytes when the slot takes another row
+                    }
                 }
             tma::mbar_arrive_expect_tx(full + to, all);
             for (int k = 0; k < kSegments; ++k)
@@ -202,13 +204,13 @@ struct Ring {
             hi = min(up(e), down(end));
         }
         __device__ __forceinline__ uint32_t bytes() const { return lo < hi ? (uint32_t)(hi - lo) : 0; }
-        // What lies before and behind them, element by element; whether there was any.
-        __device__ __forceinline__ bool copy_rest(char* place) const {
+        __device__ __forceinline__ bool whole() const { return lo <= s && hi >= e; }
+        // What lies before and behind them, element by element.
+        __device__ __forceinline__ void copy_rest(char* place) const {
             char* there = place - down(s);  // an address plus this is its place
             const uintptr_t head = lo < hi ? lo : e;
             for (uintptr_t x = s; x < head; x += 2) *reinterpret_cast<uint16_t*>(there + x) = *reinterpret_cast<const uint16_t*>(x);
             for (uintptr_t x = max(head, hi); x < e; x += 2) *reinterpret_cast<uint16_t*>(there + x) = *reinterpret_cast<const uint16_t*>(x);
-            return head > s || max(head, hi) < e;
         }
     };
 
