@@ -663,8 +663,9 @@ int dpred_embedding_grad(int64_t t, int64_t v, int64_t d, int32_t id_bytes, cons
  * fixed order that depends on the device and on the whole call, its sizes, types,
  * alignment and optional arguments: the same call gives the same bits.  A bounded
  * device-side wait that gives up records DPRED_E_TIMEOUT in the device error word.
- * The mean of a row's squares must stay below 3e38 (elements below about 1e19);
- * with eps = 0 a row of zeros gives NaN.  A NaN or an infinity stays in its row and
+ * Elements of y and r may be up to 3e18 in magnitude, products dh pre r up to 1e37;
+ * with eps = 0 the root of a row's mean square must be 1e-17 at least (a row of zeros
+ * gives NaN).  A NaN or an infinity stays in its row and
  * in the weight gradients.  Row strides in elements (at least d), any m from
  * 0 up to 2^31 - 1 and d up to 16384, any alignment to the element size.  An output
  * matrix may be an input of the same type and stride; no output may otherwise

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
     mma::grid_wait();
     const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
     RowSum sum(lanes, group);
-    const float inv_d = 1.0f / (float)a.d;
+    const float share = share_of(lanes), inv_d = mean_of(lanes, a.d);
     for (int64_t row = (int64_t)blockIdx.x * groups + group; row < a.m; row += (int64_t)gridDim.x * groups) {
         Cols<T, VEC> x[VPT];
         Cols<__nv_bfloat16, VEC> y[VPT];
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
                     const F8 f = widen(y[v]);
                     t = dot8(f, f, t);
                 }
-                float s[1] = {t.x + t.y};
+                float s[1] = {(t.x + t.y) * share};
                 sum(s);
                 iy = rsqrtf(fmaf(s[0], inv_d, a.eps));
             }
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
         float2 t = {};
 #pragma unroll
         for (int v = 0; v < VPT; ++v) t = dot8(r[v], r[v], t);
-        float s[1] = {t.x + t.y};
+        float s[1] = {(t.x + t.y) * share};
         sum(s);
         const float ir = rsqrtf(fmaf(s[0], inv_d, a.eps));
 #pragma unroll
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
     });
     __syncthreads();
     RowSum sum(lanes, group);
-    const float inv_d = 1.0f / (float)a.d;
+    const float share = share_of(lanes), inv_d = mean_of(lanes, a.d);
     const F8 scale = splat(a.scale);
     for (int64_t row = row0; row < row1; row += groups) {
         const char* slot = ring.take();
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
                 t = dot8(f, f, t);
             }
             if (has_post) {
-                float s[1] = {t.x + t.y};
+                float s[1] = {(t.x + t.y) * share};
                 sum(s);
                 iy = rsqrtf(fmaf(s[0], inv_d, a.eps));
             }
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
             float2 t = {};
 #pragma unroll
             for (int v = 0; v < VPT; ++v) t = dot8(r[v], r[v], t);
-            s[0] = t.x + t.y;
+            s[0] = (t.x + t.y) * share;
             sum(s);
         }
         // the row is in registers: its slot takes another

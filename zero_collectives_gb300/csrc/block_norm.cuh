@@ -43,6 +43,12 @@ __device__ __forceinline__ void group_sync(int group, int lanes) {
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
 }
 
+// Sums over the threads of a row are formed of their sums times 1 / lanes, and times
+// lanes / d they are means.  Powers of two round nothing, and no row overflows whose
+// threads' own sums, of at most 32 products, do not.
+__device__ __forceinline__ float share_of(int lanes) { return __uint_as_float(0x7F000000u - __float_as_uint((float)lanes)); }
+__device__ __forceinline__ float mean_of(int lanes, int d) { return (float)lanes * (1.0f / (float)d); }
+
 // Sums over the threads of a row, the same in all of them.  A row of several
 // warps has a barrier of its own; one per sum is enough, since sums in turn use
 // two places: whoever writes to one again has passed the barrier in between,

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
     const Staged<VEC, VPT> post = {weights, lanes}, pre = {weights + width, lanes};  // post: with the unit's gate
     float* buf = weights + 2 * width;
     RowSum sum(lanes, group);
-    const float inv_d = 1.0f / (float)a.d;
+    const float share = share_of(lanes), inv_d = mean_of(lanes, a.d);
     const F8 zero = splat(0.0f), scale = splat(a.scale);
     F8 dpre[VPT];
 #pragma unroll
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
                 }
                 if (has_post) yy = dot8(y8[h], y8[h], yy);
             }
-            float s[3] = {rr.x + rr.y, vr.x + vr.y, yy.x + yy.y};
+            float s[3] = {(rr.x + rr.y) * share, (vr.x + vr.y) * share, (yy.x + yy.y) * share};
             if (has_dh || has_post) sum(s);
             {
                 if (lanes == 32 || !(has_dh || has_post)) group_sync(group, lanes);
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
             }
             if (!has_y) continue;
             __nv_bfloat16* dy = a.dy + row * a.lddy;
-            float q[1] = {wn.x + wn.y};
+            float q[1] = {(wn.x + wn.y) * share};
             if (has_post) sum(q);
             const F8 mean_y = splat(has_post ? -(q[0] * inv_d) : 0.0f);  // minus the mean of w n_y
 #pragma unroll
