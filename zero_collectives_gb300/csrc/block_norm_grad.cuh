@@ -249,17 +249,20 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
                     g[v] = fma8(ir8, fma8(n, mean_r, dh8[h] * pre8(v)), g[v]);
                     dpre[v] = fma8(dh8[h], n, dpre[v]);
                 }
+                // a gate row that is read in place, before outputs that may lie over it are written
+                F8 gate;
+                const bool in_place = VPT > 2 && each && !in.seg[4].p;
+                if (in_place) gate = a.gate.load<VEC>(row, c0, lanes, a.d);
                 store_cols<VEC>(dx, c0, lanes, a.d, scale * g[v]);
                 if (!has_y) continue;
                 const F8 n = y8[h] * iy8, w8 = post8(v);
                 if (each) {
                     if (a.dgate.p) a.dgate.put8<VEC>(row, c0, lanes, a.d, g[v] * n * w8);
-                    if (VPT <= 2 || in.seg[4].p) {
+                    if (!in_place) {
                         const Weight w = {slot + in.seg[4].at + (VEC ? 0 : reinterpret_cast<uintptr_t>(in.seg[4].p + row * in.seg[4].pitch) % 16), a.gate.f32, 0};
-                        g[v] = g[v] * w.load<VEC>(0, c0, lanes, a.d);
-                    } else {
-                        g[v] = g[v] * a.gate.load<VEC>(row, c0, lanes, a.d);
+                        gate = w.load<VEC>(0, c0, lanes, a.d);
                     }
+                    g[v] = g[v] * gate;
                 }
                 dyn[v] = fma8(g[v], n, dyn[v]);
                 g[v] = g[v] * w8;
