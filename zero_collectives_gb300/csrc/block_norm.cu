@@ -34,7 +34,8 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
     mma::grid_wait();
     const int id = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
     RowSum sum(lanes, group);
-    const float share = share_of(lanes), inv_d = mean_of(lanes, a.d);
+    // only 512 threads have several vectors each
+    const float share = VPT > 1 ? 1.0f / 512 : share_of(lanes), inv_d = mean_of(lanes, a.d);
     for (int64_t row = (int64_t)blockIdx.x * groups + group; row < a.m; row += (int64_t)gridDim.x * groups) {
         Cols<T, VEC> x[VPT];
         Cols<__nv_bfloat16, VEC> y[VPT];
