@@ -491,7 +491,7 @@ int plan(const dpred_grad_tensor* g, int n, bool counted_only, std::vector<Chunk
             p.per = (int32_t)-std::min<int64_t>(row_units, 0x7FFFFFFF);
         } else {
             p.per = (int32_t)std::max<int64_t>(1, kUnit / bytes);
-            units = (p.rows + p.per - 1) / p.per;
+            units = ((int64_t)p.rows + p.per - 1) / p.per;
         }
         if (out.empty() || out.back().t.n == kTable) {
             out.emplace_back();
