@@ -705,12 +705,13 @@ int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, const void* r, 
  * No counted gradient: norm 0, c = 1.
  *
  * grads: host array, read during the call only; row strides in elements (at least
- * cols), any size from 0 (rows up to 2^31 - 1, cols up to 2^40), any alignment to
- * the element size; what lies between rows is not touched.  dpred_clip_grads
- * refuses gradients that share memory (DPRED_E_SIZE; matrices side by side in
- * wider rows do not).  norm, result: device, fp32.  workspace (device, 256-byte
- * aligned): dpred_clip_workspace_bytes(n).  Asynchronous on `stream`; may be
- * captured into a CUDA graph.  Errors: DPRED_E_INVAL, DPRED_E_ALIGN,
+ * cols), any size from 0 (rows up to 2^31 - 1, cols up to 2^40, their span up to
+ * 2^60 elements), any alignment to the element size; what lies between rows is not
+ * touched.  dpred_clip_grads refuses gradients that share memory (DPRED_E_SIZE;
+ * matrices side by side in wider rows do not).  norm, result: device, fp32.
+ * workspace (device, 256-byte aligned): dpred_clip_workspace_bytes(n).
+ * Asynchronous on `stream`; may be captured into a CUDA graph.  Errors:
+ * DPRED_E_INVAL, DPRED_E_ALIGN,
  * DPRED_E_SIZE, DPRED_E_CUDA.
  */
 typedef struct {

@@ -40,3 +40,11 @@ def test_narrow_rows_are_counted_in_whole(L, rows, cols):
     rest = UNITS - units + 1
     narrow = dict(rows=rows, cols=cols, ld=cols + 1)
     assert refused(L, narrow, dict(data=P + (1 << 50), rows=rest, cols=8192, ld=8192))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=(1 << 31) - 1, cols=1 << 33, ld=1 << 33), dict(rows=1 << 24, cols=1 << 40, ld=1 << 40), dict(rows=2, cols=1, ld=(1 << 63) - 1),
+    dict(rows=1 << 30, cols=5, ld=1 << 33), dict(rows=3, cols=4, ld=1 << 62)], ids=str)
+def test_spans_that_no_address_reaches(L, bad):
+    """Their sizes in bytes do not fit 64 bits: alone, and behind another gradient."""
+    assert refused(L, bad) and refused(L, dict(data=P // 2, rows=2, cols=3, ld=3), bad)

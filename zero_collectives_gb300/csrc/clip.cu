@@ -410,7 +410,9 @@ int check_grads(const dpred_grad_tensor* g, int n) {
         if (t.rows < 0 || t.cols < 0) return set_error(DPRED_E_INVAL, "gradient %d: a negative size (%lld x %lld)", k, (long long)t.rows, (long long)t.cols);
         if (!dtype_ok(t.dtype)) return set_error(DPRED_E_INVAL, "gradient %d: unknown type %d", k, t.dtype);
         if (t.counted != 0 && t.counted != 1) return set_error(DPRED_E_INVAL, "gradient %d: counted must be 0 or 1", k);
-        if (t.rows > 0x7FFFFFFF || t.cols > ((int64_t)1 << 40))
+        // sizes in bytes, and differences of addresses, fit 64 bits
+        const int64_t most = (int64_t)1 << 60;
+        if (t.rows > 0x7FFFFFFF || t.cols > ((int64_t)1 << 40) || (t.rows > 1 && t.ld > most / t.rows))
             return set_error(DPRED_E_SIZE, "gradient %d: %lld x %lld is too large", k, (long long)t.rows, (long long)t.cols);
         const int rc = check_matrix(t.data, t.rows, t.cols, t.ld, esize(t.dtype), "a gradient");
         if (rc != DPRED_OK) return rc;
