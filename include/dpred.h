@@ -702,7 +702,8 @@ int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, const void* r, 
  * the norm; its order depends on the device and the shapes; the same call gives the same
  * bits.  An infinity among the counted gradients gives the norm infinity and
  * c = 0 (finite values become 0, infinities NaN), a NaN gives NaN everywhere.
- * No counted gradient: norm 0, c = 1.
+ * No counted gradient, or only empty ones: norm 0, c = 1 (as with eps = 0 where all
+ * are zero).
  *
  * grads: host array, read during the call only; row strides in elements (at least
  * cols), any size from 0 (rows up to 2^31 - 1, cols up to 2^40, their span up to
@@ -711,8 +712,7 @@ int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, const void* r, 
  * matrices side by side in wider rows do not).  norm, result: device, fp32.
  * workspace (device, 256-byte aligned): dpred_clip_workspace_bytes(n).
  * Asynchronous on `stream`; may be captured into a CUDA graph.  Errors:
- * DPRED_E_INVAL, DPRED_E_ALIGN,
- * DPRED_E_SIZE, DPRED_E_CUDA.
+ * DPRED_E_INVAL, DPRED_E_ALIGN, DPRED_E_SIZE, DPRED_E_CUDA.
  */
 typedef struct {
     void* data;      /* device, [rows, cols] of dtype */

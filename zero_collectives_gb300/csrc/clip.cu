@@ -324,8 +324,9 @@ __device__ __forceinline__ double total_of(const double* partial, int n) {
     return block_sum(v);
 }
 
-// The factor of the gradients; a NaN stays one.
-__device__ __forceinline__ float factor(double norm, float max_norm, float eps) {
+// The factor of the gradients; a NaN stays one.  Where none was counted it is 1.
+__device__ __forceinline__ float factor(bool counted, double norm, float max_norm, float eps) {
+    if (!counted) return 1.0f;
     const double down = norm + (double)eps;
     const double q = down == 0.0 ? 1.0 : (double)max_norm / down;
     return q >= 1.0 ? 1.0f : (float)q;
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_kernel(const __g
     const double sum = total_of(partial, n);
     if (threadIdx.x == 0) {
         const double norm = sqrt(sum);
-        coefficient = factor(norm, max_norm, eps);
+        coefficient = factor(n > 0, norm, max_norm, eps);
         if (blockIdx.x == 0 && out) {
             out[0] = (float)norm;
             out[1] = coefficient;
@@ -387,7 +388,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
     mma::cluster_sync();  // no block leaves while its sum is read
     const double norm = sqrt(sum);
-    const float c = SCALE ? factor(norm, max_norm, eps) : 1.0f;
+    const float c = SCALE ? factor(counted > 0, norm, max_norm, eps) : 1.0f;
     if (rank == 0 && threadIdx.x == 0) {
         out[0] = (float)norm;
         if (SCALE) out[1] = c;
