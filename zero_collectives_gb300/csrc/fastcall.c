@@ -293,7 +293,7 @@ static int numbers(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want, uns
     }
     return 0;
 }
-#define DPRED_F32(i) ((float)r[i])
+#define DPRED_REAL(i) ((float)r[i])
 
 static PyObject* embedding(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
@@ -304,7 +304,7 @@ static PyObject* embedding(PyObject* self, PyObject* const* args, Py_ssize_t nar
               void*) = DPRED_PTR(0);
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = fn(v[1], v[2], v[3], DPRED_I32(4), DPRED_PTR(5), DPRED_I32(6), DPRED_PTR(7), v[8], DPRED_F32(9), DPRED_I32(10),
+    rc = fn(v[1], v[2], v[3], DPRED_I32(4), DPRED_PTR(5), DPRED_I32(6), DPRED_PTR(7), v[8], DPRED_REAL(9), DPRED_I32(10),
             DPRED_PTR(11), v[12], DPRED_PTR(13));
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
@@ -319,7 +319,7 @@ static PyObject* embedding_grad(PyObject* self, PyObject* const* args, Py_ssize_
               int64_t, void*, size_t, void*) = DPRED_PTR(0);
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = fn(v[1], v[2], v[3], DPRED_I32(4), DPRED_PTR(5), v[6], DPRED_I32(7), DPRED_PTR(8), v[9], DPRED_F32(10), DPRED_I32(11),
+    rc = fn(v[1], v[2], v[3], DPRED_I32(4), DPRED_PTR(5), v[6], DPRED_I32(7), DPRED_PTR(8), v[9], DPRED_REAL(10), DPRED_I32(11),
             DPRED_I32(12), DPRED_PTR(13), v[14], DPRED_PTR(15), (size_t)v[16], DPRED_PTR(17));
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
@@ -335,7 +335,7 @@ static PyObject* block_norm(PyObject* self, PyObject* const* args, Py_ssize_t na
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = fn(v[1], v[2], DPRED_I32(3), DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_I32(8), DPRED_PTR(9), DPRED_I32(10), DPRED_PTR(11),
-            v[12], DPRED_F32(13), DPRED_I32(14), DPRED_PTR(15), DPRED_F32(16), DPRED_PTR(17), v[18], DPRED_PTR(19), v[20], DPRED_PTR(21));
+            v[12], DPRED_REAL(13), DPRED_I32(14), DPRED_PTR(15), DPRED_REAL(16), DPRED_PTR(17), v[18], DPRED_PTR(19), v[20], DPRED_PTR(21));
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
@@ -351,7 +351,7 @@ static PyObject* block_norm_grad(PyObject* self, PyObject* const* args, Py_ssize
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = fn(v[1], v[2], DPRED_I32(3), DPRED_PTR(4), v[5], DPRED_PTR(6), v[7], DPRED_PTR(8), v[9], DPRED_PTR(10), v[11], DPRED_I32(12),
-            DPRED_PTR(13), DPRED_I32(14), DPRED_PTR(15), v[16], DPRED_F32(17), DPRED_I32(18), DPRED_PTR(19), DPRED_F32(20), DPRED_PTR(21),
+            DPRED_PTR(13), DPRED_I32(14), DPRED_PTR(15), v[16], DPRED_REAL(17), DPRED_I32(18), DPRED_PTR(19), DPRED_REAL(20), DPRED_PTR(21),
             v[22], DPRED_PTR(23), v[24], DPRED_I32(25), DPRED_PTR(26), DPRED_PTR(27), DPRED_PTR(28), DPRED_I32(29), DPRED_PTR(30),
             (size_t)v[31], DPRED_PTR(32));
     Py_END_ALLOW_THREADS
@@ -379,7 +379,7 @@ static PyObject* clip_grads(PyObject* self, PyObject* const* args, Py_ssize_t na
     int (*fn)(const dpred_grad_tensor*, int32_t, float, float, float*, void*, size_t, void*) = DPRED_PTR(0);
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = fn(DPRED_PTR(1), DPRED_I32(2), DPRED_F32(3), DPRED_F32(4), DPRED_PTR(5), DPRED_PTR(6), (size_t)v[7], DPRED_PTR(8));
+    rc = fn(DPRED_PTR(1), DPRED_I32(2), DPRED_REAL(3), DPRED_REAL(4), DPRED_PTR(5), DPRED_PTR(6), (size_t)v[7], DPRED_PTR(8));
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
