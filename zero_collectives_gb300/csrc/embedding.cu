@@ -170,7 +170,7 @@ struct Counters {
 
 template <typename I, bool HALF>
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
-    extern __shared__ uint32_t counters[];  // [warps][words]
+    extern __shared__ __align__(16) uint32_t counters[];  // [warps][words]
     __shared__ int below[kSortWarps], sums[kSortWarps], starts[kMaxRows];
     __shared__ uint32_t bits[kMaxRows / 32];
     __shared__ int2 lists[kSortWarps][kList];  // row and token, in order
