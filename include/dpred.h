@@ -702,6 +702,7 @@ int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, const void* r, 
  * the norm; its order depends on the device and the shapes; the same call gives the same
  * bits.  An infinity among the counted gradients gives the norm infinity and
  * c = 0 (finite values become 0, infinities NaN), a NaN gives NaN everywhere.
+ * max_norm and eps are finite and not negative (dpred_grad_norm is the norm alone).
  * No counted gradient, or only empty ones: norm 0, c = 1 (as with eps = 0 where all
  * are zero).
  *

@@ -100,11 +100,12 @@ __global__ void __launch_bounds__(512) forward_kernel(const __grid_constant__ Fo
     }
 }
 
-// Many rows: a block for each SM has a stretch of them, and they come through a ring of bulk copies while rows before them are worked on.  The weights
-// lie in shared memory, post and a gate that all rows share as one product.  What
-// bounds it next to HBM is issue: LANES known to the compiler turns addresses into
-// immediates, and WHOLE (y, post and pre are there, and all rows share a gate)
-// spares the loop its tests.
+// Many rows: a block for each SM has a stretch of them, and they come through a ring of
+// bulk copies while rows before them are worked on.  The weights lie in shared memory,
+// post and a gate that all rows share as one product.  What bounds it next to HBM is
+// issue: LANES known to the compiler turns addresses into immediates, and WHOLE (y, post
+// and pre are there, and all rows share a gate) spares the loop its tests.  16384 x 1024,
+// bf16: 24.6 us, floor 20.0; 43196 x 777, rows of no alignment: 62 us, floor 40.
 template <typename T, bool VEC, int VPT, int LANES, bool WHOLE>
 __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_constant__ ForwardArgs a, const __grid_constant__ Rows in) {
     extern __shared__ __align__(128) char smem[];
@@ -124,7 +125,8 @@ __global__ void __launch_bounds__(512, 1) ring_forward_kernel(const __grid_const
     float* weights = reinterpret_cast<float*>(smem + kBarrierBytes + groups * in.stages * in.slot_bytes);
     const Staged<VEC, VPT> post = {weights, lanes}, pre = {weights + staged_floats(lanes, VPT), lanes};
     fill<VEC, VPT>(lanes, a.d, [&](int c, bool in_row, int at) {
-        const float w = has_pre && in_row ? a.pre.at(0, c) : 0.0f, p = has_y && in_row ? a.post.at(0, c) : 0.0f, q = has_y && in_row && !own_gate ? a.gate.at(0, c) : 1.0f;
+        const float w = has_pre && in_row ? a.pre.at(0, c) : 0.0f, p = has_y && in_row ? a.post.at(0, c) : 0.0f,
+                    q = has_y && in_row && !own_gate ? a.gate.at(0, c) : 1.0f;
         if (has_pre) pre.at[at] = w;
         if (has_y) post.at[at] = p * q;
     });
@@ -234,7 +236,11 @@ cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
         in.slot_bytes = in.slot();
         in.err = device_error_word();
         const int room = kRoom - 2 * 4 * staged_floats(q.lanes, q.vecs), groups = ring_groups(q, in.slot_bytes, room, 512);
-        // a ring is worth its start where a row group has several rows
+        // A ring is worth its start where a row group has several rows.  Device time by
+        // rows in registers / through rings, bf16 stream: 1216 x 1024 3.6 / 3.9 us, 4864
+        // 13.3 / 10.3, 7296 18.6 / 13.4; 3648 x 256 2.8 / 4.4, 7296 5.0 / 5.4, 14592
+        // 8.5 / 8.6; 4096 columns: 300 rows 4.0 / 5.1, 1216 15.2 / 13.2, 1800 21.9 / 16.2.
+        // Rows of any alignment gain earlier: 1216 x 777 8.0 / 5.6, 4864 32 / 9.9.
         if (groups > 0 && a.m > 2 * (int64_t)groups * sm_count()) {
             in.stages = ring_stages(groups, in.slot_bytes, room);
             if (VEC && a.y && a.post.p && a.pre.p && !in.seg[2].p) return launch_ring<T, VEC, VEC>(a, q, in, groups, s);

@@ -343,7 +343,8 @@ inline int check_norm(const NormShape& n) {
     if (some && !n.y && !n.pre) return set_error(DPRED_E_INVAL, "neither y nor pre: nothing to do");
     if (some && !n.y && (n.post || n.gate)) return set_error(DPRED_E_INVAL, "post and gate need y");
     if (some && !n.y && n.scale != 1.0f) return set_error(DPRED_E_INVAL, "without y, r is x: scale must be 1");
-    const struct { const void* p; int32_t dt; const char* name; } w[] = {{n.post, n.post_dtype, "post"}, {n.gate, n.gate_dtype, "gate"}, {n.pre, n.pre_dtype, "pre"}};
+    const struct { const void* p; int32_t dt; const char* name; } w[] = {
+        {n.post, n.post_dtype, "post"}, {n.gate, n.gate_dtype, "gate"}, {n.pre, n.pre_dtype, "pre"}};
     for (const auto& x : w) {
         if (!x.p) continue;
         if ((rc = check_dtype(x.dt, x.name)) != DPRED_OK) return rc;

@@ -147,8 +147,10 @@ extern "C" int dpred_block_norm_grad(int64_t m, int64_t d, int32_t r_dtype, cons
         return DPRED_OK;
     }
     const bool each = gate && gate_rows == m && m > 1;
-    const bool vec = weights_aligned(n) && (!pre || (aligned_rows(r, m, ldr, es) && aligned_rows(dh, m, lddh, 2))) && (!dr || aligned_rows(dr, m, lddr, es)) &&
-                     aligned_rows(dx, m, lddx, es) && (!each || reinterpret_cast<uintptr_t>(gate_grad) % 16 == 0) && (!y || (aligned_rows(y, m, ldy, 2) && aligned_rows(dy, m, lddy, 2)));
+    const bool vec = weights_aligned(n) && (!pre || (aligned_rows(r, m, ldr, es) && aligned_rows(dh, m, lddh, 2))) &&
+                     (!dr || aligned_rows(dr, m, lddr, es)) && aligned_rows(dx, m, lddx, es) &&
+                     (!each || reinterpret_cast<uintptr_t>(gate_grad) % 16 == 0) &&
+                     (!y || (aligned_rows(y, m, ldy, 2) && aligned_rows(dy, m, lddy, 2)));
     const Grid g = grid_of(m, d, gate ? gate_rows : 0, vec);
     const bool gate_sums = gate_grad && !each;
     if ((post_grad || pre_grad || gate_sums) && (rc = check_workspace(workspace, workspace_bytes, partial_bytes(g, d))) != DPRED_OK) return rc;

@@ -121,7 +121,11 @@ struct Walk {
 // groups that an SM holds cannot hide that (16384 x 1024 took 74 us).  A row that
 // fills the only slot is asked for when the one before it is done.
 // VEC: aligned rows, 8 columns next to each other a thread; otherwise every
-// LANES-th, element by element, past the copies.
+// LANES-th, read from the slots and stored element by element, with one thread working
+// out where the copies of a row begin and end (43196 x 777, bf16: 284 us, floor 60;
+// 16384 x 1024 in the aligned form 44 us, floor 30).  Rows of more than 8192 columns
+// come one at a time for each SM and are read three times from shared memory
+// (2730 x 12288, bf16: 160 us, floor 60).
 //
 // Where rows share a gate row, sum of g n_y over them gives both gradients:
 // dgate = post times it, dpost = gate times it, which is added per unit.
@@ -259,7 +263,8 @@ __global__ void __launch_bounds__(LANES == 512 ? 512 : kThreads, 1)
                 if (each) {
                     if (a.dgate.p) a.dgate.put8<VEC>(row, c0, lanes, a.d, g[v] * n * w8);
                     if (!in_place) {
-                        const Weight w = {slot + in.seg[4].at + (VEC ? 0 : reinterpret_cast<uintptr_t>(in.seg[4].p + row * in.seg[4].pitch) % 16), a.gate.f32, 0};
+                        const char* p = in.seg[4].p + row * in.seg[4].pitch;
+                        const Weight w = {slot + in.seg[4].at + (VEC ? 0 : reinterpret_cast<uintptr_t>(p) % 16), a.gate.f32, 0};
                         gate = w.load<VEC>(0, c0, lanes, a.d);
                     }
                     g[v] = g[v] * gate;
@@ -351,13 +356,13 @@ cudaError_t launch_rows(const BackwardArgs& a, const Rows& in, const Grid& g, in
         if (g.q.vecs == 4) return launch_kernel<T, VEC, 4, 512, WHOLE>(a, in, g, groups, s);
         return launch_kernel<T, VEC, 1, 32, WHOLE>(a, in, g, groups, s);
     } else {
-    if (g.q.vecs == 1) return launch_kernel<T, VEC, 1, 32, WHOLE>(a, in, g, groups, s);
-    if (g.q.vecs == 4) return launch_kernel<T, VEC, 4, 512, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 32) return launch_kernel<T, VEC, 2, 32, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 64) return launch_kernel<T, VEC, 2, 64, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 128) return launch_kernel<T, VEC, 2, 128, WHOLE>(a, in, g, groups, s);
-    if (g.q.lanes == 256) return launch_kernel<T, VEC, 2, 256, WHOLE>(a, in, g, groups, s);
-    return launch_kernel<T, VEC, 2, 512, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 1) return launch_kernel<T, VEC, 1, 32, WHOLE>(a, in, g, groups, s);
+        if (g.q.vecs == 4) return launch_kernel<T, VEC, 4, 512, WHOLE>(a, in, g, groups, s);
+        if (g.q.lanes == 32) return launch_kernel<T, VEC, 2, 32, WHOLE>(a, in, g, groups, s);
+        if (g.q.lanes == 64) return launch_kernel<T, VEC, 2, 64, WHOLE>(a, in, g, groups, s);
+        if (g.q.lanes == 128) return launch_kernel<T, VEC, 2, 128, WHOLE>(a, in, g, groups, s);
+        if (g.q.lanes == 256) return launch_kernel<T, VEC, 2, 256, WHOLE>(a, in, g, groups, s);
+        return launch_kernel<T, VEC, 2, 512, WHOLE>(a, in, g, groups, s);
     }
 }
 

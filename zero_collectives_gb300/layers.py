@@ -322,7 +322,8 @@ def grad_norm(grads, out=None, workspace=None, stream=None):
 def clip_grads(grads, max_norm: float, copies=(), eps: float = 1e-6, out=None, workspace=None, stream=None):
     """Scales the gradients in place by min(1, max_norm / (norm + eps)), norm their
     2-norm together; returns fp32 [2] on the device: norm and factor (see GradClip,
-    which keeps the table of a step's gradients)."""
+    which keeps the table of a step's gradients).  max_norm is finite: grad_norm is
+    the norm alone."""
     table, n = _grad_table(list(grads), list(copies))
     ws, *space = _clip_space(n, workspace, stream)
     return _clip((ctypes.addressof(table), n), space, max_norm, float(eps), out, stream)
