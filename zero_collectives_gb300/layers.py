@@ -247,11 +247,11 @@ class GradClip:
     min(1, max_norm / (norm + eps)).  grads: bf16 or fp32 tensors on the current
     device, contiguous or with strided rows; copies: further copies of some of
     them (such as those of a parameter that several ranks hold), which are scaled
-    and not counted.  Calls of one object scale the same gradients: use one stream,
-    or order the streams.  The workspace belongs to the stream that is current here;
-    a call on another one, or one that is captured, has memory of its own, so the
-    object may go as soon as a call has returned (a graph still needs the
-    gradients)."""
+    and not counted.  Calls of one object scale the same gradients and share its
+    workspace: one at a time, on one stream or on streams that are ordered.  The
+    workspace belongs to the stream that is current here; a call on another one, or
+    one that is captured, has memory of its own, so the object (the gradients are
+    another matter) may go as soon as a call has returned."""
 
     def __init__(self, grads, copies=(), eps: float = 1e-6):
         self.grads, self.copies, self.eps = list(grads), list(copies), float(eps)
